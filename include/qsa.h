@@ -300,6 +300,114 @@ qsa_status qsa_sparse_attn(const void* q, const void* k_cache, const void* v_cac
                            float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------
+ * The KV cache held in 4 bits.  (Library addition with no counterpart in the
+ * source pages, which read the original BF16 rows.)
+ *
+ *   k_codes, v_codes    [n_slots][h_kv][head_dim/2] bytes: two e2m1 values a
+ *                       byte, the even dimension in the low nibble;
+ *   k_scales, v_scales  [n_slots][h_kv][head_dim/16] bytes: one e4m3 scale
+ *                       per block of 16 dimensions (all four 16-byte aligned);
+ *   k_scale, v_scale    one scale for the whole tensor, a power of two
+ *                       between 2^-64 and 2^63 (else QSA_ERR_INVALID_ARG).
+ *
+ *   value = e2m1(code) * e4m3(scale) * k_scale   (v_scale for V)
+ *
+ * The value is exact in BF16.  head_dim 128 or 256 (else
+ * QSA_ERR_UNSUPPORTED).  Other slots of the cache are never touched.
+ *
+ * qsa_append_kv_fp4 quantises K and V rows into their slots:
+ *   k_new, v_new   n_tok rows of [h_kv][head_dim] BF16, ld_k / ld_v elements
+ *                  apart (a multiple of 16; bases 32-byte aligned): e.g. the
+ *                  K and V columns of one projection's output.
+ *   req_tok_start [n_req+1], req_first_pos [n_req]: as qsa_append_keys; the
+ *                  row of position p of request r goes to slot(p).  Rows
+ *                  behind req_tok_start[n_req] are not read.
+ *   Per block of 16: scale = e4m3(max|x| / k_scale / 6), code =
+ *   e2m1(x / k_scale / scale), nearest values with ties to even, saturating.
+ *   A block whose scale is zero becomes zeros; a block holding an infinity or
+ *   a NaN gets the NaN scale (0x7f) and reads back as NaN.  Two positions of
+ *   one call must not share a slot (pages that requests share are only read).
+ *   A position or page out of range is skipped and latches fault bit 0.
+ *
+ * qsa_gather_kv_fp4 reads rows back: k_out, v_out [n][h_kv][head_dim] BF16
+ *   (32-byte aligned), row i from slots[i]; a negative slot gives zeros, as
+ *   does a slot >= n_slots, which also latches fault bit 0.
+ * ------------------------------------------------------------------- */
+qsa_status qsa_append_kv_fp4(const void* k_new, const void* v_new, int64_t ld_k, int64_t ld_v, int32_t n_tok,
+                             int32_t h_kv, int32_t head_dim, const int32_t* req_tok_start,
+                             const int32_t* req_first_pos, int32_t n_req, const int32_t* page_table, int64_t ld_pt,
+                             int32_t page_size, float k_scale, float v_scale, void* k_codes, void* k_scales,
+                             void* v_codes, void* v_scales, int64_t n_slots, void* stream);
+qsa_status qsa_gather_kv_fp4(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                             int64_t n_slots, int32_t h_kv, int32_t head_dim, const int32_t* slots, int64_t n,
+                             float k_scale, float v_scale, void* k_out, void* v_out, void* stream);
+
+/* ---------------------------------------------------------------------
+ * Sparse attention over the selected slots, reading the 4-bit cache:
+ * qsa_sparse_attn with k_cache and v_cache replaced by the four arrays above.
+ * The cache's values enter the dot products and the value sums exactly; the
+ * softmax statistics are FP32 and the weights keep 22 significant bits.
+ *
+ *   q          n_rows rows of [h_q][head_dim] BF16, ld_q elements apart (a
+ *              multiple of 8; base 16-byte aligned).
+ *   out        [n_rows][h_q][head_dim] FP32 (16-byte aligned); lse
+ *              [n_rows][h_q] FP32 or NULL.
+ *   workspace  qsa_sparse_attn_fp4_workspace_size() bytes (16-byte aligned),
+ *              0 except for few rows of many entries.  Calls that may overlap
+ *              on the GPU need one each.
+ *
+ * h_q / h_kv up to 16 with head_dim 128 and up to 8 with 256, any number (else
+ * QSA_ERR_UNSUPPORTED).  Entries < 0 are skipped, entries >= n_slots too, with
+ * fault bit 0; a row without a valid entry gets out = 0 and lse = -inf.
+ * ------------------------------------------------------------------- */
+size_t qsa_sparse_attn_fp4_workspace_size(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t n_idx);
+qsa_status qsa_sparse_attn_fp4(const void* q, int64_t ld_q, const void* k_codes, const void* k_scales,
+                               const void* v_codes, const void* v_scales, int64_t n_slots, int32_t n_rows, int32_t h_q,
+                               int32_t h_kv, int32_t head_dim, const int32_t* slots, int64_t ld_slots, int32_t n_idx,
+                               float scale, float k_scale, float v_scale, float* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------
+ * Attention over a sliding window and the first tokens, through the page
+ * table: the layers that need no index.  (Library addition with no
+ * counterpart in the source pages.)
+ *
+ * A row that sees L = row_len[t] tokens attends to position j < L when
+ * j >= L - window (its own token counts) or j < n_sink.  window >= max_len is
+ * plain causal attention.  Per query head h (KV head h / (h_q / h_kv)):
+ *   out = sum_j softmax_j(scale <q_h, k_j>) v_j,  lse = log sum_j exp(...).
+ * A row with L = 0 gets out = 0 and lse = -inf; rows behind
+ * req_row_start[n_req] are left as they were.  Masked positions are not read
+ * into the result: an infinity or NaN there has no effect.
+ *
+ *   q, lse, shapes: as qsa_sparse_attn_fp4.
+ *   k_cache, v_cache [n_slots][h_kv][head_dim] BF16 (16-byte aligned), or the
+ *              four arrays of the 4-bit cache.
+ *   window >= 1, n_sink >= 0.
+ *   out        [n_rows][h_q][head_dim] BF16 (16-byte aligned): the next
+ *              operator is a BF16 projection.
+ *   workspace  qsa_window_attn_workspace_size() bytes (16-byte aligned), 0
+ *              except for few rows with long windows; as above.
+ *
+ * A page that does not lie wholly inside the cache is skipped and latches
+ * fault bit 0; a row_len outside [0, max_len] counts as 0 (bit 3).
+ * ------------------------------------------------------------------- */
+size_t qsa_window_attn_workspace_size(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t max_len,
+                                      int32_t window, int32_t n_sink);
+qsa_status qsa_window_attn(const void* q, int64_t ld_q, const void* k_cache, const void* v_cache, int64_t n_slots,
+                           int32_t n_req, const int32_t* req_row_start, int32_t n_rows, const int32_t* row_len,
+                           int32_t max_len, int32_t max_rows_per_req, int32_t h_q, int32_t h_kv, int32_t head_dim,
+                           const int32_t* page_table, int64_t ld_pt, int32_t page_size, int32_t window, int32_t n_sink,
+                           float scale, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+qsa_status qsa_window_attn_fp4(const void* q, int64_t ld_q, const void* k_codes, const void* k_scales,
+                               const void* v_codes, const void* v_scales, int64_t n_slots, int32_t n_req,
+                               const int32_t* req_row_start, int32_t n_rows, const int32_t* row_len, int32_t max_len,
+                               int32_t max_rows_per_req, int32_t h_q, int32_t h_kv, int32_t head_dim,
+                               const int32_t* page_table, int64_t ld_pt, int32_t page_size, int32_t window,
+                               int32_t n_sink, float scale, float k_scale, float v_scale, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------
  * Top-k_blk blocks of given block scores, expanded and translated, one
  * call  ([QSA] 512-block selection, 4 token positions per block followed by
  * the pending tokens; [TOPK] selection fused with the page-table transform).

@@ -21,7 +21,7 @@ __all__ = [
     "indexer_select", "indexer_select_workspace_size", "device_status", "out_width",
     "select_blocks", "indexshare_slots", "indexshare_width", "sparse_attn", "append_keys", "decode_step",
     "rope_queries", "quantize_keys_fp8", "index_scores_fp8", "indexer_select_fp8", "index_scores_gated",
-    "indexer_select_gated",
+    "indexer_select_gated", "append_kv_fp4", "gather_kv_fp4", "sparse_attn_fp4", "window_attn", "window_attn_fp4",
     "HEAD_DIM", "HEADS", "BLOCK", "MAX_K",
 ]
 
@@ -43,8 +43,8 @@ def lib():
             raise ImportError(f"libqsa.so not built at {LIB_PATH}: run build() first "
                               "(there is no CPU fallback)")
         L = ctypes.CDLL(LIB_PATH)
-        p, i32, i64, sz, d = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
-                              ctypes.c_double)
+        p, i32, i64, sz, d, f = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
+                                 ctypes.c_double, ctypes.c_float)
         sig = {
             "qsa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "qsa_version": (ctypes.c_int, []),
@@ -80,11 +80,22 @@ def lib():
                                                      i64, i32, i32, p, p, p, p, i64, p, sz, p]),
             "qsa_indexer_select_gated": (ctypes.c_int, [p, p, p, i64, i32, p, i32, p, i32, i32, p, i64, i32,
                                                         i32, p, p, p, p, i64, p, sz, p]),
+            "qsa_append_kv_fp4": (ctypes.c_int, [p, p, i64, i64, i32, i32, i32, p, p, i32, p, i64, i32, f, f, p, p,
+                                                 p, p, i64, p]),
+            "qsa_gather_kv_fp4": (ctypes.c_int, [p, p, p, p, i64, i32, i32, p, i64, f, f, p, p, p]),
+            "qsa_sparse_attn_fp4_workspace_size": (sz, [i32, i32, i32, i32, i32]),
+            "qsa_sparse_attn_fp4": (ctypes.c_int, [p, i64, p, p, p, p, i64, i32, i32, i32, i32, p, i64, i32, f, f, f,
+                                                   p, p, p, sz, p]),
+            "qsa_window_attn_workspace_size": (sz, [i32, i32, i32, i32, i32, i32, i32]),
+            "qsa_window_attn": (ctypes.c_int, [p, i64, p, p, i64, i32, p, i32, p, i32, i32, i32, i32, i32, p, i64,
+                                               i32, i32, i32, f, p, p, p, sz, p]),
+            "qsa_window_attn_fp4": (ctypes.c_int, [p, i64, p, p, p, p, i64, i32, p, i32, p, i32, i32, i32, i32, i32,
+                                                   p, i64, i32, i32, i32, f, f, f, p, p, p, sz, p]),
         }
         for name, (res, args) in sig.items():
-            f = getattr(L, name)
-            f.restype = res
-            f.argtypes = args
+            fn = getattr(L, name)
+            fn.restype = res
+            fn.argtypes = args
         _lib = L
     return _lib
 
@@ -600,3 +611,203 @@ def _indexer_select_call(fn, key_ptrs, pool_rows, q, req_row_start, row_len, pag
     if scores_out is not None:
         out["scores"] = scores_out
     return out
+
+
+# ----------------------------------------------------------------- 4-bit KV cache, window attention
+def _rows3(t, name):
+    """A BF16 tensor [n][heads][head_dim] whose rows are contiguous (they may
+    lie further apart, e.g. columns of a projection's output): its row pitch."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d != 1) or (s1 != d and h != 1):
+        raise ValueError(f"{name} must have contiguous rows of [heads][head_dim]")
+    return s0 if n > 1 else h * d
+
+
+def _cache4(k_codes, k_scales, v_codes, v_scales):
+    """Checks the four arrays of a 4-bit cache; returns (n_slots, h_kv, head_dim)."""
+    u8 = _torch().uint8
+    _dev(k_codes, u8, "k_codes", 3)
+    _dev(k_scales, u8, "k_scales", 3)
+    _dev(v_codes, u8, "v_codes", 3)
+    _dev(v_scales, u8, "v_scales", 3)
+    shape = k_codes.shape
+    n, h, w = shape
+    if v_codes.shape != shape or k_scales.shape != v_scales.shape or tuple(k_scales.shape) != (n, h, w // 8) or w % 8:
+        raise ValueError("codes must be [n_slots][h_kv][head_dim/2] and scales [n_slots][h_kv][head_dim/16]")
+    return n, h, 2 * w
+
+
+def _launch(fn, stream, first, others, *args):
+    """Calls `fn` on the device of tensor `first` (all tensors must be there),
+    on `stream` or that device's current stream."""
+    torch = _torch()
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn}: all tensors must be on the same device")
+    if dev == torch.cuda.current_device():
+        _check(fn, _call(fn, *args, _stream(stream, first.device)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, _call(fn, *args, _stream(stream, first.device)))
+
+
+def _attn_out(q, n_rows, h_q, d, dtype, out, lse, want_lse):
+    torch = _torch()
+    if out is None:
+        out = torch.empty((n_rows, h_q, d), dtype=dtype, device=q.device)
+    elif tuple(_dev(out, dtype, "out", 3).shape) != (n_rows, h_q, d):
+        raise ValueError("out must have q's shape")
+    if not want_lse:
+        return out, None
+    if lse is None:
+        lse = torch.empty((n_rows, h_q), dtype=torch.float32, device=q.device)
+    elif tuple(_dev(lse, torch.float32, "lse", 2).shape) != (n_rows, h_q):
+        raise ValueError("lse must be [n_rows][h_q]")
+    return out, lse
+
+
+def _attn_workspace(nbytes, workspace, q):
+    if workspace is None:
+        if not nbytes:
+            return None, 0
+        workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=q.device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def append_kv_fp4(k_new, v_new, req_tok_start, req_first_pos, k_codes, k_scales, v_codes, v_scales, page_table,
+                  page_size, k_scale=1.0, v_scale=1.0, stream=None):
+    """Quantises K and V rows [n_tok][h_kv][head_dim] bf16 into the 4-bit
+    cache (in place): request r's rows req_tok_start[r] .. go to the slots of
+    positions req_first_pos[r], req_first_pos[r]+1, ...  k_scale and v_scale
+    (powers of two) scale the whole tensors.  Returns the four arrays."""
+    torch = _torch()
+    ld_k, ld_v = _rows3(k_new, "k_new"), _rows3(v_new, "v_new")
+    _dev(req_tok_start, torch.int32, "req_tok_start", 1)
+    _dev(req_first_pos, torch.int32, "req_first_pos", 1)
+    _dev(page_table, torch.int32, "page_table", 2)
+    n_slots, h_kv, d = _cache4(k_codes, k_scales, v_codes, v_scales)
+    n_tok = k_new.shape[0]
+    n_req = req_first_pos.numel()
+    if tuple(k_new.shape) != (n_tok, h_kv, d) or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [n_tok][h_kv][head_dim] like the cache")
+    if req_tok_start.numel() != n_req + 1 or page_table.shape[0] != n_req:
+        raise ValueError("req_tok_start must have n_req+1 entries and page_table n_req rows")
+    _launch("qsa_append_kv_fp4", stream, k_codes,
+            (k_new, v_new, req_tok_start, req_first_pos, k_scales, v_codes, v_scales, page_table), k_new.data_ptr(),
+            v_new.data_ptr(), ld_k, ld_v, n_tok, h_kv, d, req_tok_start.data_ptr(), req_first_pos.data_ptr(), n_req,
+            page_table.data_ptr(), page_table.shape[1], int(page_size), float(k_scale), float(v_scale),
+            k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), n_slots)
+    return k_codes, k_scales, v_codes, v_scales
+
+
+def gather_kv_fp4(k_codes, k_scales, v_codes, v_scales, slots, k_scale=1.0, v_scale=1.0, k_out=None, v_out=None,
+                  stream=None):
+    """Reads the rows at slots (int32, any shape) back from the 4-bit cache:
+    (k, v) [*slots.shape][h_kv][head_dim] bf16; a negative slot gives zeros."""
+    torch = _torch()
+    n_slots, h_kv, d = _cache4(k_codes, k_scales, v_codes, v_scales)
+    _dev(slots, torch.int32, "slots")
+    shape = (*slots.shape, h_kv, d)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    _dev(k_out, torch.bfloat16, "k_out")
+    _dev(v_out, torch.bfloat16, "v_out")
+    if tuple(k_out.shape) != shape or tuple(v_out.shape) != shape:
+        raise ValueError("k_out and v_out must be [*slots.shape][h_kv][head_dim]")
+    _launch("qsa_gather_kv_fp4", stream, k_codes, (k_scales, v_codes, v_scales, slots, k_out, v_out),
+            k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), n_slots, h_kv, d,
+            slots.data_ptr(), slots.numel(), float(k_scale), float(v_scale), k_out.data_ptr(), v_out.data_ptr())
+    return k_out, v_out
+
+
+def sparse_attn_fp4(q, k_codes, k_scales, v_codes, v_scales, slots, scale=None, k_scale=1.0, v_scale=1.0, n_idx=None,
+                    out=None, lse=None, want_lse=True, workspace=None, stream=None):
+    """sparse_attn over the 4-bit cache: softmax attention of q
+    [n_rows][h_q][head_dim] bf16 over the rows at slots [n_rows][w] (int32,
+    -1 skipped).  Returns (out float32, lse [n_rows][h_q] or None)."""
+    torch = _torch()
+    ld_q = _rows3(q, "q")
+    n_slots, h_kv, d = _cache4(k_codes, k_scales, v_codes, v_scales)
+    _dev(slots, torch.int32, "slots", 2)
+    n_rows, h_q, d_q = q.shape
+    rows, width = slots.shape
+    if d_q != d or rows != n_rows:
+        raise ValueError("q, the cache and slots shapes disagree")
+    if n_idx is None:
+        n_idx = width
+    out, lse = _attn_out(q, n_rows, h_q, d, torch.float32, out, lse, want_lse)
+    workspace, ws_bytes = _attn_workspace(
+        _call("qsa_sparse_attn_fp4_workspace_size", n_rows, h_q, h_kv, d, int(n_idx)) if workspace is None else 0,
+        workspace, q)
+    _launch("qsa_sparse_attn_fp4", stream, q, (k_codes, k_scales, v_codes, v_scales, slots, out, lse, workspace),
+            q.data_ptr(), ld_q, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+            n_slots, n_rows, h_q, h_kv, d, slots.data_ptr(), width, int(n_idx),
+            float(d ** -0.5 if scale is None else scale), float(k_scale), float(v_scale), out.data_ptr(), _ptr(lse),
+            _ptr(workspace), ws_bytes)
+    return out, lse
+
+
+def window_attn(q, k_cache, v_cache, req_row_start, row_len, page_table, page_size, max_len, window, n_sink=0,
+                scale=None, max_rows_per_req=None, out=None, lse=None, want_lse=True, workspace=None, stream=None):
+    """Attention of q [n_rows][h_q][head_dim] bf16 over the last `window`
+    tokens each row sees (row_len, its own among them) and the first n_sink,
+    through the page table, on the BF16 cache [n_slots][h_kv][head_dim].
+    Returns (out bfloat16, lse [n_rows][h_q] float32 or None)."""
+    torch = _torch()
+    _dev(k_cache, torch.bfloat16, "k_cache", 3)
+    _dev(v_cache, torch.bfloat16, "v_cache", 3)
+    n_slots, h_kv, d = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    return _window_call("qsa_window_attn", (k_cache.data_ptr(), v_cache.data_ptr()), (), (k_cache, v_cache), n_slots,
+                        h_kv, d, q, req_row_start, row_len, page_table, page_size, max_len, window, n_sink, scale,
+                        max_rows_per_req, out, lse, want_lse, workspace, stream)
+
+
+def window_attn_fp4(q, k_codes, k_scales, v_codes, v_scales, req_row_start, row_len, page_table, page_size, max_len,
+                    window, n_sink=0, scale=None, k_scale=1.0, v_scale=1.0, max_rows_per_req=None, out=None, lse=None,
+                    want_lse=True, workspace=None, stream=None):
+    """window_attn over the 4-bit cache (for the rows of decode and verify
+    steps; for whole prompts read the window back with gather_kv_fp4)."""
+    n_slots, h_kv, d = _cache4(k_codes, k_scales, v_codes, v_scales)
+    return _window_call("qsa_window_attn_fp4",
+                        (k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr()),
+                        (float(k_scale), float(v_scale)), (k_codes, k_scales, v_codes, v_scales), n_slots, h_kv, d, q,
+                        req_row_start, row_len, page_table, page_size, max_len, window, n_sink, scale,
+                        max_rows_per_req, out, lse, want_lse, workspace, stream)
+
+
+def _window_call(fn, cache_ptrs, scales, cache, n_slots, h_kv, d, q, req_row_start, row_len, page_table, page_size,
+                 max_len, window, n_sink, scale, max_rows_per_req, out, lse, want_lse, workspace, stream):
+    torch = _torch()
+    ld_q = _rows3(q, "q")
+    _dev(req_row_start, torch.int32, "req_row_start", 1)
+    _dev(row_len, torch.int32, "row_len", 1)
+    _dev(page_table, torch.int32, "page_table", 2)
+    n_rows, h_q, d_q = q.shape
+    n_req, ld_pt = page_table.shape
+    if d_q != d or row_len.numel() != n_rows or req_row_start.numel() != n_req + 1:
+        raise ValueError("q, the cache, row_len, req_row_start and page_table shapes disagree")
+    if max_rows_per_req is None:
+        max_rows_per_req = n_rows
+    out, lse = _attn_out(q, n_rows, h_q, d, torch.bfloat16, out, lse, want_lse)
+    workspace, ws_bytes = _attn_workspace(
+        _call("qsa_window_attn_workspace_size", n_rows, h_q, h_kv, d, int(max_len), int(window), int(n_sink))
+        if workspace is None else 0, workspace, q)
+    _launch(fn, stream, q, (*cache, req_row_start, row_len, page_table, out, lse, workspace), q.data_ptr(), ld_q,
+            *cache_ptrs, n_slots, n_req, req_row_start.data_ptr(), n_rows, row_len.data_ptr(), int(max_len),
+            int(max_rows_per_req), h_q, h_kv, d, page_table.data_ptr(), ld_pt, int(page_size), int(window),
+            int(n_sink), float(d ** -0.5 if scale is None else scale), *scales, out.data_ptr(), _ptr(lse),
+            _ptr(workspace), ws_bytes)
+    return out, lse

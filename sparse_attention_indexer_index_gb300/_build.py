@@ -4,6 +4,7 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+import tempfile
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(_HERE, "csrc")
@@ -12,7 +13,7 @@ INCLUDE = os.path.join(os.path.dirname(_HERE), "include")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",
-    "-Xptxas", "-v", "-shared", "-Xcompiler", "-fPIC", "-I", INCLUDE,
+    "-Xptxas", "-v", "-Xcompiler", "-fPIC", "-I", INCLUDE,
 ]
 
 
@@ -40,12 +41,22 @@ def _build_lib(force: bool, verbose: bool) -> str:
     if not os.path.exists(nvcc) and os.path.exists("/usr/local/cuda/bin/nvcc"):
         nvcc = "/usr/local/cuda/bin/nvcc"
     tmp = LIB_PATH + f".{os.getpid()}.tmp"
-    cmd = [nvcc, *NVCC_FLAGS, "-o", tmp, *_sources()]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+    with tempfile.TemporaryDirectory() as obj_dir:
+        # one object per source, compiled side by side, then linked
+        objs, runs = [], []
+        for src in _sources():
+            objs.append(os.path.join(obj_dir, os.path.basename(src) + ".o"))
+            runs.append(subprocess.Popen([nvcc, *NVCC_FLAGS, "-c", "-o", objs[-1], src], stdout=subprocess.PIPE,
+                                         stderr=subprocess.PIPE, text=True))
+        said = [r.communicate() for r in runs]
+        for r, (out, err) in zip(runs, said):
+            if r.returncode != 0:
+                raise RuntimeError(f"nvcc failed ({r.returncode}):\n{out}\n{err}")
+        r = subprocess.run([nvcc, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
     if verbose:
-        print(r.stderr)
+        print("\n".join(err for _, err in said))
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -130,6 +130,127 @@ static PyObject* fc_indexer_select_gated(PyObject* self, PyObject* const* a, Py_
   return indexer_select_impl(a, n, 1);
 }
 
+/* The calls of the 4-bit cache and the window attention: one argument after
+ * the other in the C function's order. */
+static float arg_f32(PyObject* const* a, Py_ssize_t i) { return (float)PyFloat_AsDouble(a[i]); }
+
+static PyObject* fc_append_kv_fp4(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 21, "append_kv_fp4")) return NULL;
+  const void *k_new = arg_ptr(a, 0), *v_new = arg_ptr(a, 1);
+  const int64_t ld_k = arg_i64(a, 2), ld_v = arg_i64(a, 3);
+  const int32_t n_tok = arg_i32(a, 4), h_kv = arg_i32(a, 5), d = arg_i32(a, 6);
+  const int32_t *start = arg_ptr(a, 7), *first = arg_ptr(a, 8);
+  const int32_t n_req = arg_i32(a, 9);
+  const int32_t* pt = arg_ptr(a, 10);
+  const int64_t ld_pt = arg_i64(a, 11);
+  const int32_t page = arg_i32(a, 12);
+  const float ks = arg_f32(a, 13), vs = arg_f32(a, 14);
+  void *c0 = arg_ptr(a, 15), *c1 = arg_ptr(a, 16), *c2 = arg_ptr(a, 17), *c3 = arg_ptr(a, 18);
+  const int64_t n_slots = arg_i64(a, 19);
+  void* stream = arg_ptr(a, 20);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromLong((long)qsa_append_kv_fp4(k_new, v_new, ld_k, ld_v, n_tok, h_kv, d, start, first, n_req, pt,
+                                                 ld_pt, page, ks, vs, c0, c1, c2, c3, n_slots, stream));
+}
+
+static PyObject* fc_gather_kv_fp4(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 14, "gather_kv_fp4")) return NULL;
+  const void *c0 = arg_ptr(a, 0), *c1 = arg_ptr(a, 1), *c2 = arg_ptr(a, 2), *c3 = arg_ptr(a, 3);
+  const int64_t n_slots = arg_i64(a, 4);
+  const int32_t h_kv = arg_i32(a, 5), d = arg_i32(a, 6);
+  const int32_t* slots = arg_ptr(a, 7);
+  const int64_t cnt = arg_i64(a, 8);
+  const float ks = arg_f32(a, 9), vs = arg_f32(a, 10);
+  void *k_out = arg_ptr(a, 11), *v_out = arg_ptr(a, 12), *stream = arg_ptr(a, 13);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromLong((long)qsa_gather_kv_fp4(c0, c1, c2, c3, n_slots, h_kv, d, slots, cnt, ks, vs, k_out, v_out,
+                                                 stream));
+}
+
+static PyObject* fc_sparse_attn_fp4(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 22, "sparse_attn_fp4")) return NULL;
+  const void* q = arg_ptr(a, 0);
+  const int64_t ld_q = arg_i64(a, 1);
+  const void *c0 = arg_ptr(a, 2), *c1 = arg_ptr(a, 3), *c2 = arg_ptr(a, 4), *c3 = arg_ptr(a, 5);
+  const int64_t n_slots = arg_i64(a, 6);
+  const int32_t n_rows = arg_i32(a, 7), h_q = arg_i32(a, 8), h_kv = arg_i32(a, 9), d = arg_i32(a, 10);
+  const int32_t* slots = arg_ptr(a, 11);
+  const int64_t ld_slots = arg_i64(a, 12);
+  const int32_t n_idx = arg_i32(a, 13);
+  const float scale = arg_f32(a, 14), ks = arg_f32(a, 15), vs = arg_f32(a, 16);
+  float *out = arg_ptr(a, 17), *lse = arg_ptr(a, 18);
+  void* ws = arg_ptr(a, 19);
+  const size_t ws_bytes = arg_size(a, 20);
+  void* stream = arg_ptr(a, 21);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromLong((long)qsa_sparse_attn_fp4(q, ld_q, c0, c1, c2, c3, n_slots, n_rows, h_q, h_kv, d, slots,
+                                                   ld_slots, n_idx, scale, ks, vs, out, lse, ws, ws_bytes, stream));
+}
+
+/* qsa_window_attn (two cache arrays, no tensor scales) and
+ * qsa_window_attn_fp4 (four arrays, two scales). */
+static PyObject* window_attn_impl(PyObject* const* a, Py_ssize_t n, int fp4) {
+  const Py_ssize_t c = fp4 ? 2 : 0;
+  if (!want_args(n, 25 + 2 * c, fp4 ? "window_attn_fp4" : "window_attn")) return NULL;
+  const void* q = arg_ptr(a, 0);
+  const int64_t ld_q = arg_i64(a, 1);
+  const void *c0 = arg_ptr(a, 2), *c1 = arg_ptr(a, 3);
+  const void *c2 = fp4 ? arg_ptr(a, 4) : NULL, *c3 = fp4 ? arg_ptr(a, 5) : NULL;
+  const int64_t n_slots = arg_i64(a, 4 + c);
+  const int32_t n_req = arg_i32(a, 5 + c);
+  const int32_t* start = arg_ptr(a, 6 + c);
+  const int32_t n_rows = arg_i32(a, 7 + c);
+  const int32_t* row_len = arg_ptr(a, 8 + c);
+  const int32_t max_len = arg_i32(a, 9 + c), max_rows = arg_i32(a, 10 + c);
+  const int32_t h_q = arg_i32(a, 11 + c), h_kv = arg_i32(a, 12 + c), d = arg_i32(a, 13 + c);
+  const int32_t* pt = arg_ptr(a, 14 + c);
+  const int64_t ld_pt = arg_i64(a, 15 + c);
+  const int32_t page = arg_i32(a, 16 + c), window = arg_i32(a, 17 + c), sinks = arg_i32(a, 18 + c);
+  const float scale = arg_f32(a, 19 + c);
+  const float ks = fp4 ? arg_f32(a, 22) : 1.0f, vs = fp4 ? arg_f32(a, 23) : 1.0f;
+  void* out = arg_ptr(a, 20 + 2 * c);
+  float* lse = arg_ptr(a, 21 + 2 * c);
+  void* ws = arg_ptr(a, 22 + 2 * c);
+  const size_t ws_bytes = arg_size(a, 23 + 2 * c);
+  void* stream = arg_ptr(a, 24 + 2 * c);
+  if (PyErr_Occurred()) return NULL;
+  const qsa_status st =
+      fp4 ? qsa_window_attn_fp4(q, ld_q, c0, c1, c2, c3, n_slots, n_req, start, n_rows, row_len, max_len, max_rows,
+                                h_q, h_kv, d, pt, ld_pt, page, window, sinks, scale, ks, vs, out, lse, ws, ws_bytes,
+                                stream)
+          : qsa_window_attn(q, ld_q, c0, c1, n_slots, n_req, start, n_rows, row_len, max_len, max_rows, h_q, h_kv, d,
+                            pt, ld_pt, page, window, sinks, scale, out, lse, ws, ws_bytes, stream);
+  return PyLong_FromLong((long)st);
+}
+static PyObject* fc_window_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  return window_attn_impl(a, n, 0);
+}
+static PyObject* fc_window_attn_fp4(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  return window_attn_impl(a, n, 1);
+}
+
+/* The workspace queries of those calls: int32 arguments, a size. */
+static PyObject* fc_sparse_attn_fp4_workspace_size(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 5, "sparse_attn_fp4_workspace_size")) return NULL;
+  const int32_t v0 = arg_i32(a, 0), v1 = arg_i32(a, 1), v2 = arg_i32(a, 2), v3 = arg_i32(a, 3), v4 = arg_i32(a, 4);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromSize_t(qsa_sparse_attn_fp4_workspace_size(v0, v1, v2, v3, v4));
+}
+static PyObject* fc_window_attn_workspace_size(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 7, "window_attn_workspace_size")) return NULL;
+  const int32_t v0 = arg_i32(a, 0), v1 = arg_i32(a, 1), v2 = arg_i32(a, 2), v3 = arg_i32(a, 3), v4 = arg_i32(a, 4);
+  const int32_t v5 = arg_i32(a, 5), v6 = arg_i32(a, 6);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromSize_t(qsa_window_attn_workspace_size(v0, v1, v2, v3, v4, v5, v6));
+}
+
 static PyMethodDef fc_methods[] = {
     {"qsa_decode_step", (PyCFunction)(void (*)(void))fc_decode_step, METH_FASTCALL, "qsa_decode_step"},
     {"qsa_decode_step_gated", (PyCFunction)(void (*)(void))fc_decode_step_gated, METH_FASTCALL,
@@ -137,6 +258,13 @@ static PyMethodDef fc_methods[] = {
     {"qsa_indexer_select", (PyCFunction)(void (*)(void))fc_indexer_select, METH_FASTCALL, "qsa_indexer_select"},
     {"qsa_indexer_select_gated", (PyCFunction)(void (*)(void))fc_indexer_select_gated, METH_FASTCALL,
      "qsa_indexer_select_gated"},
+    {"qsa_append_kv_fp4", (PyCFunction)(void (*)(void))fc_append_kv_fp4, METH_FASTCALL, "qsa_append_kv_fp4"},
+    {"qsa_gather_kv_fp4", (PyCFunction)(void (*)(void))fc_gather_kv_fp4, METH_FASTCALL, "qsa_gather_kv_fp4"},
+    {"qsa_sparse_attn_fp4", (PyCFunction)(void (*)(void))fc_sparse_attn_fp4, METH_FASTCALL, "qsa_sparse_attn_fp4"},
+    {"qsa_window_attn", (PyCFunction)(void (*)(void))fc_window_attn, METH_FASTCALL, "qsa_window_attn"},
+    {"qsa_window_attn_fp4", (PyCFunction)(void (*)(void))fc_window_attn_fp4, METH_FASTCALL, "qsa_window_attn_fp4"},
+    {"qsa_sparse_attn_fp4_workspace_size", (PyCFunction)(void (*)(void))fc_sparse_attn_fp4_workspace_size, METH_FASTCALL, "qsa_sparse_attn_fp4_workspace_size"},
+    {"qsa_window_attn_workspace_size", (PyCFunction)(void (*)(void))fc_window_attn_workspace_size, METH_FASTCALL, "qsa_window_attn_workspace_size"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef fc_module = {PyModuleDef_HEAD_INIT,

@@ -1,0 +1,222 @@
+// kv4.cuh -- the 4-bit KV cache: its format, the kernel that quantises K and
+// V rows as they are written, and the kernel that reads rows back.
+//
+// Format.  A physical KV slot holds, per KV head, D e2m1 values (two to a
+// byte, the even dimension in the low nibble) and one e4m3 scale per block
+// of 16 of them:
+//     codes  [n_slots][h_kv][D/2]     scales [n_slots][h_kv][D/16]
+//     value = e2m1(code) * e4m3(scale) * g
+// g is one scale for the whole tensor, a power of two given by the caller.
+// 4.5 bits a value.  e2m1 has a 2-bit and e4m3 a 4-bit significand, so a
+// value has at most 6 significant bits: the product is exact in FP16 without
+// g (largest 6 * 448 = 2688, smallest 2^-10) and exact in BF16 with it.
+// Reading the cache therefore rounds nothing; only writing does.
+//
+// Writing a block x[0..15]:
+//     scale = e4m3(max|x| / g / 6)     (nearest even; max|x| / g is exact)
+//     code  = e2m1(x / g / scale)      (nearest even, saturating at 6)
+// Both divisions are FP32.  x / g is a BF16 number and the rounding borders
+// are products of at most 6 significant bits, so a quotient that is not on a
+// border is at least 2^-14 away from it and the FP32 rounding of the
+// division never decides.  A block whose scale rounds to zero holds zeros; a
+// block with an infinity or a NaN gets the NaN scale and reads back as NaN,
+// so that a broken row shows instead of being clipped.
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace qsa {
+
+constexpr int kKvBlock = 16;     // values per scale
+constexpr int kKvThreads = 128;  // threads per CTA of the write and read kernels
+
+// 32 bytes in one instruction (32-byte aligned).
+struct U8 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ U8 ld_stream_32(const void* p) {
+  U8 r;
+  asm("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+        "=r"(r.w[7])
+      : "l"(p));
+  return r;
+}
+__device__ __forceinline__ void st_32(void* p, const U8& r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]),
+               "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+               : "memory");
+}
+
+// One block of 16 BF16 values -> its codes (8 bytes) and scale byte.
+__device__ __forceinline__ uint2 kv4_quantise(const U8& x, float inv_g, uint8_t& scale) {
+  // max |x| on the bit patterns: infinities and NaN come out on top
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx = __vmaxu2(mx, x.w[i] & 0x7fff7fffu);
+  const uint32_t top = max(mx & 0xffffu, mx >> 16);
+  float inv = 0.f;
+  if (top >= 0x7f80u) {
+    scale = 0x7f;
+  } else {
+    scale = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top << 16) * inv_g, 6.0f), __NV_SATFINITE,
+                                           __NV_E4M3);
+    const __half_raw s = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)scale, __NV_E4M3);
+    inv = __half2float(__half(s));
+  }
+  uint32_t c[2] = {0u, 0u};
+  if (inv != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float2 f = bf16x2_to_float2(x.w[i]);
+      f.x = __fdiv_rn(f.x * inv_g, inv);
+      f.y = __fdiv_rn(f.y * inv_g, inv);
+      const uint32_t b = __nv_cvt_float2_to_fp4x2(f, __NV_E2M1, cudaRoundNearest);
+      c[i >> 2] |= (b & 0xffu) << (8 * (i & 3));
+    }
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+// Two codes of a byte -> two FP16 values (exact).
+__device__ __forceinline__ __half2 kv4_pair(uint32_t byte) {
+  return __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1));
+}
+// Two scale bytes -> two FP16 scales (exact).
+__device__ __forceinline__ __half2 kv4_scales(uint32_t two) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
+}
+
+// One block's codes and scale -> 16 BF16 values.
+__device__ __forceinline__ U8 kv4_read(uint2 codes, uint32_t scale, float g) {
+  const __half2 s = kv4_scales(scale | (scale << 8));
+  const uint32_t c[2] = {codes.x, codes.y};
+  U8 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __half22float2(__hmul2(kv4_pair((c[i >> 2] >> (8 * (i & 3))) & 0xffu), s));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * g, f.y * g);
+    r.w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return r;
+}
+
+// Request of row t by a whole warp: the r with start[r] <= t < start[r+1],
+// or -1 when t lies behind start[n_req] (or before start[0]).  32 samples a
+// round, so one round trip to memory for up to 32 requests and two for up to
+// 1024 (a binary search takes five and ten).
+__device__ __forceinline__ int warp_row_request(const int32_t* __restrict__ start, int n_req, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = n_req + 1;  // candidates lo .. lo + n - 1 of the last start <= t
+  while (true) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const bool le = i < n && __ldg(start + lo + i) <= t;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));  // starts do not decrease
+    if (c == 0) return -1;
+    lo += (c - 1) * step;
+    n = min(step, n - (c - 1) * step);
+    if (step == 1) break;
+  }
+  return lo < n_req ? lo : -1;
+}
+
+struct KvWriteArgs {
+  const uint16_t* k_new;         // [n_tok] rows of h_kv * D BF16, ld_k apart
+  const uint16_t* v_new;
+  int64_t ld_k, ld_v;
+  int32_t n_tok, h_kv;
+  int32_t blocks;                // blocks of a token: h_kv * D / 16
+  const int32_t* req_tok_start;  // [n_req+1]
+  const int32_t* req_first_pos;  // [n_req]
+  int32_t n_req;
+  const int32_t* page_table;
+  int64_t ld_pt;
+  int32_t page_size;
+  int64_t n_slots;
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  float k_inv, v_inv;            // 1 / g
+};
+
+// K and V rows quantised into their slots.  One thread per block of 16 of K
+// and the same block of V.  Per block 64 B read and 18 B written: HBM-bound
+// in bulk, a chain of four dependent loads (request, position, page, data)
+// in a decode step; the data loads go out before the slot is known.
+__global__ void __launch_bounds__(kKvThreads)
+append_kv_fp4_kernel(KvWriteArgs a) {
+  const int64_t u0 = (int64_t)blockIdx.x * kKvThreads + (threadIdx.x & ~31);
+  const int64_t total = (int64_t)a.n_tok * a.blocks;
+  if (u0 >= total) return;  // the whole warp
+  const int64_t u = u0 + (threadIdx.x & 31);
+  const bool ok = u < total;
+  const int t = ok ? (int)(u / a.blocks) : a.n_tok - 1;
+  const int b = ok ? (int)(u - (int64_t)t * a.blocks) : 0;
+  U8 kx{}, vx{};
+  if (ok) {
+    kx = ld_stream_32(a.k_new + (int64_t)t * a.ld_k + b * kKvBlock);
+    vx = ld_stream_32(a.v_new + (int64_t)t * a.ld_v + b * kKvBlock);
+  }
+  int r = warp_row_request(a.req_tok_start, a.n_req, (int)(u0 / a.blocks));  // of the warp's first token
+  if (!ok || r < 0) return;
+  while (r < a.n_req && t >= __ldg(a.req_tok_start + r + 1)) ++r;  // a warp may span tokens
+  if (r >= a.n_req) return;  // behind the last request
+  const int64_t pos = (int64_t)__ldg(a.req_first_pos + r) + (t - __ldg(a.req_tok_start + r));
+  const int64_t pi = pos / a.page_size;
+  if (pos < 0 || pi >= a.ld_pt) {
+    raise_fault(kFaultIndex);
+    return;
+  }
+  const int64_t page = __ldg(a.page_table + (int64_t)r * a.ld_pt + pi);
+  const int64_t slot = page * a.page_size + (pos - pi * a.page_size);
+  if (page < 0 || slot >= a.n_slots) {
+    raise_fault(kFaultIndex);
+    return;
+  }
+  const int64_t at = slot * a.blocks + b;
+  uint8_t sk, sv;
+  const uint2 ck = kv4_quantise(kx, a.k_inv, sk);
+  const uint2 cv = kv4_quantise(vx, a.v_inv, sv);
+  reinterpret_cast<uint2*>(a.k_codes)[at] = ck;
+  reinterpret_cast<uint2*>(a.v_codes)[at] = cv;
+  a.k_scales[at] = sk;
+  a.v_scales[at] = sv;
+}
+
+struct KvReadArgs {
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int64_t n_slots;
+  int32_t blocks;        // blocks of a slot
+  const int32_t* slots;  // [n]
+  int64_t n;
+  float k_g, v_g;
+  uint16_t *k_out, *v_out;  // [n][h_kv][D] BF16
+};
+
+// Rows read back at slots: one thread per block of 16 of K and of V.  Per
+// block 18 B read and 64 B written, HBM-bound by the writes.
+__global__ void __launch_bounds__(kKvThreads)
+gather_kv_fp4_kernel(KvReadArgs a) {
+  const int64_t u = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
+  if (u >= a.n * a.blocks) return;
+  const int64_t i = u / a.blocks;
+  const int b = (int)(u - i * a.blocks);
+  const int32_t s = __ldg(a.slots + i);
+  U8 k{}, v{};
+  if (s >= 0 && s < a.n_slots) {
+    const int64_t at = (int64_t)s * a.blocks + b;
+    const uint2 ck = __ldg(reinterpret_cast<const uint2*>(a.k_codes) + at);
+    const uint2 cv = __ldg(reinterpret_cast<const uint2*>(a.v_codes) + at);
+    const uint32_t sk = __ldg(a.k_scales + at), sv = __ldg(a.v_scales + at);
+    k = kv4_read(ck, sk, a.k_g);
+    v = kv4_read(cv, sv, a.v_g);
+  } else if (s >= 0 && b == 0) {
+    raise_fault(kFaultIndex);
+  }
+  st_32(a.k_out + u * kKvBlock, k);
+  st_32(a.v_out + u * kKvBlock, v);
+}
+
+}  // namespace qsa

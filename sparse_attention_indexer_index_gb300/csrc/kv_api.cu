@@ -1,0 +1,383 @@
+// kv_api.cu -- the extern "C" entry points of the 4-bit KV cache and of the
+// attention over a window: host-side argument checks, launch shapes, and
+// launches on the caller's stream.  Contracts are in include/qsa.h.
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "../../include/qsa.h"
+#include "common.cuh"
+#include "host_util.cuh"
+#include "kv4.cuh"
+#include "kv_attn.cuh"
+
+using namespace qsa;
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+template <int D, int NT, bool kFp4, bool kWindow>
+bool set_ka_smem() {
+  return cudaFuncSetAttribute(kv_attn_kernel<D, NT, kFp4, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)ka_smem_bytes<D, NT, kFp4>()) == cudaSuccess;
+}
+
+// Per-device one-time set-up: the shared-memory opt-in of the kernels.
+bool g_ready[kMaxDevices];
+std::mutex g_mu;
+qsa_status kv_device_ready() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QSA_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_ready[dev]) return QSA_OK;
+  if (!set_ka_smem<256, 1, true, false>() || !set_ka_smem<128, 1, true, false>() ||
+      !set_ka_smem<128, 2, true, false>() || !set_ka_smem<256, 1, true, true>() ||
+      !set_ka_smem<128, 1, true, true>() || !set_ka_smem<128, 2, true, true>() ||
+      !set_ka_smem<256, 1, false, true>() || !set_ka_smem<128, 1, false, true>() ||
+      !set_ka_smem<128, 2, false, true>()) {
+    cudaGetLastError();
+    return QSA_ERR_CUDA;
+  }
+  g_ready[dev] = true;
+  return QSA_OK;
+}
+
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+// A tensor scale: a positive power of two between 2^-64 and 2^63.
+bool scale_ok(float g) {
+  int e = 0;
+  return std::isfinite(g) && g > 0.f && std::frexp(g, &e) == 0.5f && e >= -63 && e <= 64;
+}
+
+// Heads and head dims of the calls here: 128 with up to 16 query heads per
+// KV head, 256 with up to 8.
+bool kv_shape_ok(int32_t h_q, int32_t h_kv, int32_t d) {
+  if (h_q <= 0 || h_kv <= 0 || h_kv > 65535 || h_q % h_kv != 0) return false;
+  const int group = h_q / h_kv;
+  return (d == 128 && group <= 16) || (d == 256 && group <= 8);
+}
+
+// Clusters per (row, KV head).  One, unless the clusters of 8 CTAs are too
+// few to fill the GPU and a row is long enough to pay for the merge launch.
+// The size of the workspace follows from it, so it depends on the arguments
+// alone (152 SMs, two CTAs each).
+constexpr int kKaCtaSlots = 304;
+int ka_groups(int64_t units, int64_t entries) {
+  const int64_t fill = kKaCtaSlots / (units * kKaMaxCluster);
+  const int64_t steps = entries / (kKaTile * kKaWarps * kKaMaxCluster);  // of a warp, with one cluster
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, 16), steps / 8));
+}
+
+// CTAs per cluster: the least of waves * (steps of a warp + start and end).
+int ka_cluster(int64_t units, int64_t entries, int slots) {
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int c = 1; c <= kKaMaxCluster; ++c) {
+    const int64_t waves = (units * c + slots - 1) / slots;
+    const int64_t steps = (entries + (int64_t)kKaTile * kKaWarps * c - 1) / ((int64_t)kKaTile * kKaWarps * c);
+    const int64_t cost = waves * (steps + 4);
+    if (cost < least) {
+      least = cost;
+      best = c;
+    }
+  }
+  return best;
+}
+
+template <int D, int NT, bool kFp4, bool kWindow>
+qsa_status launch_ka(const KvAttnArgs& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.n_rows * a.cluster * a.n_group), (unsigned)a.h_kv, 1);
+  cfg.blockDim = dim3(kKaThreads, 1, 1);
+  cfg.dynamicSmemBytes = ka_smem_bytes<D, NT, kFp4>();
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NT, kFp4, kWindow>, a);
+  if (e == cudaSuccess && a.n_group > 1)
+    e = launch_pdl(kv_attn_merge_kernel<D>, dim3((unsigned)((int64_t)a.n_rows * a.h_q)), dim3(D), 0, stream, a,
+                   kFp4 ? 10.0f : 0.0f);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return QSA_ERR_CUDA;
+  }
+  return QSA_OK;
+}
+
+template <bool kFp4, bool kWindow>
+qsa_status launch_ka_shape(KvAttnArgs& a, int d, int64_t entries, void* workspace, cudaStream_t stream) {
+  const int64_t units = (int64_t)a.n_rows * a.h_kv;
+  a.group = a.h_q / a.h_kv;
+  a.n_group = ka_groups(units, entries);
+  a.cluster = a.n_group > 1 ? kKaMaxCluster
+                            : ka_cluster(units, entries, kKaCtaSlots / ((!kFp4 && d == 256) ? 2 : 1));
+  a.part = static_cast<float*>(workspace);
+  if ((int64_t)a.n_rows * std::max(a.cluster * a.n_group, a.h_q) > INT32_MAX) return QSA_ERR_UNSUPPORTED;
+  if (entries > (1 << 30)) return QSA_ERR_UNSUPPORTED;  // entry indices stay clear of 2^31
+  if (qsa_status st = kv_device_ready()) return st;
+  if (d == 256) return launch_ka<256, 1, kFp4, kWindow>(a, stream);
+  return a.group <= 8 ? launch_ka<128, 1, kFp4, kWindow>(a, stream) : launch_ka<128, 2, kFp4, kWindow>(a, stream);
+}
+
+size_t ka_workspace(int64_t n_rows, int32_t h_q, int32_t h_kv, int32_t d, int64_t entries) {
+  if (n_rows <= 0 || entries <= 0 || !kv_shape_ok(h_q, h_kv, d)) return 0;
+  const int ng = ka_groups(n_rows * h_kv, entries);
+  return ng > 1 ? (size_t)(n_rows * h_q * ng * (d + 2) * 4) : 0;
+}
+
+int64_t window_entries(int32_t max_len, int32_t window, int32_t n_sink) {
+  return std::min<int64_t>(max_len, (int64_t)window + n_sink);
+}
+
+qsa_status check_workspace(size_t need, const void* workspace, size_t bytes) {
+  if (need == 0) return QSA_OK;
+  if (!workspace || bytes < need) return QSA_ERR_WORKSPACE_TOO_SMALL;
+  return aligned16(workspace) ? QSA_OK : QSA_ERR_INVALID_ARG;
+}
+
+// The 4-bit cache's four arrays (any of them may be NULL with n_slots 0).
+qsa_status check_cache4(const void* kc, const void* ks, const void* vc, const void* vs, int64_t n_slots) {
+  if (n_slots < 0 || n_slots > INT32_MAX) return QSA_ERR_INVALID_ARG;
+  if (n_slots > 0 && (!kc || !ks || !vc || !vs)) return QSA_ERR_INVALID_ARG;
+  return aligned16(kc) && aligned16(ks) && aligned16(vc) && aligned16(vs) ? QSA_OK : QSA_ERR_INVALID_ARG;
+}
+
+// Arguments that both window calls share.
+qsa_status check_window(const void* q, int64_t ld_q, int64_t n_slots, int32_t n_req, const int32_t* req_row_start,
+                        int32_t n_rows, const int32_t* row_len, int32_t max_len, int32_t max_rows_per_req, int32_t h_q,
+                        int32_t h_kv, int32_t d, const int32_t* page_table, int64_t ld_pt, int32_t page_size,
+                        int32_t window, int32_t n_sink, const void* out, const void* lse) {
+  if (window < 1 || n_sink < 0 || max_rows_per_req < 0 || n_slots < 0 || n_slots > INT32_MAX) return QSA_ERR_INVALID_ARG;
+  if (!kv_shape_ok(h_q, h_kv, d)) return QSA_ERR_UNSUPPORTED;
+  if (qsa_status st = check_rows(n_req, req_row_start, n_rows, row_len, max_len)) return st;
+  if (n_rows == 0) return QSA_OK;
+  if (qsa_status st = check_paging(page_table, ld_pt, page_size, max_len)) return st;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || (lse && !aligned4(lse))) return QSA_ERR_INVALID_ARG;
+  if (ld_q < (int64_t)h_q * d || ld_q % 8 != 0) return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
+
+void set_window(KvAttnArgs& a, const void* q, int64_t ld_q, int64_t n_slots, int32_t n_req,
+                const int32_t* req_row_start, int32_t n_rows, const int32_t* row_len, int32_t max_len, int32_t h_q,
+                int32_t h_kv, const int32_t* page_table, int64_t ld_pt, int32_t page_size, int32_t window,
+                int32_t n_sink, void* out, float* lse) {
+  a.q = static_cast<const uint16_t*>(q);
+  a.ld_q = ld_q;
+  a.n_slots = n_slots;
+  a.n_rows = n_rows;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.n_req = n_req;
+  a.req_row_start = req_row_start;
+  a.row_len = row_len;
+  a.max_len = max_len;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.page_table = page_table;
+  a.ld_pt = ld_pt;
+  a.page_size = page_size;
+  a.out_bf16 = 1;
+  a.out = out;
+  a.lse = lse;
+}
+
+}  // namespace
+
+namespace qsa {
+bool kv_fault_word(cudaStream_t stream, bool clear, unsigned* bits) {
+  if (cudaMemcpyFromSymbolAsync(bits, g_fault_word, sizeof(*bits), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return false;
+  if (clear && *bits) {
+    const unsigned zero = 0;
+    if (cudaMemcpyToSymbolAsync(g_fault_word, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess)
+      return false;
+  }
+  return true;
+}
+}  // namespace qsa
+
+extern "C" {
+
+qsa_status qsa_append_kv_fp4(const void* k_new, const void* v_new, int64_t ld_k, int64_t ld_v, int32_t n_tok,
+                             int32_t h_kv, int32_t head_dim, const int32_t* req_tok_start,
+                             const int32_t* req_first_pos, int32_t n_req, const int32_t* page_table, int64_t ld_pt,
+                             int32_t page_size, float k_scale, float v_scale, void* k_codes, void* k_scales,
+                             void* v_codes, void* v_scales, int64_t n_slots, void* stream) {
+  if (n_tok < 0 || n_req < 0 || h_kv <= 0) return QSA_ERR_INVALID_ARG;
+  if ((head_dim != 128 && head_dim != 256) || h_kv > 65535 || n_req > 65535) return QSA_ERR_UNSUPPORTED;
+  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return QSA_ERR_INVALID_ARG;
+  if (n_tok == 0 || n_req == 0) return QSA_OK;
+  if (!k_new || !v_new || !req_tok_start || !req_first_pos) return QSA_ERR_INVALID_ARG;
+  if (qsa_status st = check_paging(page_table, ld_pt, page_size, 0)) return st;
+  if (qsa_status st = check_cache4(k_codes, k_scales, v_codes, v_scales, n_slots)) return st;
+  const int64_t row = (int64_t)h_kv * head_dim;
+  if (!aligned32(k_new) || !aligned32(v_new) || ld_k % 16 != 0 || ld_v % 16 != 0 || ld_k < row || ld_v < row)
+    return QSA_ERR_INVALID_ARG;
+  KvWriteArgs a{};
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.ld_k = ld_k;
+  a.ld_v = ld_v;
+  a.n_tok = n_tok;
+  a.h_kv = h_kv;
+  a.blocks = h_kv * (head_dim / kKvBlock);
+  a.req_tok_start = req_tok_start;
+  a.req_first_pos = req_first_pos;
+  a.n_req = n_req;
+  a.page_table = page_table;
+  a.ld_pt = ld_pt;
+  a.page_size = page_size;
+  a.n_slots = n_slots;
+  a.k_codes = static_cast<uint8_t*>(k_codes);
+  a.k_scales = static_cast<uint8_t*>(k_scales);
+  a.v_codes = static_cast<uint8_t*>(v_codes);
+  a.v_scales = static_cast<uint8_t*>(v_scales);
+  a.k_inv = 1.0f / k_scale;
+  a.v_inv = 1.0f / v_scale;
+  const int64_t ctas = ((int64_t)n_tok * a.blocks + kKvThreads - 1) / kKvThreads;
+  if (ctas > INT32_MAX) return QSA_ERR_UNSUPPORTED;
+  append_kv_fp4_kernel<<<(unsigned)ctas, kKvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+}
+
+qsa_status qsa_gather_kv_fp4(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                             int64_t n_slots, int32_t h_kv, int32_t head_dim, const int32_t* slots, int64_t n,
+                             float k_scale, float v_scale, void* k_out, void* v_out, void* stream) {
+  if (n < 0 || h_kv <= 0) return QSA_ERR_INVALID_ARG;
+  if ((head_dim != 128 && head_dim != 256) || h_kv > 65535) return QSA_ERR_UNSUPPORTED;
+  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return QSA_ERR_INVALID_ARG;
+  if (n == 0) return QSA_OK;
+  if (!slots || !k_out || !v_out || !aligned4(slots) || !aligned32(k_out) || !aligned32(v_out))
+    return QSA_ERR_INVALID_ARG;
+  if (qsa_status st = check_cache4(k_codes, k_scales, v_codes, v_scales, n_slots)) return st;
+  KvReadArgs a{};
+  a.k_codes = static_cast<const uint8_t*>(k_codes);
+  a.k_scales = static_cast<const uint8_t*>(k_scales);
+  a.v_codes = static_cast<const uint8_t*>(v_codes);
+  a.v_scales = static_cast<const uint8_t*>(v_scales);
+  a.n_slots = n_slots;
+  a.blocks = h_kv * (head_dim / kKvBlock);
+  a.slots = slots;
+  a.n = n;
+  a.k_g = k_scale;
+  a.v_g = v_scale;
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.v_out = static_cast<uint16_t*>(v_out);
+  if (n > INT64_MAX / a.blocks / 2 || (n * a.blocks + kKvThreads - 1) / kKvThreads > INT32_MAX)
+    return QSA_ERR_UNSUPPORTED;
+  const int64_t ctas = (n * a.blocks + kKvThreads - 1) / kKvThreads;
+  gather_kv_fp4_kernel<<<(unsigned)ctas, kKvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+}
+
+size_t qsa_sparse_attn_fp4_workspace_size(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t n_idx) {
+  return ka_workspace(n_rows, h_q, h_kv, head_dim, n_idx);
+}
+
+qsa_status qsa_sparse_attn_fp4(const void* q, int64_t ld_q, const void* k_codes, const void* k_scales,
+                               const void* v_codes, const void* v_scales, int64_t n_slots, int32_t n_rows, int32_t h_q,
+                               int32_t h_kv, int32_t head_dim, const int32_t* slots, int64_t ld_slots, int32_t n_idx,
+                               float scale, float k_scale, float v_scale, float* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  if (n_rows < 0 || n_idx < 0 || ld_slots < n_idx) return QSA_ERR_INVALID_ARG;
+  if (!kv_shape_ok(h_q, h_kv, head_dim)) return QSA_ERR_UNSUPPORTED;
+  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return QSA_ERR_INVALID_ARG;
+  if (n_rows == 0) return QSA_OK;
+  if (!q || !out || (n_idx > 0 && !slots) || !aligned16(q) || !aligned16(out) || (lse && !aligned4(lse)) ||
+      !aligned4(slots))
+    return QSA_ERR_INVALID_ARG;
+  if (ld_q < (int64_t)h_q * head_dim || ld_q % 8 != 0) return QSA_ERR_INVALID_ARG;
+  if (qsa_status st = check_cache4(k_codes, k_scales, v_codes, v_scales, n_slots)) return st;
+  if (qsa_status st = check_workspace(ka_workspace(n_rows, h_q, h_kv, head_dim, n_idx), workspace, workspace_bytes))
+    return st;
+  KvAttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.ld_q = ld_q;
+  a.k = static_cast<const uint8_t*>(k_codes);
+  a.v = static_cast<const uint8_t*>(v_codes);
+  a.ks = static_cast<const uint8_t*>(k_scales);
+  a.vs = static_cast<const uint8_t*>(v_scales);
+  a.n_slots = n_slots;
+  a.n_rows = n_rows;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.slots = slots;
+  a.ld_slots = ld_slots;
+  a.n_idx = n_idx;
+  a.scale = scale * k_scale;
+  a.v_g = v_scale;
+  a.out = out;
+  a.lse = lse;
+  return launch_ka_shape<true, false>(a, head_dim, n_idx, workspace, static_cast<cudaStream_t>(stream));
+}
+
+size_t qsa_window_attn_workspace_size(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t max_len,
+                                      int32_t window, int32_t n_sink) {
+  if (window < 1 || n_sink < 0) return 0;
+  return ka_workspace(n_rows, h_q, h_kv, head_dim, window_entries(max_len, window, n_sink));
+}
+
+qsa_status qsa_window_attn(const void* q, int64_t ld_q, const void* k_cache, const void* v_cache, int64_t n_slots,
+                           int32_t n_req, const int32_t* req_row_start, int32_t n_rows, const int32_t* row_len,
+                           int32_t max_len, int32_t max_rows_per_req, int32_t h_q, int32_t h_kv, int32_t head_dim,
+                           const int32_t* page_table, int64_t ld_pt, int32_t page_size, int32_t window, int32_t n_sink,
+                           float scale, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (qsa_status st = check_window(q, ld_q, n_slots, n_req, req_row_start, n_rows, row_len, max_len, max_rows_per_req,
+                                   h_q, h_kv, head_dim, page_table, ld_pt, page_size, window, n_sink, out, lse))
+    return st;
+  if (n_rows == 0) return QSA_OK;
+  if ((n_slots > 0 && (!k_cache || !v_cache)) || !aligned16(k_cache) || !aligned16(v_cache)) return QSA_ERR_INVALID_ARG;
+  const int64_t entries = window_entries(max_len, window, n_sink);
+  if (qsa_status st = check_workspace(ka_workspace(n_rows, h_q, h_kv, head_dim, entries), workspace, workspace_bytes))
+    return st;
+  KvAttnArgs a{};
+  set_window(a, q, ld_q, n_slots, n_req, req_row_start, n_rows, row_len, max_len, h_q, h_kv, page_table, ld_pt,
+             page_size, window, n_sink, out, lse);
+  a.k = static_cast<const uint8_t*>(k_cache);
+  a.v = static_cast<const uint8_t*>(v_cache);
+  a.scale = scale;
+  a.v_g = 1.0f;
+  return launch_ka_shape<false, true>(a, head_dim, entries, workspace, static_cast<cudaStream_t>(stream));
+}
+
+qsa_status qsa_window_attn_fp4(const void* q, int64_t ld_q, const void* k_codes, const void* k_scales,
+                               const void* v_codes, const void* v_scales, int64_t n_slots, int32_t n_req,
+                               const int32_t* req_row_start, int32_t n_rows, const int32_t* row_len, int32_t max_len,
+                               int32_t max_rows_per_req, int32_t h_q, int32_t h_kv, int32_t head_dim,
+                               const int32_t* page_table, int64_t ld_pt, int32_t page_size, int32_t window,
+                               int32_t n_sink, float scale, float k_scale, float v_scale, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return QSA_ERR_INVALID_ARG;
+  if (qsa_status st = check_window(q, ld_q, n_slots, n_req, req_row_start, n_rows, row_len, max_len, max_rows_per_req,
+                                   h_q, h_kv, head_dim, page_table, ld_pt, page_size, window, n_sink, out, lse))
+    return st;
+  if (n_rows == 0) return QSA_OK;
+  if (qsa_status st = check_cache4(k_codes, k_scales, v_codes, v_scales, n_slots)) return st;
+  const int64_t entries = window_entries(max_len, window, n_sink);
+  if (qsa_status st = check_workspace(ka_workspace(n_rows, h_q, h_kv, head_dim, entries), workspace, workspace_bytes))
+    return st;
+  KvAttnArgs a{};
+  set_window(a, q, ld_q, n_slots, n_req, req_row_start, n_rows, row_len, max_len, h_q, h_kv, page_table, ld_pt,
+             page_size, window, n_sink, out, lse);
+  a.k = static_cast<const uint8_t*>(k_codes);
+  a.v = static_cast<const uint8_t*>(v_codes);
+  a.ks = static_cast<const uint8_t*>(k_scales);
+  a.vs = static_cast<const uint8_t*>(v_scales);
+  a.scale = scale * k_scale;
+  a.v_g = v_scale;
+  return launch_ka_shape<true, true>(a, head_dim, entries, workspace, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -10,6 +10,7 @@
 
 #include "../../include/qsa.h"
 #include "common.cuh"
+#include "host_util.cuh"
 #include "compress.cuh"
 #include "expand.cuh"
 #include "score_decode.cuh"
@@ -173,9 +174,6 @@ qsa_status device_info(DeviceInfo** out) {
   return QSA_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 // RoPE turn fractions for one base, cached (the last few bases used).
 // frac[i] = round(2^64 * base^(-2i/128) / (2 pi)).
 std::mutex g_rope_mu;
@@ -198,25 +196,6 @@ RopeTurns rope_turns(double base) {
     e.turns.frac[i] = (uint64_t)std::llround(std::ldexp(turns, 62)) << 2;  // turns < 1/4
   }
   return e.turns;
-}
-
-// Launch with programmatic stream serialisation: the grid may become
-// resident before the previous kernel on the stream finishes; every kernel
-// launched this way executes griddepcontrol.wait before reading its inputs.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                       Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 qsa_status launch_status() {
@@ -585,22 +564,6 @@ qsa_status launch_select(const SelectArgs& a, bool pdl, cudaStream_t stream, int
   return QSA_OK;
 }
 
-// cuTensorMapEncodeTiled, reached through the runtime's driver entry point
-// (the library does not link libcuda directly).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 // The compressed-key pool for the TMA scorer, with the 128-byte swizzle.
 // 4-D view (pool_rows a multiple of 8): [row / 8][K-half][row % 8][64 BF16],
 // one box of box_rows / 8 groups covers a run of box_rows keys, both
@@ -860,21 +823,6 @@ qsa_status launch_scores_tc(const ScoreArgs& s, int max_rows_per_req, int sm_cou
   return QSA_OK;
 }
 
-qsa_status check_rows(int32_t n_req, const int32_t* req_row_start, int32_t n_rows,
-                      const int32_t* row_len, int32_t max_len) {
-  if (n_req < 0 || n_rows < 0 || max_len < 0) return QSA_ERR_INVALID_ARG;
-  if (n_rows > 0 && (n_req < 1 || !req_row_start || !row_len)) return QSA_ERR_INVALID_ARG;
-  if (n_req > 65535) return QSA_ERR_UNSUPPORTED;
-  return QSA_OK;
-}
-
-qsa_status check_paging(const int32_t* page_table, int64_t ld_pt, int32_t page_size,
-                        int32_t max_len) {
-  if (!page_table || page_size <= 0 || ld_pt < 0) return QSA_ERR_INVALID_ARG;
-  if (page_size % kBlock != 0) return QSA_ERR_UNSUPPORTED;
-  if (max_len > 0 && (int64_t)(max_len - 1) / page_size >= ld_pt) return QSA_ERR_INVALID_ARG;
-  return QSA_OK;
-}
 
 // Persistent scorer: two CTAs per SM walk balanced ranges of 128-block
 // tiles.  Requests are handled in windows of at most kScoreMaxReq per launch.
@@ -981,6 +929,9 @@ qsa_status qsa_device_status(void* stream, int clear, uint32_t* h_bits) {
         cudaStreamSynchronize(st) != cudaSuccess)
       return QSA_ERR_CUDA;
   }
+  unsigned kv_bits = 0;
+  if (!kv_fault_word(st, clear != 0, &kv_bits)) return QSA_ERR_CUDA;
+  bits |= kv_bits;
   if (h_bits) *h_bits = bits;
   return bits ? QSA_ERR_DEVICE_FAULT : QSA_OK;
 }
