@@ -384,7 +384,7 @@ qsa_status qsa_sparse_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
  *   k_cache, v_cache [n_slots][h_kv][head_dim] BF16 (16-byte aligned), or the
  *              four arrays of the 4-bit cache.
  *   window >= 1, n_sink >= 0.
- *   out        [n_rows][h_q][head_dim] BF16 (16-byte aligned): the next
+ *   out        [n_rows][h_q][head_dim] BF16 (32-byte aligned): the next
  *              operator is a BF16 projection.
  *   workspace  qsa_window_attn_workspace_size() bytes (16-byte aligned), 0
  *              except for few rows with long windows; as above.

@@ -13,6 +13,7 @@
 #include "host_util.cuh"
 #include "kv4.cuh"
 #include "kv_attn.cuh"
+#include "window_tc.cuh"
 
 using namespace qsa;
 
@@ -27,22 +28,27 @@ bool set_ka_smem() {
 }
 
 // Per-device one-time set-up: the shared-memory opt-in of the kernels.
-bool g_ready[kMaxDevices];
+// Gives the device's SM count.
+int g_sms[kMaxDevices];
 std::mutex g_mu;
-qsa_status kv_device_ready() {
+qsa_status kv_device_ready(int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QSA_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
-  if (g_ready[dev]) return QSA_OK;
+  *sms = g_sms[dev];
+  if (*sms > 0) return QSA_OK;
   if (!set_ka_smem<256, 1, true, false>() || !set_ka_smem<128, 1, true, false>() ||
       !set_ka_smem<128, 2, true, false>() || !set_ka_smem<256, 1, true, true>() ||
       !set_ka_smem<128, 1, true, true>() || !set_ka_smem<128, 2, true, true>() ||
       !set_ka_smem<256, 1, false, true>() || !set_ka_smem<128, 1, false, true>() ||
-      !set_ka_smem<128, 2, false, true>()) {
+      !set_ka_smem<128, 2, false, true>() ||
+      cudaFuncSetAttribute(window_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWtSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(window_tc_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWtSmem) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
     cudaGetLastError();
     return QSA_ERR_CUDA;
   }
-  g_ready[dev] = true;
+  g_sms[dev] = *sms;
   return QSA_OK;
 }
 
@@ -124,9 +130,69 @@ qsa_status launch_ka_shape(KvAttnArgs& a, int d, int64_t entries, void* workspac
   a.part = static_cast<float*>(workspace);
   if ((int64_t)a.n_rows * std::max(a.cluster * a.n_group, a.h_q) > INT32_MAX) return QSA_ERR_UNSUPPORTED;
   if (entries > (1 << 30)) return QSA_ERR_UNSUPPORTED;  // entry indices stay clear of 2^31
-  if (qsa_status st = kv_device_ready()) return st;
+  int sms = 0;
+  if (qsa_status st = kv_device_ready(&sms)) return st;
   if (d == 256) return launch_ka<256, 1, kFp4, kWindow>(a, stream);
   return a.group <= 8 ? launch_ka<128, 1, kFp4, kWindow>(a, stream) : launch_ka<128, 2, kFp4, kWindow>(a, stream);
+}
+
+// The cache [n_slots][h_kv * D] BF16 for window_tc_kernel: boxes of 64 columns
+// x `box` rows, 128-byte swizzled; rows past the end read as zeros.
+bool encode_cache_map(CUtensorMap* m, const void* cache, int64_t n_slots, int64_t cols, int box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)n_slots};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  const cuuint32_t bx[2] = {64, (cuuint32_t)box};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(cache), dims, strides, bx, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The tensor-core form of window_attn, for requests of more than kWtMinRows
+// rows on pages of whole 8-row groups; QSA_ERR_UNSUPPORTED where the other
+// form has to serve.
+constexpr int kWtMinRows = 8;
+qsa_status launch_window_tc(const KvAttnArgs& k, int d, int32_t max_rows_per_req, cudaStream_t stream) {
+  if (max_rows_per_req <= kWtMinRows || k.page_size % 8 != 0 || k.n_slots <= 0) return QSA_ERR_UNSUPPORTED;
+  WtArgs a{};
+  a.q = k.q;
+  a.ld_q = k.ld_q;
+  a.n_slots = k.n_slots;
+  a.n_rows = k.n_rows;
+  a.h_q = k.h_q;
+  a.h_kv = k.h_kv;
+  a.group = k.h_q / k.h_kv;
+  a.rows = 128 / a.group;
+  a.n_req = k.n_req;
+  a.req_row_start = k.req_row_start;
+  a.row_len = k.row_len;
+  a.max_len = k.max_len;
+  a.window = k.window;
+  a.n_sink = k.n_sink;
+  a.page_table = k.page_table;
+  a.ld_pt = k.ld_pt;
+  a.page_size = k.page_size;
+  a.box_shift = k.page_size % 16 == 0 ? 4 : 3;
+  a.box = 1 << a.box_shift;
+  a.tile_slots = k.n_rows / a.rows + k.n_req;
+  a.c = std::max(std::fabs(k.scale) * 1.4426950408889634f, 1e-30f);
+  a.flip = k.scale < 0.f ? 0x80008000u : 0u;
+  a.out = static_cast<uint16_t*>(k.out);
+  a.lse = k.lse;
+  const int64_t units = (int64_t)a.tile_slots * a.h_kv;
+  if (units > INT32_MAX || k.max_len > (1 << 30)) return QSA_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (qsa_status st = kv_device_ready(&sms)) return st;
+  CUtensorMap k_map, v_map;
+  if (!encode_cache_map(&k_map, k.k, k.n_slots, (int64_t)k.h_kv * d, a.box) ||
+      !encode_cache_map(&v_map, k.v, k.n_slots, (int64_t)k.h_kv * d, a.box))
+    return QSA_ERR_UNSUPPORTED;
+  const unsigned grid = (unsigned)std::min<int64_t>(units, sms);
+  if (d == 256) window_tc_kernel<256><<<grid, kWtThreads, kWtSmem, stream>>>(a, k_map, v_map);
+  else window_tc_kernel<128><<<grid, kWtThreads, kWtSmem, stream>>>(a, k_map, v_map);
+  return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 
 size_t ka_workspace(int64_t n_rows, int32_t h_q, int32_t h_kv, int32_t d, int64_t entries) {
@@ -156,13 +222,14 @@ qsa_status check_cache4(const void* kc, const void* ks, const void* vc, const vo
 qsa_status check_window(const void* q, int64_t ld_q, int64_t n_slots, int32_t n_req, const int32_t* req_row_start,
                         int32_t n_rows, const int32_t* row_len, int32_t max_len, int32_t max_rows_per_req, int32_t h_q,
                         int32_t h_kv, int32_t d, const int32_t* page_table, int64_t ld_pt, int32_t page_size,
-                        int32_t window, int32_t n_sink, const void* out, const void* lse) {
+                        int32_t window, int32_t n_sink, float scale, const void* out, const void* lse) {
+  if (!std::isfinite(scale)) return QSA_ERR_INVALID_ARG;
   if (window < 1 || n_sink < 0 || max_rows_per_req < 0 || n_slots < 0 || n_slots > INT32_MAX) return QSA_ERR_INVALID_ARG;
   if (!kv_shape_ok(h_q, h_kv, d)) return QSA_ERR_UNSUPPORTED;
   if (qsa_status st = check_rows(n_req, req_row_start, n_rows, row_len, max_len)) return st;
   if (n_rows == 0) return QSA_OK;
   if (qsa_status st = check_paging(page_table, ld_pt, page_size, max_len)) return st;
-  if (!q || !out || !aligned16(q) || !aligned16(out) || (lse && !aligned4(lse))) return QSA_ERR_INVALID_ARG;
+  if (!q || !out || !aligned16(q) || !aligned32(out) || (lse && !aligned4(lse))) return QSA_ERR_INVALID_ARG;
   if (ld_q < (int64_t)h_q * d || ld_q % 8 != 0) return QSA_ERR_INVALID_ARG;
   return QSA_OK;
 }
@@ -293,7 +360,7 @@ qsa_status qsa_sparse_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
                                size_t workspace_bytes, void* stream) {
   if (n_rows < 0 || n_idx < 0 || ld_slots < n_idx) return QSA_ERR_INVALID_ARG;
   if (!kv_shape_ok(h_q, h_kv, head_dim)) return QSA_ERR_UNSUPPORTED;
-  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return QSA_ERR_INVALID_ARG;
+  if (!scale_ok(k_scale) || !scale_ok(v_scale) || !std::isfinite(scale)) return QSA_ERR_INVALID_ARG;
   if (n_rows == 0) return QSA_OK;
   if (!q || !out || (n_idx > 0 && !slots) || !aligned16(q) || !aligned16(out) || (lse && !aligned4(lse)) ||
       !aligned4(slots))
@@ -335,7 +402,8 @@ qsa_status qsa_window_attn(const void* q, int64_t ld_q, const void* k_cache, con
                            const int32_t* page_table, int64_t ld_pt, int32_t page_size, int32_t window, int32_t n_sink,
                            float scale, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   if (qsa_status st = check_window(q, ld_q, n_slots, n_req, req_row_start, n_rows, row_len, max_len, max_rows_per_req,
-                                   h_q, h_kv, head_dim, page_table, ld_pt, page_size, window, n_sink, out, lse))
+                                   h_q, h_kv, head_dim, page_table, ld_pt, page_size, window, n_sink, scale, out,
+                                   lse))
     return st;
   if (n_rows == 0) return QSA_OK;
   if ((n_slots > 0 && (!k_cache || !v_cache)) || !aligned16(k_cache) || !aligned16(v_cache)) return QSA_ERR_INVALID_ARG;
@@ -349,6 +417,8 @@ qsa_status qsa_window_attn(const void* q, int64_t ld_q, const void* k_cache, con
   a.v = static_cast<const uint8_t*>(v_cache);
   a.scale = scale;
   a.v_g = 1.0f;
+  const qsa_status tc = launch_window_tc(a, head_dim, max_rows_per_req, static_cast<cudaStream_t>(stream));
+  if (tc != QSA_ERR_UNSUPPORTED) return tc;
   return launch_ka_shape<false, true>(a, head_dim, entries, workspace, static_cast<cudaStream_t>(stream));
 }
 
@@ -361,7 +431,8 @@ qsa_status qsa_window_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
                                void* workspace, size_t workspace_bytes, void* stream) {
   if (!scale_ok(k_scale) || !scale_ok(v_scale)) return QSA_ERR_INVALID_ARG;
   if (qsa_status st = check_window(q, ld_q, n_slots, n_req, req_row_start, n_rows, row_len, max_len, max_rows_per_req,
-                                   h_q, h_kv, head_dim, page_table, ld_pt, page_size, window, n_sink, out, lse))
+                                   h_q, h_kv, head_dim, page_table, ld_pt, page_size, window, n_sink, scale, out,
+                                   lse))
     return st;
   if (n_rows == 0) return QSA_OK;
   if (qsa_status st = check_cache4(k_codes, k_scales, v_codes, v_scales, n_slots)) return st;
