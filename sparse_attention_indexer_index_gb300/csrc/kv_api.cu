@@ -42,8 +42,8 @@ qsa_status kv_device_ready(int* sms) {
       !set_ka_smem<128, 1, true, true>() || !set_ka_smem<128, 2, true, true>() ||
       !set_ka_smem<256, 1, false, true>() || !set_ka_smem<128, 1, false, true>() ||
       !set_ka_smem<128, 2, false, true>() ||
-      cudaFuncSetAttribute(window_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWtSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(window_tc_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWtSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(window_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, wt_smem_bytes<128>()) != cudaSuccess ||
+      cudaFuncSetAttribute(window_tc_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, wt_smem_bytes<256>()) != cudaSuccess ||
       cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
     cudaGetLastError();
     return QSA_ERR_CUDA;
@@ -136,16 +136,31 @@ qsa_status launch_ka_shape(KvAttnArgs& a, int d, int64_t entries, void* workspac
   return a.group <= 8 ? launch_ka<128, 1, kFp4, kWindow>(a, stream) : launch_ka<128, 2, kFp4, kWindow>(a, stream);
 }
 
-// The cache [n_slots][h_kv * D] BF16 for window_tc_kernel: boxes of 64 columns
-// x `box` rows, 128-byte swizzled; rows past the end read as zeros.
-bool encode_cache_map(CUtensorMap* m, const void* cache, int64_t n_slots, int64_t cols, int box) {
+// The cache [n_slots][h_kv * D] BF16 for window_tc_kernel, as [row / 8][64
+// columns][row % 8][64 BF16], 128-byte swizzled: a box takes `box` rows and
+// `groups` groups of 64 columns; 8-row groups past the end read as zeros.
+bool encode_cache_map(CUtensorMap* m, const void* cache, int64_t n_slots, int64_t cols, int box, int groups) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (enc == nullptr) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)n_slots};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  const cuuint32_t bx[2] = {64, (cuuint32_t)box};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(cache), dims, strides, bx, estr,
+  const cuuint64_t dims[4] = {64, 8, (cuuint64_t)cols / 64, (cuuint64_t)n_slots / 8};
+  const cuuint64_t strides[3] = {(cuuint64_t)cols * 2, 128, (cuuint64_t)cols * 16};
+  const cuuint32_t bx[4] = {64, 8, (cuuint32_t)groups, (cuuint32_t)box / 8};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims, strides, bx, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The queries [n_rows][h_q][D]: a tile's rows x the heads of a KV head x 64
+// columns a box; rows past the end read as zeros.
+bool encode_q_map(CUtensorMap* m, const WtArgs& a, int d) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)a.h_q, (cuuint64_t)a.n_rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)a.ld_q * 2};
+  const cuuint32_t bx[3] = {64, (cuuint32_t)a.group, (cuuint32_t)a.rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q), dims, strides, bx, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -155,7 +170,7 @@ bool encode_cache_map(CUtensorMap* m, const void* cache, int64_t n_slots, int64_
 // form has to serve.
 constexpr int kWtMinRows = 8;
 qsa_status launch_window_tc(const KvAttnArgs& k, int d, int32_t max_rows_per_req, cudaStream_t stream) {
-  if (max_rows_per_req <= kWtMinRows || k.page_size % 8 != 0 || k.n_slots <= 0) return QSA_ERR_UNSUPPORTED;
+  if (max_rows_per_req <= kWtMinRows || k.page_size % 8 != 0 || k.n_slots < 8) return QSA_ERR_UNSUPPORTED;
   WtArgs a{};
   a.q = k.q;
   a.ld_q = k.ld_q;
@@ -174,24 +189,25 @@ qsa_status launch_window_tc(const KvAttnArgs& k, int d, int32_t max_rows_per_req
   a.page_table = k.page_table;
   a.ld_pt = k.ld_pt;
   a.page_size = k.page_size;
-  a.box_shift = k.page_size % 16 == 0 ? 4 : 3;
+  a.box_shift = 3;
+  while (a.box_shift < 6 && k.page_size % (2 << a.box_shift) == 0) ++a.box_shift;
   a.box = 1 << a.box_shift;
   a.tile_slots = k.n_rows / a.rows + k.n_req;
   a.c = std::max(std::fabs(k.scale) * 1.4426950408889634f, 1e-30f);
-  a.flip = k.scale < 0.f ? 0x80008000u : 0u;
+  a.flip = k.scale < 0.f ? 0x80000000u : 0u;
   a.out = static_cast<uint16_t*>(k.out);
   a.lse = k.lse;
   const int64_t units = (int64_t)a.tile_slots * a.h_kv;
   if (units > INT32_MAX || k.max_len > (1 << 30)) return QSA_ERR_UNSUPPORTED;
   int sms = 0;
   if (qsa_status st = kv_device_ready(&sms)) return st;
-  CUtensorMap k_map, v_map;
-  if (!encode_cache_map(&k_map, k.k, k.n_slots, (int64_t)k.h_kv * d, a.box) ||
-      !encode_cache_map(&v_map, k.v, k.n_slots, (int64_t)k.h_kv * d, a.box))
+  CUtensorMap q_map, k_map, v_map;
+  if (!encode_q_map(&q_map, a, d) || !encode_cache_map(&k_map, k.k, k.n_slots, (int64_t)k.h_kv * d, a.box, 2) ||
+      !encode_cache_map(&v_map, k.v, k.n_slots, (int64_t)k.h_kv * d, a.box, d / 64))
     return QSA_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)std::min<int64_t>(units, sms);
-  if (d == 256) window_tc_kernel<256><<<grid, kWtThreads, kWtSmem, stream>>>(a, k_map, v_map);
-  else window_tc_kernel<128><<<grid, kWtThreads, kWtSmem, stream>>>(a, k_map, v_map);
+  if (d == 256) window_tc_kernel<256><<<grid, kWtThreads, wt_smem_bytes<256>(), stream>>>(a, q_map, k_map, v_map);
+  else window_tc_kernel<128><<<grid, kWtThreads, wt_smem_bytes<128>(), stream>>>(a, q_map, k_map, v_map);
   return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 

@@ -14,25 +14,34 @@
 // at the full MMA rate).
 //
 // Design (GB300).  One CTA per SM walks tiles (a static stride):
-//  - warp 4 copies K and V blocks into two rings of 32 KB stages by TMA, one
-//    box of B rows (16, or 8 where the page is not a multiple of 16) x 64
-//    columns a copy, 128-byte swizzled in whole 8-row groups.  Boxes follow the page table; a page out of
-//    range is copied from beyond the tensor map, which fills zeros.
-//  - warp 5 issues the MMAs: S from Q in tensor memory (read once per tile,
-//    so K alone crosses shared memory) and K (K-major), O from P in tensor
-//    memory and V (MN-major: V's rows are keys, the transposition is the
-//    descriptor's).
-//  - warps 0-3 hold one pair per thread: they put Q into tensor memory, turn
-//    S into P in place, and write the outputs.
-//  - Two S buffers: the order PV(i) PV(i+1) QK(i+2) QK(i+3) lets each softmax
-//    run beside a product, and by the time a product may overwrite P(i) the
-//    one that reads it has long finished (its barrier is waited for).
+//  - warp 10 finds the tiles and copies Q (TMA, 3-D boxes: the rows and heads
+//    of a tile land as the 128 rows of the MMA operand), a tile ahead;
+//  - warps 8 (K) and 11 (V) copy into a ring of 32 KB stages in the order in
+//    which they are used, one TMA box of B rows (the largest power of two up
+//    to 64 that divides the page) and all the stage's columns a copy.  The
+//    instruction takes one box at a time whichever lanes ask (about 100 clocks
+//    each: boxes of 16 rows x 64 columns held the tiles at 21 bytes a clock),
+//    hence large boxes and two warps.  They follow the page table; a page out
+//    of range is copied from beyond the tensor map, which fills zeros.
+//  - warp 9 issues the MMAs: S from Q and K in shared memory (both K-major),
+//    O from P in tensor memory and V (MN-major: V's rows are keys, the
+//    transposition is the descriptor's).  128 entries a block: with 64, S
+//    waits for its A operand (measured: 78 clocks a 128x64x16 product with A
+//    in tensor memory, where the rate allows 32).
+//  - warps 0-7 hold a pair in two threads, 64 entries of a block each: they
+//    turn S into P, exchange the maximum through shared memory, and
+//    write the outputs.  (One thread a pair took 1,000 clocks for 64 entries,
+//    more than a product of D = 128.)
+//  - The products go in the order QK(i+1) PV(i), so that a softmax has the
+//    time of two products.  S has one buffer, free again as soon as the
+//    softmax warps hold it in registers; P has two, and the barrier that
+//    announces S(i) also covers PV(i-2), which read the one P(i) goes into.
 //  - The accumulator is rescaled only when a row's maximum grew by more than
 //    2^8 since the last time (the weights stay below 2^8 and the sums are
 //    FP32, so nothing is lost); otherwise m stays.
 //  - Weights enter the product as BF16, 2^-9 relative at most, one rounding
 //    like that of the output; l sums them before the rounding, in FP32.
-// Tensor memory columns: O [0, D), Q [D, 3D/2), S/P two times N after it.
+// Tensor memory columns: O [0, D), S the next 128, P two times 64.
 //
 // Entries.  With `start` the first window position of the tile rounded down
 // to a box, the entries are the boxes of the first tokens before `start`
@@ -49,17 +58,26 @@
 
 namespace qsa {
 
-constexpr int kWtThreads = 192;
-constexpr int kWtStages = 3;
+constexpr int kWtThreads = 384;          // 8 softmax warps; K, MMAs, tiles and Q, V
+constexpr int kWtN = 128;                // entries per block
 constexpr int kWtStageBytes = 32768;
-constexpr int kWtSmem = 2 * kWtStages * kWtStageBytes + 1024;
 constexpr int kWtBadRing = 8;
+constexpr int kWtTileRing = 3;
 
+// Stage contents.  K: 128 entries x 128 columns (a block of D = 256 takes
+// two); V: 64 entries x 256 columns or 128 x 128.  Both as [8-row group][64
+// columns][8 rows][128 B], 128-byte swizzled: a box of whole 8-row groups
+// fills consecutive bytes.
 template <int D>
 struct WtShape {
-  static constexpr int kN = D == 256 ? 64 : 128;  // entries per block (32 KB of K)
-  static constexpr uint32_t kColQ = D, kColS = D + D / 2;
-  static_assert(kN * D * 2 == kWtStageBytes && kColS + 2 * kN <= 512, "tensor memory");
+  static constexpr int kKs = D / 128;               // K stages of a block
+  static constexpr int kVRows = D == 256 ? 64 : 128;  // entries of a V stage
+  static constexpr int kVs = kWtN / kVRows;         // V stages of a full block
+  static constexpr uint32_t kKGroup = 2 * 1024, kVGroup = D / 64 * 1024;  // bytes of an 8-row group
+  static constexpr uint32_t kColS = D, kColP = D + kWtN;
+  static constexpr int kQBytes = 128 * D * 2;
+  static constexpr int kStages = D == 256 ? 5 : 6;  // of K and V: 224 KB with Q
+  static_assert(D + 2 * kWtN <= 512, "tensor memory");
 };
 
 struct WtArgs {
@@ -75,10 +93,10 @@ struct WtArgs {
   const int32_t* page_table;
   int64_t ld_pt;
   int32_t page_size;
-  int32_t box, box_shift;    // B: rows per copy, 8 or 16, dividing the page; its logarithm
+  int32_t box, box_shift;    // B: rows per copy, 8 to 64, dividing the page; its logarithm
   int32_t tile_slots;        // n_rows / R + n_req
   float c;                   // |scale| log2 e, positive
-  uint32_t flip;             // sign bits of q to flip (a negative scale)
+  uint32_t flip;             // sign bit to flip in S (a negative scale)
   uint16_t* out;             // [n_rows][h_q][D] BF16
   float* lse;                // [n_rows][h_q] or nullptr
 };
@@ -123,6 +141,13 @@ __device__ __forceinline__ void wt_tmem_st32(uint32_t taddr, const uint32_t (&v)
 
 __device__ __forceinline__ void wt_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void wt_tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
 // D[128][n] += A (tensor memory, BF16 pairs) * B (shared memory).
 __device__ __forceinline__ void wt_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -131,21 +156,28 @@ __device__ __forceinline__ void wt_mma_ts(uint32_t d, uint32_t a, uint64_t b_des
       "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// MN-major, 128-byte swizzle: groups of 64 columns `lbo` bytes apart, groups
-// of 8 rows (the K index) 1024 bytes apart.
-__device__ __forceinline__ uint64_t wt_desc_mn(uint32_t smem_addr, uint32_t lbo) {
+__device__ __forceinline__ void wt_tma_4d(void* dst, const CUtensorMap* map, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+// MN-major, 128-byte swizzle: groups of 64 columns 1024 bytes apart, groups
+// of 8 rows (the K index) `group` bytes apart.
+__device__ __forceinline__ uint64_t wt_desc_mn(uint32_t smem_addr, uint32_t group) {
   uint64_t d = 0;
   d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(lbo >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)(1024u >> 4) << 16;
+  d |= (uint64_t)(group >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
 }
 
 struct WtTile {
-  int r;               // request; rows 0: nothing to do
-  int t0, rows;        // rows t0 .. t0 + rows - 1
+  int r, g;            // request, KV head
+  int t0, rows;        // rows t0 .. t0 + rows - 1; 0: nothing to do, -1: no more tiles
   int start, nsr;      // see above
   int n_box, n_blk;    // boxes and blocks of N entries
   int ua, ub, uc;      // entries that some pair sees: [0, ua) and [ub, uc)
@@ -154,7 +186,6 @@ struct WtTile {
 // Tile of slot s: request r's tiles begin at slot req_row_start[r] / R + r
 // (enough room, since the requests before it have at most that many tiles);
 // slots past a request's last tile are empty.  By a whole warp.
-template <int N>
 __device__ __forceinline__ WtTile wt_tile(const WtArgs& a, int s) {
   const int lane = threadIdx.x & 31;
   WtTile w{};
@@ -196,7 +227,7 @@ __device__ __forceinline__ WtTile wt_tile(const WtArgs& a, int s) {
   w.start = first & ~(B - 1);
   w.nsr = (min(a.n_sink, w.start) + B - 1) & ~(B - 1);
   w.n_box = w.nsr / B + (last - w.start + B - 1) / B;
-  w.n_blk = (w.n_box * B + N - 1) / N;
+  w.n_blk = (w.n_box * B + kWtN - 1) / kWtN;
   w.ua = min(a.n_sink, last);
   w.ub = w.nsr + first - w.start;
   w.uc = w.nsr + last - w.start;
@@ -204,48 +235,80 @@ __device__ __forceinline__ WtTile wt_tile(const WtArgs& a, int s) {
 }
 
 struct WtCtl {
-  uint64_t k_full[kWtStages], k_empty[kWtStages], v_full[kWtStages], v_empty[kWtStages];
-  uint64_t s_full[2], p_full[2], pv_done[2], q_full, drain;
+  uint64_t full[6], empty[6];
+  uint64_t s_full, s_free, p_full[2], pv_done[2], q_full, q_empty, drain;
+  uint64_t tile_full[kWtTileRing], tile_empty[kWtTileRing];
+  uint64_t pair[4];          // the two warps of a lane quarter
+  WtTile tile[kWtTileRing];
+  float mx[2][2][128];       // [block parity][half][pair]: maxima, at the end the sums
   uint32_t bad[kWtBadRing];  // boxes of a block that are out of range
   uint32_t tmem;
   int abort;
 };
 
 template <int D>
+constexpr int wt_smem_bytes() {  // all of it dynamic, from a 1024-byte boundary
+  return WtShape<D>::kQBytes + WtShape<D>::kStages * kWtStageBytes + (int)sizeof(WtCtl);
+}
+
+// The lowest n bits (none below 0, all from 64).
+__device__ __forceinline__ uint64_t wt_low_bits(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
+// The next tile of the ring, by a whole warp; false: aborted.
+__device__ __forceinline__ bool wt_next_tile(WtCtl& ctl, int k, WtTile& w, volatile int* abort) {
+  const int sl = k % kWtTileRing;
+  const bool ok = __all_sync(0xffffffffu, tm_wait(&ctl.tile_full[sl], (uint32_t)(k / kWtTileRing) & 1u, abort));
+  if (!ok) return false;
+  w = ctl.tile[sl];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.tile_empty[sl]);
+  return true;
+}
+
+template <int D>
 __global__ void __launch_bounds__(kWtThreads, 1)
-window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUtensorMap k_map,
-                 const __grid_constant__ CUtensorMap v_map) {
+window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUtensorMap q_map,
+                 const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using Sh = WtShape<D>;
-  constexpr int N = Sh::kN;
-  constexpr int H = D / 64;                  // 64-column halves of a row
-  constexpr uint32_t kHalfBytes = N * 128;
-  extern __shared__ __align__(16) unsigned char wt_smem_raw[];
-  __shared__ WtCtl ctl;
-  unsigned char* base = wt_smem_raw + ((1024u - (smem_u32(wt_smem_raw) & 1023u)) & 1023u);
-  unsigned char* k_buf = base;
-  unsigned char* v_buf = base + kWtStages * kWtStageBytes;
+  constexpr int N = kWtN;
+  constexpr uint32_t kQHalf = 128 * 128;
+  extern __shared__ __align__(1024) unsigned char wt_smem[];
+  unsigned char* q_buf = wt_smem;
+  unsigned char* ring = q_buf + Sh::kQBytes;
+  WtCtl& ctl = *reinterpret_cast<WtCtl*>(ring + Sh::kStages * kWtStageBytes);
+  if ((smem_u32(wt_smem) & 1023u) != 0) {  // the swizzle atoms need it
+    if (threadIdx.x == 0) raise_fault(kFaultWait);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &ctl.abort;
   const float ninf = -__int_as_float(0x7f800000);
 
-  if (warp == 5) {
+  if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl.tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kWtStages; ++i) {
-      mbar_init(&ctl.k_full[i], 1);
-      mbar_init(&ctl.k_empty[i], 1);
-      mbar_init(&ctl.v_full[i], 1);
-      mbar_init(&ctl.v_empty[i], 1);
+    for (int i = 0; i < Sh::kStages; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.s_full[i], 2);   // the MMAs' commit and the issuing thread (which orders `bad`)
-      mbar_init(&ctl.p_full[i], 128);
+      mbar_init(&ctl.p_full[i], 256);
       mbar_init(&ctl.pv_done[i], 1);
     }
-    mbar_init(&ctl.q_full, 128);
+    for (int i = 0; i < kWtTileRing; ++i) {
+      mbar_init(&ctl.tile_full[i], 1);
+      mbar_init(&ctl.tile_empty[i], 11);  // softmax warps, K, V, MMAs
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&ctl.pair[i], 2);
+    mbar_init(&ctl.s_full, 2);        // the MMAs' commit and the issuing thread (which orders `bad`)
+    mbar_init(&ctl.s_free, 8);
+    mbar_init(&ctl.q_full, 1);
+    mbar_init(&ctl.q_empty, 1);
     mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     fence_mbar_init();
@@ -254,202 +317,252 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
-  const int units = a.tile_slots * a.h_kv;
 
-  if (warp == 4) {
-    // ---- producer ------------------------------------------------------------
-    const int B = a.box, per = N / B;  // boxes per block, at most 32
-    int gb = 0;                        // blocks so far
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const WtTile w = wt_tile<N>(a, u / a.h_kv);
-      const int g = u % a.h_kv;
+  if (warp == 10) {
+    // ---- tiles and Q ---------------------------------------------------------------
+    const int units = a.tile_slots * a.h_kv;
+    int k = 0, nq = 0;  // tiles published, Q copies
+    bool ok = true;
+    for (int u = blockIdx.x; ok; u += gridDim.x) {
+      WtTile w{};
+      if (u < units) {
+        w = wt_tile(a, u / a.h_kv);
+        if (w.rows == 0) continue;
+        w.g = u % a.h_kv;
+      } else {
+        w.rows = -1;
+      }
+      const int sl = k % kWtTileRing;
+      if (k >= kWtTileRing && lane == 0) ok = tm_wait(&ctl.tile_empty[sl], (uint32_t)(k / kWtTileRing - 1) & 1u, abort);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      if (lane == 0) {
+        ctl.tile[sl] = w;
+        mbar_arrive(&ctl.tile_full[sl]);
+      }
+      ++k;
+      if (w.rows < 0) break;
+      if (w.n_blk > 0 && lane == 0) {
+        if (nq > 0) ok = tm_wait(&ctl.q_empty, (uint32_t)(nq - 1) & 1u, abort);
+        if (ok) {
+          // boxes of `rows` x `group` x 64; what of the 128 rows they leave is never used
+          mbar_arrive_expect_tx(&ctl.q_full, (uint32_t)(a.rows * a.group * D * 2));
+          for (int h = 0; h < D / 64; ++h)
+            wt_tma_3d(q_buf + h * kQHalf, &q_map, h * 64, w.g * a.group, w.t0, &ctl.q_full);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (w.n_blk > 0 && ok) ++nq;
+    }
+    if (lane == 0 && nq > 0) mbar_wait_bounded(&ctl.q_full, (uint32_t)(nq - 1) & 1u, 20000000ull);
+  } else if (warp == 8 || warp == 11) {
+    // ---- K (warp 8) and V (warp 11) -----------------------------------------------------
+    const bool is_k = warp == 8;
+    const CUtensorMap* map = is_k ? &k_map : &v_map;
+    const int B = a.box, sh = a.box_shift;
+    const int per = N >> sh;                       // boxes of a block, at most 16
+    const int per_st = is_k ? per : Sh::kVRows >> sh;  // and of a stage
+    const uint32_t box_bytes = (uint32_t)B * (is_k ? 256u : D * 2u);
+    int gb = 0, rs = 0, done = 0;                  // blocks, ring stages, own last stage + 1 so far
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      WtTile w;
+      if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
       const int32_t* pt = a.page_table + (int64_t)w.r * a.ld_pt;
-      // first cache row of the block's box `lane`; n_slots (zeros) where the
-      // page is out of range
+      const int oob = (int)(a.n_slots >> 3);       // 8-row groups of the map
+      // first 8-row group of the block's box `lane`; past the map (zeros)
+      // where the page is out of range
       auto lookup = [&](int blk) -> int {
         const int j = blk * per + lane;
-        if (lane >= per || j >= w.n_box) return 0;
-        const int e = j * B;
+        if (blk >= w.n_blk || lane >= per || j >= w.n_box) return 0;
+        const int e = j << sh;
         const int pos = e < w.nsr ? e : w.start + (e - w.nsr);
         const int pi = pos / a.page_size;
         const int64_t page = __ldg(pt + pi);
-        if (page < 0 || (page + 1) * a.page_size > a.n_slots) return (int)a.n_slots;
-        return (int)(page * a.page_size) + (pos - pi * a.page_size);
+        if (page < 0 || (page + 1) * a.page_size > a.n_slots) return oob;
+        return (int)((page * a.page_size + (pos - pi * a.page_size)) >> 3);
       };
-      int next = w.n_blk > 0 ? lookup(0) : 0;
-      for (int blk = 0; blk < w.n_blk; ++blk, ++gb) {
+      int next = lookup(0);
+      for (int blk = 0; ok && blk < w.n_blk; ++blk) {
         const int row = next;
-        if (blk + 1 < w.n_blk) next = lookup(blk + 1);
+        next = lookup(blk + 1);
         const int nb = min(per, w.n_box - blk * per);
-        const int st = gb % kWtStages;
-        const uint32_t bad = __ballot_sync(0xffffffffu, lane < nb && row == (int)a.n_slots);
-        if (bad != 0 && lane == 0) raise_fault(kFaultIndex);
-        const int ops = nb * H;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint64_t* full = m == 0 ? &ctl.k_full[st] : &ctl.v_full[st];
-          uint64_t* empty = m == 0 ? &ctl.k_empty[st] : &ctl.v_empty[st];
-          bool ok = true;
-          if (gb >= kWtStages && lane == 0) ok = tm_wait(empty, (uint32_t)(gb / kWtStages - 1) & 1u, abort);
-          if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) goto produced;
+        if (is_k) {
+          const uint32_t bad = __ballot_sync(0xffffffffu, lane < nb && row == oob);
           if (lane == 0) {
-            if (m == 0) ctl.bad[gb % kWtBadRing] = bad;
-            mbar_arrive_expect_tx(full, (uint32_t)ops * (uint32_t)B * 128u);
+            if (bad != 0) raise_fault(kFaultIndex);
+            ctl.bad[(gb + blk) % kWtBadRing] = bad;
           }
+        }
+        // stages in the order of use: K(0), K(1), V(0), K(2), V(1), ...
+        int at = rs + (is_k ? Sh::kKs * blk + max(blk - 1, 0) * Sh::kVs
+                            : Sh::kKs * min(blk + 2, w.n_blk) + blk * Sh::kVs);
+        const int n_st = is_k ? Sh::kKs : (nb + per_st - 1) / per_st;
+        for (int i = 0; ok && i < n_st; ++i, ++at) {
+          const int st = at % Sh::kStages;
+          const int b0 = is_k ? 0 : i * per_st, n = is_k ? nb : min(per_st, nb - b0);
+          if (at >= Sh::kStages && lane == 0) ok = tm_wait(&ctl.empty[st], (uint32_t)(at / Sh::kStages - 1) & 1u, abort);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], (uint32_t)n * box_bytes);
           __syncwarp();
-          unsigned char* dst = (m == 0 ? k_buf : v_buf) + st * kWtStageBytes;
-          for (int i0 = 0; i0 < ops; i0 += 32) {
-            const int i = i0 + lane;
-            const int bx = i / H, hf = i % H;
-            const int y = __shfl_sync(0xffffffffu, row, bx & 31);
-            if (i < ops)
-              tma_load_2d(dst + hf * kHalfBytes + bx * B * 128, m == 0 ? &k_map : &v_map, g * D + hf * 64, y, full);
-          }
+          const int y = __shfl_sync(0xffffffffu, row, (b0 + lane) & 31);
+          if (lane < n)
+            wt_tma_4d(ring + st * kWtStageBytes + lane * box_bytes, map,
+                      w.g * (D / 64) + (is_k ? i * 2 : 0), y, &ctl.full[st]);
+          done = at + 1;
         }
       }
-    }
-  produced:
-    // every copy has landed before the shared memory is released
-    if (lane == 0) {
-      for (int j = max(0, gb - kWtStages); j <= gb; ++j) {
-        const int st = j % kWtStages;
-        const uint32_t ph = (uint32_t)(j / kWtStages) & 1u;
-        if (j < gb) {
-          mbar_wait_bounded(&ctl.k_full[st], ph, 20000000ull);
-          mbar_wait_bounded(&ctl.v_full[st], ph, 20000000ull);
-        } else if (*abort) {  // the block whose K copies may be under way
-          mbar_wait_bounded(&ctl.k_full[st], ph, 20000000ull);
-        }
+      gb += w.n_blk;
+      if (w.n_blk > 0) {
+        const int last = w.n_box * B - (w.n_blk - 1) * N;  // rows copied for the last block
+        rs += Sh::kKs * w.n_blk + (w.n_blk - 1) * Sh::kVs + (last + Sh::kVRows - 1) / Sh::kVRows;
       }
     }
-  } else if (warp == 5) {
-    // ---- MMA issuer --------------------------------------------------------------
+    // after an abort: copies under way land before the shared memory is
+    // released (else every stage was waited for by its MMAs)
+    if (lane == 0 && *abort)
+      for (int j = max(0, done - Sh::kStages); j < done; ++j)
+        mbar_wait_bounded(&ctl.full[j % Sh::kStages], (uint32_t)(j / Sh::kStages) & 1u, 20000000ull);
+  } else if (warp == 9) {
+    // ---- MMA issuer --------------------------------------------------------------------
     constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
     constexpr uint32_t kIdescO = kIdescS | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // B is MN-major
-    int gb = 0, tiles = 0;  // blocks and tiles so far
+    // descriptors: the upper words never change, the lower ones by constants
+    const uint64_t q_desc = umma_desc_sw128(smem_u32(q_buf)), k_desc0 = umma_desc_sw128(smem_u32(ring), Sh::kKGroup),
+                   v_desc0 = wt_desc_mn(smem_u32(ring), Sh::kVGroup);
+    auto add = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };  // stays inside the address field
+    int gb = 0, rs = 0, nq = 0;  // blocks, ring stages and Q copies so far
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const WtTile w = wt_tile<N>(a, u / a.h_kv);
+    for (int k = 0; ok; ++k) {
+      WtTile w;
+      if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
       if (w.n_blk == 0) continue;
       if (lane == 0) {
-        const int entries = w.n_box * a.box;
-        auto n16 = [&](int blk) { return (min(N, entries - blk * N) + 15) & ~15; };
+        auto n16 = [&](int blk) { return (min(N, w.uc - blk * N) + 15) & ~15; };
         auto qk = [&](int blk) -> bool {
-          const int x = gb + blk, st = x % kWtStages, sl = x & 1;
-          if (!tm_wait(&ctl.k_full[st], (uint32_t)(x / kWtStages) & 1u, abort)) return false;
-          // P of two blocks ago lies in this S buffer
-          if (x >= 2 && !tm_wait(&ctl.pv_done[sl], (uint32_t)((x >> 1) - 1) & 1u, abort)) return false;
-          tc_fence_after();
+          const int x = gb + blk;
+          if (x >= 1 && !tm_wait(&ctl.s_free, (uint32_t)(x - 1) & 1u, abort)) return false;
           const uint32_t idesc = kIdescS | ((uint32_t)(n16(blk) >> 3) << 17);
-          const uint32_t kb = smem_u32(k_buf + st * kWtStageBytes);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            wt_mma_ts(tmem + Sh::kColS + sl * N, tmem + Sh::kColQ + k * 8,
-                      umma_desc_sw128(kb + (k >> 2) * kHalfBytes + (k & 3) * 32), idesc, k > 0 ? 1u : 0u);
-          umma_commit(&ctl.k_empty[st]);
-          umma_commit(&ctl.s_full[sl]);
-          mbar_arrive(&ctl.s_full[sl]);
+          for (int i = 0; i < Sh::kKs; ++i) {
+            const int st = rs % Sh::kStages;
+            if (!tm_wait(&ctl.full[st], (uint32_t)(rs / Sh::kStages) & 1u, abort)) return false;
+            tc_fence_after();
+            const uint64_t kd = add(k_desc0, st * kWtStageBytes), qd = add(q_desc, i * 2 * kQHalf);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              umma_bf16(tmem + Sh::kColS, add(qd, (c >> 2) * kQHalf + (c & 3) * 32),
+                        add(kd, (c >> 2) * 1024 + (c & 3) * 32), idesc, i > 0 || c > 0 ? 1u : 0u);
+            umma_commit(&ctl.empty[st]);
+            ++rs;
+          }
+          umma_commit(&ctl.s_full);
+          mbar_arrive(&ctl.s_full);
+          if (blk + 1 == w.n_blk) umma_commit(&ctl.q_empty);
           return true;
         };
         auto pv = [&](int blk) -> bool {
-          const int x = gb + blk, st = x % kWtStages, sl = x & 1;
-          if (!tm_wait(&ctl.v_full[st], (uint32_t)(x / kWtStages) & 1u, abort)) return false;
+          const int x = gb + blk, sl = x & 1;
           if (!tm_wait(&ctl.p_full[sl], (uint32_t)(x >> 1) & 1u, abort)) return false;
-          tc_fence_after();
-          const uint32_t vb = smem_u32(v_buf + st * kWtStageBytes);
-          const int steps = n16(blk) / 16;
-          for (int k = 0; k < steps; ++k)
-            wt_mma_ts(tmem, tmem + Sh::kColS + sl * N + k * 8, wt_desc_mn(vb + k * 2048, kHalfBytes), kIdescO,
-                      blk > 0 || k > 0 ? 1u : 0u);
-          umma_commit(&ctl.v_empty[st]);
+          const int n = n16(blk), copied = min(N, w.n_box * a.box - blk * N);
+          for (int e0 = 0; e0 < copied; e0 += Sh::kVRows) {
+            const int st = rs % Sh::kStages;
+            if (!tm_wait(&ctl.full[st], (uint32_t)(rs / Sh::kStages) & 1u, abort)) return false;
+            tc_fence_after();
+            const uint64_t vd = add(v_desc0, st * kWtStageBytes);
+            const uint32_t p = tmem + Sh::kColP + sl * 64 + e0 / 2;
+            const int steps = min(Sh::kVRows, n - e0) / 16;  // none for rows past the last key
+            const uint32_t first = blk > 0 || e0 > 0 ? 1u : 0u;
+#pragma unroll
+            for (int c = 0; c < Sh::kVRows / 16; ++c)
+              if (c < steps)
+                wt_mma_ts(tmem, p + c * 8, add(vd, c * 2 * Sh::kVGroup), kIdescO, c > 0 ? 1u : first);
+            umma_commit(&ctl.empty[st]);
+            ++rs;
+          }
           umma_commit(&ctl.pv_done[sl]);
           return true;
         };
-        ok = tm_wait(&ctl.q_full, (uint32_t)tiles & 1u, abort);
-        ok = ok && qk(0) && (w.n_blk < 2 || qk(1));
-        for (int i = 0; ok && i < w.n_blk; i += 2)
-          ok = pv(i) && (i + 1 >= w.n_blk || pv(i + 1)) && (i + 2 >= w.n_blk || qk(i + 2)) &&
-               (i + 3 >= w.n_blk || qk(i + 3));
+        ok = tm_wait(&ctl.q_full, (uint32_t)nq & 1u, abort) && qk(0);
+        for (int i = 0; ok && i < w.n_blk; ++i) ok = (i + 1 >= w.n_blk || qk(i + 1)) && pv(i);
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       gb += w.n_blk;
-      ++tiles;
+      ++nq;
     }
     if (lane == 0) {  // every MMA has finished before the memories are released
       umma_commit(&ctl.drain);
       mbar_wait_bounded(&ctl.drain, 0u, 20000000ull);
     }
   } else {
-    // ---- softmax, Q and outputs: thread = pair -----------------------------------
-    const int pair = threadIdx.x;                 // MMA row = tensor-memory lane
+    // ---- softmax and outputs: a pair in two threads ------------------------------------
+    const int half = warp >> 2;                   // columns 64 half .. + 63 of S, D/2 half .. of O
+    const int pair = (warp & 3) * 32 + lane;      // MMA row = tensor-memory lane
     const int row = pair / a.group, hd = pair - row * a.group;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float thr = 8.0f / a.c;                 // growth of the maximum that forces a rescale
-    int gb = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const WtTile w = wt_tile<N>(a, u / a.h_kv);
-      if (w.rows == 0) continue;
-      const int g = u % a.h_kv;
+    uint64_t* pair_bar = &ctl.pair[warp & 3];
+    int gb = 0, rs = 0, n_pair = 0;               // blocks, ring stages, exchanges so far
+    // both warps of the pair have written what comes before
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_bar);
+      const bool ok = __all_sync(0xffffffffu, tm_wait(pair_bar, (uint32_t)n_pair & 1u, abort));
+      ++n_pair;
+      return ok;
+    };
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      WtTile w;
+      if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
       const bool mine = row < w.rows;
       const int64_t t = w.t0 + row;
       int L = mine ? __ldg(a.row_len + t) : 0;
       if (L < 0 || L > a.max_len) L = 0;
-      const int64_t hq = t * a.h_q + (int64_t)g * a.group + hd;
+      const int64_t hq = t * a.h_q + (int64_t)w.g * a.group + hd;
       float m = ninf, l = 0.f;
-      if (w.n_blk > 0) {
-        // Q row -> tensor memory (every earlier product has read the last one)
-        const uint16_t* src = a.q + t * a.ld_q + ((int64_t)g * a.group + hd) * D;
-#pragma unroll
-        for (int c0 = 0; c0 < D / 2; c0 += 32) {
-          uint32_t v[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 x = mine ? __ldg(reinterpret_cast<const uint4*>(src + c0 * 2) + i) : make_uint4(0u, 0u, 0u, 0u);
-            v[4 * i] = x.x ^ a.flip;
-            v[4 * i + 1] = x.y ^ a.flip;
-            v[4 * i + 2] = x.z ^ a.flip;
-            v[4 * i + 3] = x.w ^ a.flip;
-          }
-          wt_tmem_st32(lanes + Sh::kColQ + c0, v);
-        }
-        wt_wait_st();
-        tc_fence_before();
-        mbar_arrive(&ctl.q_full);
-      }
       // the pair sees entries [0, va) and [vb, vc)
       const int va = min(a.n_sink, L);
       const int vb = L > 0 ? w.nsr + max(0, L - a.window) - w.start : 0;
       const int vc = L > 0 ? w.nsr + L - w.start : 0;
-      const int entries = w.n_box * a.box;
-      bool ok = true;
       for (int blk = 0; blk < w.n_blk; ++blk) {
-        const int x = gb + blk, sl = x & 1, st = x % kWtStages;
-        const int e0 = blk * N, n = min(N, entries - e0);
-        ok = __all_sync(0xffffffffu, tm_wait(&ctl.s_full[sl], (uint32_t)(x >> 1) & 1u, abort));
+        const int x = gb + blk, sl = x & 1;
+        const int e0 = blk * N;
+        ok = __all_sync(0xffffffffu, tm_wait(&ctl.s_full, (uint32_t)x & 1u, abort));
         if (!ok) break;
         tc_fence_after();
         const uint32_t bad = ctl.bad[x % kWtBadRing];
-        const uint32_t s_col = lanes + Sh::kColS + sl * N;
-        uint32_t s[N];
-        {
-          uint32_t(&s0)[64] = *reinterpret_cast<uint32_t(*)[64]>(s);
-          wt_tmem_ld64(s_col, s0);
-          if constexpr (N == 128) {
-            uint32_t(&s1)[64] = *reinterpret_cast<uint32_t(*)[64]>(s + 64);
-            wt_tmem_ld64(s_col + 64, s1);
+        const int c0 = e0 + 64 * half;            // first entry of this thread
+        uint32_t s[64];
+        wt_tmem_ld64(lanes + Sh::kColS + 64 * half, s);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.s_free);
+        if (a.flip != 0) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) s[j] ^= a.flip;
+        }
+        if (__any_sync(0xffffffffu, bad != 0 || c0 < vb || c0 + 64 > vc)) {
+          uint64_t see = wt_low_bits(va - c0) | (wt_low_bits(vc - c0) & ~wt_low_bits(vb - c0));
+          if (bad != 0)
+            for (int j = 0; j < 64; j += a.box < 64 ? a.box : 64)
+              if ((bad >> ((64 * half + j) >> a.box_shift)) & 1u) see &= ~(wt_low_bits(a.box) << j);
+          const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            s[j] = (see0 >> j) & 1u ? s[j] : 0xff800000u;
+            s[32 + j] = (see1 >> j) & 1u ? s[32 + j] : 0xff800000u;
           }
         }
-        if (__any_sync(0xffffffffu, bad != 0 || e0 < vb || e0 + N > vc)) {
+        float mx4[4] = {ninf, ninf, ninf, ninf};
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const int e = e0 + j;
-            const bool see = (e < va || (e >= vb && e < vc)) && !((bad >> (j >> a.box_shift)) & 1u);
-            s[j] = see ? s[j] : 0xff800000u;
-          }
-        }
-        float mx = ninf;
-#pragma unroll
-        for (int j = 0; j < N; ++j) mx = fmaxf(mx, __uint_as_float(s[j]));
+        for (int j = 0; j < 64; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(s[j]));
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        ctl.mx[x & 1][half][pair] = mx;
+        ok = meet();
+        if (!ok) break;
+        mx = fmaxf(mx, ctl.mx[x & 1][half ^ 1][pair]);
         const bool grow = m != ninf && mx > m + thr;
         if (__any_sync(0xffffffffu, grow)) {
           // O holds every product before this block's
@@ -460,86 +573,118 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
           l *= f;
           if (m != ninf) m = fmaxf(m, mx);
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
+          for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
             uint32_t o[32];
-            wt_tmem_ld32(lanes + c0, o);
+            wt_tmem_ld32(lanes + c, o);
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            wt_tmem_st32(lanes + c0, o);
+            wt_tmem_st32(lanes + c, o);
           }
         }
         if (m == ninf) m = mx;
         const float off = m == ninf ? 0.f : -m * a.c;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t p[32];
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 64) {
-          uint32_t p[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float p0 = ka_ex2(fmaf(__uint_as_float(s[c0 + 2 * j]), a.c, off));
-            const float p1 = ka_ex2(fmaf(__uint_as_float(s[c0 + 2 * j + 1]), a.c, off));
-            l += p0 + p1;
-            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-            p[j] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          wt_tmem_st32(s_col + c0 / 2, p);
+        for (int j = 0; j < 32; ++j) {
+          const float p0 = ka_ex2(fmaf(__uint_as_float(s[2 * j]), a.c, off));
+          const float p1 = ka_ex2(fmaf(__uint_as_float(s[2 * j + 1]), a.c, off));
+          l4[j & 3] += p0 + p1;
+          const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+          p[j] = *reinterpret_cast<const uint32_t*>(&b);
         }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        wt_tmem_st32(lanes + Sh::kColP + sl * 64 + 32 * half, p);
         wt_wait_st();
         tc_fence_before();
         // V rows that no pair sees: zeros
-        const int n16 = (n + 15) & ~15;
+        const int n16 = (min(N, w.uc - e0) + 15) & ~15;
         if (e0 < w.ub || e0 + n16 > w.uc) {
-          ok = __all_sync(0xffffffffu, tm_wait(&ctl.v_full[st], (uint32_t)(x / kWtStages) & 1u, abort));
-          if (!ok) break;
-          unsigned char* vst = v_buf + st * kWtStageBytes;
-          constexpr int kPieces = D / 8;  // 16-byte pieces of a row
-          for (int i = threadIdx.x; i < n16 * kPieces; i += 128) {
-            const int r = i / kPieces, pc = i % kPieces;
-            const int e = e0 + r;
-            if (!(e < w.ua || (e >= w.ub && e < w.uc)))
-              *reinterpret_cast<uint4*>(vst + (pc >> 3) * kHalfBytes + r * 128 + (pc & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          const int at = rs + Sh::kKs * min(blk + 2, w.n_blk) + blk * Sh::kVs;  // V's first stage
+          for (int v = 0; ok && v * Sh::kVRows < n16; ++v) {
+            const int st = (at + v) % Sh::kStages;
+            ok = __all_sync(0xffffffffu, tm_wait(&ctl.full[st], (uint32_t)((at + v) / Sh::kStages) & 1u, abort));
+            if (!ok) break;
+            unsigned char* vst = ring + st * kWtStageBytes;
+            const int rows = min(Sh::kVRows, n16 - v * Sh::kVRows);
+            for (int r = warp; r < rows; r += 8) {  // a row a warp, 16 bytes a lane
+              const int e = e0 + v * Sh::kVRows + r;
+              if (!(e < w.ua || (e >= w.ub && e < w.uc)) && lane < D / 8)
+                *reinterpret_cast<uint4*>(vst + (r >> 3) * Sh::kVGroup + (lane >> 3) * 1024 + (r & 7) * 128 +
+                                          (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
+          if (!ok) break;
           fence_proxy_async_smem();
         }
         mbar_arrive(&ctl.p_full[sl]);
       }
       if (!ok) break;
       gb += w.n_blk;
-      // ---- outputs ----------------------------------------------------------------
+      if (w.n_blk > 0) {
+        const int last = w.n_box * a.box - (w.n_blk - 1) * N;  // rows copied for the last block
+        rs += Sh::kKs * w.n_blk + (w.n_blk - 1) * Sh::kVs + (last + Sh::kVRows - 1) / Sh::kVRows;
+      }
+      // ---- outputs ---------------------------------------------------------------------
       float inv = 0.f;
       if (w.n_blk > 0) {
+        ctl.mx[gb & 1][half][pair] = l;  // the last block's maxima are in the other one
+        ok = meet();
+        if (!ok) break;
+        l += ctl.mx[gb & 1][half ^ 1][pair];
+        ok = meet();  // read, before the next tile's first maxima
+        if (!ok) break;
         ok = __all_sync(0xffffffffu, tm_wait(&ctl.pv_done[(gb - 1) & 1], (uint32_t)((gb - 1) >> 1) & 1u, abort));
         if (!ok) break;
         tc_fence_after();
         inv = l == 0.f ? 0.f : 1.0f / l;
       }
+      // 32 columns at a time: 4 pieces of 16 bytes a lane, transposed over the
+      // quad so that its lanes write 64 consecutive bytes of one row (written
+      // a row a lane, every store met 32 lines: 4,000 clocks a tile)
+      const int sub = lane & 3;
       uint16_t* dst = a.out + hq * D;
-#pragma unroll 2
-      for (int c0 = 0; c0 < D; c0 += 32) {
+#pragma unroll 1
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
         uint32_t o[32];
         if (w.n_blk > 0) {
-          wt_tmem_ld32(lanes + c0, o);
+          wt_tmem_ld32(lanes + c, o);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = 0u;
         }
-        if (mine) {
+        uint32_t y[4][4];  // [piece][word]
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            U8 y;
+        for (int j = 0; j < 16; ++j) {
+          // a row that sees nothing writes zeros, whatever the accumulator holds
+          const float x0 = l == 0.f ? 0.f : __uint_as_float(o[2 * j]) * inv;
+          const float x1 = l == 0.f ? 0.f : __uint_as_float(o[2 * j + 1]) * inv;
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+          y[j >> 2][j & 3] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        // y[p] of lane q <-> y[q] of lane p
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              // a row that sees nothing writes zeros, whatever the accumulator holds
-              const float x0 = l == 0.f ? 0.f : __uint_as_float(o[16 * j + 2 * i]) * inv;
-              const float x1 = l == 0.f ? 0.f : __uint_as_float(o[16 * j + 2 * i + 1]) * inv;
-              const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
-              y.w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            st_32(dst + c0 + 16 * j, y);
-          }
+        for (int d = 1; d <= 2; d <<= 1)
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            if ((p & d) == 0)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const bool up = (sub & d) != 0;
+                const uint32_t give = up ? y[p][j] : y[p | d][j];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, d);
+                if (up) y[p][j] = got;
+                else y[p | d][j] = got;
+              }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {  // row of the quad's lane p, piece `sub`
+          const int64_t at = __shfl_sync(0xffffffffu, mine ? (long long)(dst - a.out) : -1ll, (lane & ~3) | p);
+          if (at >= 0)
+            *reinterpret_cast<uint4*>(a.out + at + c + sub * 8) = make_uint4(y[p][0], y[p][1], y[p][2], y[p][3]);
         }
       }
       tc_fence_before();
-      if (mine && a.lse != nullptr)
+      if (mine && half == 0 && a.lse != nullptr)
         a.lse[hq] = l == 0.f ? ninf : (m == ninf ? l : (fmaf(m, a.c, log2f(l))) * 0.69314718055994531f);
     }
   }
@@ -547,7 +692,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5)
+  if (warp == 9)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
