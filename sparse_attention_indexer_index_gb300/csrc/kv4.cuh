@@ -81,9 +81,16 @@ __device__ __forceinline__ uint2 kv4_quantise(const U8& x, float inv_g, uint8_t&
   return make_uint2(c[0], c[1]);
 }
 
-// Two codes of a byte -> two FP16 values (exact).
-__device__ __forceinline__ __half2 kv4_pair(uint32_t byte) {
-  return __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1));
+// The eight codes of a word -> four FP16 pairs, byte by byte (exact).
+__device__ __forceinline__ void kv4_word(uint32_t w, __half2 (&h)[4]) {
+  uint32_t r[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __half2*>(&r[i]);
 }
 // Two scale bytes -> two FP16 scales (exact).
 __device__ __forceinline__ __half2 kv4_scales(uint32_t two) {
@@ -94,10 +101,13 @@ __device__ __forceinline__ __half2 kv4_scales(uint32_t two) {
 __device__ __forceinline__ U8 kv4_read(uint2 codes, uint32_t scale, float g) {
   const __half2 s = kv4_scales(scale | (scale << 8));
   const uint32_t c[2] = {codes.x, codes.y};
+  __half2 h[2][4];
+  kv4_word(c[0], h[0]);
+  kv4_word(c[1], h[1]);
   U8 r;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float2 f = __half22float2(__hmul2(kv4_pair((c[i >> 2] >> (8 * (i & 3))) & 0xffu), s));
+    const float2 f = __half22float2(__hmul2(h[i >> 2][i & 3], s));
     const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * g, f.y * g);
     r.w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }

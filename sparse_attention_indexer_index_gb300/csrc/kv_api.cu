@@ -168,7 +168,7 @@ bool encode_q_map(CUtensorMap* m, const WtArgs& a, int d) {
 // The tensor-core form of window_attn, for requests of more than kWtMinRows
 // rows on pages of whole 8-row groups; QSA_ERR_UNSUPPORTED where the other
 // form has to serve.
-constexpr int kWtMinRows = 8;
+constexpr int kWtMinRows = 1;
 qsa_status launch_window_tc(const KvAttnArgs& k, int d, int32_t max_rows_per_req, cudaStream_t stream) {
   if (max_rows_per_req <= kWtMinRows || k.page_size % 8 != 0 || k.n_slots < 8) return QSA_ERR_UNSUPPORTED;
   WtArgs a{};

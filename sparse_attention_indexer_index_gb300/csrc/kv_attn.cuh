@@ -204,7 +204,11 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
   using Sh = KaShape<D, kFp4>;
   constexpr int KS = D / 16;   // k-steps of S
   constexpr int VN = D / 8;    // n-tiles of O
-  constexpr int kBias = kFp4 ? 10 : 0;  // weights are held as 2^kBias p, clear of FP16's subnormals
+  // Weights are held as 2^kBias p, clear of FP16's subnormals.  The running
+  // maximum follows only when it grew by more than 2^kGrow (a warp has few
+  // tiles, and every change rescales the whole accumulator), so a weight is
+  // at most 2^(kBias + kGrow) <= 2^15.
+  constexpr int kBias = kFp4 ? 10 : 0, kGrow = 5;
   extern __shared__ __align__(128) unsigned char ka_smem[];
   __shared__ uint32_t s_mask[kKaWarps][4];       // valid entries of a stage
   __shared__ float s_m[kKaWarps][NT * 8], s_l[kKaWarps][NT * 8];
@@ -384,9 +388,11 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const __half2 sk = k < 2 ? __low2half2(sc) : __high2half2(sc);
+            __half2 h[4];
+            kv4_word(w[k], h);
             uint32_t b[4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) b[y] = ka_h2(__hmul2(kv4_pair((w[k] >> (8 * y)) & 0xffu), sk));
+            for (int y = 0; y < 4; ++y) b[y] = ka_h2(__hmul2(h[y], sk));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               ka_mma<true>(s[nt][j], qa[nt][i * 8 + 2 * k][0], 0u, qa[nt][i * 8 + 2 * k][1], 0u, b[0], b[1]);
@@ -424,10 +430,9 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
         }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[nt], mx);
-      const float ms = mn == ninf ? 0.f : mn - (float)kBias;
-      if (__any_sync(0xffffffffu, mn != m[nt])) {
-        const float f = ka_ex2(m[nt] - (mn == ninf ? 0.f : mn));
+      if (__any_sync(0xffffffffu, m[nt] != ninf && mx > m[nt] + (float)kGrow)) {
+        const float mn = fmaxf(m[nt], mx);
+        const float f = m[nt] == ninf ? 1.f : ka_ex2(m[nt] - mn);  // -inf: nothing yet
         l[nt] *= f;
 #pragma unroll
         for (int i = 0; i < VN; ++i)
@@ -435,6 +440,8 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
           for (int y = 0; y < 4; ++y) o[nt][i][y] *= f;
         m[nt] = mn;
       }
+      if (m[nt] == ninf) m[nt] = mx;
+      const float ms = m[nt] == ninf ? 0.f : m[nt] - (float)kBias;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float p0 = ka_ex2(x[j][0] - ms), p1 = ka_ex2(x[j][1] - ms);
@@ -474,12 +481,15 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
         const uint32_t o0 = ((w[0][k] >> 4) & 0x0f0f0f0fu) | (w[1][k] & 0xf0f0f0f0u);
         const uint32_t e1 = (w[2][k] & 0x0f0f0f0fu) | ((w[3][k] & 0x0f0f0f0fu) << 4);
         const uint32_t o1 = ((w[2][k] >> 4) & 0x0f0f0f0fu) | (w[3][k] & 0xf0f0f0f0u);
+        __half2 he0[4], he1[4], ho0[4], ho1[4];
+        kv4_word(e0, he0);
+        kv4_word(e1, he1);
+        kv4_word(o0, ho0);
+        kv4_word(o1, ho1);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const uint32_t b0 = ka_h2(__hmul2(kv4_pair((e0 >> (8 * y)) & 0xffu), s0));
-          const uint32_t b1 = ka_h2(__hmul2(kv4_pair((e1 >> (8 * y)) & 0xffu), s1));
-          const uint32_t b2 = ka_h2(__hmul2(kv4_pair((o0 >> (8 * y)) & 0xffu), s0));
-          const uint32_t b3 = ka_h2(__hmul2(kv4_pair((o1 >> (8 * y)) & 0xffu), s1));
+          const uint32_t b0 = ka_h2(__hmul2(he0[y], s0)), b1 = ka_h2(__hmul2(he1[y], s1));
+          const uint32_t b2 = ka_h2(__hmul2(ho0[y], s0)), b3 = ka_h2(__hmul2(ho1[y], s1));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             ka_mma<true>(o[nt][8 * k + 2 * y], pa[nt][0], pa[nt][1], pa[nt][2], pa[nt][3], b0, b1);
