@@ -614,98 +614,118 @@ def _indexer_select_call(fn, key_ptrs, pool_rows, q, req_row_start, row_len, pag
 
 
 # ----------------------------------------------------------------- 4-bit KV cache, window attention
-def _rows3(t, name):
-    """A BF16 tensor [n][heads][head_dim] whose rows are contiguous (they may
-    lie further apart, e.g. columns of a projection's output): its row pitch."""
+# The checks of these calls run in two forms: one pass over cheap attributes,
+# and only when that finds something (_explain) the one that says what.  A
+# decode step's calls cost the host a few microseconds each, mostly these.
+_types = None
+
+
+def _t():
+    """(torch.bfloat16, torch.float32, torch.int32, torch.uint8, current device index)."""
+    global _types
+    if _types is None:
+        torch = _torch()
+        _types = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
+                  getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
+    return _types
+
+
+def _all(dev, dtype, *ts):
+    """Whether every tensor lies contiguous on device `dev` with this dtype."""
+    for t in ts:
+        if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+            return False
+    return True
+
+
+def _rows_ok(t, dev, dtype):
+    """A tensor [n][heads][head_dim] whose rows are contiguous (they may lie
+    further apart, e.g. columns of a projection's output)."""
+    if t.get_device() != dev or t.dtype is not dtype or t.dim() != 3:
+        return False
+    _, h, d = t.shape
+    _, s1, s2 = t.stride()
+    return (s2 == 1 or d == 1) and (s1 == d or h == 1)
+
+
+def _explain(fn, first, rows=(), i32=(), u8=(), bf16=(), f32=()):
+    """Raises for the first (tensor, name, dims) that is not what the call
+    takes: rows (see _rows_ok), the others contiguous; dims None: any."""
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims")
-    n, h, d = t.shape
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 and d != 1) or (s1 != d and h != 1):
-        raise ValueError(f"{name} must have contiguous rows of [heads][head_dim]")
-    return s0 if n > 1 else h * d
+    for t, name in rows:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must have 3 dims")
+        if not _rows_ok(t, t.get_device(), torch.bfloat16):
+            raise ValueError(f"{name} must have contiguous rows of [heads][head_dim]")
+    for dtype, ts in ((torch.int32, i32), (torch.uint8, u8), (torch.bfloat16, bf16), (torch.float32, f32)):
+        for t, name, dims in ts:
+            if t is not None:
+                _dev(t, dtype, name, dims)
+    for t, name, *_ in (*rows, *i32, *u8, *bf16, *f32):
+        if t is not None and t.get_device() != first.get_device():
+            raise ValueError(f"{fn}: all tensors must be on the same device ({name} is not)")
+    raise ValueError(f"{fn}: the arguments' shapes do not fit together")
 
 
-def _cache4(k_codes, k_scales, v_codes, v_scales):
-    """Checks the four arrays of a 4-bit cache; returns (n_slots, h_kv, head_dim)."""
-    u8 = _torch().uint8
-    _dev(k_codes, u8, "k_codes", 3)
-    _dev(k_scales, u8, "k_scales", 3)
-    _dev(v_codes, u8, "v_codes", 3)
-    _dev(v_scales, u8, "v_scales", 3)
-    shape = k_codes.shape
-    n, h, w = shape
-    if v_codes.shape != shape or k_scales.shape != v_scales.shape or tuple(k_scales.shape) != (n, h, w // 8) or w % 8:
-        raise ValueError("codes must be [n_slots][h_kv][head_dim/2] and scales [n_slots][h_kv][head_dim/16]")
-    return n, h, 2 * w
-
-
-def _launch(fn, stream, first, others, *args):
-    """Calls `fn` on the device of tensor `first` (all tensors must be there),
-    on `stream` or that device's current stream."""
+def _launch(fn, dev, stream, *args):
+    """Calls `fn` on device `dev`, on `stream` or that device's current one;
+    the status."""
+    if dev == _t()[4]():
+        return _call(fn, *args, _raw_stream(dev) if _raw_stream and stream is None else _stream(stream))
     torch = _torch()
-    dev = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{fn}: all tensors must be on the same device")
-    if dev == torch.cuda.current_device():
-        _check(fn, _call(fn, *args, _stream(stream, first.device)))
-    else:
-        with torch.cuda.device(dev):
-            _check(fn, _call(fn, *args, _stream(stream, first.device)))
+    with torch.cuda.device(dev):
+        return _call(fn, *args, _stream(stream))
 
 
-def _attn_out(q, n_rows, h_q, d, dtype, out, lse, want_lse):
-    torch = _torch()
-    if out is None:
-        out = torch.empty((n_rows, h_q, d), dtype=dtype, device=q.device)
-    elif tuple(_dev(out, dtype, "out", 3).shape) != (n_rows, h_q, d):
-        raise ValueError("out must have q's shape")
-    if not want_lse:
-        return out, None
-    if lse is None:
-        lse = torch.empty((n_rows, h_q), dtype=torch.float32, device=q.device)
-    elif tuple(_dev(lse, torch.float32, "lse", 2).shape) != (n_rows, h_q):
-        raise ValueError("lse must be [n_rows][h_q]")
-    return out, lse
-
-
-def _attn_workspace(nbytes, workspace, q):
+def _launch_ws(fn, dev, stream, size_fn, size_args, workspace, *args):
+    """_launch of a call that ends in (workspace, bytes): without one given,
+    the call itself says whether it needs one."""
     if workspace is None:
-        if not nbytes:
-            return None, 0
-        workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=q.device)
-    return workspace, workspace.numel() * workspace.element_size()
+        st = _launch(fn, dev, stream, *args, None, 0)
+        if st != -3:
+            return _check(fn, st)
+        torch = _torch()
+        workspace = torch.empty(_call(size_fn, *size_args), dtype=torch.uint8, device=torch.device("cuda", dev))
+    _check(fn, _launch(fn, dev, stream, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size()))
 
 
 def append_kv_fp4(k_new, v_new, req_tok_start, req_first_pos, k_codes, k_scales, v_codes, v_scales, page_table,
                   page_size, k_scale=1.0, v_scale=1.0, stream=None):
     """Quantises K and V rows [n_tok][h_kv][head_dim] bf16 into the 4-bit
     cache (in place): request r's rows req_tok_start[r] .. go to the slots of
-    positions req_first_pos[r], req_first_pos[r]+1, ...  k_scale and v_scale
-    (powers of two) scale the whole tensors.  Returns the four arrays."""
-    torch = _torch()
-    ld_k, ld_v = _rows3(k_new, "k_new"), _rows3(v_new, "v_new")
-    _dev(req_tok_start, torch.int32, "req_tok_start", 1)
-    _dev(req_first_pos, torch.int32, "req_first_pos", 1)
-    _dev(page_table, torch.int32, "page_table", 2)
-    n_slots, h_kv, d = _cache4(k_codes, k_scales, v_codes, v_scales)
-    n_tok = k_new.shape[0]
-    n_req = req_first_pos.numel()
-    if tuple(k_new.shape) != (n_tok, h_kv, d) or v_new.shape != k_new.shape:
-        raise ValueError("k_new and v_new must be [n_tok][h_kv][head_dim] like the cache")
-    if req_tok_start.numel() != n_req + 1 or page_table.shape[0] != n_req:
-        raise ValueError("req_tok_start must have n_req+1 entries and page_table n_req rows")
-    _launch("qsa_append_kv_fp4", stream, k_codes,
-            (k_new, v_new, req_tok_start, req_first_pos, k_scales, v_codes, v_scales, page_table), k_new.data_ptr(),
-            v_new.data_ptr(), ld_k, ld_v, n_tok, h_kv, d, req_tok_start.data_ptr(), req_first_pos.data_ptr(), n_req,
-            page_table.data_ptr(), page_table.shape[1], int(page_size), float(k_scale), float(v_scale),
-            k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), n_slots)
+    positions req_first_pos[r], req_first_pos[r]+1, ...  The rows may be
+    columns of one projection's output.  k_scale and v_scale (powers of two)
+    scale the whole tensors.  Returns the four arrays."""
+    bf16, _, i32, u8, _ = _t()
+    try:
+        dev = k_codes.get_device()
+        shape = n_slots, h_kv, w = k_codes.shape
+        n_tok = k_new.shape[0]
+        n_req, ld_pt = page_table.shape
+        ok = (dev >= 0 and _all(dev, u8, k_codes, k_scales, v_codes, v_scales)
+              and _all(dev, i32, req_tok_start, req_first_pos, page_table)
+              and _rows_ok(k_new, dev, bf16) and _rows_ok(v_new, dev, bf16) and w % 8 == 0
+              and v_codes.shape == shape and k_scales.shape == (n_slots, h_kv, w // 8) == v_scales.shape
+              and k_new.shape == (n_tok, h_kv, 2 * w) == v_new.shape
+              and req_tok_start.shape == (n_req + 1,) and req_first_pos.shape == (n_req,))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain("append_kv_fp4", k_codes, rows=((k_new, "k_new"), (v_new, "v_new")),
+                 i32=((req_tok_start, "req_tok_start", 1), (req_first_pos, "req_first_pos", 1),
+                      (page_table, "page_table", 2)),
+                 u8=((k_codes, "k_codes", 3), (k_scales, "k_scales", 3), (v_codes, "v_codes", 3),
+                     (v_scales, "v_scales", 3)))
+    row = 2 * h_kv * w
+    _check("qsa_append_kv_fp4", _launch(
+        "qsa_append_kv_fp4", dev, stream, k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0) if n_tok > 1 else row,
+        v_new.stride(0) if n_tok > 1 else row, n_tok, h_kv, 2 * w, req_tok_start.data_ptr(),
+        req_first_pos.data_ptr(), n_req, page_table.data_ptr(), ld_pt, page_size, k_scale, v_scale,
+        k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), n_slots))
     return k_codes, k_scales, v_codes, v_scales
 
 
@@ -713,21 +733,30 @@ def gather_kv_fp4(k_codes, k_scales, v_codes, v_scales, slots, k_scale=1.0, v_sc
                   stream=None):
     """Reads the rows at slots (int32, any shape) back from the 4-bit cache:
     (k, v) [*slots.shape][h_kv][head_dim] bf16; a negative slot gives zeros."""
-    torch = _torch()
-    n_slots, h_kv, d = _cache4(k_codes, k_scales, v_codes, v_scales)
-    _dev(slots, torch.int32, "slots")
-    shape = (*slots.shape, h_kv, d)
+    bf16, _, i32, u8, _ = _t()
+    try:
+        dev = k_codes.get_device()
+        shape = n_slots, h_kv, w = k_codes.shape
+        out_shape = (*slots.shape, h_kv, 2 * w)
+        ok = (dev >= 0 and _all(dev, u8, k_codes, k_scales, v_codes, v_scales) and _all(dev, i32, slots)
+              and w % 8 == 0 and v_codes.shape == shape and k_scales.shape == (n_slots, h_kv, w // 8) == v_scales.shape
+              and (k_out is None or _all(dev, bf16, k_out) and k_out.shape == out_shape)
+              and (v_out is None or _all(dev, bf16, v_out) and v_out.shape == out_shape))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain("gather_kv_fp4", k_codes, i32=((slots, "slots", None),),
+                 u8=((k_codes, "k_codes", 3), (k_scales, "k_scales", 3), (v_codes, "v_codes", 3),
+                     (v_scales, "v_scales", 3)),
+                 bf16=((k_out, "k_out", None), (v_out, "v_out", None)))
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+        k_out = _torch().empty(out_shape, dtype=bf16, device=slots.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
-    _dev(k_out, torch.bfloat16, "k_out")
-    _dev(v_out, torch.bfloat16, "v_out")
-    if tuple(k_out.shape) != shape or tuple(v_out.shape) != shape:
-        raise ValueError("k_out and v_out must be [*slots.shape][h_kv][head_dim]")
-    _launch("qsa_gather_kv_fp4", stream, k_codes, (k_scales, v_codes, v_scales, slots, k_out, v_out),
-            k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), n_slots, h_kv, d,
-            slots.data_ptr(), slots.numel(), float(k_scale), float(v_scale), k_out.data_ptr(), v_out.data_ptr())
+        v_out = _torch().empty(out_shape, dtype=bf16, device=slots.device)
+    _check("qsa_gather_kv_fp4", _launch(
+        "qsa_gather_kv_fp4", dev, stream, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+        v_scales.data_ptr(), n_slots, h_kv, 2 * w, slots.data_ptr(), slots.numel(), k_scale, v_scale,
+        k_out.data_ptr(), v_out.data_ptr()))
     return k_out, v_out
 
 
@@ -736,25 +765,37 @@ def sparse_attn_fp4(q, k_codes, k_scales, v_codes, v_scales, slots, scale=None, 
     """sparse_attn over the 4-bit cache: softmax attention of q
     [n_rows][h_q][head_dim] bf16 over the rows at slots [n_rows][w] (int32,
     -1 skipped).  Returns (out float32, lse [n_rows][h_q] or None)."""
-    torch = _torch()
-    ld_q = _rows3(q, "q")
-    n_slots, h_kv, d = _cache4(k_codes, k_scales, v_codes, v_scales)
-    _dev(slots, torch.int32, "slots", 2)
-    n_rows, h_q, d_q = q.shape
-    rows, width = slots.shape
-    if d_q != d or rows != n_rows:
-        raise ValueError("q, the cache and slots shapes disagree")
+    bf16, f32, i32, u8, _ = _t()
+    try:
+        dev = q.get_device()
+        n_rows, h_q, d = q.shape
+        shape = n_slots, h_kv, w = k_codes.shape
+        rows, width = slots.shape
+        ok = (dev >= 0 and _rows_ok(q, dev, bf16) and _all(dev, u8, k_codes, k_scales, v_codes, v_scales)
+              and _all(dev, i32, slots) and d == 2 * w and w % 8 == 0 and rows == n_rows
+              and v_codes.shape == shape and k_scales.shape == (n_slots, h_kv, w // 8) == v_scales.shape
+              and (out is None or _all(dev, f32, out) and out.shape == (n_rows, h_q, d))
+              and (lse is None or _all(dev, f32, lse) and lse.shape == (n_rows, h_q))
+              and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous()))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain("sparse_attn_fp4", q, rows=((q, "q"),), i32=((slots, "slots", 2),),
+                 u8=((k_codes, "k_codes", 3), (k_scales, "k_scales", 3), (v_codes, "v_codes", 3),
+                     (v_scales, "v_scales", 3)), f32=((out, "out", 3), (lse, "lse", 2)))
     if n_idx is None:
         n_idx = width
-    out, lse = _attn_out(q, n_rows, h_q, d, torch.float32, out, lse, want_lse)
-    workspace, ws_bytes = _attn_workspace(
-        _call("qsa_sparse_attn_fp4_workspace_size", n_rows, h_q, h_kv, d, int(n_idx)) if workspace is None else 0,
-        workspace, q)
-    _launch("qsa_sparse_attn_fp4", stream, q, (k_codes, k_scales, v_codes, v_scales, slots, out, lse, workspace),
-            q.data_ptr(), ld_q, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-            n_slots, n_rows, h_q, h_kv, d, slots.data_ptr(), width, int(n_idx),
-            float(d ** -0.5 if scale is None else scale), float(k_scale), float(v_scale), out.data_ptr(), _ptr(lse),
-            _ptr(workspace), ws_bytes)
+    if out is None:
+        out = _torch().empty((n_rows, h_q, d), dtype=f32, device=q.device)
+    if not want_lse:
+        lse = None
+    elif lse is None:
+        lse = _torch().empty((n_rows, h_q), dtype=f32, device=q.device)
+    _launch_ws("qsa_sparse_attn_fp4", dev, stream, "qsa_sparse_attn_fp4_workspace_size",
+               (n_rows, h_q, h_kv, d, n_idx), workspace, q.data_ptr(), q.stride(0) if n_rows > 1 else h_q * d,
+               k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), n_slots, n_rows, h_q,
+               h_kv, d, slots.data_ptr(), width, n_idx, d ** -0.5 if scale is None else scale, k_scale, v_scale,
+               out.data_ptr(), _ptr(lse))
     return out, lse
 
 
@@ -764,14 +805,16 @@ def window_attn(q, k_cache, v_cache, req_row_start, row_len, page_table, page_si
     tokens each row sees (row_len, its own among them) and the first n_sink,
     through the page table, on the BF16 cache [n_slots][h_kv][head_dim].
     Returns (out bfloat16, lse [n_rows][h_q] float32 or None)."""
-    torch = _torch()
-    _dev(k_cache, torch.bfloat16, "k_cache", 3)
-    _dev(v_cache, torch.bfloat16, "v_cache", 3)
-    n_slots, h_kv, d = k_cache.shape
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    return _window_call("qsa_window_attn", (k_cache.data_ptr(), v_cache.data_ptr()), (), (k_cache, v_cache), n_slots,
-                        h_kv, d, q, req_row_start, row_len, page_table, page_size, max_len, window, n_sink, scale,
+    bf16 = _t()[0]
+    try:
+        n_slots, h_kv, d = k_cache.shape
+        ok = _all(q.get_device(), bf16, k_cache, v_cache) and v_cache.shape == k_cache.shape
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _explain("window_attn", q, bf16=((k_cache, "k_cache", 3), (v_cache, "v_cache", 3)))
+    return _window_call("qsa_window_attn", (k_cache.data_ptr(), v_cache.data_ptr()), (), n_slots, h_kv, d, q,
+                        req_row_start, row_len, page_table, page_size, max_len, window, n_sink, scale,
                         max_rows_per_req, out, lse, want_lse, workspace, stream)
 
 
@@ -780,34 +823,51 @@ def window_attn_fp4(q, k_codes, k_scales, v_codes, v_scales, req_row_start, row_
                     want_lse=True, workspace=None, stream=None):
     """window_attn over the 4-bit cache (for the rows of decode and verify
     steps; for whole prompts read the window back with gather_kv_fp4)."""
-    n_slots, h_kv, d = _cache4(k_codes, k_scales, v_codes, v_scales)
+    u8 = _t()[3]
+    try:
+        shape = n_slots, h_kv, w = k_codes.shape
+        ok = (_all(q.get_device(), u8, k_codes, k_scales, v_codes, v_scales) and w % 8 == 0
+              and v_codes.shape == shape and k_scales.shape == (n_slots, h_kv, w // 8) == v_scales.shape)
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _explain("window_attn_fp4", q, u8=((k_codes, "k_codes", 3), (k_scales, "k_scales", 3),
+                                           (v_codes, "v_codes", 3), (v_scales, "v_scales", 3)))
     return _window_call("qsa_window_attn_fp4",
                         (k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr()),
-                        (float(k_scale), float(v_scale)), (k_codes, k_scales, v_codes, v_scales), n_slots, h_kv, d, q,
-                        req_row_start, row_len, page_table, page_size, max_len, window, n_sink, scale,
-                        max_rows_per_req, out, lse, want_lse, workspace, stream)
+                        (k_scale, v_scale), n_slots, h_kv, 2 * w, q, req_row_start, row_len, page_table, page_size,
+                        max_len, window, n_sink, scale, max_rows_per_req, out, lse, want_lse, workspace, stream)
 
 
-def _window_call(fn, cache_ptrs, scales, cache, n_slots, h_kv, d, q, req_row_start, row_len, page_table, page_size,
-                 max_len, window, n_sink, scale, max_rows_per_req, out, lse, want_lse, workspace, stream):
-    torch = _torch()
-    ld_q = _rows3(q, "q")
-    _dev(req_row_start, torch.int32, "req_row_start", 1)
-    _dev(row_len, torch.int32, "row_len", 1)
-    _dev(page_table, torch.int32, "page_table", 2)
-    n_rows, h_q, d_q = q.shape
-    n_req, ld_pt = page_table.shape
-    if d_q != d or row_len.numel() != n_rows or req_row_start.numel() != n_req + 1:
-        raise ValueError("q, the cache, row_len, req_row_start and page_table shapes disagree")
+def _window_call(fn, cache_ptrs, scales, n_slots, h_kv, d, q, req_row_start, row_len, page_table, page_size, max_len,
+                 window, n_sink, scale, max_rows_per_req, out, lse, want_lse, workspace, stream):
+    bf16, f32, i32, _, _ = _t()
+    try:
+        dev = q.get_device()
+        n_rows, h_q, d_q = q.shape
+        n_req, ld_pt = page_table.shape
+        ok = (dev >= 0 and _rows_ok(q, dev, bf16) and _all(dev, i32, req_row_start, row_len, page_table)
+              and d_q == d and row_len.shape == (n_rows,) and req_row_start.shape == (n_req + 1,)
+              and (out is None or _all(dev, bf16, out) and out.shape == (n_rows, h_q, d))
+              and (lse is None or _all(dev, f32, lse) and lse.shape == (n_rows, h_q))
+              and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous()))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain(fn[4:], q, rows=((q, "q"),), i32=((req_row_start, "req_row_start", 1), (row_len, "row_len", 1),
+                                                   (page_table, "page_table", 2)),
+                 bf16=((out, "out", 3),), f32=((lse, "lse", 2),))
     if max_rows_per_req is None:
         max_rows_per_req = n_rows
-    out, lse = _attn_out(q, n_rows, h_q, d, torch.bfloat16, out, lse, want_lse)
-    workspace, ws_bytes = _attn_workspace(
-        _call("qsa_window_attn_workspace_size", n_rows, h_q, h_kv, d, int(max_len), int(window), int(n_sink))
-        if workspace is None else 0, workspace, q)
-    _launch(fn, stream, q, (*cache, req_row_start, row_len, page_table, out, lse, workspace), q.data_ptr(), ld_q,
-            *cache_ptrs, n_slots, n_req, req_row_start.data_ptr(), n_rows, row_len.data_ptr(), int(max_len),
-            int(max_rows_per_req), h_q, h_kv, d, page_table.data_ptr(), ld_pt, int(page_size), int(window),
-            int(n_sink), float(d ** -0.5 if scale is None else scale), *scales, out.data_ptr(), _ptr(lse),
-            _ptr(workspace), ws_bytes)
+    if out is None:
+        out = _torch().empty((n_rows, h_q, d), dtype=bf16, device=q.device)
+    if not want_lse:
+        lse = None
+    elif lse is None:
+        lse = _torch().empty((n_rows, h_q), dtype=f32, device=q.device)
+    _launch_ws(fn, dev, stream, "qsa_window_attn_workspace_size",
+               (n_rows, h_q, h_kv, d, max_len, window, n_sink), workspace, q.data_ptr(),
+               q.stride(0) if n_rows > 1 else h_q * d, *cache_ptrs, n_slots, n_req, req_row_start.data_ptr(), n_rows,
+               row_len.data_ptr(), max_len, max_rows_per_req, h_q, h_kv, d, page_table.data_ptr(), ld_pt, page_size,
+               window, n_sink, d ** -0.5 if scale is None else scale, *scales, out.data_ptr(), _ptr(lse))
     return out, lse

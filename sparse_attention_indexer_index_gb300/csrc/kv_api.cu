@@ -13,6 +13,7 @@
 #include "host_util.cuh"
 #include "kv4.cuh"
 #include "kv_attn.cuh"
+#include "kv4_attn.cuh"
 #include "window_tc.cuh"
 
 using namespace qsa;
@@ -21,10 +22,34 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-template <int D, int NT, bool kFp4, bool kWindow>
+// The kernel of a cache type, head dim and head tiles, and its shape.
+struct KaKernel {
+  void (*fn)(KvAttnArgs);
+  int threads;
+  size_t smem;
+  int slots;    // resident CTAs of the GPU (152 SMs)
+  int entries;  // entries of a CTA per step
+};
+template <int D, int NT>
+constexpr KaKernel ka_bf16() {
+  return {kv_attn_kernel<D, NT>, kKaThreads, ka_smem_bytes<D, NT>(), 152 * KaShape<D>::kCtas, kKaTile * kKaWarps};
+}
+template <int D, int NT, bool kWindow>
+constexpr KaKernel ka_fp4() {
+  return {kv4_attn_kernel<D, NT, kWindow>, kK4Threads, k4_smem_bytes<D, NT>(), 152 * 2, kK4Step * kK4Warps};
+}
+// [cache: BF16 window, 4-bit window, 4-bit list][D = 128 with up to 8 heads, up to 16, D = 256]
+const KaKernel kKaKernels[3][3] = {
+    {ka_bf16<128, 1>(), ka_bf16<128, 2>(), ka_bf16<256, 1>()},
+    {ka_fp4<128, 1, true>(), ka_fp4<128, 2, true>(), ka_fp4<256, 1, true>()},
+    {ka_fp4<128, 1, false>(), ka_fp4<128, 2, false>(), ka_fp4<256, 1, false>()},
+};
 bool set_ka_smem() {
-  return cudaFuncSetAttribute(kv_attn_kernel<D, NT, kFp4, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)ka_smem_bytes<D, NT, kFp4>()) == cudaSuccess;
+  for (const auto& row : kKaKernels)
+    for (const KaKernel& k : row)
+      if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem) != cudaSuccess)
+        return false;
+  return true;
 }
 
 // Per-device one-time set-up: the shared-memory opt-in of the kernels.
@@ -37,11 +62,7 @@ qsa_status kv_device_ready(int* sms) {
   std::lock_guard<std::mutex> lk(g_mu);
   *sms = g_sms[dev];
   if (*sms > 0) return QSA_OK;
-  if (!set_ka_smem<256, 1, true, false>() || !set_ka_smem<128, 1, true, false>() ||
-      !set_ka_smem<128, 2, true, false>() || !set_ka_smem<256, 1, true, true>() ||
-      !set_ka_smem<128, 1, true, true>() || !set_ka_smem<128, 2, true, true>() ||
-      !set_ka_smem<256, 1, false, true>() || !set_ka_smem<128, 1, false, true>() ||
-      !set_ka_smem<128, 2, false, true>() ||
+  if (!set_ka_smem() ||
       cudaFuncSetAttribute(window_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, wt_smem_bytes<128>()) != cudaSuccess ||
       cudaFuncSetAttribute(window_tc_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, wt_smem_bytes<256>()) != cudaSuccess ||
       cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -72,20 +93,18 @@ bool kv_shape_ok(int32_t h_q, int32_t h_kv, int32_t d) {
 // few to fill the GPU and a row is long enough to pay for the merge launch.
 // The size of the workspace follows from it, so it depends on the arguments
 // alone (152 SMs, two CTAs each).
-constexpr int kKaCtaSlots = 304;
 int ka_groups(int64_t units, int64_t entries) {
-  const int64_t fill = kKaCtaSlots / (units * kKaMaxCluster);
-  const int64_t steps = entries / (kKaTile * kKaWarps * kKaMaxCluster);  // of a warp, with one cluster
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, 16), steps / 8));
+  const int64_t fill = 304 / (units * kKaMaxCluster);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, 16), entries / 4096));
 }
 
-// CTAs per cluster: the least of waves * (steps of a warp + start and end).
-int ka_cluster(int64_t units, int64_t entries, int slots) {
+// CTAs per cluster: the least of waves * (steps + start and end, about 4).
+int ka_cluster(int64_t units, int64_t entries, const KaKernel& k) {
   int best = 1;
   int64_t least = INT64_MAX;
   for (int c = 1; c <= kKaMaxCluster; ++c) {
-    const int64_t waves = (units * c + slots - 1) / slots;
-    const int64_t steps = (entries + (int64_t)kKaTile * kKaWarps * c - 1) / ((int64_t)kKaTile * kKaWarps * c);
+    const int64_t waves = (units * c + k.slots - 1) / k.slots;
+    const int64_t steps = (entries + (int64_t)k.entries * c - 1) / ((int64_t)k.entries * c);
     const int64_t cost = waves * (steps + 4);
     if (cost < least) {
       least = cost;
@@ -95,12 +114,23 @@ int ka_cluster(int64_t units, int64_t entries, int slots) {
   return best;
 }
 
-template <int D, int NT, bool kFp4, bool kWindow>
-qsa_status launch_ka(const KvAttnArgs& a, cudaStream_t stream) {
+enum { kKaBf16Window = 0, kKaFp4Window = 1, kKaFp4List = 2 };
+
+qsa_status launch_ka(int cache, KvAttnArgs& a, int d, int64_t entries, void* workspace, cudaStream_t stream) {
+  const int64_t units = (int64_t)a.n_rows * a.h_kv;
+  a.group = a.h_q / a.h_kv;
+  const KaKernel& k = kKaKernels[cache][d == 256 ? 2 : a.group > 8 ? 1 : 0];
+  a.n_group = ka_groups(units, entries);
+  a.cluster = a.n_group > 1 ? kKaMaxCluster : ka_cluster(units, entries, k);
+  a.part = static_cast<float*>(workspace);
+  if ((int64_t)a.n_rows * std::max(a.cluster * a.n_group, a.h_q) > INT32_MAX) return QSA_ERR_UNSUPPORTED;
+  if (entries > (1 << 30)) return QSA_ERR_UNSUPPORTED;  // entry indices stay clear of 2^31
+  int sms = 0;
+  if (qsa_status st = kv_device_ready(&sms)) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)a.n_rows * a.cluster * a.n_group), (unsigned)a.h_kv, 1);
-  cfg.blockDim = dim3(kKaThreads, 1, 1);
-  cfg.dynamicSmemBytes = ka_smem_bytes<D, NT, kFp4>();
+  cfg.blockDim = dim3((unsigned)k.threads, 1, 1);
+  cfg.dynamicSmemBytes = k.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -109,31 +139,16 @@ qsa_status launch_ka(const KvAttnArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NT, kFp4, kWindow>, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k.fn, a);
   if (e == cudaSuccess && a.n_group > 1)
-    e = launch_pdl(kv_attn_merge_kernel<D>, dim3((unsigned)((int64_t)a.n_rows * a.h_q)), dim3(D), 0, stream, a,
-                   kFp4 ? 10.0f : 0.0f);
+    e = launch_pdl(d == 256 ? kv_attn_merge_kernel<256> : kv_attn_merge_kernel<128>,
+                   dim3((unsigned)((int64_t)a.n_rows * a.h_q)), dim3((unsigned)d), 0, stream, a,
+                   cache == kKaBf16Window ? 0.0f : (float)kK4Bias);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return QSA_ERR_CUDA;
   }
   return QSA_OK;
-}
-
-template <bool kFp4, bool kWindow>
-qsa_status launch_ka_shape(KvAttnArgs& a, int d, int64_t entries, void* workspace, cudaStream_t stream) {
-  const int64_t units = (int64_t)a.n_rows * a.h_kv;
-  a.group = a.h_q / a.h_kv;
-  a.n_group = ka_groups(units, entries);
-  a.cluster = a.n_group > 1 ? kKaMaxCluster
-                            : ka_cluster(units, entries, kKaCtaSlots / ((!kFp4 && d == 256) ? 2 : 1));
-  a.part = static_cast<float*>(workspace);
-  if ((int64_t)a.n_rows * std::max(a.cluster * a.n_group, a.h_q) > INT32_MAX) return QSA_ERR_UNSUPPORTED;
-  if (entries > (1 << 30)) return QSA_ERR_UNSUPPORTED;  // entry indices stay clear of 2^31
-  int sms = 0;
-  if (qsa_status st = kv_device_ready(&sms)) return st;
-  if (d == 256) return launch_ka<256, 1, kFp4, kWindow>(a, stream);
-  return a.group <= 8 ? launch_ka<128, 1, kFp4, kWindow>(a, stream) : launch_ka<128, 2, kFp4, kWindow>(a, stream);
 }
 
 // The cache [n_slots][h_kv * D] BF16 for window_tc_kernel, as [row / 8][64
@@ -329,9 +344,10 @@ qsa_status qsa_append_kv_fp4(const void* k_new, const void* v_new, int64_t ld_k,
   a.v_scales = static_cast<uint8_t*>(v_scales);
   a.k_inv = 1.0f / k_scale;
   a.v_inv = 1.0f / v_scale;
-  const int64_t ctas = ((int64_t)n_tok * a.blocks + kKvThreads - 1) / kKvThreads;
-  if (ctas > INT32_MAX) return QSA_ERR_UNSUPPORTED;
-  append_kv_fp4_kernel<<<(unsigned)ctas, kKvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  const int64_t units = (int64_t)n_tok * a.blocks;
+  if (units > (int64_t)UINT32_MAX - 4 * kKvThreads) return QSA_ERR_UNSUPPORTED;  // counted in 32 bits
+  append_kv_fp4_kernel<<<(unsigned)((units + kKvThreads - 1) / kKvThreads), kKvThreads, 0,
+                         static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 
@@ -358,8 +374,8 @@ qsa_status qsa_gather_kv_fp4(const void* k_codes, const void* k_scales, const vo
   a.v_g = v_scale;
   a.k_out = static_cast<uint16_t*>(k_out);
   a.v_out = static_cast<uint16_t*>(v_out);
-  if (n > INT64_MAX / a.blocks / 2 || (n * a.blocks + kKvThreads - 1) / kKvThreads > INT32_MAX)
-    return QSA_ERR_UNSUPPORTED;
+  // blocks are counted in 32 bits (2^32 of them would be 137 GB of output each)
+  if (n > (int64_t)(UINT32_MAX - 4 * kKvThreads) / a.blocks) return QSA_ERR_UNSUPPORTED;
   const int64_t ctas = (n * a.blocks + kKvThreads - 1) / kKvThreads;
   gather_kv_fp4_kernel<<<(unsigned)ctas, kKvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
@@ -403,7 +419,7 @@ qsa_status qsa_sparse_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
   a.v_g = v_scale;
   a.out = out;
   a.lse = lse;
-  return launch_ka_shape<true, false>(a, head_dim, n_idx, workspace, static_cast<cudaStream_t>(stream));
+  return launch_ka(kKaFp4List, a, head_dim, n_idx, workspace, static_cast<cudaStream_t>(stream));
 }
 
 size_t qsa_window_attn_workspace_size(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t max_len,
@@ -435,7 +451,7 @@ qsa_status qsa_window_attn(const void* q, int64_t ld_q, const void* k_cache, con
   a.v_g = 1.0f;
   const qsa_status tc = launch_window_tc(a, head_dim, max_rows_per_req, static_cast<cudaStream_t>(stream));
   if (tc != QSA_ERR_UNSUPPORTED) return tc;
-  return launch_ka_shape<false, true>(a, head_dim, entries, workspace, static_cast<cudaStream_t>(stream));
+  return launch_ka(kKaBf16Window, a, head_dim, entries, workspace, static_cast<cudaStream_t>(stream));
 }
 
 qsa_status qsa_window_attn_fp4(const void* q, int64_t ld_q, const void* k_codes, const void* k_scales,
@@ -464,7 +480,7 @@ qsa_status qsa_window_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
   a.vs = static_cast<const uint8_t*>(v_scales);
   a.scale = scale * k_scale;
   a.v_g = v_scale;
-  return launch_ka_shape<true, true>(a, head_dim, entries, workspace, static_cast<cudaStream_t>(stream));
+  return launch_ka(kKaFp4Window, a, head_dim, entries, workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
