@@ -63,7 +63,8 @@ kv4_attn_kernel(const __grid_constant__ KvAttnArgs a) {
   constexpr int KS = D / 16, VN = D / 8;
   extern __shared__ __align__(128) unsigned char k4_smem[];
   __shared__ float s_m[kK4Warps][NT * 8], s_l[kK4Warps][NT * 8];
-  __shared__ float c_m[NT * 8], c_l[NT * 8];      // this CTA's, read by the cluster
+  __shared__ float c_m[NT * 8], c_l[NT * 8];      // this CTA's
+  __shared__ KaJoin<D, NT> join;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, tq = lane & 3;
   const int parts = a.cluster * a.n_group;
@@ -73,6 +74,7 @@ kv4_attn_kernel(const __grid_constant__ KvAttnArgs a) {
 
   KaRow<kWindow> row;
   if (!ka_row<kWindow>(a, t, row)) return;  // behind the last request (the same for the whole cluster)
+  ka_cluster_arrive(a.cluster);
   const int steps = (row.n + kK4Step - 1) / kK4Step;
   const int first = part * kK4Warps + warp, stride = parts * kK4Warps;
 
@@ -152,22 +154,20 @@ kv4_attn_kernel(const __grid_constant__ KvAttnArgs a) {
       ka_cp8(base + Sh::kVs + lane * 8, gvs + off, slot >= 0);
     }
   };
-  auto slot_of_step = [&](int step) -> int32_t {
-    return step < steps ? ka_slot<kWindow>(a, row, step * kK4Step + lane) : -1;
-  };
-  // slots a step ahead of their copies; mask[i]: valid entries i steps ahead
-  int32_t pre[kK4Stages];
+  // a slot is fetched a step before its copies; mask[i]: valid entries i steps ahead
+  auto entry = [&](int step) -> int { return step < steps ? step * kK4Step + lane : INT32_MAX; };
+  KaFetch pre[kK4Stages];
   uint32_t mask[kK4Stages];
 #pragma unroll
-  for (int i = 0; i < kK4Stages; ++i) pre[i] = slot_of_step(first + i * stride);
+  for (int i = 0; i < kK4Stages; ++i) pre[i] = ka_fetch<kWindow>(a, row, entry(first + i * stride));
 #pragma unroll
   for (int i = 0; i < kK4Stages - 1; ++i) {
-    if (first + i * stride < steps) issue(i, pre[i]);
+    const int32_t slot = ka_slot<kWindow>(a, row, entry(first + i * stride), pre[i]);
+    if (first + i * stride < steps) issue(i, slot);
     asm volatile("cp.async.commit_group;" ::: "memory");
+    mask[i] = __ballot_sync(0xffffffffu, slot >= 0);
   }
-#pragma unroll
-  for (int i = 0; i < kK4Stages - 1; ++i) mask[i] = __ballot_sync(0xffffffffu, pre[i] >= 0);
-  int32_t next = pre[kK4Stages - 1];
+  KaFetch next = pre[kK4Stages - 1];
 
   float o[NT][VN][4];
   float m[NT], l[NT];
@@ -188,12 +188,13 @@ kv4_attn_kernel(const __grid_constant__ KvAttnArgs a) {
     const uint32_t valid = mask[0];
     {  // refill the stage that the last step emptied
       const int ahead = step + (kK4Stages - 1) * stride;
-      if (ahead < steps) issue(stage == 0 ? kK4Stages - 1 : stage - 1, next);
+      const int32_t slot = ka_slot<kWindow>(a, row, entry(ahead), next);
+      if (ahead < steps) issue(stage == 0 ? kK4Stages - 1 : stage - 1, slot);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      mask[kK4Stages - 1] = __ballot_sync(0xffffffffu, next >= 0);
+      mask[kK4Stages - 1] = __ballot_sync(0xffffffffu, slot >= 0);
 #pragma unroll
       for (int i = 0; i + 1 < kK4Stages; ++i) mask[i] = mask[i + 1];
-      next = slot_of_step(ahead + stride);
+      next = ka_fetch<kWindow>(a, row, entry(ahead + stride));
     }
 
     // S = q K^T: four n-tiles of 8 entries (lane: entry gq of each); rows gq:
@@ -367,7 +368,7 @@ kv4_attn_kernel(const __grid_constant__ KvAttnArgs a) {
     }
     *reinterpret_cast<float4*>(p0) = y;
   }
-  ka_cluster_result<D, D / 8, kK4Threads>(a, so, c_m, c_l, t, g, part % a.cluster, part / a.cluster, (float)kK4Bias);
+  ka_cluster_result<D, NT, kK4Threads>(a, so, c_m, c_l, join, t, g, part % a.cluster, part / a.cluster, (float)kK4Bias);
 }
 
 }  // namespace qsa

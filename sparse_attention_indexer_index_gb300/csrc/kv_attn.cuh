@@ -164,35 +164,50 @@ __device__ __forceinline__ void ka_split(float x, float y, uint32_t& hi, uint32_
   }
 }
 
-// The row's entries: their number, and the slot of entry e (-1: none).
+// The row's entries: their number, and the slot of entry e (-1: none) in two
+// parts: what is loaded, and what is made of it, so that no branch waits for
+// the load where it is issued (a slot is fetched a step before its copies).
 template <bool kWindow>
 struct KaRow {
   int n;             // entries
   const int32_t* p;  // list, or the request's page-table row
   int lo, sinks;     // window
 };
+struct KaFetch {
+  int32_t raw;       // slot, or page; -1: no entry
+  int32_t off;       // window: offset in the page
+};
 template <bool kWindow>
-__device__ __forceinline__ int32_t ka_slot(const KvAttnArgs& a, const KaRow<kWindow>& r, int e) {
-  if constexpr (!kWindow) {
-    if (e >= r.n) return -1;
-    const int32_t s = __ldg(r.p + e);
-    if (s < 0) return -1;
-    if (s >= a.n_slots) {
-      raise_fault(kFaultIndex);
-      return -1;
-    }
-    return s;
-  } else {
-    if (e >= r.n) return -1;
+__device__ __forceinline__ KaFetch ka_fetch(const KvAttnArgs& a, const KaRow<kWindow>& r, int e) {
+  KaFetch f{-1, 0};
+  if (e >= r.n) return f;
+  if constexpr (kWindow) {
     const int pos = e < r.sinks ? e : r.lo + (e - r.sinks);
-    const int pi = pos / a.page_size;
-    const int64_t page = __ldg(r.p + pi);  // pi < ld_pt: pos < max_len
-    // a page counts only if it lies wholly inside the cache
-    if (page < 0 || (page + 1) * a.page_size > a.n_slots) {
+    const int pi = pos / a.page_size;  // < ld_pt: pos < max_len
+    f.raw = __ldg(r.p + pi);
+    f.off = pos - pi * a.page_size;
+  } else {
+    f.raw = __ldg(r.p + e);
+  }
+  return f;
+}
+template <bool kWindow>
+__device__ __forceinline__ int32_t ka_slot(const KvAttnArgs& a, const KaRow<kWindow>& r, int e, const KaFetch& f) {
+  if (e >= r.n) return -1;
+  if constexpr (!kWindow) {
+    if (f.raw < 0) return -1;
+    if (f.raw >= a.n_slots) {
       raise_fault(kFaultIndex);
       return -1;
     }
-    return (int32_t)(page * a.page_size + (pos - pi * a.page_size));
+    return f.raw;
+  } else {
+    // a page counts only if it lies wholly inside the cache
+    if (f.raw < 0 || ((int64_t)f.raw + 1) * a.page_size > a.n_slots) {
+      raise_fault(kFaultIndex);
+      return -1;
+    }
+    return f.raw * a.page_size + f.off;
   }
 }
 
@@ -219,51 +234,75 @@ __device__ __forceinline__ bool ka_row(const KvAttnArgs& a, int t, KaRow<kWindow
   return true;
 }
 
+// Where the CTAs of a cluster join: each CTA pushes its sums into the one
+// that writes them, so that a single cluster barrier lies between (reading
+// them from the others' shared memory took two, and a round trip between).
+template <int D, int NT>
+struct KaJoin {
+  static constexpr int kQuads = NT * 8 * (D / 4) + kKaMaxCluster;  // of all CTAs together
+  float4 sum[kQuads];                     // [source CTA][own quad]
+  float2 ml[kKaMaxCluster][NT * 8];       // maximum and sum per source and head
+};
+// At the kernel's start: every CTA of the cluster runs before any is written to.
+__device__ __forceinline__ void ka_cluster_arrive(int c) {
+  if (c > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
 // The cluster's result from its CTAs' sums (so: heads x D in KaOut's layout;
-// c_m, c_l: maximum and sum per head; weights hold a factor 2^bias): CTA
-// `rank` writes its share of the columns.
-template <int D, int GS, int kThreads>
+// c_m, c_l: maximum and sum per head; weights hold a factor 2^bias).  Quad i
+// (4 columns) of the output is written by CTA i mod C.
+template <int D, int NT, int kThreads>
 __device__ __forceinline__ void ka_cluster_result(const KvAttnArgs& a, const float* so, const float* c_m,
-                                                  const float* c_l, int t, int g, int rank, int grp, float bias) {
-  using Out = KaOut<D, GS>;
+                                                  const float* c_l, KaJoin<D, NT>& join, int t, int g, int rank,
+                                                  int grp, float bias) {
+  using Out = KaOut<D, D / 8>;
   const int C = a.cluster;
   const float ninf = -__int_as_float(0x7f800000);
-  if (C > 1) cluster_sync();
-  else __syncthreads();
-  const int quads = a.group * (D / 4);
-  for (int idx = rank * kThreads + (int)threadIdx.x; idx < quads; idx += C * kThreads) {
+  const int quads = a.group * (D / 4), own = (quads + C - 1) / C;
+  if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  __syncthreads();
+  if (C > 1) {
+    for (int i = threadIdx.x; i < quads; i += kThreads) {
+      const float4 x = *reinterpret_cast<const float4*>(so + (size_t)(i / (D / 4)) * Out::kRow + Out::col(i % (D / 4) * 4));
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                       map_shared_rank(&join.sum[rank * own + i / C], (uint32_t)(i % C))),
+                   "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+                   : "memory");
+    }
+    for (int i = threadIdx.x; i < C * a.group; i += kThreads) {
+      const int h = i % a.group;
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
+                       map_shared_rank(&join.ml[rank][h], (uint32_t)(i / a.group))),
+                   "f"(c_m[h]), "f"(c_l[h])
+                   : "memory");
+    }
+    cluster_sync();
+  }
+  for (int j = threadIdx.x; j < own; j += kThreads) {
+    const int idx = j * C + rank;
+    if (idx >= quads) break;
     const int h = idx / (D / 4), d = (idx % (D / 4)) * 4;
-    const float* p0 = so + (size_t)h * Out::kRow + Out::col(d);
     float M, Lsum;
     float4 x;
     if (C == 1) {
       M = c_m[h];
       Lsum = c_l[h];
-      x = *reinterpret_cast<const float4*>(p0);
+      x = *reinterpret_cast<const float4*>(so + (size_t)h * Out::kRow + Out::col(d));
     } else {
-      float cm[kKaMaxCluster];
       M = ninf;
-#pragma unroll
-      for (int c = 0; c < kKaMaxCluster; ++c) {
-        cm[c] = c < C ? __uint_as_float(ld_dsmem_u32(map_shared_rank(&c_m[h], c))) : ninf;
-        M = fmaxf(M, cm[c]);
-      }
+      for (int c = 0; c < C; ++c) M = fmaxf(M, join.ml[c][h].x);
       Lsum = 0.f;
       x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int c = 0; c < kKaMaxCluster; ++c) {
-        if (c < C) {
-          const float f = cm[c] == ninf ? 0.f : ka_ex2(cm[c] - M);
-          Lsum += f * __uint_as_float(ld_dsmem_u32(map_shared_rank(&c_l[h], c)));
-          uint32_t y0, y1, y2, y3;
-          asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(y0), "=r"(y1), "=r"(y2), "=r"(y3)
-                       : "r"(map_shared_rank(p0, c)));
-          x.x += f * __uint_as_float(y0);
-          x.y += f * __uint_as_float(y1);
-          x.z += f * __uint_as_float(y2);
-          x.w += f * __uint_as_float(y3);
-        }
+      for (int c = 0; c < C; ++c) {
+        const float2 ml = join.ml[c][h];
+        const float4 y = join.sum[c * own + j];
+        const float f = ml.x == ninf ? 0.f : ka_ex2(ml.x - M);
+        // a CTA without a weight (or with NaN weights only) has m = -inf
+        Lsum += ml.x == ninf ? ml.y : f * ml.y;
+        x.x += f * y.x;
+        x.y += f * y.y;
+        x.z += f * y.z;
+        x.w += f * y.w;
       }
     }
     const int64_t hq = (int64_t)t * a.h_q + (int64_t)g * a.group + h;
@@ -288,7 +327,6 @@ __device__ __forceinline__ void ka_cluster_result(const KvAttnArgs& a, const flo
     if (d == 0 && a.lse != nullptr)
       a.lse[hq] = Lsum == 0.f ? ninf : (M - bias + log2f(Lsum)) * 0.69314718055994531f;
   }
-  if (C > 1) cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
 // One warp's part of a (row, KV head): NT tiles of 8 heads.
@@ -302,7 +340,8 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
   extern __shared__ __align__(128) unsigned char ka_smem[];
   __shared__ uint32_t s_mask[kKaWarps][kKaStages];       // valid entries of a stage
   __shared__ float s_m[kKaWarps][NT * 8], s_l[kKaWarps][NT * 8];
-  __shared__ float c_m[NT * 8], c_l[NT * 8];     // this CTA's, read by the cluster
+  __shared__ float c_m[NT * 8], c_l[NT * 8];     // this CTA's
+  __shared__ KaJoin<D, NT> join;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, tq = lane & 3;
   const int C = a.cluster;
@@ -314,6 +353,7 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
 
   KaRow<true> row;
   if (!ka_row<true>(a, t, row)) return;  // behind the last request (the same for the whole cluster)
+  ka_cluster_arrive(C);
   const int tiles = (row.n + kKaTile - 1) / kKaTile;
   const int first = part * kKaWarps + warp, stride = parts * kKaWarps;
 
@@ -348,18 +388,18 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
       ka_cp16(base + kVBase + v_off(r, c), gv + off, s >= 0);
     }
   };
-  auto slot_of_tile = [&](int tile) -> int32_t {
-    return lane < kKaTile && tile < tiles ? ka_slot<true>(a, row, tile * kKaTile + lane) : -1;
-  };
-  int32_t pre[kKaStages];
+  // lane's entry of a tile (none from kKaTile on, nor past the row's end)
+  auto entry = [&](int tile) -> int { return lane < kKaTile && tile < tiles ? tile * kKaTile + lane : INT32_MAX; };
+  KaFetch pre[kKaStages];
 #pragma unroll
-  for (int i = 0; i < kKaStages; ++i) pre[i] = slot_of_tile(first + i * stride);
+  for (int i = 0; i < kKaStages; ++i) pre[i] = ka_fetch<true>(a, row, entry(first + i * stride));
 #pragma unroll
   for (int i = 0; i < kKaStages - 1; ++i) {
-    if (first + i * stride < tiles) issue(i, pre[i]);
+    const int tile = first + i * stride;
+    if (tile < tiles) issue(i, ka_slot<true>(a, row, entry(tile), pre[i]));
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  int32_t next = pre[kKaStages - 1];
+  KaFetch next = pre[kKaStages - 1];
 
   // ---- q as A fragments (rows gq: heads; rows gq + 8: zero) -----------------
   // k-step s of lane tq: 4 consecutive dimensions; see the loads of K.
@@ -399,9 +439,9 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
     {  // refill the stage that the previous step emptied
       const int ahead = tile + (kKaStages - 1) * stride;
       const int st = stage == 0 ? kKaStages - 1 : stage - 1;
-      if (ahead < tiles) issue(st, next);
+      if (ahead < tiles) issue(st, ka_slot<true>(a, row, entry(ahead), next));
       asm volatile("cp.async.commit_group;" ::: "memory");
-      next = slot_of_tile(ahead + stride);
+      next = ka_fetch<true>(a, row, entry(ahead + stride));
     }
     const uint32_t base = ring + (uint32_t)stage * Sh::kStage;
     const uint32_t valid = s_mask[warp][stage];
@@ -529,7 +569,7 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
     }
     *reinterpret_cast<float4*>(p0) = x;
   }
-  ka_cluster_result<D, D / 8, kKaThreads>(a, so, c_m, c_l, t, g, rank, grp, 0.f);
+  ka_cluster_result<D, NT, kKaThreads>(a, so, c_m, c_l, join, t, g, rank, grp, 0.f);
 }
 
 // Merge of the n_group partial results of every (row, query head); `bias` is
