@@ -28,6 +28,8 @@
 //    pairs (the K index of the MMA), which are interleaved nibble by nibble
 //    before the conversion.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "kv4.cuh"
 #include "kv_attn.cuh"
@@ -197,121 +199,128 @@ kv4_attn_kernel(const __grid_constant__ KvAttnArgs a) {
       next = ka_fetch<kWindow>(a, row, entry(ahead + stride));
     }
 
-    // S = q K^T: four n-tiles of 8 entries (lane: entry gq of each); rows gq:
-    // heads 0-7, rows gq + 8: heads 8-15 or zero
-    float s[4][4];
+    // J / 4 of a step: a last step of up to 16 entries takes half the work
+    // (a selection of 512 blocks and 3 pending tokens ends in one of 3)
+    auto attend = [&](auto j_tag) {
+      constexpr int J = decltype(j_tag)::value;
+      // S = q K^T: J n-tiles of 8 entries (lane: entry gq of each); rows gq:
+      // heads 0-7, rows gq + 8: heads 8-15 or zero
+      float s[J][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      for (int j = 0; j < J; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 128; ++i) {
-      uint4 w4[4];
-      __half2 sc[4];
+      for (int i = 0; i < D / 128; ++i) {
+        uint4 w4[J];
+        __half2 sc[J];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w4[j] = ka_lds16(base + k_off(j * 8 + gq, tq + 4 * i));
-        sc[j] = kv4_scales(ka_lds_u16(base + Sh::kKs + (j * 8 + gq) * Sh::kSc + 2 * (tq + 4 * i)));
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w = k == 0 ? w4[j].x : k == 1 ? w4[j].y : k == 2 ? w4[j].z : w4[j].w;
-          const __half2 sk = k < 2 ? __low2half2(sc[j]) : __high2half2(sc[j]);
-          __half2 h[4];
-          kv4_word(w, h);
-          uint32_t b[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) b[y] = ka_h2(__hmul2(h[y], sk));
-          const int n = i * 8 + 2 * k;
-          ka_mma<true>(s[j], qa[0][n][0], NT > 1 ? qa[NT - 1][n][0] : 0u, qa[0][n][1], NT > 1 ? qa[NT - 1][n][1] : 0u,
-                       b[0], b[1]);
-          ka_mma<true>(s[j], qa[0][n + 1][0], NT > 1 ? qa[NT - 1][n + 1][0] : 0u, qa[0][n + 1][1],
-                       NT > 1 ? qa[NT - 1][n + 1][1] : 0u, b[2], b[3]);
+        for (int j = 0; j < J; ++j) {
+          w4[j] = ka_lds16(base + k_off(j * 8 + gq, tq + 4 * i));
+          sc[j] = kv4_scales(ka_lds_u16(base + Sh::kKs + (j * 8 + gq) * Sh::kSc + 2 * (tq + 4 * i)));
         }
-    }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const uint32_t w = k == 0 ? w4[j].x : k == 1 ? w4[j].y : k == 2 ? w4[j].z : w4[j].w;
+            const __half2 sk = k < 2 ? __low2half2(sc[j]) : __high2half2(sc[j]);
+            __half2 h[4];
+            kv4_word(w, h);
+            uint32_t b[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) b[y] = ka_h2(__hmul2(h[y], sk));
+            const int n = i * 8 + 2 * k;
+            ka_mma<true>(s[j], qa[0][n][0], NT > 1 ? qa[NT - 1][n][0] : 0u, qa[0][n][1], NT > 1 ? qa[NT - 1][n][1] : 0u,
+                         b[0], b[1]);
+            ka_mma<true>(s[j], qa[0][n + 1][0], NT > 1 ? qa[NT - 1][n + 1][0] : 0u, qa[0][n + 1][1],
+                         NT > 1 ? qa[NT - 1][n + 1][1] : 0u, b[2], b[3]);
+          }
+      }
 
-    // running maximum and sum; the weights as A fragments (lane: head gq,
-    // entries 2 tq, 2 tq + 1 of each n-tile)
-    uint32_t pa[NT][2][4];
+      // running maximum and sum; the weights as A fragments (lane: head gq,
+      // entries 2 tq, 2 tq + 1 of each n-tile)
+      uint32_t pa[NT][J / 2][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float x[4][2];
-      float mx = ninf;
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[J][2];
+        float mx = ninf;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          x[j][e] = (valid >> (8 * j + 2 * tq + e)) & 1u ? s[j][2 * nt + e] * mult[nt] : ninf;
-          mx = fmaxf(mx, x[j][e]);
+          for (int e = 0; e < 2; ++e) {
+            x[j][e] = (valid >> (8 * j + 2 * tq + e)) & 1u ? s[j][2 * nt + e] * mult[nt] : ninf;
+            mx = fmaxf(mx, x[j][e]);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (__any_sync(0xffffffffu, m[nt] != ninf && mx > m[nt] + (float)kKaGrow)) {
+          const float mn = fmaxf(m[nt], mx);
+          const float f = m[nt] == ninf ? 1.f : ka_ex2(m[nt] - mn);  // -inf: nothing yet
+          l[nt] *= f;
+#pragma unroll
+          for (int i = 0; i < VN; ++i)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[nt][i][y] *= f;
+          m[nt] = mn;
         }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (__any_sync(0xffffffffu, m[nt] != ninf && mx > m[nt] + (float)kKaGrow)) {
-        const float mn = fmaxf(m[nt], mx);
-        const float f = m[nt] == ninf ? 1.f : ka_ex2(m[nt] - mn);  // -inf: nothing yet
-        l[nt] *= f;
+        if (m[nt] == ninf) m[nt] = mx;
+        const float ms = m[nt] == ninf ? 0.f : m[nt] - (float)kK4Bias;
 #pragma unroll
-        for (int i = 0; i < VN; ++i)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) o[nt][i][y] *= f;
-        m[nt] = mn;
+        for (int j = 0; j < J; ++j) {
+          const float p0 = ka_ex2(x[j][0] - ms), p1 = ka_ex2(x[j][1] - ms);
+          l[nt] += p0 + p1;
+          ka_split<true>(p0, p1, pa[nt][j >> 1][2 * (j & 1)], pa[nt][j >> 1][2 * (j & 1) + 1]);
+        }
       }
-      if (m[nt] == ninf) m[nt] = mx;
-      const float ms = m[nt] == ninf ? 0.f : m[nt] - (float)kK4Bias;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p0 = ka_ex2(x[j][0] - ms), p1 = ka_ex2(x[j][1] - ms);
-        l[nt] += p0 + p1;
-        ka_split<true>(p0, p1, pa[nt][j >> 1][2 * (j & 1)], pa[nt][j >> 1][2 * (j & 1) + 1]);
-      }
-    }
 
-    // O += P V: lane: entries 2tq, 2tq+1 (b0) and 2tq+8, 2tq+9 (b1) of 16;
-    // columns gq * VN + i of n-tile i
+      // O += P V: lane: entries 2tq, 2tq+1 (b0) and 2tq+8, 2tq+9 (b1) of 16;
+      // columns gq * VN + i of n-tile i
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      constexpr int kW = D / 64;  // 4-byte words of the lane's piece: 4 or 2
-      uint32_t w[4][kW], sc[4];
+      for (int ks = 0; ks < J / 2; ++ks) {
+        constexpr int kW = D / 64;  // 4-byte words of the lane's piece: 4 or 2
+        uint32_t w[4][kW], sc[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = ks * 16 + 2 * tq + (e & 1) + (e >> 1) * 8;
-        if constexpr (D == 256) {
-          const uint4 y = ka_lds16(base + Sh::kV + v_off(r, gq));
-          w[e][0] = y.x; w[e][1] = y.y; w[e][2] = y.z; w[e][3] = y.w;
-          sc[e] = ka_lds_u16(base + Sh::kVs + r * Sh::kSc + 2 * gq);
-        } else {
-          const uint2 y = ka_lds8(base + Sh::kV + v_off(r, gq >> 1) + (gq & 1) * 8);
-          w[e][0] = y.x; w[e][1] = y.y;
-          sc[e] = ka_lds_u8(base + Sh::kVs + r * Sh::kSc + gq);
+        for (int e = 0; e < 4; ++e) {
+          const int r = ks * 16 + 2 * tq + (e & 1) + (e >> 1) * 8;
+          if constexpr (D == 256) {
+            const uint4 y = ka_lds16(base + Sh::kV + v_off(r, gq));
+            w[e][0] = y.x; w[e][1] = y.y; w[e][2] = y.z; w[e][3] = y.w;
+            sc[e] = ka_lds_u16(base + Sh::kVs + r * Sh::kSc + 2 * gq);
+          } else {
+            const uint2 y = ka_lds8(base + Sh::kV + v_off(r, gq >> 1) + (gq & 1) * 8);
+            w[e][0] = y.x; w[e][1] = y.y;
+            sc[e] = ka_lds_u8(base + Sh::kVs + r * Sh::kSc + gq);
+          }
         }
-      }
 #pragma unroll
-      for (int k = 0; k < kW; ++k) {
-        // scales of the word's block for the two entries of each register
-        const int sh = 8 * (k / 2);
-        const __half2 s0 = kv4_scales(((sc[0] >> sh) & 0xffu) | (((sc[1] >> sh) & 0xffu) << 8));
-        const __half2 s1 = kv4_scales(((sc[2] >> sh) & 0xffu) | (((sc[3] >> sh) & 0xffu) << 8));
-        const uint32_t e0 = (w[0][k] & 0x0f0f0f0fu) | ((w[1][k] & 0x0f0f0f0fu) << 4);
-        const uint32_t o0 = ((w[0][k] >> 4) & 0x0f0f0f0fu) | (w[1][k] & 0xf0f0f0f0u);
-        const uint32_t e1 = (w[2][k] & 0x0f0f0f0fu) | ((w[3][k] & 0x0f0f0f0fu) << 4);
-        const uint32_t o1 = ((w[2][k] >> 4) & 0x0f0f0f0fu) | (w[3][k] & 0xf0f0f0f0u);
-        __half2 he0[4], he1[4], ho0[4], ho1[4];
-        kv4_word(e0, he0);
-        kv4_word(e1, he1);
-        kv4_word(o0, ho0);
-        kv4_word(o1, ho1);
+        for (int k = 0; k < kW; ++k) {
+          // scales of the word's block for the two entries of each register
+          const int sh = 8 * (k / 2);
+          const __half2 s0 = kv4_scales(((sc[0] >> sh) & 0xffu) | (((sc[1] >> sh) & 0xffu) << 8));
+          const __half2 s1 = kv4_scales(((sc[2] >> sh) & 0xffu) | (((sc[3] >> sh) & 0xffu) << 8));
+          const uint32_t e0 = (w[0][k] & 0x0f0f0f0fu) | ((w[1][k] & 0x0f0f0f0fu) << 4);
+          const uint32_t o0 = ((w[0][k] >> 4) & 0x0f0f0f0fu) | (w[1][k] & 0xf0f0f0f0u);
+          const uint32_t e1 = (w[2][k] & 0x0f0f0f0fu) | ((w[3][k] & 0x0f0f0f0fu) << 4);
+          const uint32_t o1 = ((w[2][k] >> 4) & 0x0f0f0f0fu) | (w[3][k] & 0xf0f0f0f0u);
+          __half2 he0[4], he1[4], ho0[4], ho1[4];
+          kv4_word(e0, he0);
+          kv4_word(e1, he1);
+          kv4_word(o0, ho0);
+          kv4_word(o1, ho1);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const uint32_t b0 = ka_h2(__hmul2(he0[y], s0)), b1 = ka_h2(__hmul2(he1[y], s1));
-          const uint32_t b2 = ka_h2(__hmul2(ho0[y], s0)), b3 = ka_h2(__hmul2(ho1[y], s1));
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t b0 = ka_h2(__hmul2(he0[y], s0)), b1 = ka_h2(__hmul2(he1[y], s1));
+            const uint32_t b2 = ka_h2(__hmul2(ho0[y], s0)), b3 = ka_h2(__hmul2(ho1[y], s1));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            ka_mma<true>(o[nt][8 * k + 2 * y], pa[nt][ks][0], pa[nt][ks][1], pa[nt][ks][2], pa[nt][ks][3], b0, b1);
-            ka_mma<true>(o[nt][8 * k + 2 * y + 1], pa[nt][ks][0], pa[nt][ks][1], pa[nt][ks][2], pa[nt][ks][3], b2, b3);
+            for (int nt = 0; nt < NT; ++nt) {
+              ka_mma<true>(o[nt][8 * k + 2 * y], pa[nt][ks][0], pa[nt][ks][1], pa[nt][ks][2], pa[nt][ks][3], b0, b1);
+              ka_mma<true>(o[nt][8 * k + 2 * y + 1], pa[nt][ks][0], pa[nt][ks][1], pa[nt][ks][2], pa[nt][ks][3], b2, b3);
+            }
           }
         }
       }
-    }
+    };
+    if ((valid >> 16) != 0) attend(std::integral_constant<int, 4>());
+    else attend(std::integral_constant<int, 2>());
     stage = stage + 1 == kK4Stages ? 0 : stage + 1;
   }
 
