@@ -148,12 +148,31 @@ __device__ __forceinline__ void wt_tma_3d(void* dst, const CUtensorMap* map, int
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-// D[128][n] += A (tensor memory, BF16 pairs) * B (shared memory).
+// The MMA issuer runs as a whole warp and one elected lane issues: its
+// descriptors then live in uniform registers.  (Behind a branch on the lane,
+// moving them there took about 85 clocks an MMA, where a 128 x 128 x 16
+// product takes 64.)
+// D[128][n] (+)= A (shared memory) * B (shared memory).
+__device__ __forceinline__ void wt_mma_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[128][n] (+)= A (tensor memory, BF16 pairs) * B (shared memory).
 __device__ __forceinline__ void wt_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void wt_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void wt_tma_4d(void* dst, const CUtensorMap* map, int z, int w, uint64_t* bar) {
@@ -438,63 +457,60 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       WtTile w;
       if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
       if (w.n_blk == 0) continue;
-      if (lane == 0) {
-        auto n16 = [&](int blk) { return (min(N, w.uc - blk * N) + 15) & ~15; };
-        auto qk = [&](int blk) -> bool {
-          const int x = gb + blk;
-          if (x >= 1 && !tm_wait(&ctl.s_free, (uint32_t)(x - 1) & 1u, abort)) return false;
-          const uint32_t idesc = kIdescS | ((uint32_t)(n16(blk) >> 3) << 17);
+      auto n16 = [&](int blk) { return (min(N, w.uc - blk * N) + 15) & ~15; };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, tm_wait(bar, parity, abort)); };
+      auto qk = [&](int blk) -> bool {
+        const int x = gb + blk;
+        if (x >= 1 && !wait(&ctl.s_free, (uint32_t)(x - 1) & 1u)) return false;
+        const uint32_t idesc = kIdescS | ((uint32_t)(n16(blk) >> 3) << 17);
 #pragma unroll
-          for (int i = 0; i < Sh::kKs; ++i) {
-            const int st = rs % Sh::kStages;
-            if (!tm_wait(&ctl.full[st], (uint32_t)(rs / Sh::kStages) & 1u, abort)) return false;
-            tc_fence_after();
-            const uint64_t kd = add(k_desc0, st * kWtStageBytes), qd = add(q_desc, i * 2 * kQHalf);
+        for (int i = 0; i < Sh::kKs; ++i) {
+          const int st = rs % Sh::kStages;
+          if (!wait(&ctl.full[st], (uint32_t)(rs / Sh::kStages) & 1u)) return false;
+          tc_fence_after();
+          const uint64_t kd = add(k_desc0, st * kWtStageBytes), qd = add(q_desc, i * 2 * kQHalf);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              umma_bf16(tmem + Sh::kColS, add(qd, (c >> 2) * kQHalf + (c & 3) * 32),
-                        add(kd, (c >> 2) * 1024 + (c & 3) * 32), idesc, i > 0 || c > 0 ? 1u : 0u);
-            umma_commit(&ctl.empty[st]);
-            ++rs;
-          }
-          umma_commit(&ctl.s_full);
-          mbar_arrive(&ctl.s_full);
-          if (blk + 1 == w.n_blk) umma_commit(&ctl.q_empty);
-          return true;
-        };
-        auto pv = [&](int blk) -> bool {
-          const int x = gb + blk, sl = x & 1;
-          if (!tm_wait(&ctl.p_full[sl], (uint32_t)(x >> 1) & 1u, abort)) return false;
-          const int n = n16(blk), copied = min(N, w.n_box * a.box - blk * N);
-          for (int e0 = 0; e0 < copied; e0 += Sh::kVRows) {
-            const int st = rs % Sh::kStages;
-            if (!tm_wait(&ctl.full[st], (uint32_t)(rs / Sh::kStages) & 1u, abort)) return false;
-            tc_fence_after();
-            const uint64_t vd = add(v_desc0, st * kWtStageBytes);
-            const uint32_t p = tmem + Sh::kColP + sl * 64 + e0 / 2;
-            const int steps = min(Sh::kVRows, n - e0) / 16;  // none for rows past the last key
-            const uint32_t first = blk > 0 || e0 > 0 ? 1u : 0u;
+          for (int c = 0; c < 8; ++c)
+            wt_mma_ss(tmem + Sh::kColS, add(qd, (c >> 2) * kQHalf + (c & 3) * 32),
+                      add(kd, (c >> 2) * 1024 + (c & 3) * 32), idesc, i > 0 || c > 0 ? 1u : 0u);
+          wt_commit(&ctl.empty[st]);
+          ++rs;
+        }
+        wt_commit(&ctl.s_full);
+        if (lane == 0) mbar_arrive(&ctl.s_full);
+        if (blk + 1 == w.n_blk) wt_commit(&ctl.q_empty);
+        return true;
+      };
+      auto pv = [&](int blk) -> bool {
+        const int x = gb + blk, sl = x & 1;
+        if (!wait(&ctl.p_full[sl], (uint32_t)(x >> 1) & 1u)) return false;
+        const int n = n16(blk), copied = min(N, w.n_box * a.box - blk * N);
+        for (int e0 = 0; e0 < copied; e0 += Sh::kVRows) {
+          const int st = rs % Sh::kStages;
+          if (!wait(&ctl.full[st], (uint32_t)(rs / Sh::kStages) & 1u)) return false;
+          tc_fence_after();
+          const uint64_t vd = add(v_desc0, st * kWtStageBytes);
+          const uint32_t p = tmem + Sh::kColP + sl * 64 + e0 / 2;
+          const int steps = min(Sh::kVRows, n - e0) / 16;  // none for rows past the last key
+          const uint32_t first = blk > 0 || e0 > 0 ? 1u : 0u;
 #pragma unroll
-            for (int c = 0; c < Sh::kVRows / 16; ++c)
-              if (c < steps)
-                wt_mma_ts(tmem, p + c * 8, add(vd, c * 2 * Sh::kVGroup), kIdescO, c > 0 ? 1u : first);
-            umma_commit(&ctl.empty[st]);
-            ++rs;
-          }
-          umma_commit(&ctl.pv_done[sl]);
-          return true;
-        };
-        ok = tm_wait(&ctl.q_full, (uint32_t)nq & 1u, abort) && qk(0);
-        for (int i = 0; ok && i < w.n_blk; ++i) ok = (i + 1 >= w.n_blk || qk(i + 1)) && pv(i);
-      }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          for (int c = 0; c < Sh::kVRows / 16; ++c)
+            if (c < steps)
+              wt_mma_ts(tmem, p + c * 8, add(vd, c * 2 * Sh::kVGroup), kIdescO, c > 0 ? 1u : first);
+          wt_commit(&ctl.empty[st]);
+          ++rs;
+        }
+        wt_commit(&ctl.pv_done[sl]);
+        return true;
+      };
+      ok = wait(&ctl.q_full, (uint32_t)nq & 1u) && qk(0);
+      for (int i = 0; ok && i < w.n_blk; ++i) ok = (i + 1 >= w.n_blk || qk(i + 1)) && pv(i);
       gb += w.n_blk;
       ++nq;
     }
-    if (lane == 0) {  // every MMA has finished before the memories are released
-      umma_commit(&ctl.drain);
-      mbar_wait_bounded(&ctl.drain, 0u, 20000000ull);
-    }
+    // every MMA has finished before the memories are released
+    wt_commit(&ctl.drain);
+    mbar_wait_bounded(&ctl.drain, 0u, 20000000ull);
   } else {
     // ---- softmax and outputs: a pair in two threads ------------------------------------
     const int half = warp >> 2;                   // columns 64 half .. + 63 of S, D/2 half .. of O
