@@ -166,14 +166,14 @@ bool encode_cache_map(CUtensorMap* m, const void* cache, int64_t n_slots, int64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The queries [n_rows][h_q][D]: a CTA's rows x the heads of a KV head x 64
+// The queries [n_rows][h_q][D]: a tile's rows x the heads of a KV head x 64
 // columns a box; rows past the end read as zeros.
 bool encode_q_map(CUtensorMap* m, const WtArgs& a, int d) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)a.h_q, (cuuint64_t)a.n_rows};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)a.ld_q * 2};
-  const cuuint32_t bx[3] = {64, (cuuint32_t)a.group, (cuuint32_t)a.rows / 2};
+  const cuuint32_t bx[3] = {64, (cuuint32_t)a.group, (cuuint32_t)a.rows};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q), dims, strides, bx, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -194,7 +194,7 @@ qsa_status launch_window_tc(const KvAttnArgs& k, int d, int32_t max_rows_per_req
   a.h_q = k.h_q;
   a.h_kv = k.h_kv;
   a.group = k.h_q / k.h_kv;
-  a.rows = 128 / a.group * 2;
+  a.rows = 128 / a.group;
   a.n_req = k.n_req;
   a.req_row_start = k.req_row_start;
   a.row_len = k.row_len;
@@ -217,10 +217,10 @@ qsa_status launch_window_tc(const KvAttnArgs& k, int d, int32_t max_rows_per_req
   int sms = 0;
   if (qsa_status st = kv_device_ready(&sms)) return st;
   CUtensorMap q_map, k_map, v_map;
-  if (!encode_q_map(&q_map, a, d) || !encode_cache_map(&k_map, k.k, k.n_slots, (int64_t)k.h_kv * d, a.box, d / 64) ||
-      !encode_cache_map(&v_map, k.v, k.n_slots, (int64_t)k.h_kv * d, a.box, d / 128))
+  if (!encode_q_map(&q_map, a, d) || !encode_cache_map(&k_map, k.k, k.n_slots, (int64_t)k.h_kv * d, a.box, 2) ||
+      !encode_cache_map(&v_map, k.v, k.n_slots, (int64_t)k.h_kv * d, a.box, d / 64))
     return QSA_ERR_UNSUPPORTED;
-  const unsigned grid = 2u * (unsigned)std::min<int64_t>(units, sms / 2);  // a pair of CTAs a tile
+  const unsigned grid = (unsigned)std::min<int64_t>(units, sms);
   if (d == 256) window_tc_kernel<256><<<grid, kWtThreads, wt_smem_bytes<256>(), stream>>>(a, q_map, k_map, v_map);
   else window_tc_kernel<128><<<grid, kWtThreads, wt_smem_bytes<128>(), stream>>>(a, q_map, k_map, v_map);
   return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;

@@ -2,39 +2,36 @@
 // requests with many rows (prompts, chunks), on the fifth-generation tensor
 // cores: the prefill form of window_attn on the BF16 cache.
 //
-// A tile is 2 R consecutive rows of one request and one KV head, R =
-// floor(128 / G): its 2 R * G (row, query head) pairs are the 256 rows of the
-// MMA, so the heads that share K and V share their tiles too.  Over the keys
-// that any of its rows sees, in blocks of 128 entries:
+// A tile is R = floor(128 / G) consecutive rows of one request and one KV
+// head: its R * G (row, query head) pairs are the 128 rows of the MMA, so the
+// heads that share K and V share their tiles too.  Over the keys that any of
+// its rows sees, in blocks of N entries:
 //     S = Q K^T, P = exp2(c S - c m), O += P V, l += sum P
 // with the running maximum m per pair; out = O / l, lse = ln 2 (c m + log2 l).
 //
-// Bound: 4 D flops per (pair, key): the tensor cores, as long as shared memory
-// feeds them.
+// Bound: 4 D flops per (pair, key), 512 of them per byte of K and V that a
+// tile reads: tensor-bound once the copies keep up (64 bytes a clock and SM
+// at the full MMA rate).
 //
-// Design (GB300).  A cluster of two CTAs on a pair of SMs walks tiles (a
-// static stride); each holds R rows, half of every K block (64 entries) and
-// half of V's columns, and the products are cta_group::2 ones (256 x 128 x 16
-// and 256 x D x 16).  One CTA a tile had to copy and read whole K and V
-// blocks: per 128 entries at D = 256, 320 KB through shared memory at 128
-// bytes a clock, 2,500 clocks for products of 2,048 (measured: about 3,600).
-// Per CTA:
+// Design (GB300).  One CTA per SM walks tiles (a static stride):
 //  - warp 10 finds the tiles and copies Q (TMA, 3-D boxes: the rows and heads
-//    of a tile land as the rows of the MMA operand), a tile ahead;
-//  - warps 8 (K) and 11 (V) copy into a ring of stages in the order in which
-//    they are used, one TMA box of B rows (the largest power of two up to 64
-//    that divides the page) and all the stage's columns a copy.  The
+//    of a tile land as the 128 rows of the MMA operand), a tile ahead;
+//  - warps 8 (K) and 11 (V) copy into a ring of 32 KB stages in the order in
+//    which they are used, one TMA box of B rows (the largest power of two up
+//    to 64 that divides the page) and all the stage's columns a copy.  The
 //    instruction takes one box at a time whichever lanes ask (about 100 clocks
 //    each: boxes of 16 rows x 64 columns held the tiles at 21 bytes a clock),
 //    hence large boxes and two warps.  They follow the page table; a page out
 //    of range is copied from beyond the tensor map, which fills zeros.
-//  - warp 9 issues the MMAs in the first CTA: S from Q and K in shared memory
-//    (both K-major), O from P in tensor memory and V (MN-major: V's rows are
-//    keys, the transposition is the descriptor's).  In the second CTA it tells
-//    the first of copies that have landed.
+//  - warp 9 issues the MMAs: S from Q and K in shared memory (both K-major),
+//    O from P in tensor memory and V (MN-major: V's rows are keys, the
+//    transposition is the descriptor's).  128 entries a block: with 64, S
+//    waits for its A operand (measured: 78 clocks a 128x64x16 product with A
+//    in tensor memory, where the rate allows 32).
 //  - warps 0-7 hold a pair in two threads, 64 entries of a block each: they
-//    turn S into P, exchange the maximum through shared memory, and write the
-//    outputs.  (One thread a pair took 1,000 clocks for 64 entries.)
+//    turn S into P, exchange the maximum through shared memory, and
+//    write the outputs.  (One thread a pair took 1,000 clocks for 64 entries,
+//    more than a product of D = 128.)
 //  - The products go in the order QK(i+1) PV(i), so that a softmax has the
 //    time of two products.  S has one buffer, free again as soon as the
 //    softmax warps hold it in registers; P has two, and the barrier that
@@ -51,8 +48,7 @@
 // (nsr of them, rounded up to a box; all lie below start), then the positions
 // from start on.  A pair sees entries [0, a) and [b, c).  V rows that no pair
 // of the tile sees are zeroed in shared memory (a weight of 0 times an
-// infinity there would be NaN), or left out of the product where 16 of them
-// lie together.
+// infinity there would be NaN).
 #pragma once
 #include <cuda.h>
 
@@ -64,20 +60,23 @@ namespace qsa {
 
 constexpr int kWtThreads = 384;          // 8 softmax warps; K, MMAs, tiles and Q, V
 constexpr int kWtN = 128;                // entries per block
+constexpr int kWtStageBytes = 32768;
+constexpr int kWtBadRing = 8;
 constexpr int kWtTileRing = 3;
 
-// Stage contents of a CTA.  K: its 64 of the block's entries x D columns; V:
-// 128 entries x its half of the columns.  Both as [8-row group][64 columns][8
-// rows][128 B], 128-byte swizzled: a box of whole 8-row groups fills
-// consecutive bytes.
+// Stage contents.  K: 128 entries x 128 columns (a block of D = 256 takes
+// two); V: 64 entries x 256 columns or 128 x 128.  Both as [8-row group][64
+// columns][8 rows][128 B], 128-byte swizzled: a box of whole 8-row groups
+// fills consecutive bytes.
 template <int D>
 struct WtShape {
-  static constexpr int kStageBytes = 128 * D;
-  static constexpr uint32_t kKGroup = D / 64 * 1024, kVGroup = D / 128 * 1024;  // bytes of an 8-row group
+  static constexpr int kKs = D / 128;               // K stages of a block
+  static constexpr int kVRows = D == 256 ? 64 : 128;  // entries of a V stage
+  static constexpr int kVs = kWtN / kVRows;         // V stages of a full block
+  static constexpr uint32_t kKGroup = 2 * 1024, kVGroup = D / 64 * 1024;  // bytes of an 8-row group
   static constexpr uint32_t kColS = D, kColP = D + kWtN;
   static constexpr int kQBytes = 128 * D * 2;
-  static constexpr int kStages = D == 256 ? 4 : 8;  // of K and V
-  static constexpr int kOutBytes = 8 * 4096;        // 32 pairs x 64 columns a softmax warp
+  static constexpr int kStages = D == 256 ? 5 : 6;  // of K and V: 224 KB with Q
   static_assert(D + 2 * kWtN <= 512, "tensor memory");
 };
 
@@ -86,7 +85,7 @@ struct WtArgs {
   int64_t ld_q;
   int64_t n_slots;
   int32_t n_rows, h_q, h_kv, group;
-  int32_t rows;              // 2 R: rows per tile
+  int32_t rows;              // R: rows per tile
   int32_t n_req;
   const int32_t* req_row_start;
   const int32_t* row_len;
@@ -95,7 +94,7 @@ struct WtArgs {
   int64_t ld_pt;
   int32_t page_size;
   int32_t box, box_shift;    // B: rows per copy, 8 to 64, dividing the page; its logarithm
-  int32_t tile_slots;        // n_rows / (2 R) + n_req
+  int32_t tile_slots;        // n_rows / R + n_req
   float c;                   // |scale| log2 e, positive
   uint32_t flip;             // sign bit to flip in S (a negative scale)
   uint16_t* out;             // [n_rows][h_q][D] BF16
@@ -153,64 +152,28 @@ __device__ __forceinline__ void wt_tma_3d(void* dst, const CUtensorMap* map, int
 // descriptors then live in uniform registers.  (Behind a branch on the lane,
 // moving them there took about 85 clocks an MMA, where a 128 x 128 x 16
 // product takes 64.)
-// D[256][n] (+)= A (shared memory) * B (shared memory), over both CTAs.
+// D[128][n] (+)= A (shared memory) * B (shared memory).
 __device__ __forceinline__ void wt_mma_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// D[256][n] (+)= A (tensor memory, BF16 pairs) * B (shared memory).
+// D[128][n] (+)= A (tensor memory, BF16 pairs) * B (shared memory).
 __device__ __forceinline__ void wt_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// The products so far arrive on this barrier of both CTAs.
 __device__ __forceinline__ void wt_commit(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
-}
-// Arrive on the first CTA's barrier.  What it announces are tensor-memory
-// accesses (ordered by tcgen05's own fences) and landed copies; only V rows
-// zeroed by threads need a release at cluster scope, which takes about 1,000
-// clocks (every arrival with one: 84 -> 103 us for a 4,096-row chunk).
-__device__ __forceinline__ void wt_arrive_first(uint64_t* bar, bool wrote = false) {
-  const uint32_t to = map_shared_rank(bar, 0);
-  if (wrote) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(to) : "memory");
-  else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(to) : "memory");
-}
-// tm_wait for an arrival of the other CTA after it wrote to shared memory.
-__device__ __forceinline__ bool wt_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wt_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (wt_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!wt_try_wait_cluster(bar, parity)) {
-    if (*abort) return false;
-    if (global_timer_ns() - t0 > 200000000ull) {
-      *abort = 1;
-      raise_fault(kFaultWait);
-      return false;
-    }
-  }
-  return true;
 }
 __device__ __forceinline__ void wt_tma_4d(void* dst, const CUtensorMap* map, int z, int w, uint64_t* bar) {
   asm volatile(
@@ -237,18 +200,7 @@ struct WtTile {
   int start, nsr;      // see above
   int n_box, n_blk;    // boxes and blocks of N entries
   int ua, ub, uc;      // entries that some pair sees: [0, ua) and [ub, uc)
-  int bad;             // a page of the tile is out of range
 };
-
-// First 8-row group of cache box j; -1 where its page is out of range.
-__device__ __forceinline__ int wt_box(const WtArgs& a, const WtTile& w, int j) {
-  const int e = j << a.box_shift;
-  const int pos = e < w.nsr ? e : w.start + (e - w.nsr);
-  const int pi = pos / a.page_size;
-  const int64_t page = __ldg(a.page_table + (int64_t)w.r * a.ld_pt + pi);
-  if (page < 0 || (page + 1) * a.page_size > a.n_slots) return -1;
-  return (int)((page * a.page_size + (pos - pi * a.page_size)) >> 3);
-}
 
 // Tile of slot s: request r's tiles begin at slot req_row_start[r] / R + r
 // (enough room, since the requests before it have at most that many tiles);
@@ -298,48 +250,29 @@ __device__ __forceinline__ WtTile wt_tile(const WtArgs& a, int s) {
   w.ua = min(a.n_sink, last);
   w.ub = w.nsr + first - w.start;
   w.uc = w.nsr + last - w.start;
-  for (int j = lane; j < w.n_box; j += 32) w.bad |= wt_box(a, w, j) < 0;
-  w.bad = __any_sync(0xffffffffu, w.bad != 0);
-  if (w.bad && lane == 0) raise_fault(kFaultIndex);
   return w;
 }
 
 struct WtCtl {
-  uint64_t full[8], empty[8];
-  uint64_t peer_full[8], peer_q;  // in the first CTA: the second one's copies have landed
+  uint64_t full[6], empty[6];
   uint64_t s_full, s_free, p_full[2], pv_done[2], q_full, q_empty, drain;
   uint64_t tile_full[kWtTileRing], tile_empty[kWtTileRing];
   uint64_t pair[4];          // the two warps of a lane quarter
   WtTile tile[kWtTileRing];
   float mx[2][2][128];       // [block parity][half][pair]: maxima, at the end the sums
+  uint32_t bad[kWtBadRing];  // boxes of a block that are out of range
   uint32_t tmem;
   int abort;
 };
 
 template <int D>
 constexpr int wt_smem_bytes() {  // all of it dynamic, from a 1024-byte boundary
-  return WtShape<D>::kQBytes + WtShape<D>::kStages * WtShape<D>::kStageBytes + WtShape<D>::kOutBytes + (int)sizeof(WtCtl);
+  return WtShape<D>::kQBytes + WtShape<D>::kStages * kWtStageBytes + (int)sizeof(WtCtl);
 }
 
 // The lowest n bits (none below 0, all from 64).
 __device__ __forceinline__ uint64_t wt_low_bits(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
-}
-
-// The groups of 16 entries of a block that hold one that some pair sees.
-__device__ __forceinline__ uint32_t wt_steps(const WtTile& w, int blk) {
-  uint32_t use = 0;
-#pragma unroll
-  for (int c = 0; c < kWtN / 16; ++c) {
-    const int e = blk * kWtN + c * 16;
-    if (e < w.ua || (e + 16 > w.ub && e < w.uc)) use |= 1u << c;
-  }
-  return use;
-}
-
-// Whether a block may hold V rows that no pair sees.
-__device__ __forceinline__ bool wt_edge(const WtTile& w, int blk) {
-  return blk * kWtN < w.ub || (blk + 1) * kWtN > w.uc;
 }
 
 // The next tile of the ring, by a whole warp; false: aborted.
@@ -354,7 +287,7 @@ __device__ __forceinline__ bool wt_next_tile(WtCtl& ctl, int k, WtTile& w, volat
 }
 
 template <int D>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
+__global__ void __launch_bounds__(kWtThreads, 1)
 window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUtensorMap q_map,
                  const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using Sh = WtShape<D>;
@@ -363,30 +296,27 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
   extern __shared__ __align__(1024) unsigned char wt_smem[];
   unsigned char* q_buf = wt_smem;
   unsigned char* ring = q_buf + Sh::kQBytes;
-  unsigned char* out_buf = ring + Sh::kStages * Sh::kStageBytes;
-  WtCtl& ctl = *reinterpret_cast<WtCtl*>(out_buf + Sh::kOutBytes);
-  if ((smem_u32(wt_smem) & 1023u) != 0) {  // the swizzle atoms need it (alike in both CTAs)
+  WtCtl& ctl = *reinterpret_cast<WtCtl*>(ring + Sh::kStages * kWtStageBytes);
+  if ((smem_u32(wt_smem) & 1023u) != 0) {  // the swizzle atoms need it
     if (threadIdx.x == 0) raise_fault(kFaultWait);
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_ctarank();
   volatile int* abort = &ctl.abort;
   const float ninf = -__int_as_float(0x7f800000);
 
   if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl.tmem))
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl.tmem))
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kStages; ++i) {
       mbar_init(&ctl.full[i], 1);
       mbar_init(&ctl.empty[i], 1);
-      mbar_init(&ctl.peer_full[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.p_full[i], 16);   // softmax warps of both CTAs
+      mbar_init(&ctl.p_full[i], 256);
       mbar_init(&ctl.pv_done[i], 1);
     }
     for (int i = 0; i < kWtTileRing; ++i) {
@@ -394,27 +324,25 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       mbar_init(&ctl.tile_empty[i], 11);  // softmax warps, K, V, MMAs
     }
     for (int i = 0; i < 4; ++i) mbar_init(&ctl.pair[i], 2);
-    mbar_init(&ctl.s_full, 1);
-    mbar_init(&ctl.s_free, 16);
+    mbar_init(&ctl.s_full, 2);        // the MMAs' commit and the issuing thread (which orders `bad`)
+    mbar_init(&ctl.s_free, 8);
     mbar_init(&ctl.q_full, 1);
     mbar_init(&ctl.q_empty, 1);
-    mbar_init(&ctl.peer_q, 1);
     mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
 
   if (warp == 10) {
     // ---- tiles and Q ---------------------------------------------------------------
-    const int units = a.tile_slots * a.h_kv, half_rows = a.rows / 2;
+    const int units = a.tile_slots * a.h_kv;
     int k = 0, nq = 0;  // tiles published, Q copies
     bool ok = true;
-    for (int u = blockIdx.x >> 1; ok; u += gridDim.x >> 1) {
+    for (int u = blockIdx.x; ok; u += gridDim.x) {
       WtTile w{};
       if (u < units) {
         w = wt_tile(a, u / a.h_kv);
@@ -436,10 +364,10 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       if (w.n_blk > 0 && lane == 0) {
         if (nq > 0) ok = tm_wait(&ctl.q_empty, (uint32_t)(nq - 1) & 1u, abort);
         if (ok) {
-          // boxes of R x `group` x 64; what of the 128 rows they leave is never used
-          mbar_arrive_expect_tx(&ctl.q_full, (uint32_t)(half_rows * a.group * D * 2));
+          // boxes of `rows` x `group` x 64; what of the 128 rows they leave is never used
+          mbar_arrive_expect_tx(&ctl.q_full, (uint32_t)(a.rows * a.group * D * 2));
           for (int h = 0; h < D / 64; ++h)
-            wt_tma_3d(q_buf + h * kQHalf, &q_map, h * 64, w.g * a.group, w.t0 + rank * half_rows, &ctl.q_full);
+            wt_tma_3d(q_buf + h * kQHalf, &q_map, h * 64, w.g * a.group, w.t0, &ctl.q_full);
         }
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -451,73 +379,74 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
     const bool is_k = warp == 8;
     const CUtensorMap* map = is_k ? &k_map : &v_map;
     const int B = a.box, sh = a.box_shift;
-    const int per = N >> sh;                         // boxes of a block, at most 16
-    const int per_st = is_k ? per / 2 : per;         // and of a stage
-    const int b0 = is_k ? rank * per_st : 0;         // the stage's first box in the block
-    const uint32_t box_bytes = (uint32_t)B * (is_k ? D * 2u : (uint32_t)D);
-    const int oob = (int)(a.n_slots >> 3);           // 8-row groups of the map: zeros from there on
-    int rs = 0, done = 0;                            // ring stages, own last stage + 1 so far
+    const int per = N >> sh;                       // boxes of a block, at most 16
+    const int per_st = is_k ? per : Sh::kVRows >> sh;  // and of a stage
+    const uint32_t box_bytes = (uint32_t)B * (is_k ? 256u : D * 2u);
+    int gb = 0, rs = 0, done = 0;                  // blocks, ring stages, own last stage + 1 so far
     bool ok = true;
     for (int k = 0; ok; ++k) {
       WtTile w;
       if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
+      const int32_t* pt = a.page_table + (int64_t)w.r * a.ld_pt;
+      const int oob = (int)(a.n_slots >> 3);       // 8-row groups of the map
+      // first 8-row group of the block's box `lane`; past the map (zeros)
+      // where the page is out of range
       auto lookup = [&](int blk) -> int {
-        const int j = blk * per + b0 + lane;
-        if (blk >= w.n_blk || lane >= per_st || j >= w.n_box) return -1;
-        const int y = wt_box(a, w, j);
-        return y < 0 ? oob : y;
+        const int j = blk * per + lane;
+        if (blk >= w.n_blk || lane >= per || j >= w.n_box) return 0;
+        const int e = j << sh;
+        const int pos = e < w.nsr ? e : w.start + (e - w.nsr);
+        const int pi = pos / a.page_size;
+        const int64_t page = __ldg(pt + pi);
+        if (page < 0 || (page + 1) * a.page_size > a.n_slots) return oob;
+        return (int)((page * a.page_size + (pos - pi * a.page_size)) >> 3);
       };
       int next = lookup(0);
       for (int blk = 0; ok && blk < w.n_blk; ++blk) {
-        const int y = next;
+        const int row = next;
         next = lookup(blk + 1);
-        // the order of use: K(0), K(1), V(0), K(2), V(1), ...
-        const int at = rs + (is_k ? blk + max(blk - 1, 0) : min(blk + 2, w.n_blk) + blk);
-        const int st = at % Sh::kStages;
-        const int n = max(0, min(per_st, w.n_box - blk * per - b0));  // 0: none of this CTA's entries
-        if (at >= Sh::kStages && lane == 0) ok = tm_wait(&ctl.empty[st], (uint32_t)(at / Sh::kStages - 1) & 1u, abort);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], (uint32_t)n * box_bytes);
-        __syncwarp();
-        if (lane < n)
-          wt_tma_4d(ring + st * Sh::kStageBytes + lane * box_bytes, map,
-                    w.g * (D / 64) + (is_k ? 0 : rank * (D / 128)), y, &ctl.full[st]);
-        done = at + 1;
+        const int nb = min(per, w.n_box - blk * per);
+        if (is_k) {
+          const uint32_t bad = __ballot_sync(0xffffffffu, lane < nb && row == oob);
+          if (lane == 0) {
+            if (bad != 0) raise_fault(kFaultIndex);
+            ctl.bad[(gb + blk) % kWtBadRing] = bad;
+          }
+        }
+        // stages in the order of use: K(0), K(1), V(0), K(2), V(1), ...
+        int at = rs + (is_k ? Sh::kKs * blk + max(blk - 1, 0) * Sh::kVs
+                            : Sh::kKs * min(blk + 2, w.n_blk) + blk * Sh::kVs);
+        const int n_st = is_k ? Sh::kKs : (nb + per_st - 1) / per_st;
+        for (int i = 0; ok && i < n_st; ++i, ++at) {
+          const int st = at % Sh::kStages;
+          const int b0 = is_k ? 0 : i * per_st, n = is_k ? nb : min(per_st, nb - b0);
+          if (at >= Sh::kStages && lane == 0) ok = tm_wait(&ctl.empty[st], (uint32_t)(at / Sh::kStages - 1) & 1u, abort);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], (uint32_t)n * box_bytes);
+          __syncwarp();
+          const int y = __shfl_sync(0xffffffffu, row, (b0 + lane) & 31);
+          if (lane < n)
+            wt_tma_4d(ring + st * kWtStageBytes + lane * box_bytes, map,
+                      w.g * (D / 64) + (is_k ? i * 2 : 0), y, &ctl.full[st]);
+          done = at + 1;
+        }
       }
-      rs += 2 * w.n_blk;
+      gb += w.n_blk;
+      if (w.n_blk > 0) {
+        const int last = w.n_box * B - (w.n_blk - 1) * N;  // rows copied for the last block
+        rs += Sh::kKs * w.n_blk + (w.n_blk - 1) * Sh::kVs + (last + Sh::kVRows - 1) / Sh::kVRows;
+      }
     }
     // after an abort: copies under way land before the shared memory is
     // released (else every stage was waited for by its MMAs)
     if (lane == 0 && *abort)
       for (int j = max(0, done - Sh::kStages); j < done; ++j)
         mbar_wait_bounded(&ctl.full[j % Sh::kStages], (uint32_t)(j / Sh::kStages) & 1u, 20000000ull);
-  } else if (warp == 9 && rank == 1) {
-    // ---- the second CTA's copies, told to the first --------------------------------------
-    int rs = 0, nq = 0;
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      WtTile w;
-      if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
-      if (w.n_blk == 0) continue;
-      if (lane == 0) {
-        ok = tm_wait(&ctl.q_full, (uint32_t)nq & 1u, abort);
-        if (ok) wt_arrive_first(&ctl.peer_q);
-        for (int i = 0; ok && i < 2 * w.n_blk; ++i) {
-          const int st = (rs + i) % Sh::kStages;
-          ok = tm_wait(&ctl.full[st], (uint32_t)((rs + i) / Sh::kStages) & 1u, abort);
-          if (ok) wt_arrive_first(&ctl.peer_full[st]);
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      rs += 2 * w.n_blk;
-      ++nq;
-    }
   } else if (warp == 9) {
     // ---- MMA issuer --------------------------------------------------------------------
-    constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((256u >> 4) << 24);
-    constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(N >> 3) << 17);
-    constexpr uint32_t kIdescO = kIdesc | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // B is MN-major
+    constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
+    constexpr uint32_t kIdescO = kIdescS | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // B is MN-major
     // descriptors: the upper words never change, the lower ones by constants
     const uint64_t q_desc = umma_desc_sw128(smem_u32(q_buf)), k_desc0 = umma_desc_sw128(smem_u32(ring), Sh::kKGroup),
                    v_desc0 = wt_desc_mn(smem_u32(ring), Sh::kVGroup);
@@ -528,51 +457,53 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       WtTile w;
       if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
       if (w.n_blk == 0) continue;
+      auto n16 = [&](int blk) { return (min(N, w.uc - blk * N) + 15) & ~15; };
       auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, tm_wait(bar, parity, abort)); };
-      auto landed = [&](int st) {
-        const uint32_t ph = (uint32_t)(rs / Sh::kStages) & 1u;
-        return wait(&ctl.full[st], ph) && wait(&ctl.peer_full[st], ph);
-      };
       auto qk = [&](int blk) -> bool {
-        const int x = gb + blk, st = rs % Sh::kStages;
+        const int x = gb + blk;
         if (x >= 1 && !wait(&ctl.s_free, (uint32_t)(x - 1) & 1u)) return false;
-        if (!landed(st)) return false;
-        tc_fence_after();
-        const uint64_t kd = add(k_desc0, st * Sh::kStageBytes);
+        const uint32_t idesc = kIdescS | ((uint32_t)(n16(blk) >> 3) << 17);
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-          wt_mma_ss(tmem + Sh::kColS, add(q_desc, (c >> 2) * kQHalf + (c & 3) * 32),
-                    add(kd, (c >> 2) * 1024 + (c & 3) * 32), kIdescS, c > 0 ? 1u : 0u);
-        wt_commit(&ctl.empty[st]);
-        ++rs;
+        for (int i = 0; i < Sh::kKs; ++i) {
+          const int st = rs % Sh::kStages;
+          if (!wait(&ctl.full[st], (uint32_t)(rs / Sh::kStages) & 1u)) return false;
+          tc_fence_after();
+          const uint64_t kd = add(k_desc0, st * kWtStageBytes), qd = add(q_desc, i * 2 * kQHalf);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            wt_mma_ss(tmem + Sh::kColS, add(qd, (c >> 2) * kQHalf + (c & 3) * 32),
+                      add(kd, (c >> 2) * 1024 + (c & 3) * 32), idesc, i > 0 || c > 0 ? 1u : 0u);
+          wt_commit(&ctl.empty[st]);
+          ++rs;
+        }
         wt_commit(&ctl.s_full);
+        if (lane == 0) mbar_arrive(&ctl.s_full);
         if (blk + 1 == w.n_blk) wt_commit(&ctl.q_empty);
         return true;
       };
       auto pv = [&](int blk) -> bool {
-        const int x = gb + blk, sl = x & 1, st = rs % Sh::kStages;
-        if (!landed(st)) return false;
-        const uint32_t ph = (uint32_t)(x >> 1) & 1u;
-        if (wt_edge(w, blk) ? !__all_sync(0xffffffffu, wt_wait_cluster(&ctl.p_full[sl], ph, abort))
-                            : !wait(&ctl.p_full[sl], ph))
-          return false;
-        tc_fence_after();
-        const uint64_t vd = add(v_desc0, st * Sh::kStageBytes);
-        const uint32_t p = tmem + Sh::kColP + sl * 64;
-        const uint32_t use = wt_steps(w, blk);
-        uint32_t acc = blk > 0 ? 1u : 0u;
+        const int x = gb + blk, sl = x & 1;
+        if (!wait(&ctl.p_full[sl], (uint32_t)(x >> 1) & 1u)) return false;
+        const int n = n16(blk), copied = min(N, w.n_box * a.box - blk * N);
+        for (int e0 = 0; e0 < copied; e0 += Sh::kVRows) {
+          const int st = rs % Sh::kStages;
+          if (!wait(&ctl.full[st], (uint32_t)(rs / Sh::kStages) & 1u)) return false;
+          tc_fence_after();
+          const uint64_t vd = add(v_desc0, st * kWtStageBytes);
+          const uint32_t p = tmem + Sh::kColP + sl * 64 + e0 / 2;
+          const int steps = min(Sh::kVRows, n - e0) / 16;  // none for rows past the last key
+          const uint32_t first = blk > 0 || e0 > 0 ? 1u : 0u;
 #pragma unroll
-        for (int c = 0; c < N / 16; ++c)
-          if ((use >> c) & 1u) {
-            wt_mma_ts(tmem, p + c * 8, add(vd, c * 2 * Sh::kVGroup), kIdescO, acc);
-            acc = 1u;
-          }
-        wt_commit(&ctl.empty[st]);
-        ++rs;
+          for (int c = 0; c < Sh::kVRows / 16; ++c)
+            if (c < steps)
+              wt_mma_ts(tmem, p + c * 8, add(vd, c * 2 * Sh::kVGroup), kIdescO, c > 0 ? 1u : first);
+          wt_commit(&ctl.empty[st]);
+          ++rs;
+        }
         wt_commit(&ctl.pv_done[sl]);
         return true;
       };
-      ok = wait(&ctl.q_full, (uint32_t)nq & 1u) && wait(&ctl.peer_q, (uint32_t)nq & 1u) && qk(0);
+      ok = wait(&ctl.q_full, (uint32_t)nq & 1u) && qk(0);
       for (int i = 0; ok && i < w.n_blk; ++i) ok = (i + 1 >= w.n_blk || qk(i + 1)) && pv(i);
       gb += w.n_blk;
       ++nq;
@@ -584,8 +515,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
     // ---- softmax and outputs: a pair in two threads ------------------------------------
     const int half = warp >> 2;                   // columns 64 half .. + 63 of S, D/2 half .. of O
     const int pair = (warp & 3) * 32 + lane;      // MMA row = tensor-memory lane
-    const int row = rank * (a.rows / 2) + pair / a.group, hd = pair % a.group;
-    const bool held = pair < a.rows / 2 * a.group;
+    const int row = pair / a.group, hd = pair - row * a.group;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float thr = 8.0f / a.c;                 // growth of the maximum that forces a rescale
     uint64_t* pair_bar = &ctl.pair[warp & 3];
@@ -598,17 +528,15 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       ++n_pair;
       return ok;
     };
-    auto length = [&](const WtTile& w) -> int {
-      if (!held || row >= w.rows) return 0;
-      const int L = __ldg(a.row_len + w.t0 + row);
-      return L < 0 || L > a.max_len ? 0 : L;
-    };
-    WtTile w;
-    bool ok = wt_next_tile(ctl, 0, w, abort) && w.rows >= 0;
-    int L = ok ? length(w) : 0;
-    for (int k = 1; ok; ++k) {
-      const bool mine = held && row < w.rows;
-      const int64_t hq = ((int64_t)w.t0 + row) * a.h_q + (int64_t)w.g * a.group + hd;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      WtTile w;
+      if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
+      const bool mine = row < w.rows;
+      const int64_t t = w.t0 + row;
+      int L = mine ? __ldg(a.row_len + t) : 0;
+      if (L < 0 || L > a.max_len) L = 0;
+      const int64_t hq = t * a.h_q + (int64_t)w.g * a.group + hd;
       float m = ninf, l = 0.f;
       // the pair sees entries [0, va) and [vb, vc)
       const int va = min(a.n_sink, L);
@@ -616,26 +544,26 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       const int vc = L > 0 ? w.nsr + L - w.start : 0;
       for (int blk = 0; blk < w.n_blk; ++blk) {
         const int x = gb + blk, sl = x & 1;
-        const int e0 = blk * N, c0 = e0 + 64 * half;  // c0: first entry of this thread
+        const int e0 = blk * N;
         ok = __all_sync(0xffffffffu, tm_wait(&ctl.s_full, (uint32_t)x & 1u, abort));
         if (!ok) break;
         tc_fence_after();
+        const uint32_t bad = ctl.bad[x % kWtBadRing];
+        const int c0 = e0 + 64 * half;            // first entry of this thread
         uint32_t s[64];
         wt_tmem_ld64(lanes + Sh::kColS + 64 * half, s);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) wt_arrive_first(&ctl.s_free);
+        if (lane == 0) mbar_arrive(&ctl.s_free);
         if (a.flip != 0) {
 #pragma unroll
           for (int j = 0; j < 64; ++j) s[j] ^= a.flip;
         }
-        if (__any_sync(0xffffffffu, w.bad != 0 || c0 < vb || c0 + 64 > vc)) {
+        if (__any_sync(0xffffffffu, bad != 0 || c0 < vb || c0 + 64 > vc)) {
           uint64_t see = wt_low_bits(va - c0) | (wt_low_bits(vc - c0) & ~wt_low_bits(vb - c0));
-          if (w.bad)
-            for (int j = 0; j < 64; j += a.box) {
-              const int bx = (c0 + j) >> a.box_shift;
-              if (bx < w.n_box && wt_box(a, w, bx) < 0) see &= ~(wt_low_bits(a.box) << j);
-            }
+          if (bad != 0)
+            for (int j = 0; j < 64; j += a.box < 64 ? a.box : 64)
+              if ((bad >> ((64 * half + j) >> a.box_shift)) & 1u) see &= ~(wt_low_bits(a.box) << j);
           const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -685,33 +613,34 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         wt_tmem_st32(lanes + Sh::kColP + sl * 64 + 32 * half, p);
         wt_wait_st();
         tc_fence_before();
-        // V rows that no pair sees, where the product takes them: zeros
-        const bool edge = wt_edge(w, blk);
-        if (edge) {
-          const int at = rs + min(blk + 2, w.n_blk) + blk, st = at % Sh::kStages;  // V's stage
-          ok = __all_sync(0xffffffffu, tm_wait(&ctl.full[st], (uint32_t)(at / Sh::kStages) & 1u, abort));
-          if (!ok) break;
-          unsigned char* vst = ring + st * Sh::kStageBytes;
-          const uint32_t use = wt_steps(w, blk);
-          for (int r = warp; r < N; r += 8) {  // a row a warp, 16 bytes a lane
-            const int e = e0 + r;
-            if (((use >> (r >> 4)) & 1u) && !(e < w.ua || (e >= w.ub && e < w.uc)) && lane < D / 16)
-              *reinterpret_cast<uint4*>(vst + (r >> 3) * Sh::kVGroup + (lane >> 3) * 1024 + (r & 7) * 128 +
-                                        (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        // V rows that no pair sees: zeros
+        const int n16 = (min(N, w.uc - e0) + 15) & ~15;
+        if (e0 < w.ub || e0 + n16 > w.uc) {
+          const int at = rs + Sh::kKs * min(blk + 2, w.n_blk) + blk * Sh::kVs;  // V's first stage
+          for (int v = 0; ok && v * Sh::kVRows < n16; ++v) {
+            const int st = (at + v) % Sh::kStages;
+            ok = __all_sync(0xffffffffu, tm_wait(&ctl.full[st], (uint32_t)((at + v) / Sh::kStages) & 1u, abort));
+            if (!ok) break;
+            unsigned char* vst = ring + st * kWtStageBytes;
+            const int rows = min(Sh::kVRows, n16 - v * Sh::kVRows);
+            for (int r = warp; r < rows; r += 8) {  // a row a warp, 16 bytes a lane
+              const int e = e0 + v * Sh::kVRows + r;
+              if (!(e < w.ua || (e >= w.ub && e < w.uc)) && lane < D / 8)
+                *reinterpret_cast<uint4*>(vst + (r >> 3) * Sh::kVGroup + (lane >> 3) * 1024 + (r & 7) * 128 +
+                                          (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
+          if (!ok) break;
           fence_proxy_async_smem();
         }
-        __syncwarp();
-        if (lane == 0) wt_arrive_first(&ctl.p_full[sl], edge);
+        mbar_arrive(&ctl.p_full[sl]);
       }
       if (!ok) break;
       gb += w.n_blk;
-      rs += 2 * w.n_blk;
-      // the next tile's rows, while the last products run
-      WtTile nw;
-      ok = wt_next_tile(ctl, k, nw, abort);
-      if (!ok) break;
-      const int nL = nw.rows > 0 ? length(nw) : 0;
+      if (w.n_blk > 0) {
+        const int last = w.n_box * a.box - (w.n_blk - 1) * N;  // rows copied for the last block
+        rs += Sh::kKs * w.n_blk + (w.n_blk - 1) * Sh::kVs + (last + Sh::kVRows - 1) / Sh::kVRows;
+      }
       // ---- outputs ---------------------------------------------------------------------
       float inv = 0.f;
       if (w.n_blk > 0) {
@@ -726,59 +655,61 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         tc_fence_after();
         inv = l == 0.f ? 0.f : 1.0f / l;
       }
-      // 64 columns at a time through 4 KB of shared memory, so that 8 lanes
-      // write 128 consecutive bytes of a row (a row a lane, every store met 32
-      // lines: 4,000 clocks a tile)
-      unsigned char* stage = out_buf + warp * 4096;
-      const int64_t at = mine ? hq * D : -1;
+      // 32 columns at a time: 4 pieces of 16 bytes a lane, transposed over the
+      // quad so that its lanes write 64 consecutive bytes of one row (written
+      // a row a lane, every store met 32 lines: 4,000 clocks a tile)
+      const int sub = lane & 3;
+      uint16_t* dst = a.out + hq * D;
 #pragma unroll 1
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 64) {
-        uint32_t o[64];
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+        uint32_t o[32];
         if (w.n_blk > 0) {
-          wt_tmem_ld64(lanes + c, o);
+          wt_tmem_ld32(lanes + c, o);
         } else {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) o[j] = 0u;
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
         }
+        uint32_t y[4][4];  // [piece][word]
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // a row that sees nothing writes zeros, whatever the accumulator holds
-            const float x0 = l == 0.f ? 0.f : __uint_as_float(o[8 * j + 2 * i]) * inv;
-            const float x1 = l == 0.f ? 0.f : __uint_as_float(o[8 * j + 2 * i + 1]) * inv;
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
-            y[i] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+        for (int j = 0; j < 16; ++j) {
+          // a row that sees nothing writes zeros, whatever the accumulator holds
+          const float x0 = l == 0.f ? 0.f : __uint_as_float(o[2 * j]) * inv;
+          const float x1 = l == 0.f ? 0.f : __uint_as_float(o[2 * j + 1]) * inv;
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+          y[j >> 2][j & 3] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        __syncwarp();
+        // y[p] of lane q <-> y[q] of lane p
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + (lane >> 3);
-          const int64_t to = __shfl_sync(0xffffffffu, at, r);
-          if (to >= 0)
-            *reinterpret_cast<uint4*>(a.out + to + c + (lane & 7) * 8) =
-                *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        for (int d = 1; d <= 2; d <<= 1)
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            if ((p & d) == 0)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const bool up = (sub & d) != 0;
+                const uint32_t give = up ? y[p][j] : y[p | d][j];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, d);
+                if (up) y[p][j] = got;
+                else y[p | d][j] = got;
+              }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {  // row of the quad's lane p, piece `sub`
+          const int64_t at = __shfl_sync(0xffffffffu, mine ? (long long)(dst - a.out) : -1ll, (lane & ~3) | p);
+          if (at >= 0)
+            *reinterpret_cast<uint4*>(a.out + at + c + sub * 8) = make_uint4(y[p][0], y[p][1], y[p][2], y[p][3]);
         }
-        __syncwarp();
       }
       tc_fence_before();
       if (mine && half == 0 && a.lse != nullptr)
         a.lse[hq] = l == 0.f ? ninf : (m == ninf ? l : (fmaf(m, a.c, log2f(l))) * 0.69314718055994531f);
-      w = nw;
-      L = nL;
-      if (w.rows < 0) break;
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // neither CTA's memories are in use any more
   tc_fence_after();
   if (warp == 9)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 }  // namespace qsa
