@@ -33,15 +33,16 @@
 //    write the outputs.  (One thread a pair took 1,000 clocks for 64 entries,
 //    more than a product of D = 128.)
 //  - The products go in the order QK(i+1) PV(i), so that a softmax has the
-//    time of two products.  S has one buffer, free again as soon as the
-//    softmax warps hold it in registers; P has two, and the barrier that
-//    announces S(i) also covers PV(i-2), which read the one P(i) goes into.
+//    time of two products.  S has two buffers and P(i) takes the place of
+//    S(i), so that QK(i+1) waits for no softmax, only for its keys: the pipe
+//    runs one thread's MMAs in order, and PV(i-1), which read the buffer,
+//    went before.  The barrier that announces S(i) covers PV(i-2) too.
 //  - The accumulator is rescaled only when a row's maximum grew by more than
 //    2^8 since the last time (the weights stay below 2^8 and the sums are
 //    FP32, so nothing is lost); otherwise m stays.
 //  - Weights enter the product as BF16, 2^-9 relative at most, one rounding
 //    like that of the output; l sums them before the rounding, in FP32.
-// Tensor memory columns: O [0, D), S the next 128, P two times 64.
+// Tensor memory columns: O [0, D), S two times 128, P in the first 64 of its S.
 //
 // Entries.  With `start` the first window position of the tile rounded down
 // to a box, the entries are the boxes of the first tokens before `start`
@@ -74,7 +75,7 @@ struct WtShape {
   static constexpr int kVRows = D == 256 ? 64 : 128;  // entries of a V stage
   static constexpr int kVs = kWtN / kVRows;         // V stages of a full block
   static constexpr uint32_t kKGroup = 2 * 1024, kVGroup = D / 64 * 1024;  // bytes of an 8-row group
-  static constexpr uint32_t kColS = D, kColP = D + kWtN;
+  static constexpr uint32_t kColS = D;  // two buffers of N
   static constexpr int kQBytes = 128 * D * 2;
   static constexpr int kStages = D == 256 ? 5 : 6;  // of K and V: 224 KB with Q
   static_assert(D + 2 * kWtN <= 512, "tensor memory");
@@ -255,7 +256,7 @@ __device__ __forceinline__ WtTile wt_tile(const WtArgs& a, int s) {
 
 struct WtCtl {
   uint64_t full[6], empty[6];
-  uint64_t s_full, s_free, p_full[2], pv_done[2], q_full, q_empty, drain;
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty, drain;
   uint64_t tile_full[kWtTileRing], tile_empty[kWtTileRing];
   uint64_t pair[4];          // the two warps of a lane quarter
   WtTile tile[kWtTileRing];
@@ -316,7 +317,8 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       mbar_init(&ctl.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.p_full[i], 256);
+      mbar_init(&ctl.s_full[i], 2);   // the MMAs' commit and the issuing warp (which orders `bad`)
+      mbar_init(&ctl.p_full[i], 8);
       mbar_init(&ctl.pv_done[i], 1);
     }
     for (int i = 0; i < kWtTileRing; ++i) {
@@ -324,8 +326,6 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       mbar_init(&ctl.tile_empty[i], 11);  // softmax warps, K, V, MMAs
     }
     for (int i = 0; i < 4; ++i) mbar_init(&ctl.pair[i], 2);
-    mbar_init(&ctl.s_full, 2);        // the MMAs' commit and the issuing thread (which orders `bad`)
-    mbar_init(&ctl.s_free, 8);
     mbar_init(&ctl.q_full, 1);
     mbar_init(&ctl.q_empty, 1);
     mbar_init(&ctl.drain, 1);
@@ -451,54 +451,57 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
     const uint64_t q_desc = umma_desc_sw128(smem_u32(q_buf)), k_desc0 = umma_desc_sw128(smem_u32(ring), Sh::kKGroup),
                    v_desc0 = wt_desc_mn(smem_u32(ring), Sh::kVGroup);
     auto add = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };  // stays inside the address field
-    int gb = 0, rs = 0, nq = 0;  // blocks, ring stages and Q copies so far
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, tm_wait(bar, parity, abort)); };
+    int gb = 0, nq = 0;          // blocks and Q copies so far
+    int st = 0;                  // next ring stage and its parity
+    uint32_t ph = 0;
     bool ok = true;
+    auto next_stage = [&]() {
+      wt_commit(&ctl.empty[st]);
+      if (++st == Sh::kStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    };
     for (int k = 0; ok; ++k) {
       WtTile w;
       if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
       if (w.n_blk == 0) continue;
       auto n16 = [&](int blk) { return (min(N, w.uc - blk * N) + 15) & ~15; };
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, tm_wait(bar, parity, abort)); };
       auto qk = [&](int blk) -> bool {
-        const int x = gb + blk;
-        if (x >= 1 && !wait(&ctl.s_free, (uint32_t)(x - 1) & 1u)) return false;
-        const uint32_t idesc = kIdescS | ((uint32_t)(n16(blk) >> 3) << 17);
+        const int sl = (gb + blk) & 1;
+        const uint32_t idesc = kIdescS | ((uint32_t)(n16(blk) >> 3) << 17), d = tmem + Sh::kColS + sl * N;
 #pragma unroll
         for (int i = 0; i < Sh::kKs; ++i) {
-          const int st = rs % Sh::kStages;
-          if (!wait(&ctl.full[st], (uint32_t)(rs / Sh::kStages) & 1u)) return false;
-          tc_fence_after();
+          if (!wait(&ctl.full[st], ph)) return false;
           const uint64_t kd = add(k_desc0, st * kWtStageBytes), qd = add(q_desc, i * 2 * kQHalf);
 #pragma unroll
           for (int c = 0; c < 8; ++c)
-            wt_mma_ss(tmem + Sh::kColS, add(qd, (c >> 2) * kQHalf + (c & 3) * 32),
-                      add(kd, (c >> 2) * 1024 + (c & 3) * 32), idesc, i > 0 || c > 0 ? 1u : 0u);
-          wt_commit(&ctl.empty[st]);
-          ++rs;
+            wt_mma_ss(d, add(qd, (c >> 2) * kQHalf + (c & 3) * 32), add(kd, (c >> 2) * 1024 + (c & 3) * 32), idesc,
+                      i > 0 || c > 0 ? 1u : 0u);
+          next_stage();
         }
-        wt_commit(&ctl.s_full);
-        if (lane == 0) mbar_arrive(&ctl.s_full);
+        wt_commit(&ctl.s_full[sl]);
+        if (lane == 0) mbar_arrive(&ctl.s_full[sl]);
         if (blk + 1 == w.n_blk) wt_commit(&ctl.q_empty);
         return true;
       };
       auto pv = [&](int blk) -> bool {
         const int x = gb + blk, sl = x & 1;
         if (!wait(&ctl.p_full[sl], (uint32_t)(x >> 1) & 1u)) return false;
+        tc_fence_after();
         const int n = n16(blk), copied = min(N, w.n_box * a.box - blk * N);
         for (int e0 = 0; e0 < copied; e0 += Sh::kVRows) {
-          const int st = rs % Sh::kStages;
-          if (!wait(&ctl.full[st], (uint32_t)(rs / Sh::kStages) & 1u)) return false;
-          tc_fence_after();
+          if (!wait(&ctl.full[st], ph)) return false;
           const uint64_t vd = add(v_desc0, st * kWtStageBytes);
-          const uint32_t p = tmem + Sh::kColP + sl * 64 + e0 / 2;
+          const uint32_t p = tmem + Sh::kColS + sl * N + e0 / 2;
           const int steps = min(Sh::kVRows, n - e0) / 16;  // none for rows past the last key
           const uint32_t first = blk > 0 || e0 > 0 ? 1u : 0u;
 #pragma unroll
           for (int c = 0; c < Sh::kVRows / 16; ++c)
             if (c < steps)
               wt_mma_ts(tmem, p + c * 8, add(vd, c * 2 * Sh::kVGroup), kIdescO, c > 0 ? 1u : first);
-          wt_commit(&ctl.empty[st]);
-          ++rs;
+          next_stage();
         }
         wt_commit(&ctl.pv_done[sl]);
         return true;
@@ -545,16 +548,14 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       for (int blk = 0; blk < w.n_blk; ++blk) {
         const int x = gb + blk, sl = x & 1;
         const int e0 = blk * N;
-        ok = __all_sync(0xffffffffu, tm_wait(&ctl.s_full, (uint32_t)x & 1u, abort));
+        ok = __all_sync(0xffffffffu, tm_wait(&ctl.s_full[sl], (uint32_t)(x >> 1) & 1u, abort));
         if (!ok) break;
         tc_fence_after();
         const uint32_t bad = ctl.bad[x % kWtBadRing];
         const int c0 = e0 + 64 * half;            // first entry of this thread
         uint32_t s[64];
-        wt_tmem_ld64(lanes + Sh::kColS + 64 * half, s);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.s_free);
+        wt_tmem_ld64(lanes + Sh::kColS + sl * N + 64 * half, s);
+        tc_fence_before();  // the other half's P goes where this half's S was: after the exchange
         if (a.flip != 0) {
 #pragma unroll
           for (int j = 0; j < 64; ++j) s[j] ^= a.flip;
@@ -578,6 +579,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         ctl.mx[x & 1][half][pair] = mx;
         ok = meet();
         if (!ok) break;
+        tc_fence_after();
         mx = fmaxf(mx, ctl.mx[x & 1][half ^ 1][pair]);
         const bool grow = m != ninf && mx > m + thr;
         if (__any_sync(0xffffffffu, grow)) {
@@ -610,7 +612,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
           p[j] = *reinterpret_cast<const uint32_t*>(&b);
         }
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        wt_tmem_st32(lanes + Sh::kColP + sl * 64 + 32 * half, p);
+        wt_tmem_st32(lanes + Sh::kColS + sl * N + 32 * half, p);
         wt_wait_st();
         tc_fence_before();
         // V rows that no pair sees: zeros
@@ -633,7 +635,8 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
           if (!ok) break;
           fence_proxy_async_smem();
         }
-        mbar_arrive(&ctl.p_full[sl]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.p_full[sl]);
       }
       if (!ok) break;
       gb += w.n_blk;
