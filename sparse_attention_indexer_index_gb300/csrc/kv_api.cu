@@ -184,6 +184,25 @@ bool encode_q_map(CUtensorMap* m, const WtArgs& a, int d) {
 // rows on pages of whole 8-row groups; QSA_ERR_UNSUPPORTED where the other
 // form has to serve.
 constexpr int kWtMinRows = 1;
+// CTAs that share a tile, where there are few: a single tile of 9 blocks takes
+// 29.8 us on one CTA, 25.7 on two, 23.7 on four, 21.6 on eight, one of 33
+// blocks 68.7, 46.2, 33.9 and 27.7 (in a graph, with what it adds).  At most
+// 128 CTAs so, and 64 in clusters of eight: beyond that the clusters no longer
+// run at once (16 tiles of 9 blocks: 38.0 us in eights, 23.7 in fours).  From
+// 65 tiles on, one CTA a tile, launched without the cluster attribute: sharing
+// the last round's gained nothing (the 512 tiles of a 4,096-row chunk: 85 us
+// either way), and a cluster launch cost 1 us.  How many tiles there are is
+// known on the device only; the estimate takes requests of equal length.
+int wt_cluster(const WtArgs& a) {
+  if (a.n_req > kWtExactReq) return 1;
+  const int64_t per_req = ((int64_t)a.n_rows + a.n_req - 1) / a.n_req;
+  const int64_t tiles = a.n_req * ((per_req + a.rows - 1) / a.rows) * a.h_kv;
+  const int64_t blocks = (std::min<int64_t>(a.max_len, (int64_t)a.window + a.n_sink + a.rows) + kWtN - 1) / kWtN;
+  int c = 1;
+  while (c < 8 && tiles * 2 * c <= (c < 4 ? 128 : 64) && blocks >= std::max(4, 2 * c)) c *= 2;
+  return c;
+}
+
 qsa_status launch_window_tc(const KvAttnArgs& k, int d, int32_t max_rows_per_req, cudaStream_t stream) {
   if (max_rows_per_req <= kWtMinRows || k.page_size % 8 != 0 || k.n_slots < 8) return QSA_ERR_UNSUPPORTED;
   WtArgs a{};
@@ -213,17 +232,32 @@ qsa_status launch_window_tc(const KvAttnArgs& k, int d, int32_t max_rows_per_req
   a.out = static_cast<uint16_t*>(k.out);
   a.lse = k.lse;
   const int64_t units = (int64_t)a.tile_slots * a.h_kv;
-  if (units > INT32_MAX || k.max_len > (1 << 30)) return QSA_ERR_UNSUPPORTED;
+  if (units > (1 << 30) || k.max_len > (1 << 30)) return QSA_ERR_UNSUPPORTED;
   int sms = 0;
   if (qsa_status st = kv_device_ready(&sms)) return st;
   CUtensorMap q_map, k_map, v_map;
   if (!encode_q_map(&q_map, a, d) || !encode_cache_map(&k_map, k.k, k.n_slots, (int64_t)k.h_kv * d, a.box, 2) ||
       !encode_cache_map(&v_map, k.v, k.n_slots, (int64_t)k.h_kv * d, a.box, d / 64))
     return QSA_ERR_UNSUPPORTED;
-  const unsigned grid = (unsigned)std::min<int64_t>(units, sms);
-  if (d == 256) window_tc_kernel<256><<<grid, kWtThreads, wt_smem_bytes<256>(), stream>>>(a, q_map, k_map, v_map);
-  else window_tc_kernel<128><<<grid, kWtThreads, wt_smem_bytes<128>(), stream>>>(a, q_map, k_map, v_map);
-  return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+  a.cluster = wt_cluster(a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(units, sms / a.cluster) * a.cluster), 1, 1);
+  cfg.blockDim = dim3(kWtThreads, 1, 1);
+  cfg.dynamicSmemBytes = d == 256 ? wt_smem_bytes<256>() : wt_smem_bytes<128>();
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, d == 256 ? window_tc_kernel<256> : window_tc_kernel<128>, a, q_map, k_map, v_map) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return QSA_ERR_CUDA;
+  }
+  return QSA_OK;
 }
 
 size_t ka_workspace(int64_t n_rows, int32_t h_q, int32_t h_kv, int32_t d, int64_t entries) {

@@ -13,7 +13,10 @@
 // tile reads: tensor-bound once the copies keep up (64 bytes a clock and SM
 // at the full MMA rate).
 //
-// Design (GB300).  One CTA per SM walks tiles (a static stride):
+// Design (GB300).  One CTA per SM walks tiles (a static stride).  Where there
+// are few tiles, the CTAs of a cluster share one: each takes a part of its
+// blocks, and they exchange their sums through shared memory, D / C columns
+// to each.  In a CTA:
 //  - warp 10 finds the tiles and copies Q (TMA, 3-D boxes: the rows and heads
 //    of a tile land as the 128 rows of the MMA operand), a tile ahead;
 //  - warps 8 (K) and 11 (V) copy into a ring of 32 KB stages in the order in
@@ -96,6 +99,7 @@ struct WtArgs {
   int32_t page_size;
   int32_t box, box_shift;    // B: rows per copy, 8 to 64, dividing the page; its logarithm
   int32_t tile_slots;        // n_rows / R + n_req
+  int32_t cluster;           // C: CTAs that share a tile, 1 to 8 (1 from kWtExactReq requests on)
   float c;                   // |scale| log2 e, positive
   uint32_t flip;             // sign bit to flip in S (a negative scale)
   uint16_t* out;             // [n_rows][h_q][D] BF16
@@ -142,10 +146,21 @@ __device__ __forceinline__ void wt_tmem_st32(uint32_t taddr, const uint32_t (&v)
 
 __device__ __forceinline__ void wt_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The copies and what announces them: by one elected lane of a whole warp, as the MMAs.
+__device__ __forceinline__ void wt_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void wt_prefetch(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void wt_tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(smem_u32(dst)),
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];\n\t}" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
@@ -153,21 +168,44 @@ __device__ __forceinline__ void wt_tma_3d(void* dst, const CUtensorMap* map, int
 // descriptors then live in uniform registers.  (Behind a branch on the lane,
 // moving them there took about 85 clocks an MMA, where a 128 x 128 x 16
 // product takes 64.)
-// D[128][n] (+)= A (shared memory) * B (shared memory).
-__device__ __forceinline__ void wt_mma_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// A K stage's product: S (+)= Q K^T over 128 columns, eight MMAs of 16 (four
+// to a 64-column tile of Q, 16 KB, and to one of the stage's two groups of
+// K's, 1 KB).  One statement, one election: eight statements made the chunk of
+// 4,096 rows 84.7 us instead of 81.0.
+__device__ __forceinline__ void wt_mma_qk(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 1024;\n\tadd.u64 b, %2, 64;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 1026;\n\tadd.u64 b, %2, 66;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 1028;\n\tadd.u64 b, %2, 68;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 1030;\n\tadd.u64 b, %2, 70;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "}" ::"r"(d),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// D[128][n] (+)= A (tensor memory, BF16 pairs) * B (shared memory).
-__device__ __forceinline__ void wt_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// Up to four MMAs of 16 entries, O (+)= P V: P (tensor memory, 8 columns each)
+// and V's rows, G descriptor units apart; the first n of them.
+template <uint32_t G>
+__device__ __forceinline__ void wt_mma_pv(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                                          int n) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q, t, u;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "setp.gt.and.s32 u, %5, 0, q;\n\t@u tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "setp.gt.and.s32 u, %5, 1, q;\n\tadd.u32 a, %1, 8;\n\tadd.u64 b, %2, %6;\n\t"
+      "@u tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "setp.gt.and.s32 u, %5, 2, q;\n\tadd.u32 a, %1, 16;\n\tadd.u64 b, %2, %7;\n\t"
+      "@u tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "setp.gt.and.s32 u, %5, 3, q;\n\tadd.u32 a, %1, 24;\n\tadd.u64 b, %2, %8;\n\t"
+      "@u tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(n), "n"(G), "n"(2 * G), "n"(3 * G)
       : "memory");
 }
 __device__ __forceinline__ void wt_commit(uint64_t* bar) {
@@ -178,8 +216,8 @@ __device__ __forceinline__ void wt_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void wt_tma_4d(void* dst, const CUtensorMap* map, int z, int w, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], "
-      "[%5];" ::"r"(smem_u32(dst)),
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], "
+      "[%5];\n\t}" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
@@ -197,18 +235,67 @@ __device__ __forceinline__ uint64_t wt_desc_mn(uint32_t smem_addr, uint32_t grou
 
 struct WtTile {
   int r, g;            // request, KV head
+  int parts;           // CTAs of the cluster that share the tile
   int t0, rows;        // rows t0 .. t0 + rows - 1; 0: nothing to do, -1: no more tiles
   int start, nsr;      // see above
-  int n_box, n_blk;    // boxes and blocks of N entries
-  int ua, ub, uc;      // entries that some pair sees: [0, ua) and [ub, uc)
+  int j0;              // first box of this CTA's part
+  int n_box, n_blk;    // boxes from there on, blocks of N entries of the part
+  int ua, ub, uc;      // entries that some pair sees, from the part's first: [0, ua) and [ub, uc)
 };
 
-// Tile of slot s: request r's tiles begin at slot req_row_start[r] / R + r
-// (enough room, since the requests before it have at most that many tiles);
-// slots past a request's last tile are empty.  By a whole warp.
-__device__ __forceinline__ WtTile wt_tile(const WtArgs& a, int s) {
+// Tiles of request i; 0 where the grouping is wrong.
+__device__ __forceinline__ int wt_request_tiles(const WtArgs& a, int i) {
+  if (i >= a.n_req) return 0;
+  const int row0 = __ldg(a.req_row_start + i), row1 = __ldg(a.req_row_start + i + 1);
+  if (row0 < 0 || row1 < row0 || row1 > a.n_rows) {
+    raise_fault(kFaultGrouping);
+    return 0;
+  }
+  return (row1 - row0 + a.rows - 1) / a.rows;
+}
+
+// Up to kWtExactReq requests: lane g's number of tiles before requests
+// 32 g .. 32 g + 31; the return value is the number of all tiles.
+constexpr int kWtExactReq = 1024;
+__device__ __forceinline__ int wt_count(const WtArgs& a, int& before) {
   const int lane = threadIdx.x & 31;
-  WtTile w{};
+  int mine = 0;
+#pragma unroll 4
+  for (int g = 0; g * 32 < a.n_req; ++g) {
+    const int n = __reduce_add_sync(0xffffffffu, wt_request_tiles(a, g * 32 + lane));
+    if (lane == g) mine = n;
+  }
+  int incl = mine;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  before = incl - mine;
+  return __shfl_sync(0xffffffffu, incl, 31);
+}
+
+// Request of tile `rank`, which becomes the tile's number in the request.
+__device__ __forceinline__ int wt_find(const WtArgs& a, int before, int& rank) {
+  const int lane = threadIdx.x & 31;
+  const int g = 31 - __clz(__ballot_sync(0xffffffffu, before <= rank && lane * 32 < a.n_req));
+  rank -= __shfl_sync(0xffffffffu, before, g);
+  const int n = wt_request_tiles(a, g * 32 + lane);
+  int incl = n;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  const int l = __ffs(__ballot_sync(0xffffffffu, incl > rank)) - 1;
+  rank -= __shfl_sync(0xffffffffu, incl - n, l);
+  return g * 32 + l;
+}
+
+// More requests: slot s, with request r's tiles from slot req_row_start[r] / R
+// + r on (enough room, since the requests before it have at most that many
+// tiles); slots past a request's last tile are empty (-1).  `rank` becomes the
+// tile's number in the request.
+__device__ __forceinline__ int wt_find_slot(const WtArgs& a, int s, int& rank) {
+  const int lane = threadIdx.x & 31;
   int lo = 0, n = a.n_req + 1;  // the last i with start[i] / R + i <= s, 32 samples a round
   while (true) {
     const int step = (n + 31) / 32;
@@ -219,17 +306,20 @@ __device__ __forceinline__ WtTile wt_tile(const WtArgs& a, int s) {
     n = min(step, n - (k - 1) * step);
     if (step == 1) break;
   }
-  if (lo >= a.n_req) return w;
-  const int row0 = __ldg(a.req_row_start + lo), row1 = __ldg(a.req_row_start + lo + 1);
-  if (row0 < 0 || row1 < row0 || row1 > a.n_rows) {
-    if (lane == 0) raise_fault(kFaultGrouping);
-    return w;
-  }
-  const int64_t t0 = row0 + (int64_t)(s - (row0 / a.rows + lo)) * a.rows;
-  if (t0 < row0 || t0 >= row1) return w;
-  w.r = lo;
-  w.t0 = (int)t0;
-  w.rows = min(a.rows, row1 - (int)t0);
+  if (lo >= a.n_req) return -1;
+  rank = s - (__ldg(a.req_row_start + lo) / a.rows + lo);
+  return rank < wt_request_tiles(a, lo) ? lo : -1;
+}
+
+// Tile `rank` of request r, or this CTA's part of it.  By a whole warp.
+__device__ __forceinline__ WtTile wt_tile(const WtArgs& a, int r, int rank, int parts, int part) {
+  const int lane = threadIdx.x & 31;
+  WtTile w{};
+  w.r = r;
+  w.parts = parts;
+  w.t0 = __ldg(a.req_row_start + r) + rank * a.rows;
+  w.rows = min(a.rows, __ldg(a.req_row_start + r + 1) - w.t0);
+  const int t0 = w.t0;
   int first = INT32_MAX, last = 0;
   for (int i = lane; i < w.rows; i += 32) {
     const int L = __ldg(a.row_len + t0 + i);
@@ -246,11 +336,14 @@ __device__ __forceinline__ WtTile wt_tile(const WtArgs& a, int s) {
   const int B = a.box;
   w.start = first & ~(B - 1);
   w.nsr = (min(a.n_sink, w.start) + B - 1) & ~(B - 1);
-  w.n_box = w.nsr / B + (last - w.start + B - 1) / B;
-  w.n_blk = (w.n_box * B + kWtN - 1) / kWtN;
-  w.ua = min(a.n_sink, last);
-  w.ub = w.nsr + first - w.start;
-  w.uc = w.nsr + last - w.start;
+  const int n_box = w.nsr / B + (last - w.start + B - 1) / B, n_blk = (n_box * B + kWtN - 1) / kWtN;
+  const int b0 = n_blk * part / parts, e0 = b0 * kWtN;
+  w.j0 = e0 / B;
+  w.n_box = n_box - w.j0;
+  w.n_blk = n_blk * (part + 1) / parts - b0;
+  w.ua = min(a.n_sink, last) - e0;
+  w.ub = w.nsr + first - w.start - e0;
+  w.uc = w.nsr + last - w.start - e0;
   return w;
 }
 
@@ -259,6 +352,7 @@ struct WtCtl {
   uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty, drain;
   uint64_t tile_full[kWtTileRing], tile_empty[kWtTileRing];
   uint64_t pair[4];          // the two warps of a lane quarter
+  uint64_t join_free, join_full;  // the cluster's CTAs take sums; all sums are here
   WtTile tile[kWtTileRing];
   float mx[2][2][128];       // [block parity][half][pair]: maxima, at the end the sums
   uint32_t bad[kWtBadRing];  // boxes of a block that are out of range
@@ -276,15 +370,154 @@ __device__ __forceinline__ uint64_t wt_low_bits(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
 }
 
+// Bounded wait by a whole warp, which stays together: every branch hangs on a
+// vote.  (With branches on a lane's own result the
+// chunk of 4,096 rows took 80.2 us instead of 73.4.)
+__device__ __forceinline__ bool wt_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    const bool late = global_timer_ns() - t0 > 200000000ull;
+    if (__any_sync(0xffffffffu, late || *abort != 0)) {
+      if ((threadIdx.x & 31) == 0) {
+        if (*abort == 0) raise_fault(kFaultWait);
+        *abort = 1;
+      }
+      return false;
+    }
+  }
+  return true;
+}
+
 // The next tile of the ring, by a whole warp; false: aborted.
 __device__ __forceinline__ bool wt_next_tile(WtCtl& ctl, int k, WtTile& w, volatile int* abort) {
   const int sl = k % kWtTileRing;
-  const bool ok = __all_sync(0xffffffffu, tm_wait(&ctl.tile_full[sl], (uint32_t)(k / kWtTileRing) & 1u, abort));
-  if (!ok) return false;
+  if (!wt_wait(&ctl.tile_full[sl], (uint32_t)(k / kWtTileRing) & 1u, abort)) return false;
   w = ctl.tile[sl];
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.tile_empty[sl]);
   return true;
+}
+
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void wt_store32(uint16_t* dst, const uint32_t* y) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+               "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+               : "memory");
+}
+// The cluster barrier, by threads of any branch.
+__device__ __forceinline__ void wt_cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void wt_cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// One arrival at every CTA's barrier for what the warp wrote to them.
+__device__ __forceinline__ void wt_arrive_all(uint64_t* bar, int n_cta) {
+  __syncwarp();
+  const int lane = threadIdx.x & 31;
+  if (lane < n_cta)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_shared_rank(bar, lane)) : "memory");
+}
+// Wait (bounded) for arrivals from the cluster: phase 0, by a whole warp.
+__device__ __forceinline__ bool wt_wait_cluster(uint64_t* bar, volatile int* abort) {
+  auto arrived = [&]() -> bool {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar))
+        : "memory");
+    return done != 0;
+  };
+  bool ok = true;
+  const uint64_t t0 = global_timer_ns();
+  while (ok && !arrived()) {
+    if (*abort || global_timer_ns() - t0 > 200000000ull) {
+      if (!*abort) raise_fault(kFaultWait);
+      *abort = 1;
+      ok = false;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void wt_tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// A tile that the cluster's C CTAs shared: out = sum_s f_s O_s / sum_s f_s l_s,
+// f_s = exp2(c (m_s - max m)), by the softmax warps.  CTA j writes columns
+// [j S, (j + 1) S), S = D / C, and gets them from all (itself too) in its
+// ring, which nothing uses any more: [source][4 columns][pair] vectors of
+// 4, a source's groups of 4 columns kJoinGroup bytes apart (an odd number of
+// vectors: no bank conflicts either way), then the l and m of all pairs.
+constexpr int kWtJoinGroup = 129 * 16;
+template <int D>
+__device__ __forceinline__ void wt_join(const WtArgs& a, const WtTile& w, unsigned char* ring, WtCtl& ctl,
+                                        uint32_t lanes, int half, int pair, bool mine, float m, float l, int rank,
+                                        volatile int* abort) {
+  static_assert(D / 4 * kWtJoinGroup + 8 * 1024 <= WtShape<D>::kStages * kWtStageBytes, "ring");
+  const int C = a.cluster, S = D / C, groups = S / 4;
+  float* lm = reinterpret_cast<float*>(ring + D / 4 * kWtJoinGroup);  // [source][l, m][pair]
+  // this CTA's ring is free: its products are done, and no copy is under way
+  wt_arrive_all(&ctl.join_free, C);
+  if (!wt_wait_cluster(&ctl.join_free, abort)) return;
+#pragma unroll 1
+  for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
+    if (w.n_blk == 0) break;  // m says so
+    uint32_t o[8];
+    wt_tmem_ld8(lanes + c, o);
+    const int to = c / S;
+    const uint32_t at = map_shared_rank(ring + (rank * groups + (c - to * S) / 4) * kWtJoinGroup + pair * 16, to);
+    if (mine) {
+      asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                   "r"(o[3])
+                   : "memory");
+      asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kWtJoinGroup), "r"(o[4]), "r"(o[5]),
+                   "r"(o[6]), "r"(o[7])
+                   : "memory");
+    }
+  }
+  for (int to = half; to < C; to += 2) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_shared_rank(lm + rank * 256 + pair, to)), "f"(l) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_shared_rank(lm + rank * 256 + 128 + pair, to)), "f"(m)
+                 : "memory");
+  }
+  wt_arrive_all(&ctl.join_full, C);
+  if (!wt_wait_cluster(&ctl.join_full, abort)) return;
+  const float ninf = -__int_as_float(0x7f800000);
+  const int vecs = S / 8, n = w.rows * a.group * vecs;  // 8 columns a thread, a row's next to each other
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const int p = i / vecs, v = i - p * vecs;
+    float mx = ninf, ls = 0.f, acc[8] = {};
+    for (int s = 0; s < C; ++s) mx = fmaxf(mx, lm[s * 256 + 128 + p]);
+    for (int s = 0; s < C; ++s) {
+      const float ms = lm[s * 256 + 128 + p], l_s = lm[s * 256 + p];
+      if (l_s == 0.f) continue;  // nothing seen: the sums may hold anything
+      const float f = ms == mx ? 1.f : ka_ex2((ms - mx) * a.c);
+      ls = fmaf(f, l_s, ls);
+      const unsigned char* src = ring + (s * groups + 2 * v) * kWtJoinGroup + p * 16;
+      const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + kWtJoinGroup);
+      acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]);
+      acc[2] = fmaf(f, x.z, acc[2]), acc[3] = fmaf(f, x.w, acc[3]);
+      acc[4] = fmaf(f, y.x, acc[4]), acc[5] = fmaf(f, y.y, acc[5]);
+      acc[6] = fmaf(f, y.z, acc[6]), acc[7] = fmaf(f, y.w, acc[7]);
+    }
+    const float inv = ls == 0.f ? 0.f : 1.0f / ls;
+    uint32_t y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+      y[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    const int row = p / a.group;
+    const int64_t hq = (int64_t)(w.t0 + row) * a.h_q + (int64_t)w.g * a.group + (p - row * a.group);
+    *reinterpret_cast<uint4*>(a.out + hq * D + rank * S + v * 8) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (rank == 0 && v == 0 && a.lse != nullptr)
+      a.lse[hq] = ls == 0.f ? ninf : mx == ninf ? ls : fmaf(mx, a.c, log2f(ls)) * 0.69314718055994531f;
+  }
 }
 
 template <int D>
@@ -311,6 +544,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (warp == 10 && lane < 3) wt_prefetch(lane == 0 ? &q_map : lane == 1 ? &k_map : &v_map);
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kStages; ++i) {
       mbar_init(&ctl.full[i], 1);
@@ -329,6 +563,8 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
     mbar_init(&ctl.q_full, 1);
     mbar_init(&ctl.q_empty, 1);
     mbar_init(&ctl.drain, 1);
+    mbar_init(&ctl.join_free, 8 * a.cluster);
+    mbar_init(&ctl.join_full, 8 * a.cluster);
     ctl.abort = 0;
     fence_mbar_init();
   }
@@ -336,42 +572,57 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
+  const int n_cta = a.cluster, rank = n_cta > 1 ? (int)cluster_ctarank() : 0;
+  bool met = n_cta == 1;  // the cluster's CTAs all run
+  if (n_cta > 1) wt_cluster_arrive();
 
   if (warp == 10) {
     // ---- tiles and Q ---------------------------------------------------------------
-    const int units = a.tile_slots * a.h_kv;
+    const bool exact = a.n_req <= kWtExactReq;
+    int before = 0;
+    const int units = (exact ? wt_count(a, before) : a.tile_slots) * a.h_kv;
+    // whole rounds of units, then a last one: shared by the clusters if there are enough
+    const int grid = gridDim.x, whole = units / grid * grid;
+    const bool share = n_cta > 1 && (units - whole) * n_cta <= grid;
     int k = 0, nq = 0;  // tiles published, Q copies
-    bool ok = true;
-    for (int u = blockIdx.x; ok; u += gridDim.x) {
-      WtTile w{};
-      if (u < units) {
-        w = wt_tile(a, u / a.h_kv);
-        if (w.rows == 0) continue;
-        w.g = u % a.h_kv;
-      } else {
-        w.rows = -1;
-      }
+    auto publish = [&](const WtTile& w) -> bool {
       const int sl = k % kWtTileRing;
-      if (k >= kWtTileRing && lane == 0) ok = tm_wait(&ctl.tile_empty[sl], (uint32_t)(k / kWtTileRing - 1) & 1u, abort);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (!ok) break;
+      if (k >= kWtTileRing && !wt_wait(&ctl.tile_empty[sl], (uint32_t)(k / kWtTileRing - 1) & 1u, abort)) return false;
       if (lane == 0) {
         ctl.tile[sl] = w;
         mbar_arrive(&ctl.tile_full[sl]);
       }
       ++k;
-      if (w.rows < 0) break;
-      if (w.n_blk > 0 && lane == 0) {
-        if (nq > 0) ok = tm_wait(&ctl.q_empty, (uint32_t)(nq - 1) & 1u, abort);
-        if (ok) {
-          // boxes of `rows` x `group` x 64; what of the 128 rows they leave is never used
-          mbar_arrive_expect_tx(&ctl.q_full, (uint32_t)(a.rows * a.group * D * 2));
-          for (int h = 0; h < D / 64; ++h)
-            wt_tma_3d(q_buf + h * kQHalf, &q_map, h * 64, w.g * a.group, w.t0, &ctl.q_full);
-        }
+      return true;
+    };
+    bool ok = true, end = false;
+    for (int u = blockIdx.x; ok && !end; u += grid) {
+      end = u >= whole;  // the last round
+      const bool part = share && end;
+      const int v = part ? whole + (int)blockIdx.x / n_cta : u;
+      if (v >= units) break;
+      int i = v / a.h_kv;  // the tile's number, then its number in the request
+      const int req = exact ? wt_find(a, before, i) : wt_find_slot(a, i, i);
+      if (req < 0) continue;
+      WtTile w = wt_tile(a, req, i, part ? n_cta : 1, part ? rank : 0);
+      w.g = v % a.h_kv;
+      ok = publish(w);
+      if (!ok) break;
+      if (w.n_blk > 0) {
+        ok = nq == 0 || wt_wait(&ctl.q_empty, (uint32_t)(nq - 1) & 1u, abort);
+        if (!ok) break;
+        // boxes of `rows` x `group` x 64; what of the 128 rows they leave is never used
+        wt_expect(&ctl.q_full, (uint32_t)(a.rows * a.group * D * 2));
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          wt_tma_3d(q_buf + h * kQHalf, &q_map, h * 64, w.g * a.group, w.t0, &ctl.q_full);
+        ++nq;
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (w.n_blk > 0 && ok) ++nq;
+    }
+    if (ok) {
+      WtTile none{};
+      none.rows = -1;
+      publish(none);
     }
     if (lane == 0 && nq > 0) mbar_wait_bounded(&ctl.q_full, (uint32_t)(nq - 1) & 1u, 20000000ull);
   } else if (warp == 8 || warp == 11) {
@@ -394,7 +645,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       auto lookup = [&](int blk) -> int {
         const int j = blk * per + lane;
         if (blk >= w.n_blk || lane >= per || j >= w.n_box) return 0;
-        const int e = j << sh;
+        const int e = (w.j0 + j) << sh;
         const int pos = e < w.nsr ? e : w.start + (e - w.nsr);
         const int pi = pos / a.page_size;
         const int64_t page = __ldg(pt + pi);
@@ -420,21 +671,18 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         for (int i = 0; ok && i < n_st; ++i, ++at) {
           const int st = at % Sh::kStages;
           const int b0 = is_k ? 0 : i * per_st, n = is_k ? nb : min(per_st, nb - b0);
-          if (at >= Sh::kStages && lane == 0) ok = tm_wait(&ctl.empty[st], (uint32_t)(at / Sh::kStages - 1) & 1u, abort);
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          ok = at < Sh::kStages || wt_wait(&ctl.empty[st], (uint32_t)(at / Sh::kStages - 1) & 1u, abort);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], (uint32_t)n * box_bytes);
-          __syncwarp();
-          const int y = __shfl_sync(0xffffffffu, row, (b0 + lane) & 31);
-          if (lane < n)
-            wt_tma_4d(ring + st * kWtStageBytes + lane * box_bytes, map,
-                      w.g * (D / 64) + (is_k ? i * 2 : 0), y, &ctl.full[st]);
+          wt_expect(&ctl.full[st], (uint32_t)n * box_bytes);
+          for (int j = 0; j < n; ++j)
+            wt_tma_4d(ring + st * kWtStageBytes + j * box_bytes, map, w.g * (D / 64) + (is_k ? i * 2 : 0),
+                      __shfl_sync(0xffffffffu, row, b0 + j), &ctl.full[st]);
           done = at + 1;
         }
       }
       gb += w.n_blk;
       if (w.n_blk > 0) {
-        const int last = w.n_box * B - (w.n_blk - 1) * N;  // rows copied for the last block
+        const int last = min(N, w.n_box * B - (w.n_blk - 1) * N);  // rows copied for the last block
         rs += Sh::kKs * w.n_blk + (w.n_blk - 1) * Sh::kVs + (last + Sh::kVRows - 1) / Sh::kVRows;
       }
     }
@@ -451,7 +699,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
     const uint64_t q_desc = umma_desc_sw128(smem_u32(q_buf)), k_desc0 = umma_desc_sw128(smem_u32(ring), Sh::kKGroup),
                    v_desc0 = wt_desc_mn(smem_u32(ring), Sh::kVGroup);
     auto add = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };  // stays inside the address field
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, tm_wait(bar, parity, abort)); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wt_wait(bar, parity, abort); };
     int gb = 0, nq = 0;          // blocks and Q copies so far
     int st = 0;                  // next ring stage and its parity
     uint32_t ph = 0;
@@ -475,10 +723,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         for (int i = 0; i < Sh::kKs; ++i) {
           if (!wait(&ctl.full[st], ph)) return false;
           const uint64_t kd = add(k_desc0, st * kWtStageBytes), qd = add(q_desc, i * 2 * kQHalf);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            wt_mma_ss(d, add(qd, (c >> 2) * kQHalf + (c & 3) * 32), add(kd, (c >> 2) * 1024 + (c & 3) * 32), idesc,
-                      i > 0 || c > 0 ? 1u : 0u);
+          wt_mma_qk(d, qd, kd, idesc, i > 0 ? 1u : 0u);
           next_stage();
         }
         wt_commit(&ctl.s_full[sl]);
@@ -498,9 +743,9 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
           const int steps = min(Sh::kVRows, n - e0) / 16;  // none for rows past the last key
           const uint32_t first = blk > 0 || e0 > 0 ? 1u : 0u;
 #pragma unroll
-          for (int c = 0; c < Sh::kVRows / 16; ++c)
-            if (c < steps)
-              wt_mma_ts(tmem, p + c * 8, add(vd, c * 2 * Sh::kVGroup), kIdescO, c > 0 ? 1u : first);
+          for (int c = 0; c < Sh::kVRows / 16; c += 4)
+            wt_mma_pv<(2 * Sh::kVGroup >> 4)>(tmem, p + c * 8, add(vd, c * 2 * Sh::kVGroup), kIdescO,
+                                              c > 0 ? 1u : first, steps - c);
           next_stage();
         }
         wt_commit(&ctl.pv_done[sl]);
@@ -527,28 +772,31 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
     auto meet = [&]() -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(pair_bar);
-      const bool ok = __all_sync(0xffffffffu, tm_wait(pair_bar, (uint32_t)n_pair & 1u, abort));
+      const bool ok = wt_wait(pair_bar, (uint32_t)n_pair & 1u, abort);
       ++n_pair;
       return ok;
     };
-    bool ok = true;
+    bool ok = true, shared = false;
+    float m = ninf, l = 0.f;
+    WtTile w;
     for (int k = 0; ok; ++k) {
-      WtTile w;
       if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
       const bool mine = row < w.rows;
       const int64_t t = w.t0 + row;
       int L = mine ? __ldg(a.row_len + t) : 0;
       if (L < 0 || L > a.max_len) L = 0;
       const int64_t hq = t * a.h_q + (int64_t)w.g * a.group + hd;
-      float m = ninf, l = 0.f;
-      // the pair sees entries [0, va) and [vb, vc)
-      const int va = min(a.n_sink, L);
-      const int vb = L > 0 ? w.nsr + max(0, L - a.window) - w.start : 0;
-      const int vc = L > 0 ? w.nsr + L - w.start : 0;
+      m = ninf;
+      l = 0.f;
+      // the pair sees entries [0, va) and [vb, vc) of the part
+      const int part0 = w.j0 << a.box_shift;
+      const int va = min(a.n_sink, L) - part0;
+      const int vb = (L > 0 ? w.nsr + max(0, L - a.window) - w.start : 0) - part0;
+      const int vc = (L > 0 ? w.nsr + L - w.start : 0) - part0;
       for (int blk = 0; blk < w.n_blk; ++blk) {
         const int x = gb + blk, sl = x & 1;
         const int e0 = blk * N;
-        ok = __all_sync(0xffffffffu, tm_wait(&ctl.s_full[sl], (uint32_t)(x >> 1) & 1u, abort));
+        ok = wt_wait(&ctl.s_full[sl], (uint32_t)(x >> 1) & 1u, abort);
         if (!ok) break;
         tc_fence_after();
         const uint32_t bad = ctl.bad[x % kWtBadRing];
@@ -584,7 +832,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         const bool grow = m != ninf && mx > m + thr;
         if (__any_sync(0xffffffffu, grow)) {
           // O holds every product before this block's
-          ok = __all_sync(0xffffffffu, tm_wait(&ctl.pv_done[sl ^ 1], (uint32_t)((x - 1) >> 1) & 1u, abort));
+          ok = wt_wait(&ctl.pv_done[sl ^ 1], (uint32_t)((x - 1) >> 1) & 1u, abort);
           if (!ok) break;
           tc_fence_after();
           const float f = m != ninf && mx > m ? ka_ex2((m - mx) * a.c) : 1.0f;
@@ -621,7 +869,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
           const int at = rs + Sh::kKs * min(blk + 2, w.n_blk) + blk * Sh::kVs;  // V's first stage
           for (int v = 0; ok && v * Sh::kVRows < n16; ++v) {
             const int st = (at + v) % Sh::kStages;
-            ok = __all_sync(0xffffffffu, tm_wait(&ctl.full[st], (uint32_t)((at + v) / Sh::kStages) & 1u, abort));
+            ok = wt_wait(&ctl.full[st], (uint32_t)((at + v) / Sh::kStages) & 1u, abort);
             if (!ok) break;
             unsigned char* vst = ring + st * kWtStageBytes;
             const int rows = min(Sh::kVRows, n16 - v * Sh::kVRows);
@@ -641,7 +889,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       if (!ok) break;
       gb += w.n_blk;
       if (w.n_blk > 0) {
-        const int last = w.n_box * a.box - (w.n_blk - 1) * N;  // rows copied for the last block
+        const int last = min(N, w.n_box * a.box - (w.n_blk - 1) * N);  // rows copied for the last block
         rs += Sh::kKs * w.n_blk + (w.n_blk - 1) * Sh::kVs + (last + Sh::kVRows - 1) / Sh::kVRows;
       }
       // ---- outputs ---------------------------------------------------------------------
@@ -653,61 +901,63 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         l += ctl.mx[gb & 1][half ^ 1][pair];
         ok = meet();  // read, before the next tile's first maxima
         if (!ok) break;
-        ok = __all_sync(0xffffffffu, tm_wait(&ctl.pv_done[(gb - 1) & 1], (uint32_t)((gb - 1) >> 1) & 1u, abort));
+        ok = wt_wait(&ctl.pv_done[(gb - 1) & 1], (uint32_t)((gb - 1) >> 1) & 1u, abort);
         if (!ok) break;
         tc_fence_after();
         inv = l == 0.f ? 0.f : 1.0f / l;
       }
-      // 32 columns at a time: 4 pieces of 16 bytes a lane, transposed over the
-      // quad so that its lanes write 64 consecutive bytes of one row (written
-      // a row a lane, every store met 32 lines: 4,000 clocks a tile)
-      const int sub = lane & 3;
-      uint16_t* dst = a.out + hq * D;
+      shared = w.parts > 1;
+      if (shared) break;  // the cluster's last tile, and this CTA's
+      // 32 columns at a time: two pieces of 32 bytes a lane, exchanged with the
+      // next lane so that the two write 64 consecutive bytes of a row (written
+      // a row a lane, 16 bytes each, every store met 32 lines: 4,000 clocks a tile)
+      const bool odd = (lane & 1) != 0;
+      const uint32_t keep = l == 0.f ? 0u : ~0u;  // a row that sees nothing: zeros, whatever the sums hold
+      const long long own = mine ? (long long)(hq * D) + half * (D / 2) : -1ll;
+      const long long at0 = __shfl_sync(0xffffffffu, own, lane & ~1), at1 = __shfl_sync(0xffffffffu, own, lane | 1);
 #pragma unroll 1
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+      for (int c = 0; c < D / 2; c += 32) {
         uint32_t o[32];
         if (w.n_blk > 0) {
-          wt_tmem_ld32(lanes + c, o);
+          wt_tmem_ld32(lanes + half * (D / 2) + c, o);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = 0u;
         }
-        uint32_t y[4][4];  // [piece][word]
+        uint32_t y[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          // a row that sees nothing writes zeros, whatever the accumulator holds
-          const float x0 = l == 0.f ? 0.f : __uint_as_float(o[2 * j]) * inv;
-          const float x1 = l == 0.f ? 0.f : __uint_as_float(o[2 * j + 1]) * inv;
-          const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
-          y[j >> 2][j & 3] = *reinterpret_cast<const uint32_t*>(&b);
+          const __nv_bfloat162 b =
+              __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+          y[j] = *reinterpret_cast<const uint32_t*>(&b) & keep;
         }
-        // y[p] of lane q <-> y[q] of lane p
 #pragma unroll
-        for (int d = 1; d <= 2; d <<= 1)
-#pragma unroll
-          for (int p = 0; p < 4; ++p)
-            if ((p & d) == 0)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const bool up = (sub & d) != 0;
-                const uint32_t give = up ? y[p][j] : y[p | d][j];
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, d);
-                if (up) y[p][j] = got;
-                else y[p | d][j] = got;
-              }
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {  // row of the quad's lane p, piece `sub`
-          const int64_t at = __shfl_sync(0xffffffffu, mine ? (long long)(dst - a.out) : -1ll, (lane & ~3) | p);
-          if (at >= 0)
-            *reinterpret_cast<uint4*>(a.out + at + c + sub * 8) = make_uint4(y[p][0], y[p][1], y[p][2], y[p][3]);
+        for (int j = 0; j < 8; ++j) {  // the even lane's second piece <-> the odd lane's first
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? y[j] : y[8 + j], 1);
+          if (odd) y[j] = got;
+          else y[8 + j] = got;
         }
+        const int piece = c + (odd ? 16 : 0);
+        if (at0 >= 0) wt_store32(a.out + at0 + piece, y);
+        if (at1 >= 0) wt_store32(a.out + at1 + piece, y + 8);
       }
       tc_fence_before();
       if (mine && half == 0 && a.lse != nullptr)
         a.lse[hq] = l == 0.f ? ninf : (m == ninf ? l : (fmaf(m, a.c, log2f(l))) * 0.69314718055994531f);
     }
+    if (shared) {
+      if (!met) wt_cluster_wait();
+      met = true;
+      wt_join<D>(a, w, ring, ctl, lanes, half, pair, row < w.rows, m, l, rank, abort);
+    }
   }
 
+  // no CTA of the cluster leaves before all have written to each other
+  if (n_cta > 1) {
+    if (!met) wt_cluster_wait();
+    wt_cluster_arrive();
+    wt_cluster_wait();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
