@@ -154,6 +154,12 @@ __device__ __forceinline__ void wt_expect(uint64_t* bar, uint32_t bytes) {
       "r"(bytes)
       : "memory");
 }
+__device__ __forceinline__ void wt_arrive(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ void wt_prefetch(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -395,7 +401,7 @@ __device__ __forceinline__ bool wt_next_tile(WtCtl& ctl, int k, WtTile& w, volat
   if (!wt_wait(&ctl.tile_full[sl], (uint32_t)(k / kWtTileRing) & 1u, abort)) return false;
   w = ctl.tile[sl];
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.tile_empty[sl]);
+  wt_arrive(&ctl.tile_empty[sl]);
   return true;
 }
 
@@ -714,6 +720,11 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
     for (int k = 0; ok; ++k) {
       WtTile w;
       if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
+      // the same in all lanes, now known to be: the stage counter and the
+      // descriptors stay in uniform registers (76.5 -> 74.7 us, in a graph)
+      w.n_blk = __reduce_max_sync(0xffffffffu, w.n_blk);
+      w.n_box = __reduce_max_sync(0xffffffffu, w.n_box);
+      w.uc = __reduce_max_sync(0xffffffffu, w.uc);
       if (w.n_blk == 0) continue;
       auto n16 = [&](int blk) { return (min(N, w.uc - blk * N) + 15) & ~15; };
       auto qk = [&](int blk) -> bool {
@@ -727,7 +738,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
           next_stage();
         }
         wt_commit(&ctl.s_full[sl]);
-        if (lane == 0) mbar_arrive(&ctl.s_full[sl]);
+        wt_arrive(&ctl.s_full[sl]);
         if (blk + 1 == w.n_blk) wt_commit(&ctl.q_empty);
         return true;
       };
@@ -771,7 +782,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
     // both warps of the pair have written what comes before
     auto meet = [&]() -> bool {
       __syncwarp();
-      if (lane == 0) mbar_arrive(pair_bar);
+      wt_arrive(pair_bar);
       const bool ok = wt_wait(pair_bar, (uint32_t)n_pair & 1u, abort);
       ++n_pair;
       return ok;
@@ -884,7 +895,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_full[sl]);
+        wt_arrive(&ctl.p_full[sl]);
       }
       if (!ok) break;
       gb += w.n_blk;
