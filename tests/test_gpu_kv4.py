@@ -516,6 +516,109 @@ def test_window_attn_offsets_past_32_bits(qsa, rows):
     assert torch.equal(out, want) and torch.equal(lse, want_l)
 
 
+@pytest.mark.parametrize("h_q,h_kv,d,page", [(16, 2, 256, 64), (16, 4, 128, 16), (5, 1, 256, 24), (16, 16, 128, 64)])
+@pytest.mark.parametrize("window,n_sink", [(1024, 4), (4000, 0), (700, 200)])
+def test_window_attn_shared_tiles(qsa, h_q, h_kv, d, page, window, n_sink):
+    """A few requests of a few rows: the CTAs of a cluster share each tile,
+    also those of rows too short to give all of them a part, and of no tokens."""
+    rng = np.random.default_rng(window + h_q + d)
+    window_check(qsa, rng, [list(range(4495, 4501))], page, h_q, h_kv, d, window, n_sink, False, spare_rows=2)
+    window_check(qsa, rng, [[7, 0, 8], [0, 0, 0], [], list(range(2995, 3001)), [1], [129, 130]], page, h_q, h_kv, d,
+                 window, n_sink, False, spare_rows=2)
+    window_check(qsa, rng, [[900 + 37 * r, 0, 901 + 37 * r] for r in range(20)], page, h_q, h_kv, d, window, n_sink, False)
+
+
+def test_window_attn_shared_tiles_of_poisoned_and_missing_pages(qsa):
+    """As test_window_attn_masked_positions_have_no_effect and
+    test_window_attn_bad_pages_are_skipped_and_flagged, in shared tiles."""
+    rng = np.random.default_rng(40)
+    window, n_sink, ctx, page, d = 1000, 70, 1800, 64, 256
+
+    def poison(pt, cache):
+        seen = set()
+        for length in range(ctx - 5, ctx + 1):
+            seen |= set(ref.slots_of(pt[0], ref.window_positions(length, window, n_sink), page).tolist())
+        hide = np.array([s for s in range(cache[0].shape[0]) if s not in seen])
+        for c in cache:
+            c[hide[0::3]], c[hide[1::3]], c[hide[2::3]] = 0x7F80, 0xFF80, 0x7FC0  # inf, -inf, NaN
+        return cache
+
+    window_check(qsa, rng, [list(range(ctx - 5, ctx + 1))], page, 8, 1, d, window, n_sink, False, cache=poison)
+    pt, n_slots = page_table(rng, [ctx], page)
+    k, v, q = (normal_bf16(rng, s) for s in ((n_slots, 1, d), (n_slots, 1, d), (6, 8, d)))
+    bad = pt.copy()
+    bad[0, 1], bad[0, 20], bad[0, 28] = n_slots // page, -7, 2**31 - 1
+    lens = np.arange(ctx - 5, ctx + 1).astype(np.int32)
+    out, lse = qsa.window_attn(*map(bf16_dev, (q, k, v)), to_dev(np.array([0, 6], np.int32)), to_dev(lens), to_dev(bad),
+                               page, ctx, window, n_sink)
+    assert qsa.device_status(clear=True) == 1
+    kf, vf = ref.bf16_to_f64(k), ref.bf16_to_f64(v)
+    for t in range(6):
+        pos = ref.window_positions(lens[t], window, n_sink)
+        pos = pos[~np.isin(pos // page, [1, 20, 28])]
+        sl = ref.slots_of(pt[0], pos, page)
+        ro, rl, a, big, spread = ref.attend(ref.bf16_to_f64(q[t]), kf[sl], vf[sl], d ** -0.5)
+        tol, tol_l = ref.tolerance(d, pos.size, ro, a, big, spread, W_BF16, BF16_HALF_STEP, False, 0.0)
+        assert (np.abs(bits_to_f64(out)[t] - ro) <= tol).all(), t
+        assert (np.abs(host(lse)[t] - rl) <= tol_l + 2.0 ** -23 * np.abs(rl)).all()
+
+
+@pytest.mark.parametrize("n_req", [33, 1024, 1025, 1400])
+def test_window_attn_many_requests(qsa, n_req):
+    """Requests of 0 to 3 rows; the tiles are found by counting up to 1,024
+    requests, by a search from there on."""
+    rng = np.random.default_rng(n_req)
+    lens = [rng.integers(0, 60, rng.integers(0, 4)).tolist() for _ in range(n_req)]
+    lens[n_req // 2] = list(range(20, 60))
+    window_check(qsa, rng, lens, 16, 4, 1, 128, 20, 2, False, spare_rows=1)
+
+
+@pytest.mark.parametrize("n_req", [300, 1100])
+def test_window_attn_many_tiles_of_no_tokens(qsa, n_req):
+    """Tiles without a block of entries between tiles with some."""
+    rng = np.random.default_rng(n_req + 1)
+    lens = [[0] * 5 if r % 50 else [3, 0, 200, 201] for r in range(n_req)]
+    window_check(qsa, rng, lens, 64, 8, 4, 128, 64, 1, False)
+
+
+@pytest.mark.parametrize("scale", [-0.07, 0.0, -30.0, 1e-20])
+@pytest.mark.parametrize("rows", [1, 6, 40])
+@pytest.mark.parametrize("fp4", [False, True])
+def test_window_attn_scales(qsa, fp4, rows, scale):
+    rng = np.random.default_rng(41 + rows)
+    lens = [list(range(300 - rows, 300))]
+    window_check(qsa, rng, lens, 32, 8, 2, 128, 150, 3, fp4, scale=scale)
+
+
+@pytest.mark.parametrize("d,h_kv", [(256, 2), (128, 4)])
+def test_window_attn_single_rows_keep_both_parts_of_the_weights(qsa, d, h_kv):
+    """One row a request: the weights are held as a BF16 and its remainder."""
+    rng = np.random.default_rng(42)
+    window_check(qsa, rng, [[700], [33], [1], [0], [2000]], 16, 16, h_kv, d, 900, 4, False, weight_eps=W_BF16X2)
+
+
+def test_graphs_sharing_a_workspace(qsa):
+    """Two captured graphs that split long rows over the same workspace, in
+    turn on one stream."""
+    import torch
+    rng = np.random.default_rng(43)
+    arrays = list(map(to_dev, (*random_cache4(rng, 4000, 1, 128), *random_cache4(rng, 4000, 1, 128))))
+    q = [bf16_dev(normal_bf16(rng, (2, 8, 128))) for _ in range(2)]
+    slots = [to_dev(rng.integers(0, 4000, (2, n)).astype(np.int32)) for n in (20000, 12000)]
+    need = max(qsa.lib().qsa_sparse_attn_fp4_workspace_size(2, 8, 1, 128, s.shape[1]) for s in slots)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = [[t.clone() for t in qsa.sparse_attn_fp4(q[i], *arrays, slots[i])] for i in range(2)]
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            outs.append(qsa.sparse_attn_fp4(q[i], *arrays, slots[i], workspace=ws))
+    for i in (0, 1, 1, 0, 1, 0):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for got, exp in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(got, exp))
+
 def test_cache4_offsets_past_32_bits(qsa):
     """Append, read back and attend at the far end of a 4-bit cache whose
     codes take more than 2^32 bytes."""

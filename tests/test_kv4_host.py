@@ -20,6 +20,7 @@ def L():
 FAKE = ctypes.c_void_p(0x1000)
 ODD = ctypes.c_void_p(0x1010)  # 16-byte but not 32-byte aligned
 BAD = ctypes.c_void_p(0x1002)
+FAKE_16 = ctypes.c_void_p(0x1010)  # 16-byte aligned, not 32
 F = ctypes.c_float
 
 
@@ -148,9 +149,9 @@ def test_workspace_sizes(L):
 
 def window(L, fp4=False, q=FAKE, ld_q=4096, k=FAKE, v=FAKE, ks=FAKE, vs=FAKE, n_slots=256, n_req=1, start=FAKE,
            n_rows=1, row_len=FAKE, max_len=200, max_rows=1, h_q=16, h_kv=2, d=256, pt=FAKE, ld_pt=4, page=64, window=50,
-           n_sink=2, gk=1.0, gv=1.0, out=FAKE, lse=None, ws=None, ws_bytes=0):
+           n_sink=2, gk=1.0, gv=1.0, out=FAKE, lse=None, ws=None, ws_bytes=0, scale=0.1):
     rest = (n_slots, n_req, start, n_rows, row_len, max_len, max_rows, h_q, h_kv, d, pt, ld_pt, page, window, n_sink,
-            F(0.1))
+            F(scale))
     if fp4:
         return L.qsa_window_attn_fp4(q, ld_q, k, ks, v, vs, *rest, F(gk), F(gv), out, lse, ws, ws_bytes, None)
     return L.qsa_window_attn(q, ld_q, k, v, *rest, out, lse, ws, ws_bytes, None)
@@ -166,6 +167,17 @@ def window(L, fp4=False, q=FAKE, ld_q=4096, k=FAKE, v=FAKE, ks=FAKE, vs=FAKE, n_
     (dict(max_len=90000, ld_pt=2000, window=80000), -3), (dict(n_rows=0, q=None), 0)])
 def test_window_attn_refusals(L, fp4, change, status):
     assert window(L, fp4, **change) == status
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_window_attn_refuses_a_scale_that_is_not_finite(L, fp4, scale):
+    assert window(L, fp4, scale=scale) == -1
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_window_attn_refuses_outputs_off_a_32_byte_boundary(L, fp4):
+    assert window(L, fp4, out=FAKE_16) == -1
 
 
 def test_window_attn_fp4_refuses_other_scales(L):
