@@ -27,16 +27,15 @@ struct KaKernel {
   void (*fn)(KvAttnArgs);
   int threads;
   size_t smem;
-  int slots;    // resident CTAs of the GPU (152 SMs)
   int entries;  // entries of a CTA per step
 };
 template <int D, int NT>
 constexpr KaKernel ka_bf16() {
-  return {kv_attn_kernel<D, NT>, kKaThreads, ka_smem_bytes<D, NT>(), 152 * KaShape<D>::kCtas, kKaTile * kKaWarps};
+  return {kv_attn_kernel<D, NT>, kKaThreads, ka_smem_bytes<D, NT>(), kKaTile * kKaWarps};
 }
 template <int D, int NT, bool kWindow>
 constexpr KaKernel ka_fp4() {
-  return {kv4_attn_kernel<D, NT, kWindow>, kK4Threads, k4_smem_bytes<D, NT>(), 152 * 2, kK4Step * kK4Warps};
+  return {kv4_attn_kernel<D, NT, kWindow>, kK4Threads, k4_smem_bytes<D, NT>(), kK4Step * kK4Warps};
 }
 // [cache: BF16 window, 4-bit window, 4-bit list][D = 128 with up to 8 heads, up to 16, D = 256]
 const KaKernel kKaKernels[3][3] = {
@@ -52,24 +51,78 @@ bool set_ka_smem() {
   return true;
 }
 
-// Per-device one-time set-up: the shared-memory opt-in of the kernels.
-// Gives the device's SM count.
-int g_sms[kMaxDevices];
+// A launch of clusters of c CTAs along x (c = 1: without the attribute).
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr = {};
+  ClusterLaunch(dim3 grid, int threads, size_t smem, int c, cudaStream_t stream) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)c;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = c > 1 ? 1 : 0;
+  }
+  ClusterLaunch(const ClusterLaunch&) = delete;
+};
+
+// Per-device one-time set-up: the shared-memory opt-in of the kernels, and
+// how many of their clusters run at once.
+constexpr int kWtMaxCluster = 8;
+struct KvDevice {
+  int sms;                             // 0: not set up
+  int ka[3][3][kKaMaxCluster + 1];     // clusters of c CTAs at once
+  int wt[2][kWtMaxCluster + 1];        // D = 128, D = 256
+};
+KvDevice g_kv_dev[kMaxDevices];
 std::mutex g_mu;
-qsa_status kv_device_ready(int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QSA_ERR_CUDA;
-  std::lock_guard<std::mutex> lk(g_mu);
-  *sms = g_sms[dev];
-  if (*sms > 0) return QSA_OK;
+
+template <class F>
+bool resident_clusters(F fn, int threads, size_t smem, int c, int sms, int* n) {
+  if (c == 1) {  // without the attribute
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, fn, threads, smem) != cudaSuccess) return false;
+    *n *= sms;
+  } else {
+    ClusterLaunch l(dim3((unsigned)c), threads, smem, c, nullptr);
+    if (cudaOccupancyMaxActiveClusters(n, fn, &l.cfg) != cudaSuccess) return false;
+  }
+  return *n > 0;
+}
+
+bool set_up(KvDevice& d, int sms) {
   if (!set_ka_smem() ||
       cudaFuncSetAttribute(window_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, wt_smem_bytes<128>()) != cudaSuccess ||
-      cudaFuncSetAttribute(window_tc_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, wt_smem_bytes<256>()) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return QSA_ERR_CUDA;
+      cudaFuncSetAttribute(window_tc_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, wt_smem_bytes<256>()) != cudaSuccess)
+    return false;
+  for (int i = 0; i < 9; ++i) {
+    const KaKernel& k = kKaKernels[i / 3][i % 3];
+    for (int c = 1; c <= kKaMaxCluster; ++c)
+      if (!resident_clusters(k.fn, k.threads, k.smem, c, sms, &d.ka[i / 3][i % 3][c])) return false;
   }
-  g_sms[dev] = *sms;
+  for (int c = 1; c <= kWtMaxCluster; c *= 2)
+    if (!resident_clusters(window_tc_kernel<128>, kWtThreads, wt_smem_bytes<128>(), c, sms, &d.wt[0][c]) ||
+        !resident_clusters(window_tc_kernel<256>, kWtThreads, wt_smem_bytes<256>(), c, sms, &d.wt[1][c]))
+      return false;
+  return true;
+}
+
+qsa_status kv_device(const KvDevice** out) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QSA_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_mu);
+  KvDevice& d = g_kv_dev[dev];
+  if (d.sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !set_up(d, sms)) {
+      cudaGetLastError();
+      return QSA_ERR_CUDA;
+    }
+    d.sms = sms;
+  }
+  *out = &d;
   return QSA_OK;
 }
 
@@ -99,11 +152,14 @@ int ka_groups(int64_t units, int64_t entries) {
 }
 
 // CTAs per cluster: the least of waves * (steps + start and end, about 4).
-int ka_cluster(int64_t units, int64_t entries, const KaKernel& k) {
+// How many clusters run at once is the device's answer: on 152 SMs, 16
+// clusters of 7 do not where a CTA fills an SM (1,028 entries of D = 256: 23.7
+// us, in clusters of 6, which do, 17.6).
+int ka_cluster(int64_t units, int64_t entries, const KaKernel& k, const int* resident) {
   int best = 1;
   int64_t least = INT64_MAX;
   for (int c = 1; c <= kKaMaxCluster; ++c) {
-    const int64_t waves = (units * c + k.slots - 1) / k.slots;
+    const int64_t waves = (units + resident[c] - 1) / resident[c];
     const int64_t steps = (entries + (int64_t)k.entries * c - 1) / ((int64_t)k.entries * c);
     const int64_t cost = waves * (steps + 4);
     if (cost < least) {
@@ -119,27 +175,18 @@ enum { kKaBf16Window = 0, kKaFp4Window = 1, kKaFp4List = 2 };
 qsa_status launch_ka(int cache, KvAttnArgs& a, int d, int64_t entries, void* workspace, cudaStream_t stream) {
   const int64_t units = (int64_t)a.n_rows * a.h_kv;
   a.group = a.h_q / a.h_kv;
-  const KaKernel& k = kKaKernels[cache][d == 256 ? 2 : a.group > 8 ? 1 : 0];
+  const int shape = d == 256 ? 2 : a.group > 8 ? 1 : 0;
+  const KaKernel& k = kKaKernels[cache][shape];
+  const KvDevice* dev = nullptr;
+  if (qsa_status st = kv_device(&dev)) return st;
   a.n_group = ka_groups(units, entries);
-  a.cluster = a.n_group > 1 ? kKaMaxCluster : ka_cluster(units, entries, k);
+  a.cluster = a.n_group > 1 ? kKaMaxCluster : ka_cluster(units, entries, k, dev->ka[cache][shape]);
   a.part = static_cast<float*>(workspace);
   if ((int64_t)a.n_rows * std::max(a.cluster * a.n_group, a.h_q) > INT32_MAX) return QSA_ERR_UNSUPPORTED;
   if (entries > (1 << 30)) return QSA_ERR_UNSUPPORTED;  // entry indices stay clear of 2^31
-  int sms = 0;
-  if (qsa_status st = kv_device_ready(&sms)) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.n_rows * a.cluster * a.n_group), (unsigned)a.h_kv, 1);
-  cfg.blockDim = dim3((unsigned)k.threads, 1, 1);
-  cfg.dynamicSmemBytes = k.smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)a.cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k.fn, a);
+  const ClusterLaunch l(dim3((unsigned)((int64_t)a.n_rows * a.cluster * a.n_group), (unsigned)a.h_kv), k.threads, k.smem,
+                        a.cluster, stream);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, k.fn, a);
   if (e == cudaSuccess && a.n_group > 1)
     e = launch_pdl(d == 256 ? kv_attn_merge_kernel<256> : kv_attn_merge_kernel<128>,
                    dim3((unsigned)((int64_t)a.n_rows * a.h_q)), dim3((unsigned)d), 0, stream, a,
@@ -180,31 +227,45 @@ bool encode_q_map(CUtensorMap* m, const WtArgs& a, int d) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The tensor-core form of window_attn, for requests of more than kWtMinRows
-// rows on pages of whole 8-row groups; QSA_ERR_UNSUPPORTED where the other
-// form has to serve.
-constexpr int kWtMinRows = 1;
 // CTAs that share a tile, where there are few: a single tile of 9 blocks takes
 // 29.8 us on one CTA, 25.7 on two, 23.7 on four, 21.6 on eight, one of 33
-// blocks 68.7, 46.2, 33.9 and 27.7 (in a graph, with what it adds).  At most
-// 128 CTAs so, and 64 in clusters of eight: beyond that the clusters no longer
-// run at once (16 tiles of 9 blocks: 38.0 us in eights, 23.7 in fours).  From
-// 65 tiles on, one CTA a tile, launched without the cluster attribute: sharing
-// the last round's gained nothing (the 512 tiles of a 4,096-row chunk: 85 us
-// either way), and a cluster launch cost 1 us.  How many tiles there are is
-// known on the device only; the estimate takes requests of equal length.
-int wt_cluster(const WtArgs& a) {
+// blocks 68.7, 46.2, 33.9 and 27.7 (in a graph, with what it adds), as long as
+// all clusters run at once (16 tiles of 9 blocks: 38.0 us in eights, which do
+// not, 23.7 in fours).  From 65 tiles on, one CTA a tile, launched without the
+// cluster attribute: sharing the last round's gained nothing (the 512 tiles of
+// a 4,096-row chunk: 85 us either way), and a cluster launch cost 1 us.  How
+// many tiles there are is known on the device only; the estimate takes
+// requests of equal length.
+int wt_cluster(const WtArgs& a, const int* resident) {
   if (a.n_req > kWtExactReq) return 1;
   const int64_t per_req = ((int64_t)a.n_rows + a.n_req - 1) / a.n_req;
   const int64_t tiles = a.n_req * ((per_req + a.rows - 1) / a.rows) * a.h_kv;
   const int64_t blocks = (std::min<int64_t>(a.max_len, (int64_t)a.window + a.n_sink + a.rows) + kWtN - 1) / kWtN;
   int c = 1;
-  while (c < 8 && tiles * 2 * c <= (c < 4 ? 128 : 64) && blocks >= std::max(4, 2 * c)) c *= 2;
+  while (c < kWtMaxCluster && tiles <= std::min(64, resident[2 * c]) && blocks >= std::max(4, 2 * c)) c *= 2;
   return c;
 }
 
-qsa_status launch_window_tc(const KvAttnArgs& k, int d, int32_t max_rows_per_req, cudaStream_t stream) {
-  if (max_rows_per_req <= kWtMinRows || k.page_size % 8 != 0 || k.n_slots < 8) return QSA_ERR_UNSUPPORTED;
+// Where rows share a tile of keys the tensor cores win, except on little work,
+// where the form for single rows starts and ends sooner and spreads over more
+// SMs: of window 1,024 and D = 256, 2 KV heads (in a graph, single-row form
+// against this one) 1 request of 6 rows 14.5 against 22.7 us, 8 of 2 17.5
+// against 23.7, 8 of 4 21.6 against 23.7, 32 of 3 52 against 34, 32 of 6 75
+// against 34; of window 4,096 8 of 4 49 against 35; of window 128 8 of 6 13.4
+// against 19.6, 32 of 6 27.8 against 21.6.  The line is drawn through the
+// columns that the single rows would read of K, in one round of CTAs, for up
+// to 16 rows a request.
+constexpr int kWtFewRows = 16;
+constexpr int64_t kWtFewColumns = 20 << 20;
+bool wt_serves(const KvAttnArgs& k, int d, int32_t max_rows_per_req, int64_t entries) {
+  if (max_rows_per_req <= 1 || k.page_size % 8 != 0 || k.n_slots < 8) return false;
+  const int64_t units = (int64_t)k.n_rows * k.h_kv;
+  return max_rows_per_req > kWtFewRows || units > 152 * (256 / d) ||
+         units * d > kWtFewColumns / std::max<int64_t>(1, entries);
+}
+
+// The tensor-core form of window_attn; QSA_ERR_UNSUPPORTED where it cannot serve.
+qsa_status launch_window_tc(const KvAttnArgs& k, int d, cudaStream_t stream) {
   WtArgs a{};
   a.q = k.q;
   a.ld_q = k.ld_q;
@@ -233,26 +294,16 @@ qsa_status launch_window_tc(const KvAttnArgs& k, int d, int32_t max_rows_per_req
   a.lse = k.lse;
   const int64_t units = (int64_t)a.tile_slots * a.h_kv;
   if (units > (1 << 30) || k.max_len > (1 << 30)) return QSA_ERR_UNSUPPORTED;
-  int sms = 0;
-  if (qsa_status st = kv_device_ready(&sms)) return st;
+  const KvDevice* dev = nullptr;
+  if (qsa_status st = kv_device(&dev)) return st;
   CUtensorMap q_map, k_map, v_map;
   if (!encode_q_map(&q_map, a, d) || !encode_cache_map(&k_map, k.k, k.n_slots, (int64_t)k.h_kv * d, a.box, 2) ||
       !encode_cache_map(&v_map, k.v, k.n_slots, (int64_t)k.h_kv * d, a.box, d / 64))
     return QSA_ERR_UNSUPPORTED;
-  a.cluster = wt_cluster(a);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(units, sms / a.cluster) * a.cluster), 1, 1);
-  cfg.blockDim = dim3(kWtThreads, 1, 1);
-  cfg.dynamicSmemBytes = d == 256 ? wt_smem_bytes<256>() : wt_smem_bytes<128>();
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)a.cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, d == 256 ? window_tc_kernel<256> : window_tc_kernel<128>, a, q_map, k_map, v_map) !=
+  a.cluster = wt_cluster(a, dev->wt[d == 256]);
+  const ClusterLaunch l(dim3((unsigned)(std::min<int64_t>(units, dev->sms / a.cluster) * a.cluster)), kWtThreads,
+                        d == 256 ? wt_smem_bytes<256>() : wt_smem_bytes<128>(), a.cluster, stream);
+  if (cudaLaunchKernelEx(&l.cfg, d == 256 ? window_tc_kernel<256> : window_tc_kernel<128>, a, q_map, k_map, v_map) !=
       cudaSuccess) {
     cudaGetLastError();
     return QSA_ERR_CUDA;
@@ -483,8 +534,10 @@ qsa_status qsa_window_attn(const void* q, int64_t ld_q, const void* k_cache, con
   a.v = static_cast<const uint8_t*>(v_cache);
   a.scale = scale;
   a.v_g = 1.0f;
-  const qsa_status tc = launch_window_tc(a, head_dim, max_rows_per_req, static_cast<cudaStream_t>(stream));
-  if (tc != QSA_ERR_UNSUPPORTED) return tc;
+  if (wt_serves(a, head_dim, max_rows_per_req, entries)) {
+    const qsa_status tc = launch_window_tc(a, head_dim, static_cast<cudaStream_t>(stream));
+    if (tc != QSA_ERR_UNSUPPORTED) return tc;
+  }
   return launch_ka(kKaBf16Window, a, head_dim, entries, workspace, static_cast<cudaStream_t>(stream));
 }
 

@@ -581,6 +581,76 @@ def test_window_attn_many_tiles_of_no_tokens(qsa, n_req):
     window_check(qsa, rng, lens, 64, 8, 4, 128, 64, 1, False)
 
 
+@pytest.mark.parametrize("h_q,h_kv,d,page", [(16, 2, 256, 64), (5, 1, 256, 8), (8, 4, 128, 16), (16, 1, 128, 24),
+                                             (12, 1, 128, 128), (3, 3, 128, 40)])
+@pytest.mark.parametrize("window,n_sink", [(40, 4), (1, 0), (1, 1), (64, 0), (1000, 4), (33, 70)])
+def test_window_attn_edges_of_tiles(qsa, h_q, h_kv, d, page, window, n_sink):
+    """test_window_attn_edges in the form for requests of many rows."""
+    rng = np.random.default_rng(window * 7 + d + page + 1)
+    window_check(qsa, rng, EDGE_LENS, page, h_q, h_kv, d, window, n_sink, False, spare_rows=3, max_rows=17)
+
+
+@pytest.mark.parametrize("h_q,h_kv,d,page", [(16, 2, 256, 64), (16, 4, 128, 16), (5, 1, 256, 24), (16, 16, 128, 64)])
+@pytest.mark.parametrize("window,n_sink", [(1024, 4), (4000, 0), (700, 200)])
+def test_window_attn_shared_tiles_of_short_requests(qsa, h_q, h_kv, d, page, window, n_sink):
+    """test_window_attn_shared_tiles in the form for requests of many rows."""
+    rng = np.random.default_rng(window + h_q + d + 1)
+    window_check(qsa, rng, [list(range(4495, 4501))], page, h_q, h_kv, d, window, n_sink, False, 2, max_rows=17)
+    window_check(qsa, rng, [[7, 0, 8], [0, 0, 0], [], list(range(2995, 3001)), [1], [129, 130]], page, h_q, h_kv, d,
+                 window, n_sink, False, 2, max_rows=17)
+    window_check(qsa, rng, [[900 + 37 * r, 0, 901 + 37 * r] for r in range(20)], page, h_q, h_kv, d, window, n_sink,
+                 False, max_rows=17)
+
+
+@pytest.mark.parametrize("rows", [17, 24])
+def test_window_attn_shared_tiles_beside_poisoned_and_missing_pages(qsa, rows):
+    """test_window_attn_shared_tiles_of_poisoned_and_missing_pages at row
+    counts that the form for many rows serves."""
+    rng = np.random.default_rng(44 + rows)
+    window, n_sink, ctx, page, d = 1000, 70, 1800, 64, 256
+
+    def poison(pt, cache):
+        seen = set()
+        for length in range(ctx - rows + 1, ctx + 1):
+            seen |= set(ref.slots_of(pt[0], ref.window_positions(length, window, n_sink), page).tolist())
+        hide = np.array([s for s in range(cache[0].shape[0]) if s not in seen])
+        for c in cache:
+            c[hide[0::3]], c[hide[1::3]], c[hide[2::3]] = 0x7F80, 0xFF80, 0x7FC0  # inf, -inf, NaN
+        return cache
+
+    window_check(qsa, rng, [list(range(ctx - rows + 1, ctx + 1))], page, 8, 1, d, window, n_sink, False, cache=poison)
+    pt, n_slots = page_table(rng, [ctx], page)
+    k, v, q = (normal_bf16(rng, s) for s in ((n_slots, 1, d), (n_slots, 1, d), (rows, 8, d)))
+    bad = pt.copy()
+    bad[0, 1], bad[0, 20], bad[0, 28] = n_slots // page, -7, 2**31 - 1
+    lens = np.arange(ctx - rows + 1, ctx + 1).astype(np.int32)
+    out, lse = qsa.window_attn(*map(bf16_dev, (q, k, v)), to_dev(np.array([0, rows], np.int32)), to_dev(lens),
+                               to_dev(bad), page, ctx, window, n_sink)
+    assert qsa.device_status(clear=True) == 1
+    kf, vf = ref.bf16_to_f64(k), ref.bf16_to_f64(v)
+    for t in range(rows):
+        pos = ref.window_positions(lens[t], window, n_sink)
+        pos = pos[~np.isin(pos // page, [1, 20, 28])]
+        sl = ref.slots_of(pt[0], pos, page)
+        ro, rl, a, big, spread = ref.attend(ref.bf16_to_f64(q[t]), kf[sl], vf[sl], d ** -0.5)
+        tol, tol_l = ref.tolerance(d, pos.size, ro, a, big, spread, W_BF16, BF16_HALF_STEP, False, 0.0)
+        assert (np.abs(bits_to_f64(out)[t] - ro) <= tol).all(), t
+        assert (np.abs(host(lse)[t] - rl) <= tol_l + 2.0 ** -23 * np.abs(rl)).all()
+
+
+@pytest.mark.parametrize("n_req", [33, 1025])
+def test_window_attn_many_requests_of_few_rows_in_tiles(qsa, n_req):
+    rng = np.random.default_rng(n_req + 2)
+    lens = [rng.integers(0, 60, rng.integers(0, 4)).tolist() for _ in range(n_req)]
+    window_check(qsa, rng, lens, 16, 4, 1, 128, 20, 2, False, spare_rows=1, max_rows=17)
+
+
+@pytest.mark.parametrize("n_req", [300, 1100])
+def test_window_attn_tiles_of_no_tokens(qsa, n_req):
+    rng = np.random.default_rng(n_req + 3)
+    lens = [[0] * 5 if r % 50 else [3, 0, 200, 201] for r in range(n_req)]
+    window_check(qsa, rng, lens, 64, 8, 4, 128, 64, 1, False, max_rows=17)
+
 @pytest.mark.parametrize("scale", [-0.07, 0.0, -30.0, 1e-20])
 @pytest.mark.parametrize("rows", [1, 6, 40])
 @pytest.mark.parametrize("fp4", [False, True])
