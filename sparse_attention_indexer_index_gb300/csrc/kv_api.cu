@@ -134,6 +134,10 @@ bool scale_ok(float g) {
   return std::isfinite(g) && g > 0.f && std::frexp(g, &e) == 0.5f && e >= -63 && e <= 64;
 }
 
+int64_t window_entries(int32_t max_len, int32_t window, int32_t n_sink) {
+  return std::min<int64_t>(max_len, (int64_t)window + n_sink);
+}
+
 // Heads and head dims of the calls here: 128 with up to 16 query heads per
 // KV head, 256 with up to 8.
 bool kv_shape_ok(int32_t h_q, int32_t h_kv, int32_t d) {
@@ -268,6 +272,8 @@ bool wt_serves(const KvAttnArgs& k, int d, int32_t max_rows_per_req, int64_t ent
 qsa_status launch_window_tc(const KvAttnArgs& k, int d, cudaStream_t stream) {
   WtArgs a{};
   a.q = k.q;
+  a.k = reinterpret_cast<const uint16_t*>(k.k);
+  a.v = reinterpret_cast<const uint16_t*>(k.v);
   a.ld_q = k.ld_q;
   a.n_slots = k.n_slots;
   a.n_rows = k.n_rows;
@@ -292,6 +298,8 @@ qsa_status launch_window_tc(const KvAttnArgs& k, int d, cudaStream_t stream) {
   a.flip = k.scale < 0.f ? 0x80000000u : 0u;
   a.out = static_cast<uint16_t*>(k.out);
   a.lse = k.lse;
+  // 32 pairs of a warp at some 100 clocks an entry, with room
+  a.wait_ms = 200 + (int)(window_entries(k.max_len, k.window, k.n_sink) / 128);
   const int64_t units = (int64_t)a.tile_slots * a.h_kv;
   if (units > (1 << 30) || k.max_len > (1 << 30)) return QSA_ERR_UNSUPPORTED;
   const KvDevice* dev = nullptr;
@@ -315,10 +323,6 @@ size_t ka_workspace(int64_t n_rows, int32_t h_q, int32_t h_kv, int32_t d, int64_
   if (n_rows <= 0 || entries <= 0 || !kv_shape_ok(h_q, h_kv, d)) return 0;
   const int ng = ka_groups(n_rows * h_kv, entries);
   return ng > 1 ? (size_t)(n_rows * h_q * ng * (d + 2) * 4) : 0;
-}
-
-int64_t window_entries(int32_t max_len, int32_t window, int32_t n_sink) {
-  return std::min<int64_t>(max_len, (int64_t)window + n_sink);
 }
 
 qsa_status check_workspace(size_t need, const void* workspace, size_t bytes) {

@@ -86,6 +86,7 @@ struct WtShape {
 
 struct WtArgs {
   const uint16_t* q;         // rows of h_q * D BF16, ld_q apart
+  const uint16_t *k, *v;     // the cache
   int64_t ld_q;
   int64_t n_slots;
   int32_t n_rows, h_q, h_kv, group;
@@ -104,6 +105,7 @@ struct WtArgs {
   uint32_t flip;             // sign bit to flip in S (a negative scale)
   uint16_t* out;             // [n_rows][h_q][D] BF16
   float* lse;                // [n_rows][h_q] or nullptr
+  int32_t wait_ms;           // limit of a wait: 200, and what wt_redo may take meanwhile
 };
 
 // tcgen05.ld with its wait in one statement, so that no use of the registers
@@ -363,7 +365,7 @@ struct WtCtl {
   float mx[2][2][128];       // [block parity][half][pair]: maxima, at the end the sums
   uint32_t bad[kWtBadRing];  // boxes of a block that are out of range
   uint32_t tmem;
-  int abort;
+  int abort, wait_ms;        // in this order: see wt_wait
 };
 
 template <int D>
@@ -383,7 +385,7 @@ __device__ __forceinline__ bool wt_wait(uint64_t* bar, uint32_t parity, volatile
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = global_timer_ns();
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-    const bool late = global_timer_ns() - t0 > 200000000ull;
+    const bool late = global_timer_ns() - t0 > (uint64_t)abort[1] * 1000000u;  // WtCtl::wait_ms
     if (__any_sync(0xffffffffu, late || *abort != 0)) {
       if ((threadIdx.x & 31) == 0) {
         if (*abort == 0) raise_fault(kFaultWait);
@@ -436,7 +438,7 @@ __device__ __forceinline__ bool wt_wait_cluster(uint64_t* bar, volatile int* abo
   bool ok = true;
   const uint64_t t0 = global_timer_ns();
   while (ok && !arrived()) {
-    if (*abort || global_timer_ns() - t0 > 200000000ull) {
+    if (*abort || global_timer_ns() - t0 > (uint64_t)abort[1] * 1000000u) {
       if (!*abort) raise_fault(kFaultWait);
       *abort = 1;
       ok = false;
@@ -451,6 +453,51 @@ __device__ __forceinline__ void wt_tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
       : "r"(taddr)
       : "memory");
+}
+
+// In a tile, V rows that another row sees meet a weight of 0: where one holds
+// an infinity or a NaN, the sum becomes NaN for rows that do not see it.  So an
+// output that is not finite though its l is, is summed once more over the
+// row's own entries, from the cache: `cols` columns from col0 on of one (row,
+// head), by a whole warp.  m and l come from the row's own entries alone.
+// Slow (a warp takes about 100 clocks an entry), and only then.
+template <int D>
+__device__ __noinline__ void wt_redo(const WtArgs& a, int req, int64_t t, int g, int head, int col0, int cols, float m,
+                                     float l) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int L = __ldg(a.row_len + t), lo = max(0, L - a.window), n_first = min(a.n_sink, lo);
+  const int32_t* pt = a.page_table + (int64_t)req * a.ld_pt;
+  float q[kPer], acc[D / 64] = {};
+  for (int j = 0; j < kPer; ++j) q[j] = __uint_as_float((uint32_t)a.q[t * a.ld_q + head * D + lane * kPer + j] << 16);
+  for (int e = 0; e < n_first + L - lo; ++e) {
+    const int pos = e < n_first ? e : lo + e - n_first;
+    const int64_t page = __ldg(pt + pos / a.page_size);
+    if (page < 0 || (page + 1) * a.page_size > a.n_slots) continue;
+    const int64_t at = ((page * a.page_size + pos % a.page_size) * a.h_kv + g) * D;
+    float x = 0.f;
+    for (int j = 0; j < kPer; ++j) x = fmaf(q[j], __uint_as_float((uint32_t)a.k[at + lane * kPer + j] << 16), x);
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    const float p = ka_ex2((__uint_as_float(__float_as_uint(x) ^ a.flip) - m) * a.c);
+    for (int j = 0; j < D / 64; ++j)
+      if (lane + 32 * j < cols) acc[j] = fmaf(p, __uint_as_float((uint32_t)a.v[at + col0 + lane + 32 * j] << 16), acc[j]);
+  }
+  uint16_t* out = a.out + (t * a.h_q + head) * D + col0;
+  for (int j = 0; j < D / 64; ++j)
+    if (lane + 32 * j < cols) out[lane + 32 * j] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[j] / l));
+}
+// wt_redo for the lanes that ask for it, one after the other.
+template <int D>
+__device__ __forceinline__ void wt_redo_lanes(const WtArgs& a, const WtTile& w, bool ask, int pair, int col0, int cols,
+                                              float m, float l) {
+  unsigned todo = __ballot_sync(0xffffffffu, ask && l != 0.f && l == l);
+  while (todo != 0) {
+    const int i = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int p = __shfl_sync(0xffffffffu, pair, i), row = p / a.group;
+    wt_redo<D>(a, w.r, w.t0 + row, w.g, w.g * a.group + p - row * a.group, __shfl_sync(0xffffffffu, col0, i), cols,
+               __shfl_sync(0xffffffffu, m, i), __shfl_sync(0xffffffffu, l, i));
+  }
 }
 
 // A tile that the cluster's C CTAs shared: out = sum_s f_s O_s / sum_s f_s l_s,
@@ -495,7 +542,8 @@ __device__ __forceinline__ void wt_join(const WtArgs& a, const WtTile& w, unsign
   if (!wt_wait_cluster(&ctl.join_full, abort)) return;
   const float ninf = -__int_as_float(0x7f800000);
   const int vecs = S / 8, n = w.rows * a.group * vecs;  // 8 columns a thread, a row's next to each other
-  for (int i = threadIdx.x; i < n; i += 256) {
+  for (int i0 = 0; i0 < n; i0 += 256) {
+    const int i = min(i0 + (int)threadIdx.x, n - 1);  // the same once more behind the end
     const int p = i / vecs, v = i - p * vecs;
     float mx = ninf, ls = 0.f, acc[8] = {};
     for (int s = 0; s < C; ++s) mx = fmaxf(mx, lm[s * 256 + 128 + p]);
@@ -512,6 +560,9 @@ __device__ __forceinline__ void wt_join(const WtArgs& a, const WtTile& w, unsign
       acc[6] = fmaf(f, y.z, acc[6]), acc[7] = fmaf(f, y.w, acc[7]);
     }
     const float inv = ls == 0.f ? 0.f : 1.0f / ls;
+    float broken = 0.f;  // NaN once a sum is not finite
+#pragma unroll
+    for (int j = 0; j < 8; ++j) broken = fmaf(acc[j], 0.f, broken);
     uint32_t y[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -523,6 +574,8 @@ __device__ __forceinline__ void wt_join(const WtArgs& a, const WtTile& w, unsign
     *reinterpret_cast<uint4*>(a.out + hq * D + rank * S + v * 8) = make_uint4(y[0], y[1], y[2], y[3]);
     if (rank == 0 && v == 0 && a.lse != nullptr)
       a.lse[hq] = ls == 0.f ? ninf : mx == ninf ? ls : fmaf(mx, a.c, log2f(ls)) * 0.69314718055994531f;
+    __syncwarp();
+    wt_redo_lanes<D>(a, w, broken != broken && i == i0 + (int)threadIdx.x, p, rank * S + v * 8, 8, mx, ls);
   }
 }
 
@@ -572,6 +625,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
     mbar_init(&ctl.join_free, 8 * a.cluster);
     mbar_init(&ctl.join_full, 8 * a.cluster);
     ctl.abort = 0;
+    ctl.wait_ms = a.wait_ms;
     fence_mbar_init();
   }
   tc_fence_before();
@@ -926,6 +980,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       const uint32_t keep = l == 0.f ? 0u : ~0u;  // a row that sees nothing: zeros, whatever the sums hold
       const long long own = mine ? (long long)(hq * D) + half * (D / 2) : -1ll;
       const long long at0 = __shfl_sync(0xffffffffu, own, lane & ~1), at1 = __shfl_sync(0xffffffffu, own, lane | 1);
+      float broken = 0.f;  // NaN once a sum is not finite
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 32) {
         uint32_t o[32];
@@ -941,6 +996,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
           const __nv_bfloat162 b =
               __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
           y[j] = *reinterpret_cast<const uint32_t*>(&b) & keep;
+          broken = fmaf(__uint_as_float(o[2 * j]), 0.f, fmaf(__uint_as_float(o[2 * j + 1]), 0.f, broken));
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {  // the even lane's second piece <-> the odd lane's first
@@ -953,6 +1009,8 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         if (at1 >= 0) wt_store32(a.out + at1 + piece, y + 8);
       }
       tc_fence_before();
+      __syncwarp();
+      wt_redo_lanes<D>(a, w, mine && broken != broken, pair, half * (D / 2), D / 2, m, l);
       if (mine && half == 0 && a.lse != nullptr)
         a.lse[hq] = l == 0.f ? ninf : (m == ninf ? l : (fmaf(m, a.c, log2f(l))) * 0.69314718055994531f);
     }

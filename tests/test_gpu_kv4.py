@@ -651,6 +651,62 @@ def test_window_attn_tiles_of_no_tokens(qsa, n_req):
     lens = [[0] * 5 if r % 50 else [3, 0, 200, 201] for r in range(n_req)]
     window_check(qsa, rng, lens, 64, 8, 4, 128, 64, 1, False, max_rows=17)
 
+@pytest.mark.parametrize("h_q,h_kv,d,rows", [(8, 1, 256, 48), (16, 2, 128, 48), (4, 4, 128, 200), (8, 1, 256, 20)])
+@pytest.mark.parametrize("window,n_sink", [(5000, 0), (60, 3), (700, 0)])
+def test_window_attn_broken_values_reach_only_the_rows_that_see_them(qsa, h_q, h_kv, d, rows, window, n_sink):
+    """Infinities and NaN at positions that some rows of a request see and
+    others, in the same tile, do not: in the others they have no effect."""
+    rng = np.random.default_rng(45 + rows + d)
+    page, ctx = 32, 1500
+    pt, n_slots = page_table(rng, [ctx], page)
+    k, v, q = (normal_bf16(rng, s) for s in ((n_slots, h_kv, d), (n_slots, h_kv, d), (rows, h_q, d)))
+    lens = np.arange(ctx - rows + 1, ctx + 1).astype(np.int32)
+    # seen by the last rows, by the second half, and by the first quarter (where its windows begin)
+    at = [ctx - 3, ctx - rows // 2, lens[0] + rows // 4 - window]
+    at = [p for p in at if p >= 0]
+    for i, p in enumerate(at):
+        sl = ref.slots_of(pt[0], np.array([p]), page)[0]
+        k[sl, :, 5] = (0x7F80, 0x7FC0, 0xFF80)[i]
+        v[sl, :, 7 + i:d:16] = (0x7FC0, 0x7F80, 0xFF80)[i]
+    out, lse = qsa.window_attn(*map(bf16_dev, (q, k, v)), to_dev(np.array([0, rows], np.int32)), to_dev(lens), to_dev(pt),
+                               page, ctx, window, n_sink, max_rows_per_req=max(rows, 17))
+    o, l, kf, vf = bits_to_f64(out), host(lse).astype(np.float64), ref.bf16_to_f64(k), ref.bf16_to_f64(v)
+    clean = 0
+    for t in range(rows):
+        pos = ref.window_positions(lens[t], window, n_sink)
+        if np.isin(at, pos).any():
+            continue
+        clean += 1
+        sl = ref.slots_of(pt[0], pos, page)
+        ro, rl, a, big, spread = ref.attend(ref.bf16_to_f64(q[t]), kf[sl], vf[sl], d ** -0.5)
+        tol, tol_l = ref.tolerance(d, pos.size, ro, a, big, spread, W_BF16, BF16_HALF_STEP, False, 0.0)
+        assert (np.abs(o[t] - ro) <= tol).all(), t
+        assert (np.abs(l[t] - rl) <= tol_l + 2.0 ** -23 * np.abs(rl)).all()
+    assert clean >= rows // 4 - 2
+
+
+@pytest.mark.parametrize("rows", [20, 60])
+def test_window_attn_broken_values_seen_show_as_they_are(qsa, rows):
+    """An infinity of V that every row sees makes that column infinite, and
+    leaves the other columns alone."""
+    rng = np.random.default_rng(46)
+    pt, n_slots = page_table(rng, [300], 64)
+    k, v, q = (normal_bf16(rng, s) for s in ((n_slots, 1, 128), (n_slots, 1, 128), (rows, 8, 128)))
+    v[ref.slots_of(pt[0], np.array([200]), 64)[0], 0, 9] = 0x7F80
+    lens = np.arange(300 - rows + 1, 301).astype(np.int32)
+    out, _ = qsa.window_attn(*map(bf16_dev, (q, k, v)), to_dev(np.array([0, rows], np.int32)), to_dev(lens), to_dev(pt), 64,
+                             300, 250, max_rows_per_req=rows)
+    o, kf, vf = bits_to_f64(out), ref.bf16_to_f64(k), ref.bf16_to_f64(v)
+    assert np.isposinf(o[:, :, 9]).all()
+    vf[:, 0, 9] = 0
+    for t in range(rows):
+        pos = ref.window_positions(lens[t], 250, 0)
+        sl = ref.slots_of(pt[0], pos, 64)
+        ro, _, a, big, spread = ref.attend(ref.bf16_to_f64(q[t]), kf[sl], vf[sl], 128 ** -0.5)
+        tol, _ = ref.tolerance(128, pos.size, ro, a, big, spread, W_BF16, BF16_HALF_STEP, False, 0.0)
+        keep = np.arange(128) != 9
+        assert (np.abs(o[t] - ro) <= tol)[:, keep].all()
+
 @pytest.mark.parametrize("scale", [-0.07, 0.0, -30.0, 1e-20])
 @pytest.mark.parametrize("rows", [1, 6, 40])
 @pytest.mark.parametrize("fp4", [False, True])
