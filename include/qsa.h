@@ -377,13 +377,21 @@ qsa_status qsa_sparse_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
  * plain causal attention.  Per query head h (KV head h / (h_q / h_kv)):
  *   out = sum_j softmax_j(scale <q_h, k_j>) v_j,  lse = log sum_j exp(...).
  * A row with L = 0 gets out = 0 and lse = -inf; rows behind
- * req_row_start[n_req] are left as they were.  Masked positions are not read
- * into the result: an infinity or NaN there has no effect.
+ * req_row_start[n_req] are left as they were.  Positions that a row does not
+ * attend to have no effect on it, whatever they hold (a V row with an
+ * infinity or NaN that other rows of the request do attend to can make the
+ * call much slower).
  *
  *   q, lse, shapes: as qsa_sparse_attn_fp4.
  *   k_cache, v_cache [n_slots][h_kv][head_dim] BF16 (16-byte aligned), or the
  *              four arrays of the 4-bit cache.
- *   window >= 1, n_sink >= 0.
+ *   window >= 1, n_sink >= 0; scale finite, of either sign.
+ *   max_rows_per_req  as elsewhere: it picks the kernel, not the result.
+ *              Requests of several rows take 128 (row, query head) pairs at a
+ *              time on the BF16 cache if the page size is a multiple of 8,
+ *              with the weights rounded to BF16 once; otherwise each row is
+ *              taken by itself, with weights of 16 bits or more.  The 4-bit
+ *              form takes each row by itself always.
  *   out        [n_rows][h_q][head_dim] BF16 (32-byte aligned): the next
  *              operator is a BF16 projection.
  *   workspace  qsa_window_attn_workspace_size() bytes (16-byte aligned), 0
