@@ -86,11 +86,10 @@ bool resident_clusters(F fn, int threads, size_t smem, int c, int sms, int* n) {
   if (c == 1) {  // without the attribute
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, fn, threads, smem) != cudaSuccess) return false;
     *n *= sms;
-  } else {
-    ClusterLaunch l(dim3((unsigned)c), threads, smem, c, nullptr);
-    if (cudaOccupancyMaxActiveClusters(n, fn, &l.cfg) != cudaSuccess) return false;
+    return *n > 0;
   }
-  return *n > 0;
+  const ClusterLaunch l(dim3((unsigned)c), threads, smem, c, nullptr);
+  return cudaOccupancyMaxActiveClusters(n, fn, &l.cfg) == cudaSuccess;
 }
 
 bool set_up(KvDevice& d, int sms) {
@@ -162,7 +161,7 @@ int ka_groups(int64_t units, int64_t entries) {
 int ka_cluster(int64_t units, int64_t entries, const KaKernel& k, const int* resident) {
   int best = 1;
   int64_t least = INT64_MAX;
-  for (int c = 1; c <= kKaMaxCluster; ++c) {
+  for (int c = 1; c <= kKaMaxCluster && resident[c] > 0; ++c) {
     const int64_t waves = (units + resident[c] - 1) / resident[c];
     const int64_t steps = (entries + (int64_t)k.entries * c - 1) / ((int64_t)k.entries * c);
     const int64_t cost = waves * (steps + 4);

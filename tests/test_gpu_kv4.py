@@ -745,6 +745,56 @@ def test_graphs_sharing_a_workspace(qsa):
     for got, exp in zip(outs, want):
         assert all(torch.equal(a, b) for a, b in zip(got, exp))
 
+def test_window_attn_of_an_empty_context_in_tiles(qsa):
+    import torch
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    i32 = torch.int32
+    start = torch.tensor([0, 40, 40], dtype=i32, device="cuda")
+    out, lse = qsa.window_attn(z(40, 8, 128) + 1, z(64, 2, 128), z(64, 2, 128), start, z(40, dt=i32), z(2, 4, dt=i32), 16, 0, 8)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_window_attn_largest_window_and_sinks(qsa):
+    """window and n_sink at the type's limit: plain causal attention."""
+    rng = np.random.default_rng(47)
+    for lens in ([[300]], [list(range(1, 60))]):
+        for window, n_sink in ((2**31 - 1, 0), (2**31 - 1, 2**31 - 1), (1, 2**31 - 1)):
+            window_check(qsa, rng, lens, 16, 8, 2, 128, window, n_sink, False)
+
+
+def test_first_calls_inside_a_capture():
+    """A fresh process whose first use of the calls is a stream capture.  A
+    block of ones is held as 6 * 11/64: e4m3 has 10/64 and 11/64 around 1/6,
+    and 64/11 is nearer to 6 than to 4."""
+    import subprocess
+    import sys
+    code = """
+import torch, sparse_attention_indexer_index_gb300 as qsa
+qsa.lib()
+z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device='cuda')
+i32, u8 = torch.int32, torch.uint8
+q1, q2, k = z(2, 8, 128), z(40, 8, 128), z(64, 2, 128) + 1
+c = [z(64, 2, 64, dt=u8), z(64, 2, 8, dt=u8), z(64, 2, 64, dt=u8), z(64, 2, 8, dt=u8)]
+s1, s2 = (torch.tensor([0, n], dtype=i32, device='cuda') for n in (2, 40))
+l1, l2 = (torch.full((n,), 50, dtype=i32, device='cuda') for n in (2, 40))
+pt, slots, first = torch.arange(4, dtype=i32, device='cuda')[None], z(2, 30, dt=i32), z(1, dt=i32)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    qsa.append_kv_fp4(k[:40], k[:40], s2, first, *c, pt, 16)
+    a = qsa.sparse_attn_fp4(q1, *c, slots)
+    b = qsa.window_attn(q1, k, k, s1, l1, pt, 16, 64, 20)
+    d = qsa.window_attn(q2, k, k, s2, l2, pt, 16, 64, 20)
+    e = qsa.window_attn_fp4(q1, *c, s1, l1, pt, 16, 64, 20)
+g.replay()
+torch.cuda.synchronize()
+assert qsa.device_status() == 0
+assert ((a[0] - 66 / 64).abs() < 1e-6).all() and (b[0] == 1).all() and (d[0] == 1).all() and torch.isfinite(e[0]).all()
+print('fine')
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
 def test_cache4_offsets_past_32_bits(qsa):
     """Append, read back and attend at the far end of a 4-bit cache whose
     codes take more than 2^32 bytes."""
