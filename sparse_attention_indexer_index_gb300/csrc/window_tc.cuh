@@ -853,13 +853,16 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       return ok;
     };
     bool ok = true, shared = false;
+    bool ahead = false;                           // next_len is the next tile's
+    int next_len = 0;
     float m = ninf, l = 0.f;
     WtTile w;
     for (int k = 0; ok; ++k) {
       if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
       const bool mine = row < w.rows;
       const int64_t t = w.t0 + row;
-      int L = mine ? __ldg(a.row_len + t) : 0;
+      int L = next_len;
+      if (!ahead) L = mine ? __ldg(a.row_len + t) : 0;
       if (L < 0 || L > a.max_len) L = 0;
       const int64_t hq = t * a.h_q + (int64_t)w.g * a.group + hd;
       m = ninf;
@@ -948,13 +951,17 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
             ok = wt_wait(&ctl.full[st], (uint32_t)((at + v) / Sh::kStages) & 1u, abort);
             if (!ok) break;
             unsigned char* vst = ring + st * kWtStageBytes;
-            const int rows = min(Sh::kVRows, n16 - v * Sh::kVRows);
-            for (int r = warp; r < rows; r += 8) {  // a row a warp, 16 bytes a lane
-              const int e = e0 + v * Sh::kVRows + r;
-              if (!(e < w.ua || (e >= w.ub && e < w.uc)) && lane < D / 8)
-                *reinterpret_cast<uint4*>(vst + (r >> 3) * Sh::kVGroup + (lane >> 3) * 1024 + (r & 7) * 128 +
-                                          (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
+            const int ev = e0 + v * Sh::kVRows, rows = min(Sh::kVRows, n16 - v * Sh::kVRows);
+            // entries [ua, ub) and from uc on: 16 bytes a lane, all rows of a warp's pass at once
+            constexpr int kLanes = D / 8, kPass = 256 / kLanes;
+            const int r0 = threadIdx.x / kLanes, col = threadIdx.x % kLanes;
+            auto zero = [&](int from, int to) {
+              for (int r = max(from - ev, 0) + r0; r < min(to - ev, rows); r += kPass)
+                *reinterpret_cast<uint4*>(vst + (r >> 3) * Sh::kVGroup + (col >> 3) * 1024 + (r & 7) * 128 +
+                                          (col & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            };
+            zero(w.ua, min(w.ub, w.uc));
+            zero(max(w.ua, w.uc), ev + rows);
           }
           if (!ok) break;
           fence_proxy_async_smem();
@@ -967,6 +974,12 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       if (w.n_blk > 0) {
         const int last = min(N, w.n_box * a.box - (w.n_blk - 1) * N);  // rows copied for the last block
         rs += Sh::kKs * w.n_blk + (w.n_blk - 1) * Sh::kVs + (last + Sh::kVRows - 1) / Sh::kVRows;
+      }
+      // the next tile's row lengths under way beside the outputs, if it is known by now
+      {
+        const int sl = (k + 1) % kWtTileRing;
+        ahead = __all_sync(0xffffffffu, mbar_try_wait(&ctl.tile_full[sl], (uint32_t)((k + 1) / kWtTileRing) & 1u));
+        if (ahead) next_len = row < ctl.tile[sl].rows ? __ldg(a.row_len + ctl.tile[sl].t0 + row) : 0;
       }
       // ---- outputs ---------------------------------------------------------------------
       float inv = 0.f;
@@ -991,7 +1004,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       const uint32_t keep = l == 0.f ? 0u : ~0u;  // a row that sees nothing: zeros, whatever the sums hold
       const long long own = mine ? (long long)(hq * D) + half * (D / 2) : -1ll;
       const long long at0 = __shfl_sync(0xffffffffu, own, lane & ~1), at1 = __shfl_sync(0xffffffffu, own, lane | 1);
-      float broken = 0.f;  // NaN once a sum is not finite
+      __nv_bfloat162 broken2 = __floats2bfloat162_rn(0.f, 0.f);  // NaN once a sum is not finite
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 32) {
         uint32_t o[32];
@@ -1007,7 +1020,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
           const __nv_bfloat162 b =
               __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
           y[j] = *reinterpret_cast<const uint32_t*>(&b) & keep;
-          broken = fmaf(__uint_as_float(o[2 * j]), 0.f, fmaf(__uint_as_float(o[2 * j + 1]), 0.f, broken));
+          broken2 = __hfma2(b, __floats2bfloat162_rn(0.f, 0.f), broken2);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {  // the even lane's second piece <-> the odd lane's first
@@ -1021,7 +1034,8 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       }
       tc_fence_before();
       __syncwarp();
-      wt_redo_lanes<D>(a, w, mine && broken != broken, pair, half * (D / 2), D / 2, m, l);
+      wt_redo_lanes<D>(a, w, mine && !(__low2float(broken2) + __high2float(broken2) == 0.f), pair, half * (D / 2), D / 2,
+                       m, l);
       if (mine && half == 0 && a.lse != nullptr)
         a.lse[hq] = l == 0.f ? ninf : (m == ninf ? l : (fmaf(m, a.c, log2f(l))) * 0.69314718055994531f);
     }
