@@ -384,6 +384,24 @@ constexpr int wt_smem_bytes() {  // all of it dynamic, from a 1024-byte boundary
   return WtShape<D>::kQBytes + WtShape<D>::kStages * kWtStageBytes + (int)sizeof(WtCtl);
 }
 
+// Pairs of FP32 numbers, one instruction for both.
+__device__ __forceinline__ uint64_t wt_pack(float lo, float hi) {
+  return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float2 wt_unpack(uint64_t v) {
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ uint64_t wt_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t wt_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // The lowest n bits (none below 0, all from 64).
 __device__ __forceinline__ uint64_t wt_low_bits(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
@@ -928,17 +946,21 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         }
         if (m == ninf) m = mx;
         const float off = m == ninf ? 0.f : -m * a.c;
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        // two entries an instruction but for the exponentials (76 -> 74 us on
+        // the chunk, 50 -> 48 on seven prompts, in a graph)
+        const uint64_t c2 = wt_pack(a.c, a.c), off2 = wt_pack(off, off);
+        uint64_t l2[2] = {0, 0};
         uint32_t p[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const float p0 = ka_ex2(fmaf(__uint_as_float(s[2 * j]), a.c, off));
-          const float p1 = ka_ex2(fmaf(__uint_as_float(s[2 * j + 1]), a.c, off));
-          l4[j & 3] += p0 + p1;
-          const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+          const float2 x = wt_unpack(wt_fma2((uint64_t)s[2 * j + 1] << 32 | s[2 * j], c2, off2));
+          const float2 e = make_float2(ka_ex2(x.x), ka_ex2(x.y));
+          l2[j & 1] = wt_add2(l2[j & 1], wt_pack(e.x, e.y));
+          const __nv_bfloat162 b = __floats2bfloat162_rn(e.x, e.y);
           p[j] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        const float2 ls = wt_unpack(wt_add2(l2[0], l2[1]));
+        l += ls.x + ls.y;
         wt_tmem_st32(lanes + Sh::kColS + sl * N + 32 * half, p);
         wt_wait_st();
         tc_fence_before();
