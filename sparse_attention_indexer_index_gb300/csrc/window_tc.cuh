@@ -55,15 +55,16 @@
 // infinity there would be NaN); see wt_redo for those that some pairs see.
 //
 // Measured (L2 flushed): a chunk of 4,096 rows of 16 heads, 2 KV heads, D =
-// 256, window 1,024: 72 us, 960 TFLOP/s, half of the bf16 rate.  Of that the
+// 256, window 1,024: 69.6 us, 990 TFLOP/s, 0.52 of the bf16 rate.  Of that the
 // products themselves are 39 us at the full rate (with half of them left out
 // 8 us less, without exponentials, copies or output stores 0, 4 and 2 us
 // less): 512 tiles make 3.4 rounds of the 152 SMs, four in effect, and
 // accesses to tensor memory by the softmax slow the products by a sixth.
-// Seven prompts of D = 128 in windows of 500: 47 us, 0.23 of the rate, the
-// start and end of some 900 short tiles.  32 requests of 6 rows: 27 us, 2.6
-// TB/s, of which some 10 us are the chain from the launch to the first keys
-// and from the last product to the output.
+// Seven prompts of D = 128 in windows of 500: 45.1 us, 0.23 of the rate: a
+// block's chain from scores to weights takes longer than its products, and a
+// third of the time is the start and end of some 900 short tiles.  32 requests of 6 rows: 27 us, 2.6
+// TB/s: 6 us from the launch to the first copy, 11 us of copies at the full
+// HBM rate, then the last block, and 5 us in which a cluster joins.
 #pragma once
 #include <cuda.h>
 
