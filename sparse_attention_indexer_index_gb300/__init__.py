@@ -671,6 +671,16 @@ def _explain(fn, first, rows=(), i32=(), u8=(), bf16=(), f32=()):
     raise ValueError(f"{fn}: the arguments' shapes do not fit together")
 
 
+def _empty(shape, dtype, device, stream):
+    """A buffer for a call on `stream` (None: the current one), owned by that
+    stream: the allocator hands it out again in that stream's order only."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _launch(fn, dev, stream, *args):
     """Calls `fn` on device `dev`, on `stream` or that device's current one;
     the status."""
@@ -689,7 +699,7 @@ def _launch_ws(fn, dev, stream, size_fn, size_args, workspace, *args):
         if st != -3:
             return _check(fn, st)
         torch = _torch()
-        workspace = torch.empty(_call(size_fn, *size_args), dtype=torch.uint8, device=torch.device("cuda", dev))
+        workspace = _empty(_call(size_fn, *size_args), torch.uint8, torch.device("cuda", dev), stream)
     _check(fn, _launch(fn, dev, stream, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size()))
 
 
@@ -750,9 +760,9 @@ def gather_kv_fp4(k_codes, k_scales, v_codes, v_scales, slots, k_scale=1.0, v_sc
                      (v_scales, "v_scales", 3)),
                  bf16=((k_out, "k_out", None), (v_out, "v_out", None)))
     if k_out is None:
-        k_out = _torch().empty(out_shape, dtype=bf16, device=slots.device)
+        k_out = _empty(out_shape, bf16, slots.device, stream)
     if v_out is None:
-        v_out = _torch().empty(out_shape, dtype=bf16, device=slots.device)
+        v_out = _empty(out_shape, bf16, slots.device, stream)
     _check("qsa_gather_kv_fp4", _launch(
         "qsa_gather_kv_fp4", dev, stream, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
         v_scales.data_ptr(), n_slots, h_kv, 2 * w, slots.data_ptr(), slots.numel(), k_scale, v_scale,
@@ -786,11 +796,11 @@ def sparse_attn_fp4(q, k_codes, k_scales, v_codes, v_scales, slots, scale=None, 
     if n_idx is None:
         n_idx = width
     if out is None:
-        out = _torch().empty((n_rows, h_q, d), dtype=f32, device=q.device)
+        out = _empty((n_rows, h_q, d), f32, q.device, stream)
     if not want_lse:
         lse = None
     elif lse is None:
-        lse = _torch().empty((n_rows, h_q), dtype=f32, device=q.device)
+        lse = _empty((n_rows, h_q), f32, q.device, stream)
     _launch_ws("qsa_sparse_attn_fp4", dev, stream, "qsa_sparse_attn_fp4_workspace_size",
                (n_rows, h_q, h_kv, d, n_idx), workspace, q.data_ptr(), q.stride(0) if n_rows > 1 else h_q * d,
                k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), n_slots, n_rows, h_q,
@@ -860,11 +870,11 @@ def _window_call(fn, cache_ptrs, scales, n_slots, h_kv, d, q, req_row_start, row
     if max_rows_per_req is None:
         max_rows_per_req = n_rows
     if out is None:
-        out = _torch().empty((n_rows, h_q, d), dtype=bf16, device=q.device)
+        out = _empty((n_rows, h_q, d), bf16, q.device, stream)
     if not want_lse:
         lse = None
     elif lse is None:
-        lse = _torch().empty((n_rows, h_q), dtype=f32, device=q.device)
+        lse = _empty((n_rows, h_q), f32, q.device, stream)
     _launch_ws(fn, dev, stream, "qsa_window_attn_workspace_size",
                (n_rows, h_q, h_kv, d, max_len, window, n_sink), workspace, q.data_ptr(),
                q.stride(0) if n_rows > 1 else h_q * d, *cache_ptrs, n_slots, n_req, req_row_start.data_ptr(), n_rows,

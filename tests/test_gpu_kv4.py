@@ -928,6 +928,31 @@ def test_calls_on_two_streams_at_once(qsa):
             assert torch.equal(a, b)
 
 
+def test_buffers_of_a_call_on_another_stream_are_that_stream_s(qsa, monkeypatch):
+    """What a call allocates for a stream that is not the current one is not
+    handed out to the current one while the call may still run."""
+    import torch
+    rng = np.random.default_rng(48)
+    arrays = list(map(to_dev, (*random_cache4(rng, 4000, 1, 128), *random_cache4(rng, 4000, 1, 128))))
+    q, slots = bf16_dev(normal_bf16(rng, (2, 8, 128))), to_dev(rng.integers(0, 4000, (2, 20000)).astype(np.int32))
+    need = qsa.lib().qsa_sparse_attn_fp4_workspace_size(2, 8, 1, 128, 20000)
+    assert need > 0
+    want, want_l = qsa.sparse_attn_fp4(q, *arrays, slots)
+    torch.cuda.synchronize()
+    seen, call = [], qsa._call
+    monkeypatch.setattr(qsa, "_call", lambda fn, *a: (seen.append(a), call(fn, *a))[1])
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(1)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # the call's turn comes later
+    out, lse = qsa.sparse_attn_fp4(q, *arrays, slots, stream=side)
+    used = {a[-3] for a in seen if a[-2:-1] == (need,)} | {out.data_ptr(), lse.data_ptr()}
+    assert len(used) == 3
+    mine = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in (need, need, out.nbytes, lse.nbytes)]
+    assert not used & {t.data_ptr() for t in mine}
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_l)
+
 def test_same_call_twice_gives_the_same_bits(qsa):
     import torch
     rng = np.random.default_rng(32)
