@@ -183,6 +183,7 @@ append_kv_fp4_kernel(KvWriteArgs a) {
   const uint32_t u0 = blockIdx.x * kKvThreads + (threadIdx.x & ~31);
   const uint32_t total = (uint32_t)a.n_tok * (uint32_t)a.blocks;  // 32 bits: checked by the host
   if (u0 >= total) return;  // the whole warp
+  pdl_wait_primary();
   const uint32_t u = u0 + (threadIdx.x & 31);
   const bool ok = u < total;
   const int t = ok ? (int)(u / (uint32_t)a.blocks) : a.n_tok - 1;
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kKvThreads)
 gather_kv_fp4_kernel(KvReadArgs a) {
   const uint32_t u = blockIdx.x * kKvThreads + threadIdx.x;
   if (u >= (uint32_t)a.n * (uint32_t)a.blocks) return;  // 32 bits: checked by the host
+  pdl_wait_primary();
   const uint32_t i = u / (uint32_t)a.blocks;
   const int b = (int)(u - i * (uint32_t)a.blocks);
   const int32_t s = __ldg(a.slots + i);

@@ -82,6 +82,7 @@ kv4_attn_kernel(const __grid_constant__ KvAttnArgs a) {
   const int g = blockIdx.y;
   const float ninf = -__int_as_float(0x7f800000);
 
+  pdl_wait_primary();
   KaRow<kWindow> row;
   if (!ka_row<kWindow>(a, t, row)) return;  // behind the last request (the same for the whole cluster)
   ka_cluster_arrive(a.cluster);

@@ -51,24 +51,35 @@ bool set_ka_smem() {
   return true;
 }
 
-// A launch of clusters of c CTAs along x (c = 1: without the attribute).
+// A launch of clusters of c CTAs along x (c = 1: without that attribute), as
+// all here a programmatic dependent one: it may be set up while the kernel
+// before it in the stream ends.  Every kernel waits for that one's results
+// (griddepcontrol.wait) before it touches global memory.
 struct ClusterLaunch {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr = {};
+  cudaLaunchAttribute attr[2] = {};
   ClusterLaunch(dim3 grid, int threads, size_t smem, int c, cudaStream_t stream) {
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)c;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = c > 1 ? 1 : 0;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)c;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = c > 1 ? 2 : 1;
   }
   ClusterLaunch(const ClusterLaunch&) = delete;
 };
+
+qsa_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return QSA_OK;
+  cudaGetLastError();
+  return QSA_ERR_CUDA;
+}
 
 // Per-device one-time set-up: the shared-memory opt-in of the kernels, and
 // how many of their clusters run at once.
@@ -194,11 +205,7 @@ qsa_status launch_ka(int cache, KvAttnArgs& a, int d, int64_t entries, void* wor
     e = launch_pdl(d == 256 ? kv_attn_merge_kernel<256> : kv_attn_merge_kernel<128>,
                    dim3((unsigned)((int64_t)a.n_rows * a.h_q)), dim3((unsigned)d), 0, stream, a,
                    cache == kKaBf16Window ? 0.0f : (float)kK4Bias);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return QSA_ERR_CUDA;
-  }
-  return QSA_OK;
+  return launched(e);
 }
 
 // The cache [n_slots][h_kv * D] BF16 for window_tc_kernel, as [row / 8][64
@@ -310,12 +317,8 @@ qsa_status launch_window_tc(const KvAttnArgs& k, int d, cudaStream_t stream) {
   a.cluster = wt_cluster(a, dev->wt[d == 256]);
   const ClusterLaunch l(dim3((unsigned)(std::min<int64_t>(units, dev->sms / a.cluster) * a.cluster)), kWtThreads,
                         d == 256 ? wt_smem_bytes<256>() : wt_smem_bytes<128>(), a.cluster, stream);
-  if (cudaLaunchKernelEx(&l.cfg, d == 256 ? window_tc_kernel<256> : window_tc_kernel<128>, a, q_map, k_map, v_map) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return QSA_ERR_CUDA;
-  }
-  return QSA_OK;
+  return launched(cudaLaunchKernelEx(&l.cfg, d == 256 ? window_tc_kernel<256> : window_tc_kernel<128>, a, q_map, k_map,
+                                     v_map));
 }
 
 size_t ka_workspace(int64_t n_rows, int32_t h_q, int32_t h_kv, int32_t d, int64_t entries) {
@@ -434,9 +437,9 @@ qsa_status qsa_append_kv_fp4(const void* k_new, const void* v_new, int64_t ld_k,
   a.v_inv = 1.0f / v_scale;
   const int64_t units = (int64_t)n_tok * a.blocks;
   if (units > (int64_t)UINT32_MAX - 4 * kKvThreads) return QSA_ERR_UNSUPPORTED;  // counted in 32 bits
-  append_kv_fp4_kernel<<<(unsigned)((units + kKvThreads - 1) / kKvThreads), kKvThreads, 0,
-                         static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+  const ClusterLaunch l(dim3((unsigned)((units + kKvThreads - 1) / kKvThreads)), kKvThreads, 0, 1,
+                        static_cast<cudaStream_t>(stream));
+  return launched(cudaLaunchKernelEx(&l.cfg, append_kv_fp4_kernel, a));
 }
 
 qsa_status qsa_gather_kv_fp4(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
@@ -465,8 +468,8 @@ qsa_status qsa_gather_kv_fp4(const void* k_codes, const void* k_scales, const vo
   // blocks are counted in 32 bits (2^32 of them would be 137 GB of output each)
   if (n > (int64_t)(UINT32_MAX - 4 * kKvThreads) / a.blocks) return QSA_ERR_UNSUPPORTED;
   const int64_t ctas = (n * a.blocks + kKvThreads - 1) / kKvThreads;
-  gather_kv_fp4_kernel<<<(unsigned)ctas, kKvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+  const ClusterLaunch l(dim3((unsigned)ctas), kKvThreads, 0, 1, static_cast<cudaStream_t>(stream));
+  return launched(cudaLaunchKernelEx(&l.cfg, gather_kv_fp4_kernel, a));
 }
 
 size_t qsa_sparse_attn_fp4_workspace_size(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t n_idx) {

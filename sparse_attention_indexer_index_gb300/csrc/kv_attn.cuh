@@ -356,6 +356,7 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
   const int g = blockIdx.y;
   const float ninf = -__int_as_float(0x7f800000);
 
+  pdl_wait_primary();
   KaRow<true> row;
   if (!ka_row<true>(a, t, row)) return;  // behind the last request (the same for the whole cluster)
   ka_cluster_arrive(C);

@@ -661,6 +661,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait_primary();
   const uint32_t tmem = ctl.tmem;
   const int n_cta = a.cluster, rank = n_cta > 1 ? (int)cluster_ctarank() : 0;
   bool met = n_cta == 1;  // the cluster's CTAs all run
