@@ -28,10 +28,10 @@
 //    pairs (the K index of the MMA), which are interleaved nibble by nibble
 //    before the conversion.
 //
-// Measured (L2 flushed; 16 query heads): 32 rows of 2,051 entries, 2 KV heads
-// of D = 256: 18.5 us, 2.1 TB/s; 192 rows, 1 KV head of D = 128: 35.6 us, 1.7
-// TB/s; 32 windows of 4,100 entries, 2 KV heads of D = 256: 30.5 us, 2.5 TB/s;
-// one row 10.3 us.  In the middle of a long row the tensor pipe and the ALU
+// Measured (one call after the other; 16 query heads): 32 rows of 2,051 entries, 2 KV heads
+// of D = 256: 16.4 us, 2.4 TB/s; 192 rows, 1 KV head of D = 128: 33.2 us, 1.8
+// TB/s; 32 windows of 4,100 entries, 2 KV heads of D = 256: 27.5 us, 2.8 TB/s;
+// one row 8.7 us.  In the middle of a long row the tensor pipe and the ALU
 // are each busy two thirds of the time, on 8 warps an SM (250 registers a
 // thread); the rest of a short call is the chain from the launch to the first
 // keys and the join.

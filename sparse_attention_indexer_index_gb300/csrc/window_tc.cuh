@@ -54,17 +54,18 @@
 // of the tile sees are zeroed in shared memory (a weight of 0 times an
 // infinity there would be NaN); see wt_redo for those that some pairs see.
 //
-// Measured (L2 flushed): a chunk of 4,096 rows of 16 heads, 2 KV heads, D =
-// 256, window 1,024: 69.6 us, 990 TFLOP/s, 0.52 of the bf16 rate.  Of that the
-// products themselves are 39 us at the full rate (with half of them left out
-// 8 us less, without exponentials, copies or output stores 0, 4 and 2 us
-// less): 512 tiles make 3.4 rounds of the 152 SMs, four in effect, and
-// accesses to tensor memory by the softmax slow the products by a sixth.
-// Seven prompts of D = 128 in windows of 500: 45.1 us, 0.23 of the rate: a
-// block's chain from scores to weights takes longer than its products, and a
-// third of the time is the start and end of some 900 short tiles.  32 requests of 6 rows: 27 us, 2.6
-// TB/s: 6 us from the launch to the first copy, 11 us of copies at the full
-// HBM rate, then the last block, and 5 us in which a cluster joins.
+// Measured (one call after the other over several sets of inputs): a chunk of
+// 4,096 rows of 16 heads, 2 KV heads, D = 256, window 1,024: 66.2 us, 1,040
+// TFLOP/s, 0.55 of the bf16 rate.  The products themselves are 39 us of it at
+// the full rate (with half of them left out 8 us less, without exponentials,
+// copies or output stores 0, 4 and 2 us less): 512 tiles make 3.4 rounds of
+// the 152 SMs, four in effect, and accesses to tensor memory by the softmax
+// slow the products by a sixth.  Seven prompts of D = 128 in windows of 500:
+// 42.5 us, 0.25 of the rate: a block's chain from scores to weights takes
+// longer than its products, and a third of the time is the start and end of
+// some 900 short tiles.  32 requests of 6 rows: 24.7 us, 2.9 TB/s; with the L2
+// flushed, in a trace: 6 us from the launch to the first copy, 11 us of copies
+// at the full HBM rate, then the last block, and 5 us in which a cluster joins.
 #pragma once
 #include <cuda.h>
 
