@@ -766,6 +766,7 @@ def test_first_calls_inside_a_capture():
     """A fresh process whose first use of the calls is a stream capture.  A
     block of ones is held as 6 * 11/64: e4m3 has 10/64 and 11/64 around 1/6,
     and 64/11 is nearer to 6 than to 4."""
+    import pathlib
     import subprocess
     import sys
     code = """
@@ -792,7 +793,8 @@ assert qsa.device_status() == 0
 assert ((a[0] - 66 / 64).abs() < 1e-6).all() and (b[0] == 1).all() and (d[0] == 1).all() and torch.isfinite(e[0]).all()
 print('fine')
 """
-    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    root = pathlib.Path(__file__).resolve().parents[1]
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
 
 def test_cache4_offsets_past_32_bits(qsa):
