@@ -47,6 +47,23 @@
 //    like that of the output; l sums them before the rounding, in FP32.
 // Tensor memory columns: O [0, D), S two times 128, P in the first 64 of its S.
 //
+// Waits on stages.  The ring's uses are numbered in the order K(0), K(1),
+// V(0), K(2), V(1), ... over all tiles; use u is in stage u mod kStages, and
+// its phase u / kStages of that stage's barriers.  A wait by parity passes
+// wrongly where the phase before the awaited one may still be open, so each
+// role has to know by other means that use u - kStages has been there:
+//  - warp 9 waits for every use in turn, so for u - kStages itself.
+//  - warps 8 and 11 wait for `empty` of u - kStages and must know that u - 2
+//    kStages is used up: each use of their own before that was waited for, the
+//    gap between two of them is at most kStages, and stages are freed in order.
+//  - warps 0-7 wait for some V stages only.  S(blk) is there, so K(0..blk) and
+//    V(0..blk-2) were; the second V stage of a block between the first and the
+//    last at D = 256 takes the place of the first of V(blk-1), of which that
+//    says nothing (copies end in any order).  So they wait for PV(blk-1) first;
+//    before block 0, the tile before has been waited for to its end.
+// One thread issues all products and commits, and the arrivals of its commits
+// come in order: a commit waits for every product before it.
+//
 // Entries.  With `start` the first window position of the tile rounded down
 // to a box, the entries are the boxes of the first tokens before `start`
 // (nsr of them, rounded up to a box; all lie below start), then the positions
@@ -970,6 +987,9 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         // V rows that no pair sees: zeros
         const int n16 = (min(N, w.uc - e0) + 15) & ~15;
         if (e0 < w.ub || e0 + n16 > w.uc) {
+          // the stages' earlier contents have landed: see "Waits on stages"
+          ok = blk == 0 || wt_wait(&ctl.pv_done[sl ^ 1], (uint32_t)((x - 1) >> 1) & 1u, abort);
+          if (!ok) break;
           const int at = rs + Sh::kKs * min(blk + 2, w.n_blk) + blk * Sh::kVs;  // V's first stage
           for (int v = 0; ok && v * Sh::kVRows < n16; ++v) {
             const int st = (at + v) % Sh::kStages;
