@@ -591,7 +591,9 @@ __device__ __forceinline__ void wt_join(const WtArgs& a, const WtTile& w, unsign
   const float ninf = -__int_as_float(0x7f800000);
   const int vecs = S / 8, n = w.rows * a.group * vecs;  // 8 columns a thread, a row's next to each other
   for (int i0 = 0; i0 < n; i0 += 256) {
-    const int i = min(i0 + (int)threadIdx.x, n - 1);  // the same once more behind the end
+    // behind the end the last one once more, not written: another warp may have summed it again by then
+    const bool own = i0 + (int)threadIdx.x < n;
+    const int i = own ? i0 + (int)threadIdx.x : n - 1;
     const int p = i / vecs, v = i - p * vecs;
     float mx = ninf, ls = 0.f, acc[8] = {};
     for (int s = 0; s < C; ++s) mx = fmaxf(mx, lm[s * 256 + 128 + p]);
@@ -619,11 +621,11 @@ __device__ __forceinline__ void wt_join(const WtArgs& a, const WtTile& w, unsign
     }
     const int row = p / a.group;
     const int64_t hq = (int64_t)(w.t0 + row) * a.h_q + (int64_t)w.g * a.group + (p - row * a.group);
-    *reinterpret_cast<uint4*>(a.out + hq * D + rank * S + v * 8) = make_uint4(y[0], y[1], y[2], y[3]);
-    if (rank == 0 && v == 0 && a.lse != nullptr)
+    if (own) *reinterpret_cast<uint4*>(a.out + hq * D + rank * S + v * 8) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (own && rank == 0 && v == 0 && a.lse != nullptr)
       a.lse[hq] = ls == 0.f ? ninf : mx == ninf ? ls : fmaf(mx, a.c, log2f(ls)) * 0.69314718055994531f;
     __syncwarp();
-    wt_redo_lanes<D>(a, w, broken != broken && i == i0 + (int)threadIdx.x, p, rank * S + v * 8, 8, mx, ls);
+    wt_redo_lanes<D>(a, w, broken != broken && own, p, rank * S + v * 8, 8, mx, ls);
   }
 }
 

@@ -1,0 +1,51 @@
+"""window_attn in its tensor-core form, where roles of a CTA and the CTAs of a
+cluster have to keep out of each other's way."""
+import numpy as np
+import pytest
+
+import kv4_ref as ref
+from gpu_util import bf16_dev, to_dev
+from test_gpu_kv4 import (BF16_HALF_STEP, W_BF16, bits_to_f64, host, no_fault_left, page_table,  # noqa: F401
+                          qsa, window_check)
+from workloads.synth import normal_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+def check_clean_rows(qsa, q, k, v, pt, lens, page, max_len, window, n_sink, broken, rows=None):  # noqa: F811
+    """One request of len(lens) rows in tiles; positions `broken` hold infinities
+    or NaN: rows that see none of them get the formula's values.  Returns how many."""
+    d = q.shape[-1]
+    n = len(lens)
+    out, lse = qsa.window_attn(*map(bf16_dev, (q, k, v)), to_dev(np.array([0, n], np.int32)), to_dev(lens), to_dev(pt),
+                               page, max_len, window, n_sink, max_rows_per_req=max(n, 17))
+    o, l, kf, vf = bits_to_f64(out), host(lse).astype(np.float64), ref.bf16_to_f64(k), ref.bf16_to_f64(v)
+    clean = 0
+    for t in range(n) if rows is None else rows:
+        pos = ref.window_positions(lens[t], window, n_sink)
+        if np.isin(broken, pos).any():
+            continue
+        clean += 1
+        sl = ref.slots_of(pt[0], pos, page)
+        ro, rl, a, big, spread = ref.attend(ref.bf16_to_f64(q[t]), kf[sl], vf[sl], d ** -0.5)
+        tol, tol_l = ref.tolerance(d, pos.size, ro, a, big, spread, W_BF16, BF16_HALF_STEP, False, 0.0)
+        assert (np.abs(o[t] - ro) <= tol).all(), t
+        assert (np.abs(l[t] - rl) <= tol_l + 2.0 ** -23 * np.abs(rl)).all(), t
+    return clean
+
+
+@pytest.mark.parametrize("h_q,d,rows", [(3, 256, 42), (3, 256, 40), (7, 128, 17), (3, 128, 37), (1, 256, 90)])
+@pytest.mark.parametrize("window", [300, 500, 1200])
+def test_broken_values_in_a_shared_tile_of_odd_size(qsa, h_q, d, rows, window):  # noqa: F811
+    """Tiles whose pairs do not fill whole passes of the join's threads."""
+    rng = np.random.default_rng(50 + rows + window)
+    page, ctx = 32, 1500
+    pt, n_slots = page_table(rng, [ctx], page)
+    k, v, q = (normal_bf16(rng, s) for s in ((n_slots, 1, d), (n_slots, 1, d), (rows, h_q, d)))
+    lens = np.arange(ctx - rows + 1, ctx + 1).astype(np.int32)
+    lens = lens[rng.permutation(rows)]
+    lens[-1] = ctx - rows + 1  # the tile's last row sees none of them
+    broken = [ctx - 1, ctx - 2, ctx - rows // 2]
+    for i, p in enumerate(broken):
+        v[ref.slots_of(pt[0], np.array([p]), page)[0], 0, i::2] = (0x7FC0, 0x7F80, 0xFF80)[i]
+    assert check_clean_rows(qsa, q, k, v, pt, lens, page, ctx, window, 2, broken) >= rows // 4
