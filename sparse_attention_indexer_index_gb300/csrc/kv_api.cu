@@ -304,8 +304,8 @@ qsa_status launch_window_tc(const KvAttnArgs& k, int d, cudaStream_t stream) {
   a.flip = k.scale < 0.f ? 0x80000000u : 0u;
   a.out = static_cast<uint16_t*>(k.out);
   a.lse = k.lse;
-  // 32 pairs of a warp at some 100 clocks an entry, with room
-  a.wait_ms = 200 + (int)(window_entries(k.max_len, k.window, k.n_sink) / 128);
+  // the longest wait is for a whole tile: blocks of 128 entries at about a microsecond, with room
+  a.wait_ms = 200 + k.max_len / 4096;
   const int64_t units = (int64_t)a.tile_slots * a.h_kv;
   if (units > (1 << 30) || k.max_len > (1 << 30)) return QSA_ERR_UNSUPPORTED;
   const KvDevice* dev = nullptr;

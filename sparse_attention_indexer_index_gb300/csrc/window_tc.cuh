@@ -85,6 +85,9 @@
 // at the full HBM rate, then the last block, and 5 us in which a cluster joins.
 #pragma once
 #include <cuda.h>
+#include <string.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kv_attn.cuh"
@@ -135,7 +138,7 @@ struct WtArgs {
   uint32_t flip;             // sign bit to flip in S (a negative scale)
   uint16_t* out;             // [n_rows][h_q][D] BF16
   float* lse;                // [n_rows][h_q] or nullptr
-  int32_t wait_ms;           // limit of a wait: 200, and what wt_redo may take meanwhile
+  int32_t wait_ms;           // limit of a wait, without what wt_redo adds to it
 };
 
 // tcgen05.ld with its wait in one statement, so that no use of the registers
@@ -471,7 +474,9 @@ __device__ __forceinline__ void wt_arrive_all(uint64_t* bar, int n_cta) {
   if (lane < n_cta)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_shared_rank(bar, lane)) : "memory");
 }
-// Wait (bounded) for arrivals from the cluster: phase 0, by a whole warp.
+// Wait (bounded) for arrivals from the cluster: phase 0, by a whole warp.  No
+// CTA of it has summed rows once more by then (see wt_redo): tiles are shared
+// where there are fewer of them than CTAs, so a shared one is its CTAs' first.
 __device__ __forceinline__ bool wt_wait_cluster(uint64_t* bar, volatile int* abort) {
   auto arrived = [&]() -> bool {
     uint32_t done;
@@ -507,28 +512,69 @@ __device__ __forceinline__ void wt_tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
 // an infinity or a NaN, the sum becomes NaN for rows that do not see it.  So an
 // output that is not finite though its l is, is summed once more over the
 // row's own entries, from the cache: `cols` columns from col0 on of one (row,
-// head), by a whole warp.  m and l come from the row's own entries alone.
-// Slow (a warp takes about 100 clocks an entry), and only then.
+// head), by a whole warp, four entries at a time.  m and l come from the row's
+// own entries alone.  Slow (a warp takes 270 to 300 clocks an entry, a tile of
+// 128 pairs over 65,601 entries 0.3 s), and only then.  The roles that wait for
+// this warp meanwhile must not give up: the time it takes is added to the CTA's
+// limit as it passes, a millisecond or more at a time (less than that for each
+// of a warp's 32 pairs is within the limit as it is).
 template <int D>
 __device__ __noinline__ void wt_redo(const WtArgs& a, int req, int64_t t, int g, int head, int col0, int cols, float m,
-                                     float l) {
-  constexpr int kPer = D / 32;
+                                     float l, volatile int* abort) {
+  constexpr int kPer = D / 32, kU = 4;  // dimensions of a lane, entries at a time
+  using Piece = typename std::conditional<D == 256, uint4, uint2>::type;
   const int lane = threadIdx.x & 31;
   const int L = __ldg(a.row_len + t), lo = max(0, L - a.window), n_first = min(a.n_sink, lo);
+  const int n = n_first + L - lo;
+  uint64_t t0 = global_timer_ns();
   const int32_t* pt = a.page_table + (int64_t)req * a.ld_pt;
   float q[kPer], acc[D / 64] = {};
   for (int j = 0; j < kPer; ++j) q[j] = __uint_as_float((uint32_t)a.q[t * a.ld_q + head * D + lane * kPer + j] << 16);
-  for (int e = 0; e < n_first + L - lo; ++e) {
-    const int pos = e < n_first ? e : lo + e - n_first;
-    const int64_t page = __ldg(pt + pos / a.page_size);
-    if (page < 0 || (page + 1) * a.page_size > a.n_slots) continue;
-    const int64_t at = ((page * a.page_size + pos % a.page_size) * a.h_kv + g) * D;
-    float x = 0.f;
-    for (int j = 0; j < kPer; ++j) x = fmaf(q[j], __uint_as_float((uint32_t)a.k[at + lane * kPer + j] << 16), x);
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    const float p = ka_ex2((__uint_as_float(__float_as_uint(x) ^ a.flip) - m) * a.c);
-    for (int j = 0; j < D / 64; ++j)
-      if (lane + 32 * j < cols) acc[j] = fmaf(p, __uint_as_float((uint32_t)a.v[at + col0 + lane + 32 * j] << 16), acc[j]);
+  for (int e0 = 0; e0 < n; e0 += 32) {
+    const uint64_t t1 = global_timer_ns();
+    if (t1 - t0 >= 1000000u) {
+      if (lane == 0) atomicAdd(const_cast<int*>(abort) + 1, (int)((t1 - t0) / 1000000u) + 1);  // WtCtl::wait_ms
+      t0 = t1;
+    }
+    int64_t own = -1;  // where the lane's entry lies; -1: none, or on a page out of range
+    if (e0 + lane < n) {
+      const int e = e0 + lane, pos = e < n_first ? e : lo + e - n_first;
+      const int64_t page = __ldg(pt + pos / a.page_size);
+      if (page >= 0 && (page + 1) * a.page_size <= a.n_slots)
+        own = ((page * a.page_size + pos % a.page_size) * a.h_kv + g) * D;
+    }
+    for (int i0 = 0; i0 < min(32, n - e0); i0 += kU) {
+      float x[kU];
+      uint16_t v[kU][D / 64];  // loads without a branch: behind one, each waits for itself
+      int64_t at[kU];
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        at[i] = __shfl_sync(0xffffffffu, own, i0 + i);
+        const int64_t from = max(at[i], (int64_t)0);
+        const Piece piece = *reinterpret_cast<const Piece*>(a.k + from + lane * kPer);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) v[i][j] = a.v[from + col0 + min(lane + 32 * j, cols - 1)];
+        uint32_t w[kPer / 2];
+        memcpy(w, &piece, sizeof(piece));
+        x[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kPer / 2; ++j) {
+          const float2 f = bf16x2_to_float2(w[j]);
+          x[i] = fmaf(q[2 * j + 1], f.y, fmaf(q[2 * j], f.x, x[i]));
+        }
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < kU; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], d);
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        if (at[i] < 0) continue;  // the same in all lanes
+        const float p = ka_ex2((__uint_as_float(__float_as_uint(x[i]) ^ a.flip) - m) * a.c);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) acc[j] = fmaf(p, __uint_as_float((uint32_t)v[i][j] << 16), acc[j]);
+      }
+    }
   }
   uint16_t* out = a.out + (t * a.h_q + head) * D + col0;
   for (int j = 0; j < D / 64; ++j)
@@ -537,14 +583,14 @@ __device__ __noinline__ void wt_redo(const WtArgs& a, int req, int64_t t, int g,
 // wt_redo for the lanes that ask for it, one after the other.
 template <int D>
 __device__ __forceinline__ void wt_redo_lanes(const WtArgs& a, const WtTile& w, bool ask, int pair, int col0, int cols,
-                                              float m, float l) {
+                                              float m, float l, volatile int* abort) {
   unsigned todo = __ballot_sync(0xffffffffu, ask && l != 0.f && l == l);
   while (todo != 0) {
     const int i = __ffs(todo) - 1;
     todo &= todo - 1;
     const int p = __shfl_sync(0xffffffffu, pair, i), row = p / a.group;
     wt_redo<D>(a, w.r, w.t0 + row, w.g, w.g * a.group + p - row * a.group, __shfl_sync(0xffffffffu, col0, i), cols,
-               __shfl_sync(0xffffffffu, m, i), __shfl_sync(0xffffffffu, l, i));
+               __shfl_sync(0xffffffffu, m, i), __shfl_sync(0xffffffffu, l, i), abort);
   }
 }
 
@@ -625,7 +671,7 @@ __device__ __forceinline__ void wt_join(const WtArgs& a, const WtTile& w, unsign
     if (own && rank == 0 && v == 0 && a.lse != nullptr)
       a.lse[hq] = ls == 0.f ? ninf : mx == ninf ? ls : fmaf(mx, a.c, log2f(ls)) * 0.69314718055994531f;
     __syncwarp();
-    wt_redo_lanes<D>(a, w, broken != broken && own, p, rank * S + v * 8, 8, mx, ls);
+    wt_redo_lanes<D>(a, w, broken != broken && own, p, rank * S + v * 8, 8, mx, ls, abort);
   }
 }
 
@@ -1082,7 +1128,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       tc_fence_before();
       __syncwarp();
       wt_redo_lanes<D>(a, w, mine && !(__low2float(broken2) + __high2float(broken2) == 0.f), pair, half * (D / 2), D / 2,
-                       m, l);
+                       m, l, abort);
       if (mine && half == 0 && a.lse != nullptr)
         a.lse[hq] = l == 0.f ? ninf : (m == ninf ? l : (fmaf(m, a.c, log2f(l))) * 0.69314718055994531f);
     }

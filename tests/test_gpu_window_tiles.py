@@ -49,3 +49,36 @@ def test_broken_values_in_a_shared_tile_of_odd_size(qsa, h_q, d, rows, window): 
     for i, p in enumerate(broken):
         v[ref.slots_of(pt[0], np.array([p]), page)[0], 0, i::2] = (0x7FC0, 0x7F80, 0xFF80)[i]
     assert check_clean_rows(qsa, q, k, v, pt, lens, page, ctx, window, 2, broken) >= rows // 4
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("ctx", [65_601, 262_209])
+def test_broken_values_in_a_long_window_hold_up_the_next_tile(qsa, ctx, d):  # noqa: F811
+    """A tile of 16 heads and 8 rows over a long window, the last row's own V
+    broken: the other rows are summed once more, entry by entry, for longer than
+    the limit of a wait, while the CTA's other roles wait with the next tile."""
+    rng = np.random.default_rng(51 + d)
+    page, h_q, n_req, own = 64, 128 * 16 // d, 170, 40
+    rows = 128 // h_q
+    n_pages = -(-ctx // page)
+    pt = np.full((n_req, n_pages), -1, np.int32)
+    pt[0] = rng.integers(0, own, n_pages)  # positions share pages: they are only read
+    pt[0, -1] = own                        # but for the last, which holds the broken one
+    pt[1:, :2] = rng.integers(0, own, (n_req - 1, 2))
+    k, v = (normal_bf16(rng, ((own + 1) * page, 1, d)) for _ in range(2))
+    v[ref.slots_of(pt[0], np.array([ctx - 1]), page)[0], 0, ::3] = 0x7FC0
+    lens = np.concatenate([np.arange(ctx - rows + 1, ctx + 1)] + [np.arange(91, 91 + rows)] * (n_req - 1)).astype(np.int32)
+    q = normal_bf16(rng, (rows * n_req, h_q, d))
+    start = (np.arange(n_req + 1) * rows).astype(np.int32)
+    out, lse = qsa.window_attn(*map(bf16_dev, (q, k, v)), to_dev(start), to_dev(lens), to_dev(pt), page, ctx, ctx,
+                               max_rows_per_req=17)
+    assert qsa.device_status() == 0
+    o, l, kf, vf = bits_to_f64(out), host(lse).astype(np.float64), ref.bf16_to_f64(k), ref.bf16_to_f64(v)
+    assert np.isnan(o[rows - 1][:, ::3]).all()
+    for t in [0, rows - 2, *range(rows, rows * n_req, 97)]:
+        r = t // rows
+        sl = ref.slots_of(pt[r], np.arange(lens[t]), page)
+        ro, rl, a, big, spread = ref.attend(ref.bf16_to_f64(q[t]), kf[sl], vf[sl], d ** -0.5)
+        tol, tol_l = ref.tolerance(d, sl.size, ro, a, big, spread, W_BF16, BF16_HALF_STEP, False, 0.0)
+        assert (np.abs(o[t] - ro) <= tol).all(), t
+        assert (np.abs(l[t] - rl) <= tol_l + 2.0 ** -23 * np.abs(rl)).all(), t
