@@ -89,6 +89,14 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 __device__ __forceinline__ void pdl_wait_primary() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+// Load of what an earlier kernel may still be writing while this one already
+// runs and waits for it: an ordinary load, which stays behind the wait.  (The
+// read-only loads, __ldg and ld.global.nc, are for data that nothing writes
+// while the kernel runs, and the compiler may move them ahead of it.)
+template <class T>
+__device__ __forceinline__ T ld_in(const T* p) {
+  return *p;
+}
 
 // ---------------------------------------------------------------------------
 // mbarrier + bulk asynchronous copy (TMA engine, no tensor map) helpers.

@@ -36,16 +36,18 @@ namespace qsa {
 constexpr int kKvBlock = 16;     // values per scale
 constexpr int kKvThreads = 128;  // threads per CTA of the write and read kernels
 
-// 32 bytes in one instruction (32-byte aligned).
+// 32 bytes in one instruction (32-byte aligned), read once.  As ld_in, it stays
+// where it is written.
 struct U8 {
   uint32_t w[8];
 };
 __device__ __forceinline__ U8 ld_stream_32(const void* p) {
   U8 r;
-  asm("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
-        "=r"(r.w[7])
-      : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                 "=r"(r.w[7])
+               : "l"(p)
+               : "memory");
   return r;
 }
 __device__ __forceinline__ void st_32(void* p, const U8& r) {
@@ -139,13 +141,13 @@ __device__ __forceinline__ U8 kv4_read(uint2 codes, uint32_t scale, float g) {
 // or -1 when t lies behind start[n_req] (or before start[0]).  32 samples a
 // round, so one round trip to memory for up to 32 requests and two for up to
 // 1024 (a binary search takes five and ten).
-__device__ __forceinline__ int warp_row_request(const int32_t* __restrict__ start, int n_req, int t) {
+__device__ __forceinline__ int warp_row_request(const int32_t* start, int n_req, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = n_req + 1;  // candidates lo .. lo + n - 1 of the last start <= t
   while (true) {
     const int step = (n + 31) / 32;
     const int i = lane * step;
-    const bool le = i < n && __ldg(start + lo + i) <= t;
+    const bool le = i < n && ld_in(start + lo + i) <= t;
     const int c = __popc(__ballot_sync(0xffffffffu, le));  // starts do not decrease
     if (c == 0) return -1;
     lo += (c - 1) * step;
@@ -195,15 +197,15 @@ append_kv_fp4_kernel(KvWriteArgs a) {
   }
   int r = warp_row_request(a.req_tok_start, a.n_req, (int)(u0 / (uint32_t)a.blocks));  // of the warp's first token
   if (!ok || r < 0) return;  // r < 0: behind the last request, as the rest of the warp
-  while (r < a.n_req && t >= __ldg(a.req_tok_start + r + 1)) ++r;  // a warp may span tokens
+  while (r < a.n_req && t >= ld_in(a.req_tok_start + r + 1)) ++r;  // a warp may span tokens
   if (r >= a.n_req) return;
-  const int64_t pos = (int64_t)__ldg(a.req_first_pos + r) + (t - __ldg(a.req_tok_start + r));
+  const int64_t pos = (int64_t)ld_in(a.req_first_pos + r) + (t - ld_in(a.req_tok_start + r));
   const int pi = pos < 0 || pos > INT32_MAX ? INT32_MAX : (int)pos / a.page_size;
   if (pi >= a.ld_pt) {
     raise_fault(kFaultIndex);
     return;
   }
-  const int64_t page = __ldg(a.page_table + (int64_t)r * a.ld_pt + pi);
+  const int64_t page = ld_in(a.page_table + (int64_t)r * a.ld_pt + pi);
   const int64_t slot = page * a.page_size + ((int)pos - pi * a.page_size);
   if (page < 0 || slot >= a.n_slots) {
     raise_fault(kFaultIndex);
@@ -239,13 +241,13 @@ gather_kv_fp4_kernel(KvReadArgs a) {
   pdl_wait_primary();
   const uint32_t i = u / (uint32_t)a.blocks;
   const int b = (int)(u - i * (uint32_t)a.blocks);
-  const int32_t s = __ldg(a.slots + i);
+  const int32_t s = ld_in(a.slots + i);
   U8 k{}, v{};
   if (s >= 0 && s < a.n_slots) {
     const int64_t at = (int64_t)s * a.blocks + b;
-    const uint2 ck = __ldg(reinterpret_cast<const uint2*>(a.k_codes) + at);
-    const uint2 cv = __ldg(reinterpret_cast<const uint2*>(a.v_codes) + at);
-    const uint32_t sk = __ldg(a.k_scales + at), sv = __ldg(a.v_scales + at);
+    const uint2 ck = ld_in(reinterpret_cast<const uint2*>(a.k_codes) + at);
+    const uint2 cv = ld_in(reinterpret_cast<const uint2*>(a.v_codes) + at);
+    const uint32_t sk = ld_in(a.k_scales + at), sv = ld_in(a.v_scales + at);
     k = kv4_read(ck, sk, a.k_g);
     v = kv4_read(cv, sv, a.v_g);
   } else if (s >= 0 && b == 0) {

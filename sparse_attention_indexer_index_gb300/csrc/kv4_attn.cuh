@@ -101,7 +101,7 @@ kv4_attn_kernel(const __grid_constant__ KvAttnArgs a) {
     for (int i = 0; i < D / 32; ++i) {
       // the lane's K pieces hold 32 dimensions each, four of q's
       const int piece = (tq + 4 * (i >> 2)) * 4 + (i & 3);
-      const uint4 u = h < a.group ? __ldg(reinterpret_cast<const uint4*>(src) + piece) : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 u = h < a.group ? ld_in(reinterpret_cast<const uint4*>(src) + piece) : make_uint4(0u, 0u, 0u, 0u);
       qa[nt][2 * i][0] = u.x;
       qa[nt][2 * i][1] = u.y;
       qa[nt][2 * i + 1][0] = u.z;

@@ -189,10 +189,10 @@ __device__ __forceinline__ KaFetch ka_fetch(const KvAttnArgs& a, const KaRow<kWi
   if constexpr (kWindow) {
     const int pos = e < r.sinks ? e : r.lo + (e - r.sinks);
     const int pi = pos / a.page_size;  // < ld_pt: pos < max_len
-    f.raw = __ldg(r.p + pi);
+    f.raw = ld_in(r.p + pi);
     f.off = pos - pi * a.page_size;
   } else {
-    f.raw = __ldg(r.p + e);
+    f.raw = ld_in(r.p + e);
   }
   return f;
 }
@@ -220,7 +220,7 @@ __device__ __forceinline__ int32_t ka_slot(const KvAttnArgs& a, const KaRow<kWin
 template <bool kWindow>
 __device__ __forceinline__ bool ka_row(const KvAttnArgs& a, int t, KaRow<kWindow>& row) {
   if constexpr (kWindow) {
-    int L = __ldg(a.row_len + t);
+    int L = ld_in(a.row_len + t);
     const int r = warp_row_request(a.req_row_start, a.n_req, t);
     if (r < 0) return false;
     if (L < 0 || L > a.max_len) {
@@ -419,7 +419,7 @@ kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int piece = tq + 4 * i;  // 8 of every 32 dimensions
-      const uint4 u = h < a.group ? __ldg(reinterpret_cast<const uint4*>(src) + piece) : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 u = h < a.group ? ld_in(reinterpret_cast<const uint4*>(src) + piece) : make_uint4(0u, 0u, 0u, 0u);
       qa[nt][2 * i][0] = u.x;
       qa[nt][2 * i][1] = u.y;
       qa[nt][2 * i + 1][0] = u.z;
@@ -586,7 +586,7 @@ kv_attn_merge_kernel(const __grid_constant__ KvAttnArgs a, float bias) {
   pdl_wait_primary();
   const int64_t hq = blockIdx.x;
   if (a.n_req > 0) {  // window rows behind the last request are left as they were
-    if ((int)(hq / a.h_q) >= __ldg(a.req_row_start + a.n_req)) return;
+    if ((int)(hq / a.h_q) >= ld_in(a.req_row_start + a.n_req)) return;
   }
   const int e = threadIdx.x;
   const float ninf = -__int_as_float(0x7f800000);

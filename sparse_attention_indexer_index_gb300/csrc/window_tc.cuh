@@ -287,7 +287,7 @@ struct WtTile {
 // Tiles of request i; 0 where the grouping is wrong.
 __device__ __forceinline__ int wt_request_tiles(const WtArgs& a, int i) {
   if (i >= a.n_req) return 0;
-  const int row0 = __ldg(a.req_row_start + i), row1 = __ldg(a.req_row_start + i + 1);
+  const int row0 = ld_in(a.req_row_start + i), row1 = ld_in(a.req_row_start + i + 1);
   if (row0 < 0 || row1 < row0 || row1 > a.n_rows) {
     raise_fault(kFaultGrouping);
     return 0;
@@ -341,14 +341,14 @@ __device__ __forceinline__ int wt_find_slot(const WtArgs& a, int s, int& rank) {
   while (true) {
     const int step = (n + 31) / 32;
     const int i = lane * step;
-    const bool le = i < n && __ldg(a.req_row_start + lo + i) / a.rows + lo + i <= s;
+    const bool le = i < n && ld_in(a.req_row_start + lo + i) / a.rows + lo + i <= s;
     const int k = max(1, __popc(__ballot_sync(0xffffffffu, le)));
     lo += (k - 1) * step;
     n = min(step, n - (k - 1) * step);
     if (step == 1) break;
   }
   if (lo >= a.n_req) return -1;
-  rank = s - (__ldg(a.req_row_start + lo) / a.rows + lo);
+  rank = s - (ld_in(a.req_row_start + lo) / a.rows + lo);
   return rank < wt_request_tiles(a, lo) ? lo : -1;
 }
 
@@ -358,12 +358,12 @@ __device__ __forceinline__ WtTile wt_tile(const WtArgs& a, int r, int rank, int 
   WtTile w{};
   w.r = r;
   w.parts = parts;
-  w.t0 = __ldg(a.req_row_start + r) + rank * a.rows;
-  w.rows = min(a.rows, __ldg(a.req_row_start + r + 1) - w.t0);
+  w.t0 = ld_in(a.req_row_start + r) + rank * a.rows;
+  w.rows = min(a.rows, ld_in(a.req_row_start + r + 1) - w.t0);
   const int t0 = w.t0;
   int first = INT32_MAX, last = 0;
   for (int i = lane; i < w.rows; i += 32) {
-    const int L = __ldg(a.row_len + t0 + i);
+    const int L = ld_in(a.row_len + t0 + i);
     if (L < 0 || L > a.max_len) {
       raise_fault(kFaultGrouping);
     } else if (L > 0) {
@@ -524,7 +524,7 @@ __device__ __noinline__ void wt_redo(const WtArgs& a, int req, int64_t t, int g,
   constexpr int kPer = D / 32, kU = 4;  // dimensions of a lane, entries at a time
   using Piece = typename std::conditional<D == 256, uint4, uint2>::type;
   const int lane = threadIdx.x & 31;
-  const int L = __ldg(a.row_len + t), lo = max(0, L - a.window), n_first = min(a.n_sink, lo);
+  const int L = ld_in(a.row_len + t), lo = max(0, L - a.window), n_first = min(a.n_sink, lo);
   const int n = n_first + L - lo;
   uint64_t t0 = global_timer_ns();
   const int32_t* pt = a.page_table + (int64_t)req * a.ld_pt;
@@ -539,7 +539,7 @@ __device__ __noinline__ void wt_redo(const WtArgs& a, int req, int64_t t, int g,
     int64_t own = -1;  // where the lane's entry lies; -1: none, or on a page out of range
     if (e0 + lane < n) {
       const int e = e0 + lane, pos = e < n_first ? e : lo + e - n_first;
-      const int64_t page = __ldg(pt + pos / a.page_size);
+      const int64_t page = ld_in(pt + pos / a.page_size);
       if (page >= 0 && (page + 1) * a.page_size <= a.n_slots)
         own = ((page * a.page_size + pos % a.page_size) * a.h_kv + g) * D;
     }
@@ -805,7 +805,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
         const int e = (w.j0 + j) << sh;
         const int pos = e < w.nsr ? e : w.start + (e - w.nsr);
         const int pi = pos / a.page_size;
-        const int64_t page = __ldg(pt + pi);
+        const int64_t page = ld_in(pt + pi);
         if (page < 0 || (page + 1) * a.page_size > a.n_slots) return oob;
         return (int)((page * a.page_size + (pos - pi * a.page_size)) >> 3);
       };
@@ -948,7 +948,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       const bool mine = row < w.rows;
       const int64_t t = w.t0 + row;
       int L = next_len;
-      if (!ahead) L = mine ? __ldg(a.row_len + t) : 0;
+      if (!ahead) L = mine ? ld_in(a.row_len + t) : 0;
       if (L < 0 || L > a.max_len) L = 0;
       const int64_t hq = t * a.h_q + (int64_t)w.g * a.group + hd;
       m = ninf;
@@ -1072,7 +1072,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       {
         const int sl = (k + 1) % kWtTileRing;
         ahead = __all_sync(0xffffffffu, mbar_try_wait(&ctl.tile_full[sl], (uint32_t)((k + 1) / kWtTileRing) & 1u));
-        if (ahead) next_len = row < ctl.tile[sl].rows ? __ldg(a.row_len + ctl.tile[sl].t0 + row) : 0;
+        if (ahead) next_len = row < ctl.tile[sl].rows ? ld_in(a.row_len + ctl.tile[sl].t0 + row) : 0;
       }
       // ---- outputs ---------------------------------------------------------------------
       float inv = 0.f;
