@@ -59,7 +59,7 @@ struct ScoreArgs {
 
 // Gate of (row, head): 1 without gates (then the products below are exact).
 __device__ __forceinline__ float head_gate(const float* gates, int64_t row, int head) {
-  return gates != nullptr ? __ldg(gates + row * kHeads + head) : 1.f;
+  return gates != nullptr ? ld_in(gates + row * kHeads + head) : 1.f;
 }
 
 constexpr int kScoreThreads = 256;
@@ -94,14 +94,14 @@ __device__ __forceinline__ float reduce_scatter4_x16(float a0, float a1, float a
 
 // Visible blocks of request r: the longest of its rows, / 4.
 __device__ __forceinline__ int request_blocks(const ScoreArgs& a, int r) {
-  const int row0 = __ldg(a.req_row_start + r), row1 = __ldg(a.req_row_start + r + 1);
+  const int row0 = ld_in(a.req_row_start + r), row1 = ld_in(a.req_row_start + r + 1);
   if (row0 < 0 || row1 < row0 || row1 > a.n_rows) {
     raise_fault(kFaultGrouping);
     return 0;
   }
   int nb = 0;
   for (int t = row0; t < row1; ++t) {
-    int L = __ldg(a.row_len + t);
+    int L = ld_in(a.row_len + t);
     if (L < 0 || L > a.max_len) { raise_fault(kFaultGrouping); L = 0; }
     nb = max(nb, L / kBlock);
   }
@@ -122,7 +122,7 @@ __device__ __forceinline__ void load_tile_keys(const ScoreArgs& a, int r, int j,
     if (b < nb_req) {
       const int page_idx = b / kpp;
       if (page_idx < a.ld_pt) {
-        const int64_t page = __ldg(pt_row + page_idx);
+        const int64_t page = ld_in(pt_row + page_idx);
         const int64_t row = page * kpp + (b - page_idx * kpp);
         if (page >= 0 && row < a.pool_rows) kv[u] = ld_stream_16(a.pool + row * kDim + 8 * lane16);
         else if (lane16 == 0) raise_fault(kFaultPool);
@@ -228,7 +228,7 @@ score_decode_kernel(ScoreArgs a) {
     }
     cur_r = r;
 
-    const int row0 = __ldg(a.req_row_start + r), row1 = __ldg(a.req_row_start + r + 1);
+    const int row0 = ld_in(a.req_row_start + r), row1 = ld_in(a.req_row_start + r + 1);
     const int b_base = j * kScoreTile;
     for (int g0 = row0; g0 < row1; g0 += kScoreRowGroup) {
       const int g1 = min(row1, g0 + kScoreRowGroup);
@@ -238,13 +238,13 @@ score_decode_kernel(ScoreArgs a) {
         const int pieces = (g1 - g0) * (kHeads * kDim / 8);
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)g0 * kHeads * kDim);
         uint4* dst = reinterpret_cast<uint4*>(&sh.q[0][0][0]);
-        for (int i = threadIdx.x; i < pieces; i += kScoreThreads) dst[i] = __ldg(src + i);
+        for (int i = threadIdx.x; i < pieces; i += kScoreThreads) dst[i] = ld_in(src + i);
         __syncthreads();
         staged_r = r;
         staged_g0 = g0;
       }
       for (int t = g0; t < g1; ++t) {
-        const int L = __ldg(a.row_len + t);
+        const int L = ld_in(a.row_len + t);
         const int nb_t = (L < 0 || L > a.max_len) ? 0 : L / kBlock;
         float* srow = a.scores + (int64_t)t * a.ld_scores;
         if (b_base < nb_t) {

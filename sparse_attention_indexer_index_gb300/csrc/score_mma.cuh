@@ -135,10 +135,10 @@ __global__ void __launch_bounds__(kSmThreads, kSmMinCtas) score_mma_kernel(Score
   const bool single = a.n_req == 1;
   int pf_rs0 = 0, pf_rs1 = 0, pf_np = 0, pf_len = 0;
   if (single) {
-    pf_rs0 = __ldg(a.req_row_start);
-    pf_rs1 = __ldg(a.req_row_start + 1);
-    if (relaxed) pf_np = __ldg(a.new_pos);
-    if (lane < min(a.n_rows, 2 * NT)) pf_len = __ldg(a.row_len + lane);
+    pf_rs0 = ld_in(a.req_row_start);
+    pf_rs1 = ld_in(a.req_row_start + 1);
+    if (relaxed) pf_np = ld_in(a.new_pos);
+    if (lane < min(a.n_rows, 2 * NT)) pf_len = ld_in(a.row_len + lane);
   }
 
   // ---- tile list: ceil(nb_r / 16) tiles per request, prefix in shared memory
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kSmThreads, kSmMinCtas) score_mma_kernel(Score
       raise_fault(kFaultIndex);
       return -1;
     }
-    const int64_t page = __ldg(a.page_table + (int64_t)r * a.ld_pt + page_idx);
+    const int64_t page = ld_in(a.page_table + (int64_t)r * a.ld_pt + page_idx);
     const int64_t row = page * kpp + (int64_t)(b - page_idx * kpp);
     if (page < 0 || row >= a.pool_rows) {
       if (single) return kRunBadPool;
@@ -254,13 +254,13 @@ __global__ void __launch_bounds__(kSmThreads, kSmMinCtas) score_mma_kernel(Score
       int L;
       if (single) {  // the loads issued at the start
         const int nrl = min(pf_rs1 - pf_rs0, 2 * NT);
-        L = lane < nrl ? (pf_rs0 == 0 ? pf_len : __ldg(a.row_len + pf_rs0 + lane)) : 0;
+        L = lane < nrl ? (pf_rs0 == 0 ? pf_len : ld_in(a.row_len + pf_rs0 + lane)) : 0;
         fn_ld = relaxed ? max(0, pf_np) / kBlock : INT_MAX;
       } else {
-        const int t0l = __ldg(a.req_row_start + r_ld);
-        const int nrl = min(__ldg(a.req_row_start + r_ld + 1) - t0l, 2 * NT);
-        L = lane < nrl ? __ldg(a.row_len + t0l + lane) : 0;
-        fn_ld = relaxed ? max(0, __ldg(a.new_pos + r_ld)) / kBlock : INT_MAX;
+        const int t0l = ld_in(a.req_row_start + r_ld);
+        const int nrl = min(ld_in(a.req_row_start + r_ld + 1) - t0l, 2 * NT);
+        L = lane < nrl ? ld_in(a.row_len + t0l + lane) : 0;
+        fn_ld = relaxed ? max(0, ld_in(a.new_pos + r_ld)) / kBlock : INT_MAX;
       }
       if (L < 0 || L > a.max_len) L = 0;
       nb_ld = __reduce_max_sync(0xffffffffu, (unsigned)(L / kBlock));
@@ -306,11 +306,11 @@ __global__ void __launch_bounds__(kSmThreads, kSmMinCtas) score_mma_kernel(Score
           f.b[2 * h + c] = v[q1] ? ld_stream_16(rb + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      f.sa = v[0] ? __ldg(a.key_scales + max(pr[0], 0) + g) : 0.f;
-      f.sb = v[1] ? __ldg(a.key_scales + max(pr[1], 0) + g) : 0.f;
+      f.sa = v[0] ? ld_in(a.key_scales + max(pr[0], 0) + g) : 0.f;
+      f.sb = v[1] ? ld_in(a.key_scales + max(pr[1], 0) + g) : 0.f;
       if constexpr (kRuns == 4) {
-        f.sc = v[2] ? __ldg(a.key_scales + max(pr[2], 0) + g) : 0.f;
-        f.sd = v[3] ? __ldg(a.key_scales + max(pr[3], 0) + g) : 0.f;
+        f.sc = v[2] ? ld_in(a.key_scales + max(pr[2], 0) + g) : 0.f;
+        f.sd = v[3] ? ld_in(a.key_scales + max(pr[3], 0) + g) : 0.f;
       }
     } else {
       const __nv_bfloat16* ra = a.pool + ((int64_t)max(pra, 0) + g) * kDim + 8 * t;
@@ -331,16 +331,16 @@ __global__ void __launch_bounds__(kSmThreads, kSmMinCtas) score_mma_kernel(Score
     if (r < 0 || i >= g_pre[r + 1]) {
       if (r < 0) r = request_of(i);
       while (i >= g_pre[r + 1]) ++r;
-      t0 = __ldg(a.req_row_start + r);
-      nrows = min(__ldg(a.req_row_start + r + 1) - t0, 2 * NT);
-      if (__ldg(a.req_row_start + r + 1) - t0 > 2 * NT && lane == 0) raise_fault(kFaultGrouping);
+      t0 = ld_in(a.req_row_start + r);
+      nrows = min(ld_in(a.req_row_start + r + 1) - t0, 2 * NT);
+      if (ld_in(a.req_row_start + r + 1) - t0 > 2 * NT && lane == 0) raise_fault(kFaultGrouping);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int rl = 2 * nt + (t >> 1);
         int nb = 0;
         gate_a[nt] = gate_b[nt] = 1.f;
         if (rl < nrows) {
-          const int L = __ldg(a.row_len + t0 + rl);
+          const int L = ld_in(a.row_len + t0 + rl);
           nb = (L >= 0 && L <= a.max_len) ? L / kBlock : 0;
           gate_a[nt] = head_gate(a.head_gates, t0 + rl, 2 * (t & 1));
           gate_b[nt] = head_gate(a.head_gates, t0 + rl, 2 * (t & 1) + 1);
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kSmThreads, kSmMinCtas) score_mma_kernel(Score
           const int d0 = kFp8 ? 16 * (4 * (c >> 1) + t) + 8 * (c & 1) : 8 * (4 * c + t);
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (rl < nrows)
-            v = __ldg(reinterpret_cast<const uint4*>(a.q + ((int64_t)(t0 + rl) * kHeads + head) * kDim + d0));
+            v = ld_in(reinterpret_cast<const uint4*>(a.q + ((int64_t)(t0 + rl) * kHeads + head) * kDim + d0));
           if (kFp8) {  // BF16 -> FP16, nearest (exact for |q| in [2^-14, 65504) and BF16's 8 bits)
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -83,7 +83,7 @@ __device__ __forceinline__ float tc_head_sum(const uint32_t* v) {
   return sc * kScoreScale;
 }
 __device__ __forceinline__ float tc_head_sum_gated(const uint32_t* v, const float* gates, int64_t row) {
-  const float4 g = __ldg(reinterpret_cast<const float4*>(gates) + row);
+  const float4 g = ld_in(reinterpret_cast<const float4*>(gates) + row);
   const float r0 = fmaxf(__uint_as_float(v[0]), 0.f), r1 = fmaxf(__uint_as_float(v[1]), 0.f);
   const float r2 = fmaxf(__uint_as_float(v[2]), 0.f), r3 = fmaxf(__uint_as_float(v[3]), 0.f);
   return fmaf(g.w, r3, fmaf(g.z, r2, fmaf(g.y, r1, g.x * r0))) * kScoreScale;
@@ -119,7 +119,7 @@ __device__ __forceinline__ void tc_load_keys(const TcArgs& a, int r, int kt, int
       const int page_idx = b / kpp;
       if (page_idx < a.ld_pt) {
         const int64_t page = (page_idx >= pt0 && page_idx < pt0 + pt_n) ? pt_s[page_idx - pt0]
-                                                                          : __ldg(pt_row + page_idx);
+                                                                          : ld_in(pt_row + page_idx);
         const int64_t pr = page * kpp + (b - page_idx * kpp);
         if (page >= 0 && pr < a.pool_rows) prow[j] = pr;
         else if (c == 0) raise_fault(kFaultPool);
@@ -158,7 +158,7 @@ score_tc_cpasync_kernel(TcArgs a) {
   if (a.trigger_dependents) pdl_launch_dependents();
 
   const int r = blockIdx.z;
-  const int row0 = __ldg(a.req_row_start + r), row1 = __ldg(a.req_row_start + r + 1);
+  const int row0 = ld_in(a.req_row_start + r), row1 = ld_in(a.req_row_start + r + 1);
   if (row0 < 0 || row1 < row0 || row1 > a.n_rows) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) raise_fault(kFaultGrouping);
     return;
@@ -171,7 +171,7 @@ score_tc_cpasync_kernel(TcArgs a) {
   if (t0 >= t1) return;
   // visible blocks of each row of the tile; the tile's key range ends at their max
   if (threadIdx.x < t1 - t0) {
-    int L = __ldg(a.row_len + t0 + threadIdx.x);
+    int L = ld_in(a.row_len + t0 + threadIdx.x);
     if (L < 0 || L > a.max_len) { raise_fault(kFaultGrouping); L = 0; }
     s_nb[threadIdx.x] = L / kBlock;
   }
@@ -191,7 +191,7 @@ score_tc_cpasync_kernel(TcArgs a) {
   if (pt_n < 0) pt_n = 0;
   {
     const int32_t* pt_row = a.page_table + (int64_t)r * a.ld_pt;
-    for (int i = threadIdx.x; i < pt_n; i += kTcThreads) pt_s[i] = __ldg(pt_row + pt0 + i);
+    for (int i = threadIdx.x; i < pt_n; i += kTcThreads) pt_s[i] = ld_in(pt_row + pt0 + i);
   }
   __syncthreads();
 
@@ -407,8 +407,8 @@ score_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap pool_map) {
   if (pt_n > a.ld_pt - pt0) pt_n = (int)(a.ld_pt - pt0);
   if (pt_n < 0) pt_n = 0;
   const int32_t* pt_row = a.page_table + (int64_t)r * a.ld_pt;
-  const int32_t pt_first = (int)threadIdx.x < pt_n ? __ldg(pt_row + pt0 + threadIdx.x) : 0;
-  const int row0 = __ldg(a.req_row_start + r), row1 = __ldg(a.req_row_start + r + 1);
+  const int32_t pt_first = (int)threadIdx.x < pt_n ? ld_in(pt_row + pt0 + threadIdx.x) : 0;
+  const int row0 = ld_in(a.req_row_start + r), row1 = ld_in(a.req_row_start + r + 1);
   if (row0 < 0 || row1 < row0 || row1 > a.n_rows) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) raise_fault(kFaultGrouping);
     leave();
@@ -425,7 +425,7 @@ score_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap pool_map) {
   }
   const int nrows = t1 - t0;
   if (threadIdx.x < nrows) {
-    int L = __ldg(a.row_len + t0 + threadIdx.x);
+    int L = ld_in(a.row_len + t0 + threadIdx.x);
     if (L < 0 || L > a.max_len) { raise_fault(kFaultGrouping); L = 0; }
     s_nb[threadIdx.x] = L / kBlock;
   }
@@ -442,11 +442,11 @@ score_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap pool_map) {
     return;
   }
   const int n_local = kt1 - kt0;
-  const int first_new = relaxed ? max(0, __ldg(a.new_pos + r)) / kBlock : 0;
+  const int first_new = relaxed ? max(0, ld_in(a.new_pos + r)) / kBlock : 0;
 
   // ---- page-table entries of this CTA's key range, staged once ------------
   if ((int)threadIdx.x < pt_n) pt_s[threadIdx.x] = pt_first;
-  for (int i = threadIdx.x + kThreads; i < pt_n; i += kThreads) pt_s[i] = __ldg(pt_row + pt0 + i);
+  for (int i = threadIdx.x + kThreads; i < pt_n; i += kThreads) pt_s[i] = ld_in(pt_row + pt0 + i);
 
   // ---- query rows -> B (zero columns beyond 4 * nrows) ---------------------
   const int valid_cols = 4 * nrows;
@@ -511,7 +511,7 @@ score_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap pool_map) {
         const int page_idx = b / kpp;
         if (page_idx < a.ld_pt) {
           const int64_t page = (page_idx >= pt0 && page_idx < pt0 + pt_n) ? pt_s[page_idx - pt0]
-                                                                            : __ldg(pt_row + page_idx);
+                                                                            : ld_in(pt_row + page_idx);
           const int64_t pr = page * kpp + (b - page_idx * kpp);
           if (page >= 0 && pr < a.pool_rows) {
             valid = true;
@@ -649,7 +649,7 @@ score_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap pool_map) {
 __global__ void fill_neginf_kernel(const int32_t* row_len, int32_t max_len, float* scores, int64_t ld,
                                    int64_t n_fill) {
   const int t = blockIdx.x;
-  int L = __ldg(row_len + t);
+  int L = ld_in(row_len + t);
   if (L < 0 || L > max_len) L = 0;
   for (int64_t b = L / kBlock + threadIdx.x; b < n_fill; b += blockDim.x)
     scores[(int64_t)t * ld + b] = -__int_as_float(0x7f800000);

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(1024) plan_rows_kernel(PlanArgs p) {
   for (int base = 0; base < p.n_rows; base += 1024) {
     const int t = base + tid;
     int n = 0;
-    if (t < p.n_rows) n = p.row_len ? __ldg(p.row_len + t) / kBlock : (p.n_valid ? __ldg(p.n_valid + t) : p.n_max);
+    if (t < p.n_rows) n = p.row_len ? ld_in(p.row_len + t) / kBlock : (p.n_valid ? ld_in(p.n_valid + t) : p.n_max);
     const bool is_long = t < p.n_rows && n > p.cut, is_short = t < p.n_rows && !is_long;
     const unsigned bl = __ballot_sync(0xffffffffu, is_long), bs = __ballot_sync(0xffffffffu, is_short);
     if (lane == 0) {
@@ -396,7 +396,7 @@ __device__ __forceinline__ void load4_keys(const float* sm, int bulk, const floa
       uint32_t x = 0u;
       if (i + e < cnt) {
         if (i + e < bulk) x = already_keys ? __float_as_uint(sm[i + e]) : order_key(sm[i + e]);
-        else x = order_key(__ldg(gl + i + e));
+        else x = order_key(ld_in(gl + i + e));
       }
       kk[e] = x;
     }
@@ -577,7 +577,7 @@ select_kernel(SelectArgs a) {
     {
       const int64_t i = (int64_t)threadIdx.x * n / kSelThreads;
       const uint32_t kq = a.resident ? reinterpret_cast<const uint32_t*>(row_area)[i]
-                                     : order_key(__ldg(r.row + i));
+                                     : order_key(ld_in(r.row + i));
       atomicAdd(&fx.hist[0][kq >> 21], 1u);
     }
     __syncthreads();

@@ -216,7 +216,7 @@ select_cluster_kernel(SelectArgs a) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int p = (int)(((int64_t)(tid + kScThreads * u) * n) >> 10);
-        sk[u] = order_key(__ldg(row + p));
+        sk[u] = order_key(ld_in(row + p));
       }
     }
     // ---- this CTA's slice, thread t's contiguous run in registers --------
@@ -233,12 +233,12 @@ select_cluster_kernel(SelectArgs a) {
       v[j] = make_float4(nan, nan, nan, nan);
       if (j < J) {
         if (a.vec_ok && i + 3 < s1) {
-          v[j] = __ldg(reinterpret_cast<const float4*>(row + i));
+          v[j] = ld_in(reinterpret_cast<const float4*>(row + i));
         } else {
-          if (i < s1) v[j].x = __ldg(row + i);
-          if (i + 1 < s1) v[j].y = __ldg(row + i + 1);
-          if (i + 2 < s1) v[j].z = __ldg(row + i + 2);
-          if (i + 3 < s1) v[j].w = __ldg(row + i + 3);
+          if (i < s1) v[j].x = ld_in(row + i);
+          if (i + 1 < s1) v[j].y = ld_in(row + i + 1);
+          if (i + 2 < s1) v[j].z = ld_in(row + i + 2);
+          if (i + 3 < s1) v[j].w = ld_in(row + i + 3);
         }
       }
     }
@@ -387,7 +387,7 @@ select_cluster_kernel(SelectArgs a) {
         const int nshift = shift - nb;
         const uint32_t mask = (1u << nb) - 1u;
         for (int i = tid; i < n; i += kScThreads) {
-          const uint32_t key = order_key(__ldg(row + i));
+          const uint32_t key = order_key(ld_in(row + i));
           if (shift == 32 || (key >> shift) == prefix) atomicAdd(&hist[(key >> nshift) & mask], 1u);
         }
         __syncthreads();
@@ -402,14 +402,14 @@ select_cluster_kernel(SelectArgs a) {
       const int l0 = min(n, q * tid), l1 = min(n, l0 + q);
       uint32_t pk = 0u;  // above (low 16 bits), equal (high 16 bits); n <= 32768
       for (int i = l0; i < l1; ++i) {
-        const uint32_t hb = order_key(__ldg(row + i)) >> shift;
+        const uint32_t hb = order_key(ld_in(row + i)) >> shift;
         pk += hb > prefix ? 1u : (hb == prefix ? 0x10000u : 0u);
       }
       uint32_t tot;
       const uint32_t bs = sc_block_excl_scan(pk, fx.wsum, tot);
       uint32_t gb = bs & 0xffffu, qb = bs >> 16;
       for (int i = l0; i < l1; ++i) {
-        const uint32_t hb = order_key(__ldg(row + i)) >> shift;
+        const uint32_t hb = order_key(ld_in(row + i)) >> shift;
         const bool gt = hb > prefix, eq = hb == prefix;
         const uint32_t pos = gb + (qb < need ? qb : need);
         if ((gt || (eq && qb < need)) && pos < (uint32_t)k) sel_s[pos] = i;

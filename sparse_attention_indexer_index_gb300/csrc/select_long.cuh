@@ -174,16 +174,16 @@ __device__ __forceinline__ SlBound sl_bound(uint64_t K) {
   return b;
 }
 
-__device__ __forceinline__ float4 sl_load4(const float* __restrict__ row, int i, int end, bool vec) {
+__device__ __forceinline__ float4 sl_load4(const float* row, int i, int end, bool vec) {
   const float nan = __uint_as_float(0x7fffffffu);
   float4 v = make_float4(nan, nan, nan, nan);
   if (vec && i + 3 < end) {
-    v = __ldg(reinterpret_cast<const float4*>(row + i));
+    v = ld_in(reinterpret_cast<const float4*>(row + i));
   } else {
-    if (i < end) v.x = __ldg(row + i);
-    if (i + 1 < end) v.y = __ldg(row + i + 1);
-    if (i + 2 < end) v.z = __ldg(row + i + 2);
-    if (i + 3 < end) v.w = __ldg(row + i + 3);
+    if (i < end) v.x = ld_in(row + i);
+    if (i + 1 < end) v.y = ld_in(row + i + 1);
+    if (i + 2 < end) v.z = ld_in(row + i + 2);
+    if (i + 3 < end) v.w = ld_in(row + i + 3);
   }
   return v;
 }

@@ -198,12 +198,12 @@ select_resident_kernel(SelectArgs a) {
         v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (j < nch) {
           if (a.vec_ok && i + 3 < n) {
-            v[j] = __ldg(reinterpret_cast<const float4*>(row + i));
+            v[j] = ld_in(reinterpret_cast<const float4*>(row + i));
           } else {
-            if (i < n) v[j].x = __ldg(row + i);
-            if (i + 1 < n) v[j].y = __ldg(row + i + 1);
-            if (i + 2 < n) v[j].z = __ldg(row + i + 2);
-            if (i + 3 < n) v[j].w = __ldg(row + i + 3);
+            if (i < n) v[j].x = ld_in(row + i);
+            if (i + 1 < n) v[j].y = ld_in(row + i + 1);
+            if (i + 2 < n) v[j].z = ld_in(row + i + 2);
+            if (i + 3 < n) v[j].w = ld_in(row + i + 3);
           }
         }
       }

@@ -211,7 +211,7 @@ select_rows_kernel(SelectArgs a) {
       if (vec && c0 + 128 * kSrUnroll <= w1) {
 #pragma unroll
         for (int u = 0; u < kSrUnroll; ++u)
-          v[u] = __ldg(reinterpret_cast<const float4*>(row + c0 + 128 * u + 4 * lane));
+          v[u] = ld_in(reinterpret_cast<const float4*>(row + c0 + 128 * u + 4 * lane));
 #pragma unroll
         for (int u = 0; u < kSrUnroll; ++u) f(c0 + 128 * u + 4 * lane, v[u], std::true_type{});
       } else {
@@ -233,7 +233,7 @@ select_rows_kernel(SelectArgs a) {
       if (vec && c0 + 128 * kSrUnroll <= w1) {
 #pragma unroll
         for (int u = 0; u < kSrUnroll; ++u)
-          v[u] = __ldg(reinterpret_cast<const float4*>(row + c0 + 128 * u + 4 * lane));
+          v[u] = ld_in(reinterpret_cast<const float4*>(row + c0 + 128 * u + 4 * lane));
 #pragma unroll
         for (int u = 0; u < kSrUnroll; u += 2) f2(c0 + 128 * u + 4 * lane, v[u], v[u + 1], std::true_type{});
       } else {

@@ -154,3 +154,29 @@ def test_window_attn_reads_inputs_that_arrive_late(qsa, late_copy, rows, max_row
     fn = qsa.window_attn_fp4 if fp4 else qsa.window_attn
     window = ctx if ctx > 1000 else 100
     check_late(late_copy, inputs(), inputs(), lambda x: fn(*x, page, ctx, window, 3, max_rows_per_req=max_rows))
+
+
+@pytest.mark.parametrize("lens,page", [([[4099, 4100, 4101], [1030]], 64), ([[800], [900], [33]], 8),
+                                       ([list(range(3000, 3064))], 64)])
+def test_indexer_reads_inputs_that_arrive_late(qsa, late_copy, lens, page):  # noqa: F811
+    """Scores and selection: a verify step, single rows on small pages, a chunk."""
+    import torch
+    from workloads import decode_workload
+
+    def inputs(seed):
+        w = decode_workload(seed, lens, page_size=page, k_blk=512)
+        pool = normal_bf16(np.random.default_rng(seed), (w.pool_rows, 128))
+        return w, [bf16_dev(w.q), bf16_dev(pool), *map(to_dev, (w.req_row_start, w.row_len, w.page_table))]
+
+    (w, first), (_, second) = inputs(64), inputs(65)
+    assert all(a.shape == b.shape for a, b in zip(first, second))
+    scores = torch.zeros((w.n_rows, -(-w.max_len // 4)), device="cuda")
+
+    def call(x):
+        out = qsa.indexer_select(*x, page, w.max_len, w.max_rows_per_req, k_blk=512, want_blocks=True, scores_out=scores)
+        return out["blocks"], out["slots"]
+
+    check_late(late_copy, first, second, call)
+    # scores past a row's length are not written
+    check_late(late_copy, first, second,
+               lambda x: [qsa.index_scores(*x, page, w.max_len, w.max_rows_per_req, scores=scores)], scores.zero_)
