@@ -820,6 +820,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
             if (bad != 0) raise_fault(kFaultIndex);
             ctl.bad[(gb + blk) % kWtBadRing] = bad;
           }
+          __syncwarp();  // before the arrivals of whichever lane is elected
         }
         // stages in the order of use: K(0), K(1), V(0), K(2), V(1), ...
         int at = rs + (is_k ? Sh::kKs * blk + max(blk - 1, 0) * Sh::kVs

@@ -130,3 +130,10 @@ def test_waits_of_the_copies_on_empty_stages(d, kind):
                 continue
             assert u < 2 * n_st or freed >= u - 2 * n_st, (tiles, u)
             freed = u - n_st
+
+
+def test_what_one_lane_writes_is_ordered_before_the_arrival_of_another():
+    """Lane 0 writes a block's list of missing boxes, an elected lane, which may
+    be any, announces its copies: the warp meets in between."""
+    k = SRC[SRC.index("ctl.bad[(gb + blk) % kWtBadRing] = bad;"):]
+    assert "__syncwarp();" in k[:k.index("wt_expect(&ctl.full[st]")]
