@@ -397,8 +397,9 @@ qsa_status qsa_sparse_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
  *   workspace  qsa_window_attn_workspace_size() bytes (16-byte aligned), 0
  *              except for few rows with long windows; as above.
  *
- * A page that does not lie wholly inside the cache is skipped and latches
- * fault bit 0; a row_len outside [0, max_len] counts as 0 (bit 3).
+ * A page that a row attends to and that does not lie wholly inside the cache
+ * is skipped and latches fault bit 0 (others may be anything: pages behind a
+ * window can be given back); a row_len outside [0, max_len] counts as 0 (bit 3).
  * ------------------------------------------------------------------- */
 size_t qsa_window_attn_workspace_size(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t max_len,
                                       int32_t window, int32_t n_sink);

@@ -82,3 +82,39 @@ def test_broken_values_in_a_long_window_hold_up_the_next_tile(qsa, ctx, d):  # n
         tol, tol_l = ref.tolerance(d, sl.size, ro, a, big, spread, W_BF16, BF16_HALF_STEP, False, 0.0)
         assert (np.abs(o[t] - ro) <= tol).all(), t
         assert (np.abs(l[t] - rl) <= tol_l + 2.0 ** -23 * np.abs(rl)).all(), t
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("d,page", [(128, 64), (256, 16)])
+@pytest.mark.parametrize("rows,max_rows", [(2, 1), (2, 17), (20, 20)])
+@pytest.mark.parametrize("n_sink", [0, 3])
+def test_pages_that_no_row_attends_to_may_be_gone(qsa, rows, max_rows, d, page, fp4, n_sink):  # noqa: F811
+    """Rows of a request whose windows lie apart: the pages between them, which
+    were given back, are no fault; a page that a row attends to is one."""
+    rng = np.random.default_rng(52)
+    window, near, far = 64, 200, 2000
+
+    def gone(pt, cache):
+        for r in range(2):
+            lens = [near] + [far - i for i in range(rows - 1)]
+            seen = np.unique(np.concatenate([ref.window_positions(x, window, n_sink) for x in lens]) // page)
+            keep = np.isin(np.arange(pt.shape[1]), seen)
+            pt[r, ~keep] = np.where(np.arange((~keep).sum()) % 2, -1, 2**31 - 1)
+        return cache
+
+    lens = [[near] + [far - i for i in range(rows - 1)]] * 2
+    window_check(qsa, rng, lens, page, 8, 1, d, window, n_sink, fp4, cache=gone, max_rows=max_rows)
+    assert qsa.device_status() == 0
+
+    def one_more(pt, cache):
+        gone(pt, cache)
+        pt[1, (near - 1) // page] = -1
+        return cache
+
+    pt, n_slots = page_table(rng, [far, far], page)
+    k, v = (bf16_dev(normal_bf16(rng, (n_slots, 1, d))) for _ in range(2))
+    one_more(pt, None)
+    q = bf16_dev(normal_bf16(rng, (2 * rows, 8, d)))
+    qsa.window_attn(q, k, v, to_dev(np.array([0, rows, 2 * rows], np.int32)), to_dev(np.array(sum(lens, []), np.int32)),
+                    to_dev(pt), page, far, window, n_sink, max_rows_per_req=max_rows)
+    assert qsa.device_status(clear=True) == 1
