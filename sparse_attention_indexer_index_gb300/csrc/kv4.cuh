@@ -178,8 +178,8 @@ struct KvWriteArgs {
 // and the same block of V.  Per block 64 B read and 18 B written.  In bulk the
 // conversions bound it (60,374 rows of 2 x 256: 31 us, 5.1 TB/s, 0.7 of the
 // issue slots; two and four blocks a thread took 32 and 37 us); a decode step
-// is a chain of dependent loads (request, position, page), beside which the
-// data loads are already under way.
+// is a chain of dependent loads (request, position, page), the data beside the
+// last two of them.
 __global__ void __launch_bounds__(kKvThreads)
 append_kv_fp4_kernel(KvWriteArgs a) {
   const uint32_t u0 = blockIdx.x * kKvThreads + (threadIdx.x & ~31);
@@ -190,15 +190,13 @@ append_kv_fp4_kernel(KvWriteArgs a) {
   const bool ok = u < total;
   const int t = ok ? (int)(u / (uint32_t)a.blocks) : a.n_tok - 1;
   const int b = ok ? (int)(u - (uint32_t)t * (uint32_t)a.blocks) : 0;
-  U8 kx{}, vx{};
-  if (ok) {
-    kx = ld_stream_32(a.k_new + (int64_t)t * a.ld_k + b * kKvBlock);
-    vx = ld_stream_32(a.v_new + (int64_t)t * a.ld_v + b * kKvBlock);
-  }
   int r = warp_row_request(a.req_tok_start, a.n_req, (int)(u0 / (uint32_t)a.blocks));  // of the warp's first token
   if (!ok || r < 0) return;  // r < 0: behind the last request, as the rest of the warp
   while (r < a.n_req && t >= ld_in(a.req_tok_start + r + 1)) ++r;  // a warp may span tokens
   if (r >= a.n_req) return;
+  // not before: rows behind the last request may lie past the end of the buffers
+  const U8 kx = ld_stream_32(a.k_new + (int64_t)t * a.ld_k + b * kKvBlock);
+  const U8 vx = ld_stream_32(a.v_new + (int64_t)t * a.ld_v + b * kKvBlock);
   const int64_t pos = (int64_t)ld_in(a.req_first_pos + r) + (t - ld_in(a.req_tok_start + r));
   const int pi = pos < 0 || pos > INT32_MAX ? INT32_MAX : (int)pos / a.page_size;
   if (pi >= a.ld_pt) {
