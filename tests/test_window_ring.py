@@ -137,3 +137,39 @@ def test_what_one_lane_writes_is_ordered_before_the_arrival_of_another():
     be any, announces its copies: the warp meets in between."""
     k = SRC[SRC.index("ctl.bad[(gb + blk) % kWtBadRing] = bad;"):]
     assert "__syncwarp();" in k[:k.index("wt_expect(&ctl.full[st]")]
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_products_overwrite_nothing_that_another_may_read(d):
+    """Tensor memory: the order in which the pipe runs two MMAs is documented
+    only where they share accumulator and shape, so no product may write what an
+    earlier one, or the softmax, may still read."""
+    n = shape(d)[0]
+    cols = re.search(r"static constexpr uint32_t kColS = D, kColP = D \+ kWtN;", SRC)
+    assert cols, "S and P lie in different columns"
+    o, s, p = range(0, d), range(d, d + n), [range(d + n, d + n + n // 2), range(d + n + n // 2, d + 2 * n)]
+    assert p[1].stop <= 512
+    assert not (set(o) & set(s) or set(s) & (set(p[0]) | set(p[1])) or set(p[0]) & set(p[1]))
+    # where the products and the softmax go
+    assert "d = tmem + Sh::kColS;" in SRC and "p = tmem + Sh::kColP + sl * (N / 2) + e0 / 2;" in SRC
+    assert "wt_tmem_ld64(lanes + Sh::kColS + 64 * half, s);" in SRC
+    assert "wt_tmem_st32(lanes + Sh::kColP + sl * (N / 2) + 32 * half, p);" in SRC
+    # QK(x) overwrites S(x - 1): every softmax warp has arrived with it in its registers
+    qk = SRC[SRC.index("auto qk = "):SRC.index("auto pv = ")]
+    wait = "if (!wait(s ? &ctl.s_free : &ctl.full[st], s ? (uint32_t)(x - 1) & 1u : ph)) return false;"
+    assert qk.index(wait) < qk.index("tc_fence_after();") < qk.index("wt_mma_qk(")
+    assert "const bool s = i == 0 && x > 0 && (lane & 1) != 0;" in qk and "mbar_init(&ctl.s_free, 8);" in SRC
+    soft = SRC[SRC.index("wt_tmem_ld64(lanes"):]
+    assert soft.index("tc_fence_before();") < soft.index("__syncwarp();") < soft.index("wt_arrive(&ctl.s_free);")
+    # P(x) overwrites P(x - 2): S(x) is announced by a commit behind PV(x - 2)
+    for blocks in range(1, 17):
+        order = []
+        for _ in range(2):  # tiles
+            x0 = sum(e[0] == "qk" for e in order)
+            order.append(("qk", x0))
+            for b in range(blocks):
+                order += ([("qk", x0 + b + 1)] if b + 1 < blocks else []) + [("pv", x0 + b)]
+        for x in range(2, 2 * blocks):
+            assert order.index(("pv", x - 2)) < order.index(("qk", x))
+            # and its own wait ends: the scores before were announced before
+            assert order.index(("qk", x - 1)) < order.index(("qk", x))
