@@ -346,7 +346,8 @@ qsa_status qsa_gather_kv_fp4(const void* k_codes, const void* k_scales, const vo
  * Sparse attention over the selected slots, reading the 4-bit cache:
  * qsa_sparse_attn with k_cache and v_cache replaced by the four arrays above.
  * The cache's values enter the dot products and the value sums exactly; the
- * softmax statistics are FP32 and the weights keep 22 significant bits.
+ * softmax statistics are FP32 and the weights keep 22 significant bits (tiny
+ * ones less: they are held to 2^-35 of the row's largest).
  *
  *   q          n_rows rows of [h_q][head_dim] BF16, ld_q elements apart (a
  *              multiple of 8; base 16-byte aligned).
@@ -386,12 +387,17 @@ qsa_status qsa_sparse_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
  *   k_cache, v_cache [n_slots][h_kv][head_dim] BF16 (16-byte aligned), or the
  *              four arrays of the 4-bit cache.
  *   window >= 1, n_sink >= 0; scale finite, of either sign.
- *   max_rows_per_req  as elsewhere: it picks the kernel, not the result.
- *              Requests of several rows take 128 (row, query head) pairs at a
- *              time on the BF16 cache if the page size is a multiple of 8,
- *              with the weights rounded to BF16 once; otherwise each row is
- *              taken by itself, with weights of 16 bits or more.  The 4-bit
- *              form takes each row by itself always.
+ *   max_rows_per_req  host upper bound of the rows of any one request; it
+ *              picks the kernel, and with it how the softmax weights are
+ *              held, never which positions count.  On the BF16 cache, if it
+ *              is above 1 and the page size a multiple of 8, 128 (row, query
+ *              head) pairs are taken at a time (but not where up to 16 rows a
+ *              request have little to read), with each weight rounded to BF16
+ *              once: up to 2^-8 of the weight, on top of the output's own
+ *              rounding.  Otherwise each row is taken by itself, with weights
+ *              of 16 bits (BF16 cache) or 22 (4-bit cache).  The 4-bit form
+ *              takes each row by itself always: requests of many rows take
+ *              less on rows read back (qsa_gather_kv_fp4) and the BF16 form.
  *   out        [n_rows][h_q][head_dim] BF16 (32-byte aligned): the next
  *              operator is a BF16 projection.
  *   workspace  qsa_window_attn_workspace_size() bytes (16-byte aligned), 0

@@ -814,7 +814,10 @@ def window_attn(q, k_cache, v_cache, req_row_start, row_len, page_table, page_si
     """Attention of q [n_rows][h_q][head_dim] bf16 over the last `window`
     tokens each row sees (row_len, its own among them) and the first n_sink,
     through the page table, on the BF16 cache [n_slots][h_kv][head_dim].
-    Returns (out bfloat16, lse [n_rows][h_q] float32 or None)."""
+    max_rows_per_req (default: n_rows) bounds the rows of one request; give 1
+    for decode rows: it picks the kernel, and the one for requests of several
+    rows rounds the softmax weights to BF16, the one for single rows keeps 16
+    bits of them.  Returns (out bfloat16, lse [n_rows][h_q] float32 or None)."""
     bf16 = _t()[0]
     try:
         n_slots, h_kv, d = k_cache.shape

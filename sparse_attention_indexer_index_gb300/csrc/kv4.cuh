@@ -20,7 +20,7 @@
 // they differ by at least 2^-8 relative.  So no division is needed: y times
 // a reciprocal (off by 2^-22 at most) is rounded to FP16 first, which puts a
 // quotient on a border exactly there and moves no other across one.  (With
-// 17 divisions a block the kernel took 37 us where it takes 31.)  A block
+// 17 divisions a block the kernel took 37 us where it took 31.)  A block
 // whose scale rounds to zero holds zeros; a block with an infinity or a NaN
 // gets the NaN scale and reads back as NaN, so that a broken row shows
 // instead of being clipped.
@@ -175,9 +175,9 @@ struct KvWriteArgs {
 };
 
 // K and V rows quantised into their slots.  One thread per block of 16 of K
-// and the same block of V.  Per block 64 B read and 18 B written.  In bulk the
-// conversions bound it (60,374 rows of 2 x 256: 31 us, 5.1 TB/s, 0.7 of the
-// issue slots; two and four blocks a thread took 32 and 37 us); a decode step
+// and the same block of V.  Per block 64 B read and 18 B written.  60,374 rows
+// of 2 x 256: 26.4 us, 6.0 TB/s, 0.89 of the copy rate (two and four blocks a
+// thread took 32 and 37 us where one took 31); a decode step
 // is a chain of dependent loads (request, position, page), the data beside the
 // last two of them.
 __global__ void __launch_bounds__(kKvThreads)
@@ -231,7 +231,7 @@ struct KvReadArgs {
 
 // Rows read back at slots: one thread per block of 16 of K and of V.  Per
 // block 18 B read and 64 B written, HBM-bound: 131,072 rows of 512 values take
-// 52.5 us, 6.6 TB/s, 0.97 of a plain copy's rate; 12,306 selected rows 5.8 us.
+// 52.5 us, 6.6 TB/s, 0.97 of a plain copy's rate; 12,306 selected rows 5.7 us.
 __global__ void __launch_bounds__(kKvThreads)
 gather_kv_fp4_kernel(KvReadArgs a) {
   const uint32_t u = blockIdx.x * kKvThreads + threadIdx.x;

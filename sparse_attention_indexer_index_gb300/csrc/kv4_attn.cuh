@@ -31,10 +31,12 @@
 // Measured (one call after the other; 16 query heads): 32 rows of 2,051 entries, 2 KV heads
 // of D = 256: 16.4 us, 2.4 TB/s; 192 rows, 1 KV head of D = 128: 33.2 us, 1.8
 // TB/s; 32 windows of 4,100 entries, 2 KV heads of D = 256: 27.5 us, 2.8 TB/s;
-// one row 8.7 us.  In the middle of a long row the tensor pipe and the ALU
-// are each busy two thirds of the time, on 8 warps an SM (250 registers a
-// thread); the rest of a short call is the chain from the launch to the first
-// keys and the join.
+// one row 8.7 us.  From 32 rows of 2,051, 4,102, 8,204 and 16,408 entries (15.6,
+// 25.4, 43.9, 80.1 us in a graph) the middle of a row goes at 4.2 TB/s, 0.62 of
+// the copy rate, and the chain from the launch to the first keys and the join
+// take 7 us.  There (16,408 entries) the ALU is 42 %, the tensor pipe 40 % and
+// the issue slots 40 % busy, on 8 warps an SM (250 registers a thread): too few
+// to cover the waits between dependent instructions.
 #pragma once
 #include <type_traits>
 

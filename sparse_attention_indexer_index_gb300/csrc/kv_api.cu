@@ -238,12 +238,12 @@ bool encode_q_map(CUtensorMap* m, const WtArgs& a, int d) {
 }
 
 // CTAs that share a tile, where there are few: a single tile of 9 blocks takes
-// 29.8 us on one CTA, 25.7 on two, 23.7 on four, 21.6 on eight, one of 33
-// blocks 68.7, 46.2, 33.9 and 27.7 (in a graph, with what it adds), as long as
-// all clusters run at once (16 tiles of 9 blocks: 38.0 us in eights, which do
-// not, 23.7 in fours).  From 65 tiles on, one CTA a tile, launched without the
+// 19.8 us on one CTA, 17.9 on two, 14.8 on four, 13.7 on eight, one of 33
+// blocks 51.3, 33.6, 22.8 and 17.9 (in a graph), as long as all clusters run at
+// once (16 tiles of 9 blocks: 27.0 us in eights, which do not, 15.1 in fours).
+// From 65 tiles on, one CTA a tile, launched without the
 // cluster attribute: sharing the last round's gained nothing (the 512 tiles of
-// a 4,096-row chunk: 85 us either way), and a cluster launch cost 1 us.  How
+// a 4,096-row chunk: 85 us either way at the time), and a cluster launch cost 1 us.  How
 // many tiles there are is known on the device only; the estimate takes
 // requests of equal length.
 int wt_cluster(const WtArgs& a, const int* resident) {
@@ -259,12 +259,22 @@ int wt_cluster(const WtArgs& a, const int* resident) {
 // Where rows share a tile of keys the tensor cores win, except on little work,
 // where the form for single rows starts and ends sooner and spreads over more
 // SMs: of window 1,024 and D = 256, 2 KV heads (in a graph, single-row form
-// against this one) 1 request of 6 rows 14.5 against 22.7 us, 8 of 2 17.5
-// against 23.7, 8 of 4 21.6 against 23.7, 32 of 3 52 against 34, 32 of 6 75
-// against 34; of window 4,096 8 of 4 49 against 35; of window 128 8 of 6 13.4
-// against 19.6, 32 of 6 27.8 against 21.6.  The line is drawn through the
+// against this one) 1 request of 6 rows 7.8 against 14.0 us, 8 of 2 10.0
+// against 14.4, 8 of 4 15.0 against 14.5, 32 of 3 45 against 23, 32 of 6 69
+// against 24; of window 4,096 8 of 4 43 against 25; of window 128 8 of 6 7.2
+// against 11.0, 32 of 6 20.3 against 11.3.  The line is drawn through the
 // columns that the single rows would read of K, in one round of CTAs, for up
 // to 16 rows a request.
+//
+// One row a request shares no keys: the single-row form, whatever the work.
+// Single-row form / this one in us, in a graph, 1, 8, 32, 64, 128 requests:
+//   D = 256, window 128     6.0/10.6   6.1/10.9   6.9/11.0   7.5/13.6  16.6/23.0
+//            window 1,024   7.7/13.3   8.0/14.3  18.0/22.6  27.2/31.1  53.1/54.6
+//            window 4,096  14.2/17.3  19.2/24.6  46.8/50.4  83.5/86.3   171/167
+//   D = 128, window 128     4.5/9.2    4.5/9.5    5.5/10.2   5.6/16.7  12.2/29.2
+//            window 1,024   5.9/12.0   6.7/13.4  15.9/21.3  24.7/35.4  46.7/62.6
+//            window 4,096   9.6/15.7  15.8/23.4  44.2/49.4  80.6/97.5   158/192
+// (2 KV heads of D = 256, 4 of 128.)
 constexpr int kWtFewRows = 16;
 constexpr int64_t kWtFewColumns = 20 << 20;
 bool wt_serves(const KvAttnArgs& k, int d, int32_t max_rows_per_req, int64_t entries) {

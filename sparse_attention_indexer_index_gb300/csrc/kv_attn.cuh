@@ -32,10 +32,10 @@
 //  - The K index of an MMA may be permuted alike in both operands: chosen so
 //    that lanes read 16-byte pieces of the stage rows.
 //
-// Measured (BF16, in a graph, which adds some 4 us): a window of 1,028 entries
-// at 16 query heads, 2 KV heads, D = 256: one row 13.4 us (8.2 us in a stream of calls),
-// 32 rows 28 us, 64 rows 40 us (3.7 TB/s: one CTA an SM, whose three
-// stages a warp cannot keep more bytes on the way).
+// Measured (BF16, in a graph): a window of 1,028 entries at 16 query heads, 2
+// KV heads, D = 256: one row 7.5 us, 32 rows 17.8 us (3.8 TB/s), 64 rows 27.2 us
+// (4.9 TB/s: one CTA an SM, whose three stages a warp cannot keep more bytes on
+// the way).
 #pragma once
 #include "common.cuh"
 #include "kv4.cuh"

@@ -47,8 +47,11 @@
 //  - The accumulator is rescaled only when a row's maximum grew by more than
 //    2^8 since the last time (the weights stay below 2^8 and the sums are
 //    FP32, so nothing is lost); otherwise m stays.
-//  - Weights enter the product as BF16, 2^-9 relative at most, one rounding
-//    like that of the output; l sums them before the rounding, in FP32.
+//  - Weights enter the product as BF16 (both operands of it have V's type),
+//    2^-8 relative at most, one rounding like that of the output; l sums them
+//    before the rounding, in FP32.  Against FP64 the outputs of a chunk are off
+//    by 0.0023 (root mean square, relative) where the output's rounding alone
+//    gives 0.0017; a second product with the remainders would double PV.
 // Tensor memory columns: O [0, D), S 128, P two times 64.
 //
 // Waits on stages.  The ring's uses are numbered in the order K(0), K(1),
@@ -76,15 +79,15 @@
 // infinity there would be NaN); see wt_redo for those that some pairs see.
 //
 // Measured (one call after the other over several sets of inputs): a chunk of
-// 4,096 rows of 16 heads, 2 KV heads, D = 256, window 1,024: 66.2 us, 1,040
-// TFLOP/s, 0.55 of the bf16 rate.  The products themselves are 39 us of it at
-// the full rate (with half of them left out 8 us less, without exponentials,
-// copies or output stores 0, 4 and 2 us less): 512 tiles make 3.4 rounds of
-// the 152 SMs, four in effect, and accesses to tensor memory by the softmax
-// slow the products by a sixth.  Seven prompts of D = 128 in windows of 500:
-// 42.5 us, 0.25 of the rate: a block's chain from scores to weights takes
-// longer than its products, and a third of the time is the start and end of
-// some 900 short tiles.  32 requests of 6 rows: 24.7 us, 2.9 TB/s; with the L2
+// 4,096 rows of 16 heads, 2 KV heads, D = 256, window 1,024: 67.3 us, 1,020
+// TFLOP/s, 0.54 of the bf16 rate.  512 tiles make 3.4 rounds of the 152 SMs,
+// four in effect.  Windows of 256 to 4,096 take 37.6, 46.9, 67.5, 107 and 192
+// us in a graph: 1.2 to 1.3 us a block and round, where its products take 1.33
+// at the measured bf16 rate and 1.04 at 64 clocks per 128 x 128 x 16; the rest
+// is about 4 us a tile for its start and end.  Seven prompts of D = 128 in
+// windows of 500: 43.2 us, 0.24 of the rate: a block takes 0.86 us (in windows
+// of 256 to 2,048), its products 0.67, and some 900 short tiles 4 us each for
+// their start and end.  32 requests of 6 rows: 25.0 us, 2.8 TB/s; with the L2
 // flushed, in a trace: 6 us from the launch to the first copy, 11 us of copies
 // at the full HBM rate, then the last block, and 5 us in which a cluster joins.
 #pragma once
@@ -891,7 +894,7 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
       WtTile w;
       if (!wt_next_tile(ctl, k, w, abort) || w.rows < 0) break;
       // the same in all lanes, now known to be: the stage counter and the
-      // descriptors stay in uniform registers (76.5 -> 74.7 us, in a graph)
+      // descriptors stay in uniform registers (chunk 76.5 -> 74.7 us at the time, in a graph)
       w.n_blk = __reduce_max_sync(0xffffffffu, w.n_blk);
       w.n_box = __reduce_max_sync(0xffffffffu, w.n_box);
       w.uc = __reduce_max_sync(0xffffffffu, w.uc);
