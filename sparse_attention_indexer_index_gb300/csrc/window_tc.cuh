@@ -909,7 +909,10 @@ window_tc_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUten
           // waits, one after the other, leave the pipe idle (chunk 70.5 us instead of 67.7)
           const bool s = i == 0 && x > 0 && (lane & 1) != 0;
           if (!wait(s ? &ctl.s_free : &ctl.full[st], s ? (uint32_t)(x - 1) & 1u : ph)) return false;
-          if (i == 0) tc_fence_after();
+          if (i == 0) {
+            __syncwarp();  // the lane that issues knows what the others waited for
+            tc_fence_after();
+          }
           const uint64_t kd = add(k_desc0, st * kWtStageBytes), qd = add(q_desc, i * 2 * kQHalf);
           wt_mma_qk(d, qd, kd, idesc, i > 0 ? 1u : 0u);
           next_stage();

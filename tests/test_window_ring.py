@@ -157,7 +157,8 @@ def test_products_overwrite_nothing_that_another_may_read(d):
     # QK(x) overwrites S(x - 1): every softmax warp has arrived with it in its registers
     qk = SRC[SRC.index("auto qk = "):SRC.index("auto pv = ")]
     wait = "if (!wait(s ? &ctl.s_free : &ctl.full[st], s ? (uint32_t)(x - 1) & 1u : ph)) return false;"
-    assert qk.index(wait) < qk.index("tc_fence_after();") < qk.index("wt_mma_qk(")
+    # (lanes wait for different barriers, one lane issues)
+    assert qk.index(wait) < qk.index("__syncwarp();") < qk.index("tc_fence_after();") < qk.index("wt_mma_qk(")
     assert "const bool s = i == 0 && x > 0 && (lane & 1) != 0;" in qk and "mbar_init(&ctl.s_free, 8);" in SRC
     soft = SRC[SRC.index("wt_tmem_ld64(lanes"):]
     assert soft.index("tc_fence_before();") < soft.index("__syncwarp();") < soft.index("wt_arrive(&ctl.s_free);")
