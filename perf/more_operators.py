@@ -172,10 +172,10 @@ def work(c):
 
 # ------------------------------------------------------------- 8-bit blocks
 def _exponent(top):
-    """Smallest e with top <= 448 2^e, between -100 and 119 (exact: top = m 2^k, 448 = 0.875 2^9)."""
+    """Smallest e with top <= 448 2^e, between -64 and 63 (exact: top = m 2^k, 448 = 0.875 2^9)."""
     m, k = torch.frexp(top)
     e = k - 9 + (m > 0.875).to(k.dtype)
-    return torch.where(top > 0, e.clamp(-100, 119), torch.full_like(e, -100))
+    return torch.where(top > 0, e.clamp(-64, 63), torch.full_like(e, -64))
 
 
 def _pow2(e):
@@ -478,10 +478,10 @@ def _round64(x, unit):
 
 
 def _unit64(top):
-    """Smallest power of two with top <= 448 of it, from 2^-100 to 2^119."""
+    """Smallest power of two with top <= 448 of it, from 2^-64 to 2^63."""
     e = torch.frexp(top.clamp(min=1e-300) / 448.0).exponent.long()  # below 2^e, from 2^(e - 1) on
     e = torch.where(top <= 448.0 * _two(e - 1), e - 1, e)
-    return _two(e.clamp(-100, 119))
+    return _two(e.clamp(-64, 63))
 
 
 def _exact_plan(c, s):
