@@ -92,7 +92,8 @@ int qsa_version(void);
  * returns QSA_OK or QSA_ERR_DEVICE_FAULT.  *h_bits (may be NULL) receives the
  * word: bit 0 row/page index out of range, bit 1 pool row out of range,
  * bit 2 a bounded wait expired, bit 3 inconsistent row grouping, bit 4 an
- * output row too narrow for its entries (qsa_indexshare_slots). */
+ * output row too narrow for its entries (qsa_indexshare_slots), or rows or
+ * pages that did not fit (qsa_plan_step, qsa_release_pages). */
 qsa_status qsa_device_status(void* stream, int clear, uint32_t* h_bits);
 
 /* ---------------------------------------------------------------------
@@ -421,6 +422,135 @@ qsa_status qsa_window_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
                                const int32_t* page_table, int64_t ld_pt, int32_t page_size, int32_t window,
                                int32_t n_sink, float scale, float k_scale, float v_scale, void* out, float* lse,
                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------
+ * The KV cache held in 8 bits, and attention over it.  (Library additions
+ * with no counterpart in the source pages.)
+ *
+ *   k_codes, v_codes    [n_slots][h_kv][head_dim] e4m3 bytes (16-byte aligned);
+ *   k_scales, v_scales  [n_slots / block_tokens][h_kv] bytes: one scale
+ *                       2^(byte - 127) per block of block_tokens consecutive
+ *                       slots and KV head.
+ *
+ *   value = e4m3(code) * 2^(scale - 127)
+ *
+ * The value is exact in BF16.  head_dim 128 or 256; block_tokens a power of
+ * two from 4 to 128 that divides page_size (else QSA_ERR_UNSUPPORTED) and
+ * n_slots.  The scale bytes are as qsa_append_kv_fp8 writes them, 63 to 190.
+ *
+ * qsa_append_kv_fp8 quantises K and V rows into their slots:
+ *   k_new, v_new   n_tok rows of [h_kv][head_dim] BF16, ld_k / ld_v elements
+ *                  apart (a multiple of 8; bases 16-byte aligned).
+ *   req_tok_start [n_req+1], req_first_pos [n_req]: as qsa_append_keys; the
+ *                  row of position p of request r goes to slot(p).  Rows
+ *                  behind req_tok_start[n_req] are not read.
+ *   A block's scale is the smallest 2^e, e in [-64, 63], with max|x| <= 448 2^e
+ *   over the finite values of its tokens, code = e4m3(x / 2^e) (nearest, ties
+ *   to even, saturating); infinities and NaN become the NaN code.  Where the
+ *   block's first token is not among the call's, its earlier tokens (positions
+ *   below req_first_pos, written before) count with the scale they have: it
+ *   never falls, and where it grows by 2^k their codes are rounded once more,
+ *   to e4m3(code / 2^k).  What the block holds behind the call's last position
+ *   has no meaning afterwards, until it is written again: a request is
+ *   extended at its end, or cut back and extended from there.
+ *   Blocks that a position of the call lies in belong to one request (pages
+ *   that requests share are only read).  Blocks of no position keep every
+ *   byte.  A position or page out of range is skipped, with all of the call's
+ *   tokens in its block, and latches fault bit 0.
+ *
+ * qsa_gather_kv_fp8 reads rows back: k_out, v_out [n][h_kv][head_dim] BF16
+ *   (32-byte aligned), row i from slots[i]; a negative slot gives zeros, as
+ *   does a slot >= n_slots, which also latches fault bit 0.
+ *
+ * qsa_sparse_attn_fp8 is qsa_sparse_attn_fp4 on this cache (h_q / h_kv up to
+ * 16 for both head dims), qsa_window_attn_fp8 qsa_window_attn_fp4, with their
+ * arguments, outputs, masks and faults.  The cache's values enter the dot
+ * products and the value sums exactly; the softmax statistics are FP32 and
+ * the weights keep 22 significant bits (tiny ones less: weight times V scale
+ * is held to 2^-35 of the row's largest).
+ *   max_rows_per_req  host upper bound of the rows of any one request: if it is
+ *              above 1, rows of a request share what they read, up to 64 (row,
+ *              query head) pairs at a time.  It never changes which positions
+ *              count.  Requests of very many rows (chunks, prompts) take less
+ *              on rows read back (qsa_gather_kv_fp8) and qsa_window_attn.
+ *   workspace  as the matching *_workspace_size(): 0 except for few rows with
+ *              many entries.  Calls that may overlap on the GPU need one each.
+ * ------------------------------------------------------------------- */
+qsa_status qsa_append_kv_fp8(const void* k_new, const void* v_new, int64_t ld_k, int64_t ld_v, int32_t n_tok,
+                             int32_t h_kv, int32_t head_dim, const int32_t* req_tok_start,
+                             const int32_t* req_first_pos, int32_t n_req, const int32_t* page_table, int64_t ld_pt,
+                             int32_t page_size, int32_t block_tokens, void* k_codes, void* k_scales, void* v_codes,
+                             void* v_scales, int64_t n_slots, void* stream);
+qsa_status qsa_gather_kv_fp8(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                             int64_t n_slots, int32_t h_kv, int32_t head_dim, int32_t block_tokens,
+                             const int32_t* slots, int64_t n, void* k_out, void* v_out, void* stream);
+size_t qsa_sparse_attn_fp8_workspace_size(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t n_idx);
+qsa_status qsa_sparse_attn_fp8(const void* q, int64_t ld_q, const void* k_codes, const void* k_scales,
+                               const void* v_codes, const void* v_scales, int64_t n_slots, int32_t block_tokens,
+                               int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t head_dim, const int32_t* slots,
+                               int64_t ld_slots, int32_t n_idx, float scale, float* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+size_t qsa_window_attn_fp8_workspace_size(int32_t n_rows, int32_t n_req, int32_t max_rows_per_req, int32_t h_q,
+                                          int32_t h_kv, int32_t head_dim, int32_t max_len, int32_t window,
+                                          int32_t n_sink);
+qsa_status qsa_window_attn_fp8(const void* q, int64_t ld_q, const void* k_codes, const void* k_scales,
+                               const void* v_codes, const void* v_scales, int64_t n_slots, int32_t block_tokens,
+                               int32_t n_req, const int32_t* req_row_start, int32_t n_rows, const int32_t* row_len,
+                               int32_t max_len, int32_t max_rows_per_req, int32_t h_q, int32_t h_kv, int32_t head_dim,
+                               const int32_t* page_table, int64_t ld_pt, int32_t page_size, int32_t window,
+                               int32_t n_sink, float scale, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------
+ * A step's rows, slots and pages, from lengths that are on the device.
+ * (Library additions with no counterpart in the source pages, whose engines
+ * build page tables and slot maps on the host.)
+ *
+ * qsa_plan_step: request r holds ctx_len[r] tokens and gets n_new[r] more.
+ *   page_table  [n_req][ld_pt]: the first ceil(ctx_len / page_size) entries of
+ *               a row are the pages it has; the pages it needs are added
+ *               behind them.  Other entries are left as they were.
+ *   free_pages  [n_pool] list of free pages, of which the first *n_free count.
+ *               The step's pages are the last ones, handed out in the order of
+ *               the requests and of their pages; *n_free falls by their number.
+ *   n_tok       rows that the outputs hold (at most 2^30).
+ *   req_row_start [n_req+1]: sums of n_new, at most n_tok: the row (and token)
+ *               starts that the other calls take.
+ *   new_len     [n_req]: ctx_len + n_new, or ctx_len where the request was
+ *               refused (not the array ctx_len itself).
+ *   row_len     [n_tok]: the tokens that each row sees (its position + 1);
+ *   row_req     [n_tok] or NULL: its request;
+ *   slots       [n_tok]: the slot of its own token.
+ *               Rows behind the last request's get 0, -1 and -1.
+ *   A request gets all that it needs or is refused: the page table's row is
+ *   left, its rows have row_len 0 and slot -1 (with their request), and
+ *   new_len says so.  Refused are, with fault bit 4, the requests from the
+ *   first one on whose pages exceed the list (those that need none are
+ *   served) or whose rows exceed n_tok (of which there may be none or some);
+ *   a request that would outgrow its row of the table or position 2^31 - 1
+ *   (bit 0); a negative ctx_len or n_new (bit 3; a negative n_new has no
+ *   rows).  A page already there that is negative gives its rows slot -1 (bit
+ *   0).  An *n_free outside [0, n_pool] counts as 0 (bit 3).
+ *
+ * qsa_release_pages gives pages back: entries from_page[r] .. to_page[r] - 1 of
+ *   request r's row, in the requests' order, go to the end of the list and
+ *   become -1 in the table; *n_free grows by their number.  Negative entries
+ *   are skipped.  (A request that ended: 0 .. ceil(len / page_size); a draft
+ *   cut back from length b to a: ceil(a / page_size) .. ceil(b / page_size);
+ *   pages behind a window likewise.)  A range outside the row is skipped (bit
+ *   0); what does not fit the list stays in the table (bit 4), and a list with
+ *   *n_free outside [0, n_pool] takes nothing (bits 3 and 4).  A page that
+ *   several rows hold must be left out until the last of them gives it back.
+ *
+ * Calls that use one list are made one after the other (one stream, or events).
+ * ------------------------------------------------------------------- */
+qsa_status qsa_plan_step(const int32_t* ctx_len, const int32_t* n_new, int32_t n_req, int32_t* page_table,
+                         int64_t ld_pt, int32_t page_size, const int32_t* free_pages, int32_t n_pool, int32_t* n_free,
+                         int32_t n_tok, int32_t* req_row_start, int32_t* new_len, int32_t* row_len, int32_t* row_req,
+                         int32_t* slots, void* stream);
+qsa_status qsa_release_pages(int32_t* page_table, int64_t ld_pt, int32_t n_req, const int32_t* from_page,
+                             const int32_t* to_page, int32_t* free_pages, int32_t n_pool, int32_t* n_free,
+                             void* stream);
 
 /* ---------------------------------------------------------------------
  * Top-k_blk blocks of given block scores, expanded and translated, one

@@ -22,6 +22,7 @@ __all__ = [
     "select_blocks", "indexshare_slots", "indexshare_width", "sparse_attn", "append_keys", "decode_step",
     "rope_queries", "quantize_keys_fp8", "index_scores_fp8", "indexer_select_fp8", "index_scores_gated",
     "indexer_select_gated", "append_kv_fp4", "gather_kv_fp4", "sparse_attn_fp4", "window_attn", "window_attn_fp4",
+    "append_kv_fp8", "gather_kv_fp8", "sparse_attn_fp8", "window_attn_fp8", "plan_step", "release_pages",
     "HEAD_DIM", "HEADS", "BLOCK", "MAX_K",
 ]
 
@@ -91,6 +92,17 @@ def lib():
                                                i32, i32, i32, f, p, p, p, sz, p]),
             "qsa_window_attn_fp4": (ctypes.c_int, [p, i64, p, p, p, p, i64, i32, p, i32, p, i32, i32, i32, i32, i32,
                                                    p, i64, i32, i32, i32, f, f, f, p, p, p, sz, p]),
+            "qsa_append_kv_fp8": (ctypes.c_int, [p, p, i64, i64, i32, i32, i32, p, p, i32, p, i64, i32, i32, p, p, p, p,
+                                                 i64, p]),
+            "qsa_gather_kv_fp8": (ctypes.c_int, [p, p, p, p, i64, i32, i32, i32, p, i64, p, p, p]),
+            "qsa_sparse_attn_fp8_workspace_size": (sz, [i32, i32, i32, i32, i32]),
+            "qsa_sparse_attn_fp8": (ctypes.c_int, [p, i64, p, p, p, p, i64, i32, i32, i32, i32, i32, p, i64, i32, f, p,
+                                                   p, p, sz, p]),
+            "qsa_window_attn_fp8_workspace_size": (sz, [i32, i32, i32, i32, i32, i32, i32, i32, i32]),
+            "qsa_window_attn_fp8": (ctypes.c_int, [p, i64, p, p, p, p, i64, i32, i32, p, i32, p, i32, i32, i32, i32,
+                                                   i32, p, i64, i32, i32, i32, f, p, p, p, sz, p]),
+            "qsa_plan_step": (ctypes.c_int, [p, p, i32, p, i64, i32, p, i32, p, i32, p, p, p, p, p, p]),
+            "qsa_release_pages": (ctypes.c_int, [p, i64, i32, p, p, p, i32, p, p]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -613,7 +625,7 @@ def _indexer_select_call(fn, key_ptrs, pool_rows, q, req_row_start, row_len, pag
     return out
 
 
-# ----------------------------------------------------------------- 4-bit KV cache, window attention
+# ----------------------------------------------------------------- 4-bit and 8-bit KV caches, window attention, paging
 # The checks of these calls run in two forms: one pass over cheap attributes,
 # and only when that finds something (_explain) the one that says what.  A
 # decode step's calls cost the host a few microseconds each, mostly these.
@@ -853,7 +865,7 @@ def window_attn_fp4(q, k_codes, k_scales, v_codes, v_scales, req_row_start, row_
 
 
 def _window_call(fn, cache_ptrs, scales, n_slots, h_kv, d, q, req_row_start, row_len, page_table, page_size, max_len,
-                 window, n_sink, scale, max_rows_per_req, out, lse, want_lse, workspace, stream):
+                 window, n_sink, scale, max_rows_per_req, out, lse, want_lse, workspace, stream, block=()):
     bf16, f32, i32, _, _ = _t()
     try:
         dev = q.get_device()
@@ -878,9 +890,206 @@ def _window_call(fn, cache_ptrs, scales, n_slots, h_kv, d, q, req_row_start, row
         lse = None
     elif lse is None:
         lse = _empty((n_rows, h_q), f32, q.device, stream)
-    _launch_ws(fn, dev, stream, "qsa_window_attn_workspace_size",
-               (n_rows, h_q, h_kv, d, max_len, window, n_sink), workspace, q.data_ptr(),
-               q.stride(0) if n_rows > 1 else h_q * d, *cache_ptrs, n_slots, n_req, req_row_start.data_ptr(), n_rows,
+    if fn == "qsa_window_attn_fp8":
+        size_fn, size_args = fn + "_workspace_size", (n_rows, n_req, max_rows_per_req)
+    else:
+        size_fn, size_args = "qsa_window_attn_workspace_size", (n_rows,)
+    _launch_ws(fn, dev, stream, size_fn, (*size_args, h_q, h_kv, d, max_len, window, n_sink), workspace, q.data_ptr(),
+               q.stride(0) if n_rows > 1 else h_q * d, *cache_ptrs, n_slots, *block, n_req, req_row_start.data_ptr(), n_rows,
                row_len.data_ptr(), max_len, max_rows_per_req, h_q, h_kv, d, page_table.data_ptr(), ld_pt, page_size,
                window, n_sink, d ** -0.5 if scale is None else scale, *scales, out.data_ptr(), _ptr(lse))
     return out, lse
+
+
+def _cache8_ok(dev, k_codes, k_scales, v_codes, v_scales):
+    """The 8-bit cache's arrays fit together: codes [n_slots][h_kv][d], scales
+    [n_slots / block][h_kv]; (ok, tokens to a scale)."""
+    n_slots, h_kv, _ = k_codes.shape
+    n_blk = k_scales.shape[0]
+    block = n_slots // n_blk if n_blk else 4
+    return (_all(dev, _t()[3], k_codes, k_scales, v_codes, v_scales) and v_codes.shape == k_codes.shape
+            and k_scales.shape == (n_blk, h_kv) == v_scales.shape and n_blk * block == n_slots), block
+
+
+def _explain8(fn, first, k_codes, k_scales, v_codes, v_scales, **more):
+    _explain(fn, first, u8=((k_codes, "k_codes", 3), (k_scales, "k_scales", 2), (v_codes, "v_codes", 3),
+                            (v_scales, "v_scales", 2)), **more)
+
+
+def append_kv_fp8(k_new, v_new, req_tok_start, req_first_pos, k_codes, k_scales, v_codes, v_scales, page_table,
+                  page_size, stream=None):
+    """Quantises K and V rows [n_tok][h_kv][head_dim] bf16 into the 8-bit
+    cache (in place): codes [n_slots][h_kv][head_dim] and scales
+    [n_slots / block][h_kv], uint8, with `block` tokens to a scale (a power of
+    two, 4 to 128, that divides the page).  Request r's rows req_tok_start[r] ..
+    go to the slots of positions req_first_pos[r], req_first_pos[r]+1, ...; a
+    block that already holds earlier tokens keeps at least its scale, and they
+    are rounded once more where it grows.  The rows may be columns of one
+    projection's output.  Returns the four arrays."""
+    bf16, _, i32, _, _ = _t()
+    try:
+        dev = k_codes.get_device()
+        n_slots, h_kv, d = k_codes.shape
+        n_tok = k_new.shape[0]
+        n_req, ld_pt = page_table.shape
+        ok, block = _cache8_ok(dev, k_codes, k_scales, v_codes, v_scales)
+        ok = (ok and dev >= 0 and _all(dev, i32, req_tok_start, req_first_pos, page_table)
+              and _rows_ok(k_new, dev, bf16) and _rows_ok(v_new, dev, bf16)
+              and k_new.shape == (n_tok, h_kv, d) == v_new.shape
+              and req_tok_start.shape == (n_req + 1,) and req_first_pos.shape == (n_req,))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain8("append_kv_fp8", k_codes, k_codes, k_scales, v_codes, v_scales,
+                  rows=((k_new, "k_new"), (v_new, "v_new")),
+                  i32=((req_tok_start, "req_tok_start", 1), (req_first_pos, "req_first_pos", 1),
+                       (page_table, "page_table", 2)))
+    row = h_kv * d
+    _check("qsa_append_kv_fp8", _launch(
+        "qsa_append_kv_fp8", dev, stream, k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0) if n_tok > 1 else row,
+        v_new.stride(0) if n_tok > 1 else row, n_tok, h_kv, d, req_tok_start.data_ptr(), req_first_pos.data_ptr(),
+        n_req, page_table.data_ptr(), ld_pt, page_size, block, k_codes.data_ptr(), k_scales.data_ptr(),
+        v_codes.data_ptr(), v_scales.data_ptr(), n_slots))
+    return k_codes, k_scales, v_codes, v_scales
+
+
+def gather_kv_fp8(k_codes, k_scales, v_codes, v_scales, slots, k_out=None, v_out=None, stream=None):
+    """Reads the rows at slots (int32, any shape) back from the 8-bit cache:
+    (k, v) [*slots.shape][h_kv][head_dim] bf16; a negative slot gives zeros."""
+    bf16, _, i32, _, _ = _t()
+    try:
+        dev = k_codes.get_device()
+        n_slots, h_kv, d = k_codes.shape
+        out_shape = (*slots.shape, h_kv, d)
+        ok, block = _cache8_ok(dev, k_codes, k_scales, v_codes, v_scales)
+        ok = (ok and dev >= 0 and _all(dev, i32, slots)
+              and (k_out is None or _all(dev, bf16, k_out) and k_out.shape == out_shape)
+              and (v_out is None or _all(dev, bf16, v_out) and v_out.shape == out_shape))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain8("gather_kv_fp8", k_codes, k_codes, k_scales, v_codes, v_scales, i32=((slots, "slots", None),),
+                  bf16=((k_out, "k_out", None), (v_out, "v_out", None)))
+    if k_out is None:
+        k_out = _empty(out_shape, bf16, slots.device, stream)
+    if v_out is None:
+        v_out = _empty(out_shape, bf16, slots.device, stream)
+    _check("qsa_gather_kv_fp8", _launch(
+        "qsa_gather_kv_fp8", dev, stream, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+        v_scales.data_ptr(), n_slots, h_kv, d, block, slots.data_ptr(), slots.numel(), k_out.data_ptr(),
+        v_out.data_ptr()))
+    return k_out, v_out
+
+
+def sparse_attn_fp8(q, k_codes, k_scales, v_codes, v_scales, slots, scale=None, n_idx=None, out=None, lse=None,
+                    want_lse=True, workspace=None, stream=None):
+    """sparse_attn over the 8-bit cache: softmax attention of q
+    [n_rows][h_q][head_dim] bf16 over the rows at slots [n_rows][w] (int32,
+    -1 skipped).  Returns (out float32, lse [n_rows][h_q] or None)."""
+    bf16, f32, i32, _, _ = _t()
+    try:
+        dev = q.get_device()
+        n_rows, h_q, d = q.shape
+        n_slots, h_kv, w = k_codes.shape
+        rows, width = slots.shape
+        ok, block = _cache8_ok(dev, k_codes, k_scales, v_codes, v_scales)
+        ok = (ok and dev >= 0 and _rows_ok(q, dev, bf16) and _all(dev, i32, slots) and d == w and rows == n_rows
+              and (out is None or _all(dev, f32, out) and out.shape == (n_rows, h_q, d))
+              and (lse is None or _all(dev, f32, lse) and lse.shape == (n_rows, h_q))
+              and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous()))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain8("sparse_attn_fp8", q, k_codes, k_scales, v_codes, v_scales, rows=((q, "q"),),
+                  i32=((slots, "slots", 2),), f32=((out, "out", 3), (lse, "lse", 2)))
+    if n_idx is None:
+        n_idx = width
+    if out is None:
+        out = _empty((n_rows, h_q, d), f32, q.device, stream)
+    if not want_lse:
+        lse = None
+    elif lse is None:
+        lse = _empty((n_rows, h_q), f32, q.device, stream)
+    _launch_ws("qsa_sparse_attn_fp8", dev, stream, "qsa_sparse_attn_fp8_workspace_size",
+               (n_rows, h_q, h_kv, d, n_idx), workspace, q.data_ptr(), q.stride(0) if n_rows > 1 else h_q * d,
+               k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), n_slots, block, n_rows,
+               h_q, h_kv, d, slots.data_ptr(), width, n_idx, d ** -0.5 if scale is None else scale, out.data_ptr(),
+               _ptr(lse))
+    return out, lse
+
+
+def window_attn_fp8(q, k_codes, k_scales, v_codes, v_scales, req_row_start, row_len, page_table, page_size, max_len,
+                    window, n_sink=0, scale=None, max_rows_per_req=None, out=None, lse=None, want_lse=True,
+                    workspace=None, stream=None):
+    """window_attn over the 8-bit cache (a window of max_len: causal
+    attention).  max_rows_per_req (default: n_rows) bounds the rows of one
+    request: above 1, a request's rows share what they read.  For whole prompts
+    read the window back with gather_kv_fp8 and use window_attn."""
+    try:
+        n_slots, h_kv, d = k_codes.shape
+        ok, block = _cache8_ok(q.get_device(), k_codes, k_scales, v_codes, v_scales)
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain8("window_attn_fp8", q, k_codes, k_scales, v_codes, v_scales)
+    return _window_call("qsa_window_attn_fp8",
+                        (k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr()), (), n_slots,
+                        h_kv, d, q, req_row_start, row_len, page_table, page_size, max_len, window, n_sink, scale,
+                        max_rows_per_req, out, lse, want_lse, workspace, stream, (block,))
+
+
+def plan_step(ctx_len, n_new, page_table, page_size, free_pages, n_free, n_tok, req_row_start=None, new_len=None,
+              row_len=None, row_req=None, slots=None, stream=None):
+    """A step's rows, slots and pages from lengths on the device (int32):
+    request r holds ctx_len[r] tokens and gets n_new[r].  The pages it needs
+    come from the end of free_pages (the first n_free[0] count) and are written
+    behind those it has in its row of page_table; page_table and n_free are
+    updated in place.  n_tok: rows of the outputs, those behind the step's are
+    padding (length 0, request and slot -1).  Returns (req_row_start [n_req+1],
+    new_len [n_req], row_len, row_req, slots [n_tok]).  A request that does not
+    fit is refused (new_len = ctx_len; see qsa_plan_step)."""
+    _, _, i32, _, _ = _t()
+    names = ("req_row_start", "new_len", "row_len", "row_req", "slots")
+    outs = [req_row_start, new_len, row_len, row_req, slots]
+    try:
+        dev = page_table.get_device()
+        n_req, ld_pt = page_table.shape
+        sizes = (n_req + 1, n_req, n_tok, n_tok, n_tok)
+        ok = (dev >= 0 and _all(dev, i32, ctx_len, n_new, page_table, free_pages, n_free)
+              and ctx_len.shape == (n_req,) == n_new.shape and free_pages.dim() == 1 and n_free.numel() == 1
+              and all(o is None or _all(dev, i32, o) and o.shape == (n,) for o, n in zip(outs, sizes)))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain("plan_step", page_table, i32=((ctx_len, "ctx_len", 1), (n_new, "n_new", 1),
+                                               (page_table, "page_table", 2), (free_pages, "free_pages", 1),
+                                               (n_free, "n_free", 1), *((o, n, 1) for o, n in zip(outs, names))))
+    outs = [_empty((n,), i32, page_table.device, stream) if o is None else o for o, n in zip(outs, sizes)]
+    _check("qsa_plan_step", _launch(
+        "qsa_plan_step", dev, stream, ctx_len.data_ptr(), n_new.data_ptr(), n_req, page_table.data_ptr(), ld_pt,
+        page_size, free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(), n_tok, outs[0].data_ptr(),
+        outs[1].data_ptr(), outs[2].data_ptr(), outs[3].data_ptr(), outs[4].data_ptr()))
+    return tuple(outs)
+
+
+def release_pages(page_table, from_page, to_page, free_pages, n_free, stream=None):
+    """Entries from_page[r] .. to_page[r]-1 of each row of page_table (all
+    int32) go to the end of the list free_pages (n_free[0] pages long, which
+    grows) and become -1; negative entries are skipped.  Returns (page_table,
+    free_pages, n_free), updated in place."""
+    _, _, i32, _, _ = _t()
+    try:
+        dev = page_table.get_device()
+        n_req, ld_pt = page_table.shape
+        ok = (dev >= 0 and _all(dev, i32, page_table, from_page, to_page, free_pages, n_free)
+              and from_page.shape == (n_req,) == to_page.shape and free_pages.dim() == 1 and n_free.numel() == 1)
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain("release_pages", page_table, i32=((page_table, "page_table", 2), (from_page, "from_page", 1),
+                                                   (to_page, "to_page", 1), (free_pages, "free_pages", 1),
+                                                   (n_free, "n_free", 1)))
+    _check("qsa_release_pages", _launch(
+        "qsa_release_pages", dev, stream, page_table.data_ptr(), ld_pt, n_req, from_page.data_ptr(),
+        to_page.data_ptr(), free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr()))
+    return page_table, free_pages, n_free

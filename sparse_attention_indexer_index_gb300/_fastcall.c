@@ -251,6 +251,125 @@ static PyObject* fc_window_attn_workspace_size(PyObject* self, PyObject* const* 
   return PyLong_FromSize_t(qsa_window_attn_workspace_size(v0, v1, v2, v3, v4, v5, v6));
 }
 
+/* The calls of the 8-bit cache and of the paging, in the same way. */
+static PyObject* fc_append_kv_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 20, "append_kv_fp8")) return NULL;
+  const void *k_new = arg_ptr(a, 0), *v_new = arg_ptr(a, 1);
+  const int64_t ld_k = arg_i64(a, 2), ld_v = arg_i64(a, 3);
+  const int32_t n_tok = arg_i32(a, 4), h_kv = arg_i32(a, 5), d = arg_i32(a, 6);
+  const int32_t *start = arg_ptr(a, 7), *first = arg_ptr(a, 8);
+  const int32_t n_req = arg_i32(a, 9);
+  const int32_t* pt = arg_ptr(a, 10);
+  const int64_t ld_pt = arg_i64(a, 11);
+  const int32_t page = arg_i32(a, 12), block = arg_i32(a, 13);
+  void *c0 = arg_ptr(a, 14), *c1 = arg_ptr(a, 15), *c2 = arg_ptr(a, 16), *c3 = arg_ptr(a, 17);
+  const int64_t n_slots = arg_i64(a, 18);
+  void* stream = arg_ptr(a, 19);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromLong((long)qsa_append_kv_fp8(k_new, v_new, ld_k, ld_v, n_tok, h_kv, d, start, first, n_req, pt,
+                                                 ld_pt, page, block, c0, c1, c2, c3, n_slots, stream));
+}
+
+static PyObject* fc_gather_kv_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 13, "gather_kv_fp8")) return NULL;
+  const void *c0 = arg_ptr(a, 0), *c1 = arg_ptr(a, 1), *c2 = arg_ptr(a, 2), *c3 = arg_ptr(a, 3);
+  const int64_t n_slots = arg_i64(a, 4);
+  const int32_t h_kv = arg_i32(a, 5), d = arg_i32(a, 6), block = arg_i32(a, 7);
+  const int32_t* slots = arg_ptr(a, 8);
+  const int64_t cnt = arg_i64(a, 9);
+  void *k_out = arg_ptr(a, 10), *v_out = arg_ptr(a, 11), *stream = arg_ptr(a, 12);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromLong((long)qsa_gather_kv_fp8(c0, c1, c2, c3, n_slots, h_kv, d, block, slots, cnt, k_out, v_out,
+                                                 stream));
+}
+
+static PyObject* fc_sparse_attn_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 21, "sparse_attn_fp8")) return NULL;
+  const void* q = arg_ptr(a, 0);
+  const int64_t ld_q = arg_i64(a, 1);
+  const void *c0 = arg_ptr(a, 2), *c1 = arg_ptr(a, 3), *c2 = arg_ptr(a, 4), *c3 = arg_ptr(a, 5);
+  const int64_t n_slots = arg_i64(a, 6);
+  const int32_t block = arg_i32(a, 7), n_rows = arg_i32(a, 8), h_q = arg_i32(a, 9), h_kv = arg_i32(a, 10);
+  const int32_t d = arg_i32(a, 11);
+  const int32_t* slots = arg_ptr(a, 12);
+  const int64_t ld_slots = arg_i64(a, 13);
+  const int32_t n_idx = arg_i32(a, 14);
+  const float scale = arg_f32(a, 15);
+  float *out = arg_ptr(a, 16), *lse = arg_ptr(a, 17);
+  void* ws = arg_ptr(a, 18);
+  const size_t ws_bytes = arg_size(a, 19);
+  void* stream = arg_ptr(a, 20);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromLong((long)qsa_sparse_attn_fp8(q, ld_q, c0, c1, c2, c3, n_slots, block, n_rows, h_q, h_kv, d, slots,
+                                                   ld_slots, n_idx, scale, out, lse, ws, ws_bytes, stream));
+}
+
+static PyObject* fc_window_attn_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 28, "window_attn_fp8")) return NULL;
+  const void* q = arg_ptr(a, 0);
+  const int64_t ld_q = arg_i64(a, 1);
+  const void *c0 = arg_ptr(a, 2), *c1 = arg_ptr(a, 3), *c2 = arg_ptr(a, 4), *c3 = arg_ptr(a, 5);
+  const int64_t n_slots = arg_i64(a, 6);
+  const int32_t block = arg_i32(a, 7), n_req = arg_i32(a, 8);
+  const int32_t* start = arg_ptr(a, 9);
+  const int32_t n_rows = arg_i32(a, 10);
+  const int32_t* row_len = arg_ptr(a, 11);
+  const int32_t max_len = arg_i32(a, 12), max_rows = arg_i32(a, 13);
+  const int32_t h_q = arg_i32(a, 14), h_kv = arg_i32(a, 15), d = arg_i32(a, 16);
+  const int32_t* pt = arg_ptr(a, 17);
+  const int64_t ld_pt = arg_i64(a, 18);
+  const int32_t page = arg_i32(a, 19), window = arg_i32(a, 20), sinks = arg_i32(a, 21);
+  const float scale = arg_f32(a, 22);
+  void* out = arg_ptr(a, 23);
+  float* lse = arg_ptr(a, 24);
+  void* ws = arg_ptr(a, 25);
+  const size_t ws_bytes = arg_size(a, 26);
+  void* stream = arg_ptr(a, 27);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromLong((long)qsa_window_attn_fp8(q, ld_q, c0, c1, c2, c3, n_slots, block, n_req, start, n_rows,
+                                                   row_len, max_len, max_rows, h_q, h_kv, d, pt, ld_pt, page, window,
+                                                   sinks, scale, out, lse, ws, ws_bytes, stream));
+}
+
+static PyObject* fc_plan_step(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 16, "plan_step")) return NULL;
+  const int32_t *ctx_len = arg_ptr(a, 0), *n_new = arg_ptr(a, 1);
+  const int32_t n_req = arg_i32(a, 2);
+  int32_t* pt = arg_ptr(a, 3);
+  const int64_t ld_pt = arg_i64(a, 4);
+  const int32_t page = arg_i32(a, 5);
+  const int32_t* free_pages = arg_ptr(a, 6);
+  const int32_t n_pool = arg_i32(a, 7);
+  int32_t* n_free = arg_ptr(a, 8);
+  const int32_t n_tok = arg_i32(a, 9);
+  int32_t *start = arg_ptr(a, 10), *new_len = arg_ptr(a, 11), *row_len = arg_ptr(a, 12), *row_req = arg_ptr(a, 13);
+  int32_t* slots = arg_ptr(a, 14);
+  void* stream = arg_ptr(a, 15);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromLong((long)qsa_plan_step(ctx_len, n_new, n_req, pt, ld_pt, page, free_pages, n_pool, n_free, n_tok,
+                                             start, new_len, row_len, row_req, slots, stream));
+}
+
+static PyObject* fc_release_pages(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 9, "release_pages")) return NULL;
+  int32_t* pt = arg_ptr(a, 0);
+  const int64_t ld_pt = arg_i64(a, 1);
+  const int32_t n_req = arg_i32(a, 2);
+  const int32_t *from = arg_ptr(a, 3), *to = arg_ptr(a, 4);
+  int32_t* free_pages = arg_ptr(a, 5);
+  const int32_t n_pool = arg_i32(a, 6);
+  int32_t* n_free = arg_ptr(a, 7);
+  void* stream = arg_ptr(a, 8);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromLong((long)qsa_release_pages(pt, ld_pt, n_req, from, to, free_pages, n_pool, n_free, stream));
+}
+
 static PyMethodDef fc_methods[] = {
     {"qsa_decode_step", (PyCFunction)(void (*)(void))fc_decode_step, METH_FASTCALL, "qsa_decode_step"},
     {"qsa_decode_step_gated", (PyCFunction)(void (*)(void))fc_decode_step_gated, METH_FASTCALL,
@@ -265,6 +384,12 @@ static PyMethodDef fc_methods[] = {
     {"qsa_window_attn_fp4", (PyCFunction)(void (*)(void))fc_window_attn_fp4, METH_FASTCALL, "qsa_window_attn_fp4"},
     {"qsa_sparse_attn_fp4_workspace_size", (PyCFunction)(void (*)(void))fc_sparse_attn_fp4_workspace_size, METH_FASTCALL, "qsa_sparse_attn_fp4_workspace_size"},
     {"qsa_window_attn_workspace_size", (PyCFunction)(void (*)(void))fc_window_attn_workspace_size, METH_FASTCALL, "qsa_window_attn_workspace_size"},
+    {"qsa_append_kv_fp8", (PyCFunction)(void (*)(void))fc_append_kv_fp8, METH_FASTCALL, "qsa_append_kv_fp8"},
+    {"qsa_gather_kv_fp8", (PyCFunction)(void (*)(void))fc_gather_kv_fp8, METH_FASTCALL, "qsa_gather_kv_fp8"},
+    {"qsa_sparse_attn_fp8", (PyCFunction)(void (*)(void))fc_sparse_attn_fp8, METH_FASTCALL, "qsa_sparse_attn_fp8"},
+    {"qsa_window_attn_fp8", (PyCFunction)(void (*)(void))fc_window_attn_fp8, METH_FASTCALL, "qsa_window_attn_fp8"},
+    {"qsa_plan_step", (PyCFunction)(void (*)(void))fc_plan_step, METH_FASTCALL, "qsa_plan_step"},
+    {"qsa_release_pages", (PyCFunction)(void (*)(void))fc_release_pages, METH_FASTCALL, "qsa_release_pages"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef fc_module = {PyModuleDef_HEAD_INIT,

@@ -68,5 +68,7 @@ inline qsa_status check_paging(const int32_t* page_table, int64_t ld_pt, int32_t
 // Fault word of kv_api.cu's kernels: read into *bits, and cleared if asked
 // and non-zero; synchronises the stream.
 bool kv_fault_word(cudaStream_t stream, bool clear, unsigned* bits);
+// The same for kv8_api.cu's.
+bool kv8_fault_word(cudaStream_t stream, bool clear, unsigned* bits);
 
 }  // namespace qsa

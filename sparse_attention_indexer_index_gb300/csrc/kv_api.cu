@@ -11,6 +11,7 @@
 #include "../../include/qsa.h"
 #include "common.cuh"
 #include "host_util.cuh"
+#include "kv_host.cuh"
 #include "kv4.cuh"
 #include "kv_attn.cuh"
 #include "kv4_attn.cuh"
@@ -19,8 +20,6 @@
 using namespace qsa;
 
 namespace {
-
-constexpr int kMaxDevices = 64;
 
 // The kernel of a cache type, head dim and head tiles, and its shape.
 struct KaKernel {
@@ -51,36 +50,6 @@ bool set_ka_smem() {
   return true;
 }
 
-// A launch of clusters of c CTAs along x (c = 1: without that attribute), as
-// all here a programmatic dependent one: it may be set up while the kernel
-// before it in the stream ends.  Every kernel waits for that one's results
-// (griddepcontrol.wait) before it touches global memory.
-struct ClusterLaunch {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2] = {};
-  ClusterLaunch(dim3 grid, int threads, size_t smem, int c, cudaStream_t stream) {
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)c;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = c > 1 ? 2 : 1;
-  }
-  ClusterLaunch(const ClusterLaunch&) = delete;
-};
-
-qsa_status launched(cudaError_t e) {
-  if (e == cudaSuccess) return QSA_OK;
-  cudaGetLastError();
-  return QSA_ERR_CUDA;
-}
-
 // Per-device one-time set-up: the shared-memory opt-in of the kernels, and
 // how many of their clusters run at once.
 constexpr int kWtMaxCluster = 8;
@@ -91,17 +60,6 @@ struct KvDevice {
 };
 KvDevice g_kv_dev[kMaxDevices];
 std::mutex g_mu;
-
-template <class F>
-bool resident_clusters(F fn, int threads, size_t smem, int c, int sms, int* n) {
-  if (c == 1) {  // without the attribute
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, fn, threads, smem) != cudaSuccess) return false;
-    *n *= sms;
-    return *n > 0;
-  }
-  const ClusterLaunch l(dim3((unsigned)c), threads, smem, c, nullptr);
-  return cudaOccupancyMaxActiveClusters(n, fn, &l.cfg) == cudaSuccess;
-}
 
 bool set_up(KvDevice& d, int sms) {
   if (!set_ka_smem() ||
@@ -136,16 +94,10 @@ qsa_status kv_device(const KvDevice** out) {
   return QSA_OK;
 }
 
-bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
-
 // A tensor scale: a positive power of two between 2^-64 and 2^63.
 bool scale_ok(float g) {
   int e = 0;
   return std::isfinite(g) && g > 0.f && std::frexp(g, &e) == 0.5f && e >= -63 && e <= 64;
-}
-
-int64_t window_entries(int32_t max_len, int32_t window, int32_t n_sink) {
-  return std::min<int64_t>(max_len, (int64_t)window + n_sink);
 }
 
 // Heads and head dims of the calls here: 128 with up to 16 query heads per
@@ -154,34 +106,6 @@ bool kv_shape_ok(int32_t h_q, int32_t h_kv, int32_t d) {
   if (h_q <= 0 || h_kv <= 0 || h_kv > 65535 || h_q % h_kv != 0) return false;
   const int group = h_q / h_kv;
   return (d == 128 && group <= 16) || (d == 256 && group <= 8);
-}
-
-// Clusters per (row, KV head).  One, unless the clusters of 8 CTAs are too
-// few to fill the GPU and a row is long enough to pay for the merge launch.
-// The size of the workspace follows from it, so it depends on the arguments
-// alone (152 SMs, two CTAs each).
-int ka_groups(int64_t units, int64_t entries) {
-  const int64_t fill = 304 / (units * kKaMaxCluster);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, 16), entries / 4096));
-}
-
-// CTAs per cluster: the least of waves * (steps + start and end, about 4).
-// How many clusters run at once is the device's answer: on 152 SMs, 16
-// clusters of 7 do not where a CTA fills an SM (1,028 entries of D = 256: 23.7
-// us, in clusters of 6, which do, 17.6).
-int ka_cluster(int64_t units, int64_t entries, const KaKernel& k, const int* resident) {
-  int best = 1;
-  int64_t least = INT64_MAX;
-  for (int c = 1; c <= kKaMaxCluster && resident[c] > 0; ++c) {
-    const int64_t waves = (units + resident[c] - 1) / resident[c];
-    const int64_t steps = (entries + (int64_t)k.entries * c - 1) / ((int64_t)k.entries * c);
-    const int64_t cost = waves * (steps + 4);
-    if (cost < least) {
-      least = cost;
-      best = c;
-    }
-  }
-  return best;
 }
 
 enum { kKaBf16Window = 0, kKaFp4Window = 1, kKaFp4List = 2 };
@@ -194,17 +118,14 @@ qsa_status launch_ka(int cache, KvAttnArgs& a, int d, int64_t entries, void* wor
   const KvDevice* dev = nullptr;
   if (qsa_status st = kv_device(&dev)) return st;
   a.n_group = ka_groups(units, entries);
-  a.cluster = a.n_group > 1 ? kKaMaxCluster : ka_cluster(units, entries, k, dev->ka[cache][shape]);
+  a.cluster = a.n_group > 1 ? kKaMaxCluster : ka_cluster(units, entries, k.entries, dev->ka[cache][shape]);
   a.part = static_cast<float*>(workspace);
   if ((int64_t)a.n_rows * std::max(a.cluster * a.n_group, a.h_q) > INT32_MAX) return QSA_ERR_UNSUPPORTED;
   if (entries > (1 << 30)) return QSA_ERR_UNSUPPORTED;  // entry indices stay clear of 2^31
   const ClusterLaunch l(dim3((unsigned)((int64_t)a.n_rows * a.cluster * a.n_group), (unsigned)a.h_kv), k.threads, k.smem,
                         a.cluster, stream);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, k.fn, a);
-  if (e == cudaSuccess && a.n_group > 1)
-    e = launch_pdl(d == 256 ? kv_attn_merge_kernel<256> : kv_attn_merge_kernel<128>,
-                   dim3((unsigned)((int64_t)a.n_rows * a.h_q)), dim3((unsigned)d), 0, stream, a,
-                   cache == kKaBf16Window ? 0.0f : (float)kK4Bias);
+  if (e == cudaSuccess && a.n_group > 1) e = launch_merge(a, d, cache == kKaBf16Window ? 0.0f : (float)kK4Bias, stream);
   return launched(e);
 }
 
@@ -337,12 +258,6 @@ size_t ka_workspace(int64_t n_rows, int32_t h_q, int32_t h_kv, int32_t d, int64_
   return ng > 1 ? (size_t)(n_rows * h_q * ng * (d + 2) * 4) : 0;
 }
 
-qsa_status check_workspace(size_t need, const void* workspace, size_t bytes) {
-  if (need == 0) return QSA_OK;
-  if (!workspace || bytes < need) return QSA_ERR_WORKSPACE_TOO_SMALL;
-  return aligned16(workspace) ? QSA_OK : QSA_ERR_INVALID_ARG;
-}
-
 // The 4-bit cache's four arrays (any of them may be NULL with n_slots 0).
 qsa_status check_cache4(const void* kc, const void* ks, const void* vc, const void* vs, int64_t n_slots) {
   if (n_slots < 0 || n_slots > INT32_MAX) return QSA_ERR_INVALID_ARG;
@@ -350,49 +265,14 @@ qsa_status check_cache4(const void* kc, const void* ks, const void* vc, const vo
   return aligned16(kc) && aligned16(ks) && aligned16(vc) && aligned16(vs) ? QSA_OK : QSA_ERR_INVALID_ARG;
 }
 
-// Arguments that both window calls share.
-qsa_status check_window(const void* q, int64_t ld_q, int64_t n_slots, int32_t n_req, const int32_t* req_row_start,
-                        int32_t n_rows, const int32_t* row_len, int32_t max_len, int32_t max_rows_per_req, int32_t h_q,
-                        int32_t h_kv, int32_t d, const int32_t* page_table, int64_t ld_pt, int32_t page_size,
-                        int32_t window, int32_t n_sink, float scale, const void* out, const void* lse) {
-  if (!std::isfinite(scale)) return QSA_ERR_INVALID_ARG;
-  if (window < 1 || n_sink < 0 || max_rows_per_req < 0 || n_slots < 0 || n_slots > INT32_MAX) return QSA_ERR_INVALID_ARG;
-  if (!kv_shape_ok(h_q, h_kv, d)) return QSA_ERR_UNSUPPORTED;
-  if (qsa_status st = check_rows(n_req, req_row_start, n_rows, row_len, max_len)) return st;
-  if (n_rows == 0) return QSA_OK;
-  if (qsa_status st = check_paging(page_table, ld_pt, page_size, max_len)) return st;
-  if (!q || !out || !aligned16(q) || !aligned32(out) || (lse && !aligned4(lse))) return QSA_ERR_INVALID_ARG;
-  if (ld_q < (int64_t)h_q * d || ld_q % 8 != 0) return QSA_ERR_INVALID_ARG;
-  return QSA_OK;
-}
-
-void set_window(KvAttnArgs& a, const void* q, int64_t ld_q, int64_t n_slots, int32_t n_req,
-                const int32_t* req_row_start, int32_t n_rows, const int32_t* row_len, int32_t max_len, int32_t h_q,
-                int32_t h_kv, const int32_t* page_table, int64_t ld_pt, int32_t page_size, int32_t window,
-                int32_t n_sink, void* out, float* lse) {
-  a.q = static_cast<const uint16_t*>(q);
-  a.ld_q = ld_q;
-  a.n_slots = n_slots;
-  a.n_rows = n_rows;
-  a.h_q = h_q;
-  a.h_kv = h_kv;
-  a.n_req = n_req;
-  a.req_row_start = req_row_start;
-  a.row_len = row_len;
-  a.max_len = max_len;
-  a.window = window;
-  a.n_sink = n_sink;
-  a.page_table = page_table;
-  a.ld_pt = ld_pt;
-  a.page_size = page_size;
-  a.out_bf16 = 1;
-  a.out = out;
-  a.lse = lse;
-}
-
 }  // namespace
 
 namespace qsa {
+cudaError_t launch_merge(const KvAttnArgs& a, int d, float bias, cudaStream_t stream) {
+  return launch_pdl(d == 256 ? kv_attn_merge_kernel<256> : kv_attn_merge_kernel<128>,
+                    dim3((unsigned)((int64_t)a.n_rows * a.h_q)), dim3((unsigned)d), 0, stream, a, bias);
+}
+
 bool kv_fault_word(cudaStream_t stream, bool clear, unsigned* bits) {
   if (cudaMemcpyFromSymbolAsync(bits, g_fault_word, sizeof(*bits), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess)
@@ -536,7 +416,7 @@ qsa_status qsa_window_attn(const void* q, int64_t ld_q, const void* k_cache, con
                            float scale, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   if (qsa_status st = check_window(q, ld_q, n_slots, n_req, req_row_start, n_rows, row_len, max_len, max_rows_per_req,
                                    h_q, h_kv, head_dim, page_table, ld_pt, page_size, window, n_sink, scale, out,
-                                   lse))
+                                   lse, kv_shape_ok(h_q, h_kv, head_dim)))
     return st;
   if (n_rows == 0) return QSA_OK;
   if ((n_slots > 0 && (!k_cache || !v_cache)) || !aligned16(k_cache) || !aligned16(v_cache)) return QSA_ERR_INVALID_ARG;
@@ -567,7 +447,7 @@ qsa_status qsa_window_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
   if (!scale_ok(k_scale) || !scale_ok(v_scale)) return QSA_ERR_INVALID_ARG;
   if (qsa_status st = check_window(q, ld_q, n_slots, n_req, req_row_start, n_rows, row_len, max_len, max_rows_per_req,
                                    h_q, h_kv, head_dim, page_table, ld_pt, page_size, window, n_sink, scale, out,
-                                   lse))
+                                   lse, kv_shape_ok(h_q, h_kv, head_dim)))
     return st;
   if (n_rows == 0) return QSA_OK;
   if (qsa_status st = check_cache4(k_codes, k_scales, v_codes, v_scales, n_slots)) return st;

@@ -37,8 +37,10 @@
 // (4.9 TB/s: one CTA an SM, whose three stages a warp cannot keep more bytes on
 // the way).
 #pragma once
+#include <cuda_fp16.h>
+
 #include "common.cuh"
-#include "kv4.cuh"
+#include "kv_util.cuh"
 
 namespace qsa {
 

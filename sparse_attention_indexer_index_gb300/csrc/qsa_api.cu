@@ -929,9 +929,9 @@ qsa_status qsa_device_status(void* stream, int clear, uint32_t* h_bits) {
         cudaStreamSynchronize(st) != cudaSuccess)
       return QSA_ERR_CUDA;
   }
-  unsigned kv_bits = 0;
-  if (!kv_fault_word(st, clear != 0, &kv_bits)) return QSA_ERR_CUDA;
-  bits |= kv_bits;
+  unsigned kv_bits = 0, kv8_bits = 0;
+  if (!kv_fault_word(st, clear != 0, &kv_bits) || !kv8_fault_word(st, clear != 0, &kv8_bits)) return QSA_ERR_CUDA;
+  bits |= kv_bits | kv8_bits;
   if (h_bits) *h_bits = bits;
   return bits ? QSA_ERR_DEVICE_FAULT : QSA_OK;
 }
