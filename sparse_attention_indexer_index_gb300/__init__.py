@@ -715,6 +715,18 @@ def _launch_ws(fn, dev, stream, size_fn, size_args, workspace, *args):
     _check(fn, _launch(fn, dev, stream, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size()))
 
 
+def _launch_ws8(fn, dev, stream, size_args, workspace, *args):
+    """_launch of a call on the 8-bit cache: most need a workspace, so it is
+    asked for first."""
+    if workspace is None:
+        n = _call(fn + "_workspace_size", *size_args)
+        if n == 0:
+            return _check(fn, _launch(fn, dev, stream, *args, None, 0))
+        torch = _torch()
+        workspace = _empty(n, torch.uint8, torch.device("cuda", dev), stream)
+    _check(fn, _launch(fn, dev, stream, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+
+
 def append_kv_fp4(k_new, v_new, req_tok_start, req_first_pos, k_codes, k_scales, v_codes, v_scales, page_table,
                   page_size, k_scale=1.0, v_scale=1.0, stream=None):
     """Quantises K and V rows [n_tok][h_kv][head_dim] bf16 into the 4-bit
@@ -890,14 +902,15 @@ def _window_call(fn, cache_ptrs, scales, n_slots, h_kv, d, q, req_row_start, row
         lse = None
     elif lse is None:
         lse = _empty((n_rows, h_q), f32, q.device, stream)
-    if fn == "qsa_window_attn_fp8":
-        size_fn, size_args = fn + "_workspace_size", (n_rows, n_req, max_rows_per_req)
+    sizes = (h_q, h_kv, d, max_len, window, n_sink)
+    args = (q.data_ptr(), q.stride(0) if n_rows > 1 else h_q * d, *cache_ptrs, n_slots, *block, n_req,
+            req_row_start.data_ptr(), n_rows, row_len.data_ptr(), max_len, max_rows_per_req, h_q, h_kv, d,
+            page_table.data_ptr(), ld_pt, page_size, window, n_sink, d ** -0.5 if scale is None else scale, *scales,
+            out.data_ptr(), _ptr(lse))
+    if block:  # the 8-bit cache
+        _launch_ws8(fn, dev, stream, (n_rows, n_req, max_rows_per_req, *sizes), workspace, *args)
     else:
-        size_fn, size_args = "qsa_window_attn_workspace_size", (n_rows,)
-    _launch_ws(fn, dev, stream, size_fn, (*size_args, h_q, h_kv, d, max_len, window, n_sink), workspace, q.data_ptr(),
-               q.stride(0) if n_rows > 1 else h_q * d, *cache_ptrs, n_slots, *block, n_req, req_row_start.data_ptr(), n_rows,
-               row_len.data_ptr(), max_len, max_rows_per_req, h_q, h_kv, d, page_table.data_ptr(), ld_pt, page_size,
-               window, n_sink, d ** -0.5 if scale is None else scale, *scales, out.data_ptr(), _ptr(lse))
+        _launch_ws(fn, dev, stream, "qsa_window_attn_workspace_size", (n_rows, *sizes), workspace, *args)
     return out, lse
 
 
@@ -1010,11 +1023,10 @@ def sparse_attn_fp8(q, k_codes, k_scales, v_codes, v_scales, slots, scale=None, 
         lse = None
     elif lse is None:
         lse = _empty((n_rows, h_q), f32, q.device, stream)
-    _launch_ws("qsa_sparse_attn_fp8", dev, stream, "qsa_sparse_attn_fp8_workspace_size",
-               (n_rows, h_q, h_kv, d, n_idx), workspace, q.data_ptr(), q.stride(0) if n_rows > 1 else h_q * d,
-               k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), n_slots, block, n_rows,
-               h_q, h_kv, d, slots.data_ptr(), width, n_idx, d ** -0.5 if scale is None else scale, out.data_ptr(),
-               _ptr(lse))
+    _launch_ws8("qsa_sparse_attn_fp8", dev, stream, (n_rows, h_q, h_kv, d, n_idx), workspace, q.data_ptr(),
+                q.stride(0) if n_rows > 1 else h_q * d, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                v_scales.data_ptr(), n_slots, block, n_rows, h_q, h_kv, d, slots.data_ptr(), width, n_idx,
+                d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse))
     return out, lse
 
 

@@ -13,7 +13,7 @@
 #include "host_util.cuh"
 #include "kv_host.cuh"
 #include "kv8.cuh"
-#include "kv8_attn.cuh"
+#include "kv8_tc.cuh"
 #include "paging.cuh"
 
 using namespace qsa;
@@ -23,28 +23,30 @@ namespace {
 // The kernel of a tile's pairs, and its shape.
 struct K8Kernel {
   void (*fn)(Kv8AttnArgs);
-  int threads, smem;
-  int entries;  // entries of a CTA per step
+  int threads, smem, pairs, block;
 };
-template <int D, int P, int MT, bool kWindow>
+template <int D, int N, int PARTS, bool kWindow, bool kShared>
 constexpr K8Kernel k8() {
-  using Sh = K8Shape<D, P, MT>;
-  return {kv8_attn_kernel<D, P, MT, kWindow>, Sh::kThreads, Sh::kSmem, Sh::kStep * Sh::kGroups};
+  using Sh = K8Tc<D, N, PARTS, kWindow, kShared>;
+  return {kv8_tc_kernel<D, N, PARTS, kWindow, kShared>, Sh::kThreads, Sh::kSmem, N, Sh::kBlock};
 }
-// Single rows of up to 8 heads to a KV head, rows of up to 16 (a list; in a
-// window they are tiles of 16 pairs), tiles of 16 to 64 pairs.
-enum { kList8 = 0, kList16 = 1, kWindow8 = 2, kTiles = 3, kK8Kinds = 7 };
+// Lists and windows of single rows (up to 8 heads to a KV head, up to 16), and
+// the rows of a request together: 8, 16, 32 or 48 pairs.
+enum { kList8 = 0, kList16 = 1, kRow8 = 2, kTile8 = 3, kTile16 = 4, kTile32 = 5, kTile48 = 6, kK8Kinds = 7 };
 constexpr K8Kernel kK8Kernels[kK8Kinds][2] = {
-    {k8<128, 8, 1, false>(), k8<256, 8, 1, false>()},   {k8<128, 16, 1, false>(), k8<256, 16, 1, false>()},
-    {k8<128, 8, 1, true>(), k8<256, 8, 1, true>()},     {k8<128, 16, 1, true>(), k8<256, 16, 1, true>()},
-    {k8<128, 16, 2, true>(), k8<256, 16, 2, true>()},   {k8<128, 16, 3, true>(), k8<256, 16, 3, true>()},
-    {k8<128, 16, 4, true>(), k8<256, 16, 4, true>()},
+    {k8<128, 8, 4, false, false>(), k8<256, 8, 4, false, false>()},
+    {k8<128, 16, 4, false, false>(), k8<256, 16, 4, false, false>()},
+    {k8<128, 8, 4, true, false>(), k8<256, 8, 4, true, false>()},
+    {k8<128, 8, 4, true, true>(), k8<256, 8, 4, true, true>()},
+    {k8<128, 16, 3, true, true>(), k8<256, 16, 3, true, true>()},
+    {k8<128, 32, 3, true, true>(), k8<256, 32, 3, true, true>()},
+    {k8<128, 48, 3, true, true>(), k8<256, 48, 3, true, true>()},
 };
 
-// Per-device one-time set-up: the shared-memory opt-in of the kernels, and
-// how many of their clusters run at once.
+// Per-device one-time set-up: the shared-memory opt-in of the kernels, and how
+// many of their clusters run at once.
 struct Kv8Device {
-  bool ready;
+  int sms;  // 0: not set up
   int clusters[kK8Kinds][2][kKaMaxCluster + 1];
 };
 Kv8Device g_kv8_dev[kMaxDevices];
@@ -55,19 +57,19 @@ qsa_status kv8_device(const Kv8Device** out) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QSA_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
   Kv8Device& d = g_kv8_dev[dev];
-  if (!d.ready) {
+  if (d.sms == 0) {
     bool ok = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
     for (int i = 0; ok && i < kK8Kinds * 2; ++i) {
       const K8Kernel& k = kK8Kernels[i / 2][i % 2];
       ok = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) == cudaSuccess;
-      for (int c = 1; ok && c <= kKaMaxCluster; ++c)
+      for (int c = 1; ok && c <= kKaMaxCluster; c *= 2)
         ok = resident_clusters(k.fn, k.threads, (size_t)k.smem, c, sms, &d.clusters[i / 2][i % 2][c]);
     }
     if (!ok) {
       cudaGetLastError();
       return QSA_ERR_CUDA;
     }
-    d.ready = true;
+    d.sms = sms;
   }
   *out = &d;
   return QSA_OK;
@@ -97,44 +99,97 @@ qsa_status check_cache8(const void* kc, const void* ks, const void* vc, const vo
   return aligned16(kc) && aligned16(vc) ? QSA_OK : QSA_ERR_INVALID_ARG;
 }
 
-// How a window call is cut into tiles: single rows with up to 8 heads to a KV
-// head, else as many pairs as a request's rows have, 16 to 64 a tile.
+// How a call is cut into tiles, and how the work is dealt.
 struct K8Form {
-  int kind, rows;   // kernel, rows per tile
-  int64_t slots;    // tiles at most
-  int64_t units;    // tiles times KV heads for requests of equal length
+  int kind, rows;      // kernel, rows per tile
+  int64_t tile_slots;  // tiles at most
+  int64_t units;       // (tile, KV head) pairs, for requests of equal length
+  int64_t blocks;      // of a unit at most
+  bool cluster, share; // clusters, shares, else whole units
 };
-K8Form window_form(int32_t n_rows, int32_t n_req, int32_t max_rows_per_req, int32_t h_q, int32_t h_kv) {
+// Clusters where the units are few and their blocks, shared by the CTAs of a
+// cluster, few as well; shares of the blocks where units are long (their joins
+// take a second kernel, about 5 blocks' time); whole units where they are many.
+// It follows from the arguments alone (152 SMs), as the workspace does.
+K8Form finish(int kind, int d, int rows, int64_t tile_slots, int64_t units, int64_t n_req, int64_t entries) {
+  K8Form f{kind, rows, tile_slots, units, 1, false, false};
+  const int block = kK8Kernels[kind][d == 256].block;
+  f.blocks = std::max<int64_t>(1, (entries + block - 1) / block);
+  const bool list = kind <= kList16;
+  const bool fits = units < kK8MaxUnits && (list || (tile_slots <= kK8MaxTiles && n_req <= kK8MaxTiles)) &&
+                    units * f.blocks < INT32_MAX / 2;  // blocks are counted in 32 bits
+  int c = 1;
+  while (c < kKaMaxCluster && units * 2 * c <= 144 && f.blocks >= 2 * c) c *= 2;
+  const int64_t rounds = (units * c + 151) / 152;
+  const int64_t by_cluster = rounds * ((f.blocks + c - 1) / c);
+  const int64_t by_share = (units * f.blocks + 151) / 152 + 5;
+  f.cluster = rounds == 1 && (by_cluster <= by_share || !fits);
+  f.share = !f.cluster && fits;
+  return f;
+}
+K8Form list_form(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t d, int64_t n_idx) {
+  return finish(h_q / h_kv > 8 ? kList16 : kList8, d, 1, n_rows, (int64_t)n_rows * h_kv, 0, n_idx);
+}
+K8Form window_form(int32_t n_rows, int32_t n_req, int32_t max_rows_per_req, int32_t h_q, int32_t h_kv, int32_t d,
+                   int32_t max_len, int32_t window, int32_t n_sink) {
   const int group = h_q / h_kv;
-  if (max_rows_per_req <= 1 && group <= 8) return {kWindow8, 1, n_rows, (int64_t)n_rows * h_kv};
+  const int64_t entries = window_entries(max_len, window, n_sink);
+  if (max_rows_per_req <= 1 && group <= 8) return finish(kRow8, d, 1, n_rows, (int64_t)n_rows * h_kv, n_req, entries);
   const int64_t pairs = (int64_t)std::max(max_rows_per_req, 1) * group;
-  const int mt = (int)std::min<int64_t>(4, (pairs + 15) / 16);
-  const int rows = 16 * mt / group;
+  const int kind = pairs <= 8 ? kTile8 : pairs <= 16 ? kTile16 : pairs <= 32 ? kTile32 : kTile48;
+  const int rows = kK8Kernels[kind][0].pairs / group;
+  const int64_t slots = std::min<int64_t>(n_rows, n_rows / rows + (int64_t)n_req);
   const int64_t per_req = ((int64_t)n_rows + n_req - 1) / n_req;
-  return {kTiles + mt - 1, rows, n_rows / rows + (int64_t)n_req,
-          std::min<int64_t>(n_rows, (int64_t)n_req * ((per_req + rows - 1) / rows)) * h_kv};
+  // (a tile of rows in any order may span more than a row)
+  return finish(kind, d, rows, slots, std::min<int64_t>(slots, (int64_t)n_req * ((per_req + rows - 1) / rows)) * h_kv, n_req,
+                std::min<int64_t>(max_len, entries + rows));
 }
 
-size_t part_bytes(int64_t n_rows, int32_t h_q, int32_t d, int n_group) {
-  return n_group > 1 ? (size_t)(n_rows * h_q * n_group * (d + 2) * 4) : 0;
+// The jobs, then two partial results a CTA.
+constexpr size_t kJobBytes = (kK8Ctas * sizeof(int4) + 255) / 256 * 256;
+size_t form_bytes(const K8Form& f, int32_t d) {
+  return f.share ? kJobBytes + (size_t)2 * kK8Ctas * kK8Kernels[f.kind][0].pairs * (d + 2) * 4 : 0;
 }
 
-qsa_status launch_k8(int kind, Kv8AttnArgs& a, int d, int64_t tiles, int64_t units, int64_t entries, void* workspace,
-                     cudaStream_t stream) {
+qsa_status launch_k8(const K8Form& f, Kv8AttnArgs& a, int d, void* workspace, cudaStream_t stream) {
   const Kv8Device* dev = nullptr;
   if (qsa_status st = kv8_device(&dev)) return st;
-  const K8Kernel& k = kK8Kernels[kind][d == 256];
+  const K8Kernel& k = kK8Kernels[f.kind][d == 256];
   a.group = a.h_q / a.h_kv;
-  a.v_g = 1.0f;
-  a.n_group = ka_groups(units, entries);
-  a.cluster = a.n_group > 1 ? kKaMaxCluster : ka_cluster(units, entries, k.entries, dev->clusters[kind][d == 256]);
-  a.part = static_cast<float*>(workspace);
-  const int64_t ctas = tiles * a.cluster * a.n_group;
-  if (ctas > INT32_MAX || (int64_t)a.n_rows * a.h_q > INT32_MAX) return QSA_ERR_UNSUPPORTED;
-  if (entries > (1 << 30)) return QSA_ERR_UNSUPPORTED;  // entry indices stay clear of 2^31
-  const ClusterLaunch l(dim3((unsigned)ctas, (unsigned)a.h_kv), k.threads, (size_t)k.smem, a.cluster, stream);
+  a.rows = f.rows;
+  const int64_t slots = f.tile_slots * a.h_kv;
+  if (slots > INT32_MAX / kKaMaxCluster || (int64_t)a.n_rows * a.h_q > INT32_MAX) return QSA_ERR_UNSUPPORTED;
+  a.tile_slots = (int32_t)f.tile_slots;
+  a.jobs = static_cast<int4*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kJobBytes);
+  const int sms = std::min(dev->sms, kK8Ctas);
+  a.cluster = 1;
+  int64_t grid = std::min<int64_t>(sms, slots);
+  a.mode = kK8Whole;
+  if (f.share) {
+    a.mode = kK8Shares;
+    grid = sms;
+  } else if (f.cluster) {
+    // as many CTAs to a unit as run at once
+    a.mode = kK8Cluster;
+    const int* at_once = dev->clusters[f.kind][d == 256];
+    while (a.cluster < kKaMaxCluster && f.units <= at_once[2 * a.cluster] && f.blocks >= 2 * a.cluster) a.cluster *= 2;
+    grid = slots * a.cluster;
+  }
+  a.cluster_shift = log2_of(a.cluster);
+  a.group_inv = (65536 + a.group - 1) / a.group;  // exact for pairs below 4,096
+  const ClusterLaunch l(dim3((unsigned)grid), k.threads, (size_t)k.smem, a.cluster, stream);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, k.fn, a);
-  if (e == cudaSuccess && a.n_group > 1) e = launch_merge(a, d, (float)kK8Bias, stream);
+  if (e == cudaSuccess && f.share) {
+    // parts of a unit, with blocks of equal number to every CTA; lengths may differ
+    const bool many = f.blocks > 8 * (f.units * f.blocks / grid + 1);
+    const int cols = many ? 64 : d, pairs = f.rows * a.group;
+    const dim3 shape((unsigned)grid, (unsigned)(many ? pairs : (pairs * d + kK8MergeThreads - 1) / kK8MergeThreads),
+                     (unsigned)(d / cols));
+    e = launch_pdl(d == 256 ? (many ? kv8_merge_kernel<256, true> : kv8_merge_kernel<256, false>)
+                            : (many ? kv8_merge_kernel<128, true> : kv8_merge_kernel<128, false>),
+                   shape, dim3(kK8MergeThreads), 0, stream, a, k.pairs);
+  }
   return launched(e);
 }
 
@@ -144,6 +199,7 @@ void set_cache(Kv8AttnArgs& a, const void* kc, const void* ks, const void* vc, c
   a.ks = static_cast<const uint8_t*>(ks);
   a.vs = static_cast<const uint8_t*>(vs);
   a.block_shift = log2_of(block_tokens);
+  a.page_shift = a.page_size > 0 && (a.page_size & (a.page_size - 1)) == 0 ? log2_of(a.page_size) : -1;
 }
 
 qsa_status check_requests(int32_t n_req) {
@@ -291,8 +347,8 @@ qsa_status qsa_gather_kv_fp8(const void* k_codes, const void* k_scales, const vo
 }
 
 size_t qsa_sparse_attn_fp8_workspace_size(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t head_dim, int32_t n_idx) {
-  if (n_rows <= 0 || n_idx <= 0 || !kv8_shape_ok(h_q, h_kv, head_dim)) return 0;
-  return part_bytes(n_rows, h_q, head_dim, ka_groups((int64_t)n_rows * h_kv, n_idx));
+  if (n_rows <= 0 || n_idx < 0 || !kv8_shape_ok(h_q, h_kv, head_dim)) return 0;
+  return form_bytes(list_form(n_rows, h_q, h_kv, head_dim, n_idx), head_dim);
 }
 
 qsa_status qsa_sparse_attn_fp8(const void* q, int64_t ld_q, const void* k_codes, const void* k_scales,
@@ -325,20 +381,18 @@ qsa_status qsa_sparse_attn_fp8(const void* q, int64_t ld_q, const void* k_codes,
   a.ld_slots = ld_slots;
   a.n_idx = n_idx;
   a.scale = scale;
-  a.rows = 1;
   a.out = out;
   a.lse = lse;
-  return launch_k8(h_q / h_kv > 8 ? kList16 : kList8, a, head_dim, n_rows, (int64_t)n_rows * h_kv, n_idx, workspace,
-                   static_cast<cudaStream_t>(stream));
+  if (n_idx > (1 << 30)) return QSA_ERR_UNSUPPORTED;  // entry indices stay clear of 2^31
+  return launch_k8(list_form(n_rows, h_q, h_kv, head_dim, n_idx), a, head_dim, workspace, static_cast<cudaStream_t>(stream));
 }
 
 size_t qsa_window_attn_fp8_workspace_size(int32_t n_rows, int32_t n_req, int32_t max_rows_per_req, int32_t h_q,
                                           int32_t h_kv, int32_t head_dim, int32_t max_len, int32_t window,
                                           int32_t n_sink) {
-  if (n_rows <= 0 || n_req <= 0 || max_len <= 0 || window < 1 || n_sink < 0 || !kv8_shape_ok(h_q, h_kv, head_dim))
+  if (n_rows <= 0 || n_req <= 0 || max_len < 0 || window < 1 || n_sink < 0 || !kv8_shape_ok(h_q, h_kv, head_dim))
     return 0;
-  const K8Form f = window_form(n_rows, n_req, max_rows_per_req, h_q, h_kv);
-  return part_bytes(n_rows, h_q, head_dim, ka_groups(f.units, window_entries(max_len, window, n_sink)));
+  return form_bytes(window_form(n_rows, n_req, max_rows_per_req, h_q, h_kv, head_dim, max_len, window, n_sink), head_dim);
 }
 
 qsa_status qsa_window_attn_fp8(const void* q, int64_t ld_q, const void* k_codes, const void* k_scales,
@@ -359,14 +413,13 @@ qsa_status qsa_window_attn_fp8(const void* q, int64_t ld_q, const void* k_codes,
                                                                          head_dim, max_len, window, n_sink),
                                       workspace, workspace_bytes))
     return st;
-  const K8Form f = window_form(n_rows, n_req, max_rows_per_req, h_q, h_kv);
+  if (max_len > (1 << 30)) return QSA_ERR_UNSUPPORTED;  // entry indices stay clear of 2^31
   Kv8AttnArgs a{};
   set_window(a, q, ld_q, n_slots, n_req, req_row_start, n_rows, row_len, max_len, h_q, h_kv, page_table, ld_pt,
              page_size, window, n_sink, out, lse);
   set_cache(a, k_codes, k_scales, v_codes, v_scales, block_tokens);
   a.scale = scale;
-  a.rows = f.rows;
-  return launch_k8(f.kind, a, head_dim, f.slots, f.units, window_entries(max_len, window, n_sink), workspace,
+  return launch_k8(window_form(n_rows, n_req, max_rows_per_req, h_q, h_kv, head_dim, max_len, window, n_sink), a, head_dim, workspace,
                    static_cast<cudaStream_t>(stream));
 }
 

@@ -65,20 +65,30 @@ def append(codes, scales, bits, slots, block, first):
             scales[b, h] = e + 127
 
 
-def tolerance(d, n, ref, a, big, spread, out_eps, ev, p_top):
+def tolerance(d, n, ref, a, big, spread, out_eps, ev, p_top, parts):
     """Bounds of |out - ref| [h_q][d] and of |lse - ref| [h_q].
 
-    As kv4_ref.tolerance with q in FP16 and weights of 22 bits: a logit is off
-    by (d/16 + 2) 2^-22 big + 2^-25 spread, a weight by that, exp2's 2^-22, its
-    storage 2^-22 and the sums' (n/16 + 64) 2^-22.  Here the exponent of a
-    weight also holds that of the largest V scale (ev bounds both exponents'
-    magnitude), so its subtraction is off by 2^-22 ev more.  Weights times
-    their V scale are held to 2^-35 of the largest such product p_top [h_q],
-    and meet codes of up to 448: n 2^-35 448 p_top."""
-    logit = (d / 16 + 2) * 2.0 ** -22 * big + 2.0 ** -25 * spread + 2.0 ** -22 * ev
-    r = logit + 2.0 ** -21 + (n / 16 + 64) * 2.0 ** -22
-    return 2 * r[:, None] * a + n * 2.0 ** -35 * 448.0 * p_top[:, None] + out_eps * (np.abs(ref) + 2 * r[:, None] * a) \
-        + 1e-30, logit + 2.0 ** -20 + (n / 16 + 64) * 2.0 ** -22
+    A logit is accumulated in FP32 from exact products, 16 or more of them a
+    step; each step may be off by 2^-22 of sum|q k| (an adder that truncates),
+    and the factor and the subtraction of the maximum by another step each:
+    (d/16 + 2) 2^-22 big.  q is held in two e4m3 numbers, the second for the
+    remainder times 32, with the largest component in [2^7, 2^8): every
+    component is off by half of the second's smallest step at most, 2^-10 / 32
+    = 2^-15, 2^-22 of the largest: 2^-22 spread.  The exponent of a weight also
+    holds that of the largest V scale (ev bounds both exponents' magnitude),
+    so its subtraction is off by 2^-22 ev more.
+
+    A weight adds exp2's 2^-22, the sums' (n/16 + 64) 2^-22, and its storage in
+    e4m3 parts: each leaves at most 2^-4 of what it takes, so 2^(-4 parts) of
+    the weight is left, or half of the last part's smallest step: 2^-10 /
+    32^(parts - 1), where the row's largest product of weight and V scale,
+    p_top [h_q], is held as 2^3 at least; so 2^-13 / 32^(parts - 1) p_top, and
+    meets a code of up to 448."""
+    logit = (d / 16 + 2) * 2.0 ** -22 * big + 2.0 ** -22 * spread + 2.0 ** -22 * ev
+    r = logit + 2.0 ** -22 + 2.0 ** (-4 * parts) + (n / 16 + 64) * 2.0 ** -22
+    floor = n * 2.0 ** -13 / 32.0 ** (parts - 1) * 448.0 * p_top[:, None]
+    return 2 * r[:, None] * a + floor + out_eps * (np.abs(ref) + 2 * r[:, None] * a) + 1e-30, \
+        logit + 2.0 ** -20 + (n / 16 + 64) * 2.0 ** -22
 
 
 def top_products(q, k, ev, scale, lse):

@@ -222,11 +222,13 @@ def test_gather_past_the_cache_is_flagged(qsa):
 
 
 # ---------------------------------------------------------------- selections
-def one_row(q, kf, vf, ev, scale, out_eps):
-    """Reference and bounds of one row: q [h_q][d], kf, vf [n][h_kv][d], ev [n][h_kv]."""
+def one_row(q, kf, vf, ev, scale, out_eps, parts=4):
+    """Reference and bounds of one row: q [h_q][d], kf, vf [n][h_kv][d], ev
+    [n][h_kv].  parts: e4m3 parts of a weight, 3 in windows of more than 8
+    (row, head) pairs to a tile."""
     o, lse, a, big, spread = ref.attend(q, kf, vf, scale)
     top = ref.top_products(q, kf, ev, scale, lse)
-    tol, tol_l = ref.tolerance(q.shape[1], kf.shape[0], o, a, big, spread, out_eps, np.abs(ev).max(initial=0), top)
+    tol, tol_l = ref.tolerance(q.shape[1], kf.shape[0], o, a, big, spread, out_eps, np.abs(ev).max(initial=0), top, parts)
     return o, lse, tol, tol_l + 2.0 ** -23 * np.where(np.isfinite(lse), np.abs(lse), 0.0)
 
 
@@ -293,13 +295,15 @@ def test_sparse_attn_fp8_slot_past_the_cache_is_flagged(qsa):
     sparse_check(qsa, bf16_dev(normal_bf16(rng, (2, 8, 256))), arrays, 16, slots, 0.0625, faults=1)
 
 
-@pytest.mark.parametrize("w,g,h_kv,d", [(8192, 4, 1, 128), (20000, 8, 2, 256), (70001, 12, 1, 256)])
-def test_sparse_attn_fp8_long_rows_join_several_clusters(qsa, w, g, h_kv, d):
+# clusters of 8 CTAs, then shares
+@pytest.mark.parametrize("w,g,h_kv,d,shares", [(5000, 4, 1, 128, False), (3000, 8, 2, 256, False), (2500, 11, 1, 128, False),
+                                               (20000, 8, 2, 256, True), (30001, 5, 1, 128, True), (70001, 12, 1, 256, True)])
+def test_sparse_attn_fp8_long_rows_join_several_ctas(qsa, w, g, h_kv, d, shares):
     rng = np.random.default_rng(w)
     arrays = (*random_cache(rng, 4096, h_kv, d, 64), *random_cache(rng, 4096, h_kv, d, 64))
-    assert qsa.lib().qsa_sparse_attn_fp8_workspace_size(2, g * h_kv, h_kv, d, w) > 0
+    assert (qsa.lib().qsa_sparse_attn_fp8_workspace_size(2, g * h_kv, h_kv, d, w) > 0) == shares
     slots = rng.integers(0, 4096, (2, w)).astype(np.int32)
-    slots[1, 100:] = -1  # whole clusters without an entry
+    slots[1, 100:] = -1  # whole CTAs without an entry
     sparse_check(qsa, bf16_dev(normal_bf16(rng, (2, g * h_kv, d))), arrays, 64, slots, 0.05)
 
 
@@ -370,11 +374,12 @@ def window_check(qsa, rng, lens, page, block, h_q, h_kv, d, window, n_sink, spar
     kf, vf = ref.values(*cache[:2], block), ref.values(*cache[2:], block)
     ev = cache[3].astype(np.float64) - 127
     qf, o, l = bits_to_f64(q), bits_to_f64(out), host(lse).astype(np.float64)
+    parts = 4 if (max([1, *n]) if max_rows is None else max_rows) * (h_q // h_kv) <= 8 else 3
     which = range(rows) if sample is None or rows <= sample else sorted(rng.choice(rows, sample, replace=False))
     for t in which:
         r = int(np.searchsorted(start[1:], t, side="right"))
         s = ref.slots_of(pt[r], window_positions(int(flat[t]), window, n_sink), page)
-        ro, rl, tol, tol_l = one_row(qf[t], kf[s], vf[s], ev[s // block], sc, BF16_HALF_STEP)
+        ro, rl, tol, tol_l = one_row(qf[t], kf[s], vf[s], ev[s // block], sc, BF16_HALF_STEP, parts)
         same(o[t], ro, tol, (t, flat[t]))
         same(l[t], rl, tol_l, (t, flat[t]))
     assert (o[rows:] == 7.0).all() and (l[rows:] == 7.0).all()
@@ -411,7 +416,7 @@ def test_window_attn_fp8_rows_in_any_order(qsa):
 
 
 @pytest.mark.parametrize("rows,h_q,d", [(1, 8, 256), (1, 16, 128), (6, 8, 256), (3, 4, 128)])
-def test_window_attn_fp8_long_rows_join_several_clusters(qsa, rows, h_q, d):
+def test_window_attn_fp8_long_rows_join_several_ctas(qsa, rows, h_q, d):
     rng = np.random.default_rng(12 + rows)
     n = 30011
     assert qsa.lib().qsa_window_attn_fp8_workspace_size(rows, 1, rows, h_q, 1, d, n, n, 0) > 0
@@ -491,7 +496,7 @@ def test_window_attn_fp8_broken_values_reach_only_the_rows_that_see_them(qsa, h_
             assert np.isnan(o[t]).all() and np.isnan(l[t]).all()
             continue
         s = ref.slots_of(pt[0], pos, page)
-        ro, rl, tol, tol_l = one_row(ref.bf16_to_f64(q[t]), kf[s], vf[s], ev[s // block], d ** -0.5, BF16_HALF_STEP)
+        ro, rl, tol, tol_l = one_row(ref.bf16_to_f64(q[t]), kf[s], vf[s], ev[s // block], d ** -0.5, BF16_HALF_STEP, 3)
         for p, c in zip(at_v, cols):
             if p in pos:
                 ro[:, c] = np.nan
@@ -524,7 +529,7 @@ def test_window_attn_fp8_bad_pages_are_skipped_and_flagged(qsa, rows, d):
         for t in range(rows):
             pos = window_positions(lens[t], window, n_sink)
             s = ref.slots_of(pt[0], pos[~np.isin(pos // page, gone)], page)
-            ro, rl, tol, tol_l = one_row(ref.bf16_to_f64(q[t]), kf[s], vf[s], ev[s // 64], d ** -0.5, BF16_HALF_STEP)
+            ro, rl, tol, tol_l = one_row(ref.bf16_to_f64(q[t]), kf[s], vf[s], ev[s // 64], d ** -0.5, BF16_HALF_STEP, 4 if rows == 1 else 3)
             same(bits_to_f64(out)[t], ro, tol, t)
             same(host(lse)[t].astype(np.float64), rl, tol_l, t)
 
@@ -578,7 +583,7 @@ def test_offsets_past_32_bits(qsa, rows):
     out2, _ = qsa.sparse_attn_fp8(bf16_dev(q), *cache, to_dev(lst))
     ev = np.repeat(small[3], 64, 0)[:n].astype(np.float64) - 127
     for t in range(rows):
-        ro, _, tol, _ = one_row(ref.bf16_to_f64(q[t]), kf, vf, ev, d ** -0.5, BF16_HALF_STEP)
+        ro, _, tol, _ = one_row(ref.bf16_to_f64(q[t]), kf, vf, ev, d ** -0.5, BF16_HALF_STEP, 4)
         same(bits_to_f64(out)[t], ro, tol, t)
         same(host(out2)[t].astype(np.float64), ro, tol, t)
 
@@ -659,7 +664,7 @@ def test_decode_steps_from_plan_to_attention(qsa, captured):
                         (ref.bf16_to_f64(wo[t]), wl[t], ref.slots_of(h_table[r], window_positions(int(rl_h[t]), window, n_sink),
                                                                      page), BF16_HALF_STEP),
                         (so[t].astype(np.float64), sl[t], seen[t][seen[t] >= 0], 2.0 ** -24)):
-                    ro, rl, tol, tol_l = one_row(qt, kf[at], vf[at], ev[at // block], d ** -0.5, eps)
+                    ro, rl, tol, tol_l = one_row(qt, kf[at], vf[at], ev[at // block], d ** -0.5, eps, 3 if eps == BF16_HALF_STEP else 4)
                     same(got, ro, tol, (it, t))
                     same(gl.astype(np.float64), rl, tol_l, (it, t))
         h_ctx = len_h.astype(np.int64)

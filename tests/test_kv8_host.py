@@ -140,13 +140,19 @@ def test_window_attn_fp8_refusals(L, change, status):
 
 
 def test_workspace_sizes(L):
+    """Room for two partial results of every CTA (152) where the blocks of long
+    units are shared out; none where clusters or whole units take them."""
     f, w = L.qsa_sparse_attn_fp8_workspace_size, L.qsa_window_attn_fp8_workspace_size
-    assert f(32, 16, 2, 256, 2051) == 0 and f(1, 16, 2, 256, 2051) == 0
-    assert f(1, 16, 2, 256, 9000) == 16 * 2 * 258 * 4
-    assert w(1, 1, 1, 16, 2, 256, 80000, 1024, 4) == 0 and w(1, 1, 1, 16, 2, 256, 80000, 80000, 4) > 0
-    assert w(1, 1, 1, 16, 2, 256, 500, 80000, 4) == 0  # the context bounds the window
-    # six rows that share their reads are as few units as one
-    assert w(6, 1, 6, 16, 2, 256, 80000, 80000, 0) == 6 * w(1, 1, 1, 16, 2, 256, 80000, 80000, 0)
+    size = lambda pairs, d: 2560 + 2 * 152 * pairs * (d + 2) * 4  # noqa: E731
+    assert f(32, 16, 2, 256, 2051) == 0 and f(1, 16, 2, 256, 2051) == 0 and f(1, 32, 2, 128, 0) == 0
+    assert f(1, 16, 2, 256, 9000) == size(8, 256) and f(1, 32, 2, 128, 20000) == size(16, 128)
+    assert f(607, 16, 2, 256, 2051) == size(8, 256) and f(608, 16, 2, 256, 2051) == 0
+    assert w(1, 1, 1, 16, 2, 256, 80000, 1024, 4) == 0 and w(1, 1, 1, 16, 2, 256, 80000, 80000, 4) == size(8, 256)
+    assert w(6, 1, 6, 16, 2, 256, 80000, 80000, 0) == size(48, 256) and w(6, 1, 6, 16, 2, 256, 500, 9, 4) == 0
+    assert w(2, 1, 2, 8, 2, 128, 80000, 80000, 4) == size(8, 128) and w(3, 1, 3, 12, 1, 128, 80000, 80000, 4) == size(48, 128)
+    assert w(1, 1, 1, 16, 1, 128, 80000, 80000, 4) == size(16, 128)
+    assert w(9, 3, 4, 8, 1, 128, 80000, 80000, 4) == size(32, 128)
+    assert w(1216, 1216, 1, 8, 1, 256, 80000, 1024, 4) == 0 and w(300, 700, 1, 8, 1, 256, 80000, 80000, 4) == 0
     assert f(0, 16, 2, 256, 9000) == 0 and f(1, 16, 3, 256, 9000) == 0 and w(1, 1, 1, 16, 2, 256, 80000, 0, 4) == 0
 
 
