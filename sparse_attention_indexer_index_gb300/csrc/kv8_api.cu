@@ -169,6 +169,7 @@ qsa_status launch_k8(const K8Form& f, Kv8AttnArgs& a, int d, void* workspace, cu
   if (f.share) {
     a.mode = kK8Shares;
     grid = sms;
+    a.jobs_by_unit = slots <= sms;
   } else if (f.cluster) {
     // as many CTAs to a unit as run at once
     a.mode = kK8Cluster;
@@ -184,7 +185,7 @@ qsa_status launch_k8(const K8Form& f, Kv8AttnArgs& a, int d, void* workspace, cu
     // parts of a unit, with blocks of equal number to every CTA; lengths may differ
     const bool many = f.blocks > 8 * (f.units * f.blocks / grid + 1);
     const int cols = many ? 64 : d, pairs = f.rows * a.group;
-    const dim3 shape((unsigned)grid, (unsigned)(many ? pairs : (pairs * d + kK8MergeThreads - 1) / kK8MergeThreads),
+    const dim3 shape((unsigned)(a.jobs_by_unit ? slots : grid), (unsigned)(many ? pairs : (pairs * d + kK8MergeThreads - 1) / kK8MergeThreads),
                      (unsigned)(d / cols));
     e = launch_pdl(d == 256 ? (many ? kv8_merge_kernel<256, true> : kv8_merge_kernel<256, false>)
                             : (many ? kv8_merge_kernel<128, true> : kv8_merge_kernel<128, false>),

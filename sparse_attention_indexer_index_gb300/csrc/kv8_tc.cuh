@@ -81,7 +81,9 @@ struct Kv8AttnArgs : KvAttnArgs {
   int32_t rows;              // R: rows per tile
   int32_t tile_slots;        // tiles at most
   int32_t mode;              // how the work is dealt
-  int4* jobs;                // [CTAs]: what kv8_merge_kernel joins (first CTA or -1, first row, rows, KV head)
+  int4* jobs;                // [units or CTAs]: what kv8_merge_kernel joins: first CTA (-1: nothing), last CTA, first
+                             // row, KV head * 256 + rows
+  int32_t jobs_by_unit;      // a job for every unit, or (more units than CTAs) for the CTA where one ends
 };
 
 // D = 128 with 8 pairs takes blocks of 256 entries (two products each way),
@@ -632,7 +634,8 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       }
     } else {
       const int cta = blockIdx.x, ctas = gridDim.x;
-      int4 job = make_int4(-1, 0, 0, 0);
+      const int4 no_job = make_int4(-1, 0, 0, 0);
+      int4 job = no_job;
       const int same = k8_blocks<kBlock>(a.n_idx);  // a list's blocks
       const int total = (kWindow ? ctl.pre[tiles] : tiles * same) * a.h_kv;
       // the first `more` CTAs take per + 1 blocks, the others per
@@ -643,9 +646,9 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         const int bt = b / a.h_kv;  // at or behind the tile's first block, before its last head's end
         Seg w{};
         w.slot = -1;
-        int first_b, nb;
+        int first_b, nb, u_tile;
         if constexpr (kWindow) {
-          const int t = k8_search(ctl.pre, tiles, bt);
+          const int t = u_tile = k8_search(ctl.pre, tiles, bt);
           const int4 y = ctl.tile[t];
           first_b = ctl.pre[t];
           nb = ctl.pre[t + 1] - first_b;
@@ -656,7 +659,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           w.n = y.w;
           w.ns = min(a.n_sink, w.first);
         } else {
-          w.t0 = bt / same;
+          w.t0 = u_tile = bt / same;
           w.rows = 1;
           w.n = a.n_idx;
           first_b = w.t0 * same;
@@ -668,14 +671,26 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         w.j1 = min(nb, w.j0 + (end - b));
         if (w.j0 > 0) w.slot = 2 * cta;
         else if (w.j1 < nb) w.slot = 2 * cta + 1;
-        if (w.j0 > 0 && w.j1 == nb) {  // it ends here: this CTA's job names the first CTA that has a part
-          const int unit0 = b - w.j0, longer = more * (per + 1);
-          job = make_int4(unit0 < longer ? unit0 / (per + 1) : more + (unit0 - longer) / per, w.t0, w.rows, w.g);
+        if (w.j1 == nb) {  // the unit ends here: the job names the first CTA that has a part
+          int4 y = no_job;
+          if (w.j0 > 0) {
+            const int unit0 = b - w.j0, longer = more * (per + 1);
+            y = make_int4(unit0 < longer ? unit0 / (per + 1) : more + (unit0 - longer) / per, cta, w.t0, w.g * 256 + w.rows);
+          }
+          if (!a.jobs_by_unit) {
+            if (w.j0 > 0) job = y;
+          } else if (lane == 0) {
+            a.jobs[u_tile * a.h_kv + w.g] = y;
+          }
         }
         b += w.j1 - w.j0;
         ok = publish(w);
       }
-      if (lane == 0) a.jobs[cta] = job;
+      if (!a.jobs_by_unit) {
+        if (lane == 0) a.jobs[cta] = job;
+      } else if (cta == 0) {  // units that are none
+        for (int u = tiles * a.h_kv + lane; u < a.tile_slots * a.h_kv; u += 32) a.jobs[u] = no_job;
+      }
     }
     if (ok) {
       Seg none{};
@@ -1034,19 +1049,22 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             }
             ok = meet();
             if (!ok) break;
-            float f[kPer], mn[kPer];
+            // a pair a lane
+            const int lp = min(lane, kPer - 1);
+            float top = ctl.wmax[slice * W][lp];
 #pragma unroll
-            for (int p = 0; p < kPer; ++p) {
-              float y = ctl.wmax[slice * W][p];
-#pragma unroll
-              for (int i = 1; i < W; ++i) y = fmaxf(y, ctl.wmax[slice * W + i][p]);
-              y -= (float)kK8Bias;
-              const float old = first ? kK8None : ctl.mb[p0 + p];
-              mn[p] = y > old + (float)kKaGrow ? y : old;
-              f[p] = old == kK8None ? 1.f : ka_ex2(old - mn[p]);
-              l[p] = (Sh::kAhead ? was[Sh::kAhead ? p : 0] : l[p]) * f[p];
-            }
+            for (int i = 1; i < W; ++i) top = fmaxf(top, ctl.wmax[slice * W + i][lp]);
+            top -= (float)kK8Bias;
+            const float old = first ? kK8None : ctl.mb[p0 + lp];
+            const float mn = top > old + (float)kKaGrow ? top : old;
             if (!first) {
+              const float fl = old == kK8None ? 1.f : ka_ex2(old - mn);
+              float f[kPer];
+#pragma unroll
+              for (int p = 0; p < kPer; ++p) {
+                f[p] = __shfl_sync(0xffffffffu, fl, p);
+                l[p] = (Sh::kAhead ? was[Sh::kAhead ? p : 0] : l[p]) * f[p];
+              }
               // O holds every product before this block's
               ok = meet() && k8_wait(&ctl.pv_done[sl ^ 1], (uint32_t)((x - 1) >> 1) & 1u, abort);
               if (!ok) break;
@@ -1068,10 +1086,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
               tc_fence_before();
             }
             // every warp of the slice writes the same, once all have read what was there
-            if (lane == 0) {
-#pragma unroll
-              for (int p = 0; p < kPer; ++p) ctl.mb[p0 + p] = mn[p];
-            }
+            if (lane < kPer) ctl.mb[p0 + lane] = mn;
             __syncwarp();
           }
           // the weights: their sums, and parts of 4 bits for the product
@@ -1165,12 +1180,26 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       use += 2 * nb;
 
       // ---- outputs: a thread for a column of O -------------------------------------------------
+      {
+        // the lanes' sums: half of the pairs go to each half of the lanes, and so on; in the end lane
+        // 32 / kFold i has pair i (of kFold pairs, those past kPer zeros)
+        constexpr int kFold = kPer <= 8 ? 8 : 16;
+        float y[kFold];
 #pragma unroll
-      for (int p = 0; p < kPer; ++p) {
-        float y = l[p];
+        for (int p = 0; p < kFold; ++p) y[p] = p < kPer ? l[p] : 0.f;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
-        if (lane == 0) ctl.wsum[warp][p] = y;
+        for (int d = 16, n = kFold / 2; n > 0; d >>= 1, n >>= 1) {
+          const bool up = (lane & d) != 0;
+#pragma unroll
+          for (int p = 0; p < n; ++p) {
+            const float give = up ? y[p] : y[p + n], keep = up ? y[p + n] : y[p];
+            y[p] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+          }
+        }
+#pragma unroll
+        for (int d = 16 / kFold; d > 0; d >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], d);
+        const int pair = lane / (32 / kFold);
+        if (lane % (32 / kFold) == 0 && pair < kPer) ctl.wsum[warp][pair] = y[0];
       }
       // the next segment's loads on the way meanwhile
       Seg after;
@@ -1181,6 +1210,13 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       __syncwarp();
       tc_fence_after();
       const bool nans = kShared && ctl.any_nan != 0;
+      // a pair a lane: its M, sum and place
+      const int lp = min(lane, kPer - 1);
+      float sum_l = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) sum_l += ctl.wsum[slice * W + i][lp];
+      const float m_l = nb > 0 && ctl.mb[p0 + lp] != kK8None ? ctl.mb[p0 + lp] : ninf;
+      const int hq_l = ctl.out[p0 + lp];
       if (Sh::kJoinRing && C > 1) {
         // this CTA's ring is free: its products are done, and no copy is under way
         k8_arrive_all(&ctl.join_free, C);
@@ -1217,12 +1253,9 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const int p = p0 + c0 + y;
-          const int hq = ctl.out[p];
+          const int hq = __shfl_sync(0xffffffffu, hq_l, c0 + y);
+          const float L = __shfl_sync(0xffffffffu, sum_l, c0 + y), M = __shfl_sync(0xffffffffu, m_l, c0 + y);
           if (hq < 0) continue;
-          float L = 0.f;
-#pragma unroll
-          for (int i = 0; i < W; ++i) L += ctl.wsum[slice * W + i][c0 + y];
-          const float M = nb > 0 && ctl.mb[p] != kK8None ? ctl.mb[p] : ninf;
           if (C > 1) {
             const uint32_t at = map_shared_rank(join + (rank * own + (p >> a.cluster_shift)) * (D + 2), (uint32_t)(p & (C - 1)));
 #pragma unroll
@@ -1289,7 +1322,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
 }
 
 // Units that several CTAs shared: out = sum_s f_s O_s / sum_s f_s l_s, f_s =
-// 2^(M_s - max M).  CTA (k, y, z) works for the unit that ends in CTA k's share.
+// 2^(M_s - max M).  CTA (i, y, z) works for job i.
 // Few parts to a unit: its threads are D columns of 1024 / D pairs, which add
 // up their parts by themselves.  Many (kMany): 64 columns of one pair, for which
 // 16 groups take the parts in turn and meet in shared memory.
@@ -1299,11 +1332,12 @@ __global__ void __launch_bounds__(kK8MergeThreads)
 kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int n) {
   constexpr int kCols = kMany ? 64 : D, G = kK8MergeThreads / kCols;
   __shared__ float s_m[kMany ? G : 1], s_l[kMany ? G : 1], s_o[kMany ? G : 1][64];
-  const int k = blockIdx.x, grp = threadIdx.x / kCols;
+  const int grp = threadIdx.x / kCols;
   const int p = kMany ? blockIdx.y : blockIdx.y * G + grp, d = blockIdx.z * kCols + threadIdx.x % kCols;
   pdl_wait_primary();
-  const int4 job = ld_in(a.jobs + k);
-  if (job.x < 0 || p >= job.z * a.group) return;  // (with kMany the whole CTA)
+  const int4 job = ld_in(a.jobs + blockIdx.x);
+  const int k = job.y;
+  if (job.x < 0 || p >= (job.w & 255) * a.group) return;  // (with kMany the whole CTA)
   const float ninf = -__int_as_float(0x7f800000);
   // the first part begins the unit (its CTA's second slot), the others come from within it
   auto part = [&](int c) -> const float* {
@@ -1352,7 +1386,7 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int n) {
     for (int i = 0; i < G; ++i) add(s_m[i], s_l[i], s_o[i][col]);
   }
   const int row = (int)(p * a.group_inv >> 16);
-  const int64_t hq = (int64_t)(job.y + row) * a.h_q + (int64_t)job.w * a.group + (p - row * a.group);
+  const int64_t hq = (int64_t)(job.z + row) * a.h_q + (int64_t)(job.w >> 8) * a.group + (p - row * a.group);
   const float r = l == 0.f ? 0.f : o / l;
   if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[hq * D + d] = __float2bfloat16_rn(r);
   else static_cast<float*>(a.out)[hq * D + d] = r;
