@@ -57,7 +57,7 @@ struct Kv8WriteArgs {
   int32_t n_req;
   const int32_t* page_table;
   int64_t ld_pt;
-  int32_t page_size, block_shift;
+  int32_t page_size, block_shift, per_shift;  // log2 of the pieces of 8 values to a row
   int64_t n_slots;
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
 };
@@ -68,7 +68,7 @@ struct Kv8WriteArgs {
 // the maximum and the codes (kPieces * 8 of them a thread, a whole block at
 // most), so they are read once.
 template <int kPieces>
-__global__ void __launch_bounds__(kKv8Threads)
+__global__ void __launch_bounds__(kKv8Threads, kPieces <= 8 ? 4 : 2)
 append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {
   __shared__ uint32_t s_top[2][kKv8Threads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -87,11 +87,12 @@ append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {
   int turn = 0;
   while (t < stop && r < a.n_req) {
     const int s0 = ld_in(a.req_tok_start + r), s1 = min(ld_in(a.req_tok_start + r + 1), a.n_tok);
+    const int first = ld_in(a.req_first_pos + r);
     if (t >= s1) {
       ++r;
       continue;
     }
-    const int64_t pos = (int64_t)ld_in(a.req_first_pos + r) + (t - s0);
+    const int64_t pos = (int64_t)first + (t - s0);
     if (pos < 0 || pos > INT32_MAX) {
       if (tid == 0) raise_fault(kFaultIndex);
       t = pos < 0 ? (int)min((int64_t)s1, t - pos) : s1;  // on to position 0, if it comes
@@ -103,14 +104,7 @@ append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {
     const int lo = (int)pos - in;               // the block's first position
     const int pi = lo / a.page_size;
     const int64_t page = pi < a.ld_pt ? ld_in(a.page_table + (int64_t)r * a.ld_pt + pi) : -1;
-    const int64_t slot = page * a.page_size + (lo - pi * a.page_size);
-    if (page < 0 || slot + B > a.n_slots) {
-      if (tid == 0) raise_fault(kFaultIndex);
-      continue;
-    }
-    const int64_t at = (slot >> a.block_shift) * a.h_kv + h;
-    const int old = in != 0 ? (int)ld_in(scales + at) : 0;  // the scale of the block's earlier tokens
-    // the unit's values: rows t0 .. t - 1
+    // the unit's values, rows t0 .. t - 1, on the way beside the page and the block's scale
     const int pieces = (t - t0) * per;
     uint4 x[kPieces];
     __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
@@ -119,10 +113,17 @@ append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {
       const int p = i * kKv8Threads + tid;
       x[i] = make_uint4(0u, 0u, 0u, 0u);
       if (p < pieces) {
-        const int row = p / per;
-        x[i] = ld_stream_16(src + (int64_t)(t0 + row) * ld + (int64_t)h * a.d + (p - row * per) * 8);
+        const int row = p >> a.per_shift;
+        x[i] = ld_stream_16(src + (int64_t)(t0 + row) * ld + (int64_t)h * a.d + (p & (per - 1)) * 8);
       }
     }
+    const int64_t slot = page * a.page_size + (lo - pi * a.page_size);
+    if (page < 0 || slot + B > a.n_slots) {
+      if (tid == 0) raise_fault(kFaultIndex);
+      continue;
+    }
+    const int64_t at = (slot >> a.block_shift) * a.h_kv + h;
+    const int old = in != 0 ? (int)ld_in(scales + at) : 0;  // the scale of the block's earlier tokens
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const uint32_t w[4] = {x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu, x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu};
@@ -161,7 +162,7 @@ append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {
     for (int i = 0; i < kPieces; ++i) {
       const int p = i * kKv8Threads + tid;
       if (p >= pieces) break;
-      const int row = p / per;
+      const int row = p >> a.per_shift;
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       uint32_t c[4];
 #pragma unroll
@@ -176,14 +177,14 @@ append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {
         }
         c[j] = kv8_pack2(f.x, f.y);
       }
-      *reinterpret_cast<uint2*>(codes + ((slot + in + row) * a.h_kv + h) * a.d + (p - row * per) * 8) =
+      *reinterpret_cast<uint2*>(codes + ((slot + in + row) * a.h_kv + h) * a.d + (p & (per - 1)) * 8) =
           make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     }
     if (in != 0 && byte > old) {  // the earlier tokens' codes to the new scale
       const float f = kv8_pow2(max(old - byte, -126));
       for (int p = tid; p < in * per; p += kKv8Threads) {
-        const int row = p / per;
-        uint2* at8 = reinterpret_cast<uint2*>(codes + ((slot + row) * a.h_kv + h) * a.d + (p - row * per) * 8);
+        const int row = p >> a.per_shift;
+        uint2* at8 = reinterpret_cast<uint2*>(codes + ((slot + row) * a.h_kv + h) * a.d + (p & (per - 1)) * 8);
         const uint2 v = ld_in(at8);
         uint32_t c[4];
 #pragma unroll

@@ -242,11 +242,21 @@ qsa_status qsa_plan_step(const int32_t* ctx_len, const int32_t* n_new, int32_t n
                         (const void*)row_req, (const void*)slots})
     if (!aligned4(p)) return QSA_ERR_INVALID_ARG;
   if (new_len != nullptr && new_len == ctx_len) return QSA_ERR_INVALID_ARG;  // the rows are found with both
-  const StepArgs a{ctx_len, n_new, n_req, page_table, ld_pt, page_size, free_pages, n_pool, n_free,
-                   n_tok, req_row_start, new_len, row_len, row_req, slots};
+  StepArgs a{ctx_len, n_new, n_req, page_table, ld_pt, page_size, free_pages, n_pool, n_free,
+             n_tok, req_row_start, new_len, row_len, row_req, slots, 0,
+             (page_size & (page_size - 1)) == 0 ? log2_of(page_size) : -1};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(plan_step_kernel, dim3(1), dim3(kStepThreads), 0, s, a);
-  if (e == cudaSuccess && n_tok > kStepOneCta)
+  const bool table = n_req <= kStepTable;
+  // a thread for a request, for a page that the step may take, and for a row
+  const int want = std::max({n_req, n_tok / page_size + n_req, table ? n_tok : 0});
+  const int threads = std::min(kStepThreads, std::max(128, (want + 31) / 32 * 32));
+  if (table) {
+    a.cluster = 1;
+    while (a.cluster < kStepMaxCluster && n_tok > a.cluster * threads) a.cluster *= 2;
+  }
+  const ClusterLaunch l(dim3((unsigned)std::max(a.cluster, 1)), threads, 0, std::max(a.cluster, 1), s);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, plan_step_kernel, a);
+  if (e == cudaSuccess && !table && n_tok > 0)
     e = launch_pdl(step_rows_kernel, dim3((unsigned)((n_tok + kStepRowsThreads - 1) / kStepRowsThreads)),
                    dim3(kStepRowsThreads), 0, s, a);
   return launched(e);
@@ -263,7 +273,9 @@ qsa_status qsa_release_pages(int32_t* page_table, int64_t ld_pt, int32_t n_req, 
   if (!aligned4(page_table) || !aligned4(from_page) || !aligned4(to_page) || !aligned4(free_pages) || !aligned4(n_free))
     return QSA_ERR_INVALID_ARG;
   const ReleaseArgs a{page_table, ld_pt, n_req, from_page, to_page, free_pages, n_pool, n_free};
-  return launched(launch_pdl(release_pages_kernel, dim3(1), dim3(kStepThreads), 0, static_cast<cudaStream_t>(stream), a));
+  // two requests a thread, but some warps for requests of many pages
+  const int threads = n_req <= 32 ? 256 : kStepThreads;
+  return launched(launch_pdl(release_pages_kernel, dim3(1), dim3((unsigned)threads), 0, static_cast<cudaStream_t>(stream), a));
 }
 
 qsa_status qsa_append_kv_fp8(const void* k_new, const void* v_new, int64_t ld_k, int64_t ld_v, int32_t n_tok,
@@ -298,6 +310,7 @@ qsa_status qsa_append_kv_fp8(const void* k_new, const void* v_new, int64_t ld_k,
   a.ld_pt = ld_pt;
   a.page_size = page_size;
   a.block_shift = log2_of(block_tokens);
+  a.per_shift = head_dim == 256 ? 5 : 4;
   a.n_slots = n_slots;
   a.k_codes = static_cast<uint8_t*>(k_codes);
   a.k_scales = static_cast<uint8_t*>(k_scales);

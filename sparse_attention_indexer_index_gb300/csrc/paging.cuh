@@ -22,7 +22,8 @@ namespace qsa {
 constexpr int kStepThreads = 1024;
 constexpr int kStepMaxGroups = 2048;  // of 32 requests
 constexpr int kStepRowsThreads = 256;
-constexpr int kStepOneCta = 4096;     // rows that plan_step_kernel writes itself
+constexpr int kStepMaxCluster = 8;
+constexpr int kStepTable = 2048;      // requests whose sums it keeps
 
 struct StepArgs {
   const int32_t* ctx_len;    // [n_req]
@@ -40,7 +41,13 @@ struct StepArgs {
   int32_t* row_len;          // [n_tok]
   int32_t* row_req;          // [n_tok] or nullptr
   int32_t* slots;            // [n_tok]
+  int32_t cluster;           // CTAs that write rows; 0: step_rows_kernel does
+  int32_t page_shift;        // log2 of the page size, -1: not a power of two
 };
+// Whole pages in x tokens (x below 2^32).
+__device__ __forceinline__ uint32_t step_pages(const StepArgs& a, uint32_t x) {
+  return a.page_shift >= 0 ? x >> a.page_shift : x / (uint32_t)a.page_size;
+}
 
 // Sums that stop at a limit above every value that matters: associative, and
 // no sum of 65,535 counts passes 32 bits.
@@ -75,17 +82,41 @@ __device__ __forceinline__ StepNeed step_need(const StepArgs& a, int r) {
   }
   x.n = (uint32_t)max(n, 0);
   if (!x.ok || n == 0) return x;
-  // in 64 bits: positions end below 2^31, the page behind them need not
-  const int64_t end = ((int64_t)x.ctx + n + a.page_size - 1) / a.page_size;
-  const int64_t from = ((int64_t)x.ctx + a.page_size - 1) / a.page_size;
-  if (end > a.ld_pt || (int64_t)x.ctx + n > INT32_MAX) {
+  // (positions end below 2^31, so that sums with the page size stay below 2^32)
+  const uint32_t up = (uint32_t)(a.page_size - 1);
+  if ((uint32_t)x.ctx + (uint32_t)n > (uint32_t)INT32_MAX || step_pages(a, (uint32_t)x.ctx + (uint32_t)n + up) > a.ld_pt) {
     raise_fault(kFaultIndex);
     x.ok = false;
     return x;
   }
-  x.from = (int)from;
-  x.pages = (uint32_t)min(end - from, (int64_t)INT32_MAX);
+  x.from = (int)step_pages(a, (uint32_t)x.ctx + up);
+  x.pages = step_pages(a, (uint32_t)x.ctx + (uint32_t)n + up) - (uint32_t)x.from;
   return x;
+}
+
+// Row t of request r (-1: none) at position pos (-1: refused, it has rows but no
+// slots), on that page.
+__device__ __forceinline__ void step_row(const StepArgs& a, int t, int r, int pos, int page) {
+  int len = 0, slot = -1;
+  if (pos >= 0) {
+    const int64_t s = (int64_t)page * a.page_size + (pos - (int)step_pages(a, (uint32_t)pos) * a.page_size);
+    len = pos + 1;
+    if (page >= 0 && s <= INT32_MAX) slot = (int)s;
+    else raise_fault(kFaultIndex);
+  }
+  a.row_len[t] = len;
+  a.slots[t] = slot;
+  if (a.row_req != nullptr) a.row_req[t] = r;
+}
+// The last i in [0, n) with arr[i] <= x; arr does not decrease, arr[0] <= x.
+__device__ __forceinline__ int step_search(const int* arr, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (arr[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
 // 32 rows from t0 on, by a whole warp.
@@ -118,31 +149,22 @@ __device__ __forceinline__ void step_rows(const StepArgs& a, int t0) {
     base += 32;
   } while (__any_sync(0xffffffffu, r == base));
   if (t >= a.n_tok) return;
-  int len = 0, slot = -1, req = -1;
-  if (r < a.n_req) {
-    req = r;
-    const int ctx = ld_in(a.ctx_len + r);
-    if (ld_in(a.new_len + r) != ctx) {  // else refused: it has rows, but no slots
-      const int pos = ctx + (t - ld_in(a.req_row_start + r));
-      const int pi = pos / a.page_size;
-      const int page = ld_in(a.page_table + (int64_t)r * a.ld_pt + pi);
-      const int64_t s = (int64_t)page * a.page_size + (pos - pi * a.page_size);
-      len = pos + 1;
-      if (page >= 0 && s <= INT32_MAX) slot = (int)s;
-      else raise_fault(kFaultIndex);
-    }
-  }
-  a.row_len[t] = len;
-  a.slots[t] = slot;
-  if (a.row_req != nullptr) a.row_req[t] = req;
+  const bool real = r < a.n_req;
+  const int ctx = real ? ld_in(a.ctx_len + r) : 0;
+  const int pos = real && ld_in(a.new_len + r) != ctx ? ctx + t - ld_in(a.req_row_start + r) : -1;
+  step_row(a, t, real ? r : -1, pos, pos >= 0 ? ld_in(a.page_table + (int64_t)r * a.ld_pt + step_pages(a, (uint32_t)pos)) : -1);
 }
 
 __global__ void __launch_bounds__(kStepThreads)
 plan_step_kernel(const __grid_constant__ StepArgs a) {
   __shared__ uint32_t s_tok[kStepMaxGroups], s_pg[kStepMaxGroups];
   __shared__ uint32_t s_all[2], s_taken;
+  // up to kStepTable requests: sums of rows and of pages handed out before each, its tokens
+  __shared__ int s_start[kStepTable + 1], s_page[kStepTable + 1], s_ctx[kStepTable];
+  const bool table = a.n_req <= kStepTable;
+  const int rank = a.cluster > 1 ? (int)cluster_ctarank() : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (a.n_req + 31) / 32;
+  const int groups = (a.n_req + 31) / 32, warps = blockDim.x / 32;
   const uint32_t top_t = (uint32_t)a.n_tok + 1u, top_p = (uint32_t)a.n_pool + 1u;
   pdl_wait_primary();
   int n_free = ld_in(a.n_free);
@@ -150,10 +172,12 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
     if (threadIdx.x == 0) raise_fault(kFaultGrouping);
     n_free = 0;
   }
+  // every CTA has read it before the first one writes it
+  if (a.cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   // sums of 32 requests
   StepNeed x{0, 0u, 0u, 0, true};
   uint32_t it = 0, ip = 0;
-  for (int g = warp; g < groups; g += kStepThreads / 32) {
+  for (int g = warp; g < groups; g += warps) {
     x = step_need(a, g * 32 + lane);
     it = warp_sat_scan(min(x.n, top_t), top_t);
     ip = warp_sat_scan(min(x.pages, top_p), top_p);
@@ -191,7 +215,7 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
   }
   __syncthreads();
   const bool fits = s_all[0] <= (uint32_t)a.n_tok && s_all[1] <= (uint32_t)n_free;
-  const bool keep = groups <= kStepThreads / 32;  // one group a warp: still in registers
+  const bool keep = groups <= warps;  // one group a warp: still in registers
   uint32_t taken = s_all[1];
   // the request's sums up to itself, and whether it is served
   auto ends = [&](int g, uint32_t& et, uint32_t& ep) -> bool {
@@ -206,7 +230,7 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
   };
   if (!fits) {  // the pages of those that are served
     if (threadIdx.x == 0) raise_fault(kFaultCapacity);
-    for (int g = warp; g < groups; g += kStepThreads / 32) {
+    for (int g = warp; g < groups; g += warps) {
       uint32_t et, ep;
       const bool served = ends(g, et, ep);
       const uint32_t most = __reduce_max_sync(0xffffffffu, served && x.pages > 0 ? ep : 0u);
@@ -216,16 +240,27 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
     taken = s_taken;
   }
   const int base = n_free - (int)taken;
-  for (int g = warp; g < groups; g += kStepThreads / 32) {
+  for (int g = warp; g < groups; g += warps) {
     const int r = g * 32 + lane;
     uint32_t et, ep;
     const bool served = ends(g, et, ep);
     uint32_t b = __shfl_up_sync(0xffffffffu, it, 1);
     b = lane == 0 ? s_tok[g] : sat_add(s_tok[g], b, top_t);
-    if (r < a.n_req) {
+    if (r < a.n_req && rank == 0) {
       a.req_row_start[r] = (int)min(b, (uint32_t)a.n_tok);
       if (r == a.n_req - 1) a.req_row_start[a.n_req] = (int)min(et, (uint32_t)a.n_tok);
       a.new_len[r] = served ? x.ctx + (int)x.n : x.ctx;
+    }
+    if (table) {
+      // (pages of refused requests count nothing, and lie behind all others)
+      uint32_t bp = __shfl_up_sync(0xffffffffu, ip, 1);
+      bp = lane == 0 ? s_pg[g] : sat_add(s_pg[g], bp, top_p);
+      if (r < a.n_req) {
+        s_start[r] = (int)min(b, (uint32_t)a.n_tok);
+        s_page[r] = (int)min(bp, taken);
+        s_ctx[r] = served && x.n > 0 ? x.ctx : -1;
+      }
+      continue;
     }
     // pages: a warp for a request
     uint32_t todo = __ballot_sync(0xffffffffu, served && x.pages > 0);
@@ -239,11 +274,49 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
       for (int i = lane; i < pages; i += 32) row[i] = ld_in(a.free_pages + at + i);
     }
   }
-  if (a.n_req == 0 && threadIdx.x == 0) a.req_row_start[0] = 0;
-  __syncthreads();  // starts, lengths and pages are read below
-  if (threadIdx.x == 0 && taken > 0) *a.n_free = base;
-  if (a.n_tok <= kStepOneCta)
-    for (int t0 = warp * 32; t0 < a.n_tok; t0 += kStepThreads) step_rows(a, t0);
+  if (table) __syncthreads();
+  if (table && rank == 0) {
+    for (int i = threadIdx.x; i < (int)taken; i += blockDim.x) {
+      const int r = step_search(s_page, a.n_req, i);  // it has pages, and is served
+      const int from = (int)step_pages(a, (uint32_t)s_ctx[r] + (uint32_t)(a.page_size - 1));
+      a.page_table[(int64_t)r * a.ld_pt + from + (i - s_page[r])] = ld_in(a.free_pages + base + i);
+    }
+  }
+  if (a.cluster > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (rank == 0 && threadIdx.x == 0) {
+    if (a.n_req == 0) a.req_row_start[0] = 0;
+    if (taken > 0) *a.n_free = base;
+  }
+  if (a.cluster == 0) return;  // no table, or no rows
+  const int rows = (int)min(s_all[0], (uint32_t)a.n_tok), stride = a.cluster * blockDim.x;
+  int top = 1;
+  while (2 * top < a.n_req) top *= 2;
+  for (int t0 = rank * blockDim.x + threadIdx.x; t0 < a.n_tok; t0 += 4 * stride) {
+    int r[4], pos[4], page[4];  // four rows on the way together
+#pragma unroll
+    for (int y = 0; y < 4; ++y) r[y] = 0;
+    for (int d = top; d > 0; d >>= 1)  // the last request that starts at or before the row
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (r[y] + d < a.n_req && s_start[r[y] + d] <= t0 + y * stride) r[y] += d;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int t = t0 + y * stride;
+      pos[y] = page[y] = -1;
+      if (t >= rows) {
+        r[y] = -1;
+        continue;
+      }
+      const int ctx = s_ctx[r[y]];
+      if (ctx < 0) continue;
+      pos[y] = ctx + t - s_start[r[y]];
+      const int pi = (int)step_pages(a, (uint32_t)pos[y]), held = (int)step_pages(a, (uint32_t)ctx + (uint32_t)(a.page_size - 1));
+      page[y] = ld_in(pi < held ? a.page_table + (int64_t)r[y] * a.ld_pt + pi : a.free_pages + base + s_page[r[y]] + (pi - held));
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      if (t0 + y * stride < a.n_tok) step_row(a, t0 + y * stride, r[y], pos[y], page[y]);
+  }
 }
 
 __global__ void __launch_bounds__(kStepRowsThreads)
@@ -266,125 +339,134 @@ struct ReleaseArgs {
 
 // Pages given back: entries from_page .. to_page - 1 of a request's row go to
 // the end of the list in the requests' order and become -1 in the table.  One
-// CTA: a warp counts what 32 requests give, and after the sums moves it; a
-// request of more than kReleaseFew entries takes the whole warp.
+// CTA, 2,048 requests at a time: a thread counts what a request with few
+// entries gives, a warp one with many; then the sums, and the pages move in the
+// same way.
 constexpr int kReleaseFew = 4;
+constexpr int kReleaseBatch = 2 * kStepThreads;
 __global__ void __launch_bounds__(kStepThreads)
 release_pages_kernel(const __grid_constant__ ReleaseArgs a) {
-  __shared__ uint32_t s_pg[kStepMaxGroups];
-  __shared__ uint32_t s_all;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (a.n_req + 31) / 32;
+  __shared__ int s_from[kReleaseBatch], s_n[kReleaseBatch];  // a request's entries
+  __shared__ uint32_t s_count[kReleaseBatch];                // its pages, then those before it
+  __shared__ int s_many[kReleaseBatch];                      // requests with many entries
+  __shared__ int s_n_many;
+  __shared__ uint32_t s_warp[kStepThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int threads = blockDim.x, batch = 2 * threads;
   const uint32_t top = (uint32_t)a.n_pool + 1u;
   pdl_wait_primary();
   int n_free = ld_in(a.n_free);
   if (n_free < 0 || n_free > a.n_pool) {  // an unusable list takes nothing
-    if (threadIdx.x == 0) raise_fault(kFaultGrouping);
+    if (tid == 0) raise_fault(kFaultGrouping);
     n_free = a.n_pool;
   }
   const uint32_t room = (uint32_t)(a.n_pool - n_free);
-  // the lane's entries of group g
-  auto range = [&](int g, int& from, int& n) {
-    const int r = g * 32 + lane;
-    from = n = 0;
-    if (r >= a.n_req) return;
-    const int f = ld_in(a.from_page + r), t = ld_in(a.to_page + r);
-    if (f >= t) return;
-    if (f < 0 || t > a.ld_pt) {
-      raise_fault(kFaultIndex);
-      return;
-    }
-    from = f;
-    n = t - f;
-  };
-  // the pages among them
-  auto count = [&](int g, int from, int n) -> uint32_t {
-    const int32_t* row = a.page_table + (int64_t)(g * 32 + lane) * a.ld_pt + from;
-    uint32_t c = 0;
-    if (n > 0 && n <= kReleaseFew) {
+  uint32_t before = 0;                                       // pages of the batches before
+  for (int r0 = 0; r0 < a.n_req; r0 += batch) {
+    const int m = min(batch, a.n_req - r0);
+    if (tid == 0) s_n_many = 0;
+    __syncthreads();
+    int few[2][kReleaseFew];                                 // pages of the thread's requests with few entries
 #pragma unroll
-      for (int i = 0; i < kReleaseFew; ++i)
-        if (i < n) c += ld_in(row + i) >= 0;
+    for (int z = 0; z < 2; ++z) {
+      const int i = z * threads + tid;
+      int from = 0, n = 0;
+      uint32_t c = 0;
+#pragma unroll
+      for (int y = 0; y < kReleaseFew; ++y) few[z][y] = -1;
+      if (i < m) {
+        const int f = ld_in(a.from_page + r0 + i), t = ld_in(a.to_page + r0 + i);
+        if (f < t && (f < 0 || t > a.ld_pt)) {
+          raise_fault(kFaultIndex);
+        } else if (f < t) {
+          from = f;
+          n = t - f;
+        }
+      }
+      if (n > kReleaseFew) {
+        s_many[atomicAdd(&s_n_many, 1)] = i;                 // (in any order)
+      } else {
+        const int32_t* row = a.page_table + (int64_t)(r0 + i) * a.ld_pt + from;
+#pragma unroll
+        for (int y = 0; y < kReleaseFew; ++y)
+          if (y < n) few[z][y] = ld_in(row + y);
+#pragma unroll
+        for (int y = 0; y < kReleaseFew; ++y) c += few[z][y] >= 0;
+      }
+      s_from[i] = from;
+      s_n[i] = n;
+      s_count[i] = c;
     }
-    uint32_t todo = __ballot_sync(0xffffffffu, n > kReleaseFew);
-    while (todo != 0) {
-      const int l = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int nn = __shfl_sync(0xffffffffu, n, l);
-      const int32_t* rw = a.page_table + (int64_t)(g * 32 + l) * a.ld_pt + __shfl_sync(0xffffffffu, from, l);
-      uint32_t s = 0;
+    __syncthreads();
+    const int n_many = s_n_many;
+    for (int j = warp; j < n_many; j += threads / 32) {
+      const int i = s_many[j], n = s_n[i];
+      const int32_t* row = a.page_table + (int64_t)(r0 + i) * a.ld_pt + s_from[i];
+      uint32_t c = 0;
 #pragma unroll 4
-      for (int i = lane; i < nn; i += 32) s += ld_in(rw + i) >= 0;
-      s = __reduce_add_sync(0xffffffffu, s);
-      if (lane == l) c = s;
+      for (int y = lane; y < n; y += 32) c += ld_in(row + y) >= 0;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0) s_count[i] = c;
     }
-    return c;
-  };
-  int from = 0, n = 0;
-  uint32_t c = 0, ic = 0;
-  for (int g = warp; g < groups; g += kStepThreads / 32) {
-    range(g, from, n);
-    c = count(g, from, n);
-    ic = warp_sat_scan(min(c, top), top);
-    if (lane == 31) s_pg[g] = ic;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    uint32_t carry = 0;
-    for (int g0 = 0; g0 < groups; g0 += 32) {
-      const int g = g0 + lane;
-      const uint32_t s = sat_add(warp_sat_scan(g < groups ? s_pg[g] : 0u, top), carry, top);
-      uint32_t b = __shfl_up_sync(0xffffffffu, s, 1);
-      if (lane == 0) b = carry;
-      if (g < groups) s_pg[g] = b;
-      carry = __shfl_sync(0xffffffffu, s, 31);
+    __syncthreads();
+    // sums before each request: two neighbours a thread
+    const uint32_t c0 = min(s_count[2 * tid], top), c1 = min(s_count[2 * tid + 1], top);
+    const uint32_t incl = warp_sat_scan(sat_add(c0, c1, top), top);
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    uint32_t base = before, all = before;
+    for (int w = 0; w < threads / 32; ++w) {
+      if (w == warp) base = all;
+      all = sat_add(all, s_warp[w], top);
     }
-    if (lane == 0) s_all = carry;
-  }
-  __syncthreads();
-  for (int g = warp; g < groups; g += kStepThreads / 32) {
-    if (groups > kStepThreads / 32) {  // else still in registers
-      range(g, from, n);
-      c = count(g, from, n);
-      ic = warp_sat_scan(min(c, top), top);
-    }
-    uint32_t at = __shfl_up_sync(0xffffffffu, ic, 1);  // pages given back before the request's
-    at = lane == 0 ? s_pg[g] : sat_add(s_pg[g], at, top);
-    if (n > 0 && n <= kReleaseFew) {
-      int32_t* row = a.page_table + (int64_t)(g * 32 + lane) * a.ld_pt + from;
-      for (int i = 0; i < n; ++i) {
-        const int page = ld_in(row + i);
-        if (page < 0) continue;
+    const uint32_t prev = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane > 0) base = sat_add(base, prev, top);
+    s_count[2 * tid] = base;
+    s_count[2 * tid + 1] = sat_add(base, c0, top);
+    before = all;
+    __syncthreads();
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const int i = z * threads + tid;
+      uint32_t at = s_count[i];
+      int32_t* row = a.page_table + (int64_t)(r0 + i) * a.ld_pt + s_from[i];
+#pragma unroll
+      for (int y = 0; y < kReleaseFew; ++y) {
+        if (few[z][y] < 0) continue;
         if (at < room) {
-          a.free_pages[n_free + at] = page;
-          row[i] = -1;
+          a.free_pages[n_free + at] = few[z][y];
+          row[y] = -1;
         }
         ++at;
       }
     }
-    uint32_t todo = __ballot_sync(0xffffffffu, n > kReleaseFew);
-    while (todo != 0) {
-      const int l = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int nn = __shfl_sync(0xffffffffu, n, l);
-      uint32_t b = __shfl_sync(0xffffffffu, at, l);
-      int32_t* rw = a.page_table + (int64_t)(g * 32 + l) * a.ld_pt + __shfl_sync(0xffffffffu, from, l);
-      for (int i0 = 0; i0 < nn; i0 += 32) {
-        const int i = i0 + lane;
-        const int page = i < nn ? ld_in(rw + i) : -1;
-        const uint32_t has = __ballot_sync(0xffffffffu, page >= 0);
-        const uint32_t mine = b + __popc(has & ((1u << lane) - 1u));
-        if (page >= 0 && mine < room) {
-          a.free_pages[n_free + mine] = page;
-          rw[i] = -1;
+    for (int j = warp; j < n_many; j += threads / 32) {
+      const int i = s_many[j], n = s_n[i];
+      uint32_t at = s_count[i];
+      int32_t* row = a.page_table + (int64_t)(r0 + i) * a.ld_pt + s_from[i];
+      for (int y0 = 0; y0 < n; y0 += 128) {                  // four loads on the way together
+        int page[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int y = y0 + z * 32 + lane;
+          page[z] = y < n ? ld_in(row + y) : -1;
         }
-        b += __popc(has);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const uint32_t has = __ballot_sync(0xffffffffu, page[z] >= 0);
+          const uint32_t mine = sat_add(at, __popc(has & ((1u << lane) - 1u)), top);
+          if (page[z] >= 0 && mine < room) {
+            a.free_pages[n_free + mine] = page[z];
+            row[y0 + z * 32 + lane] = -1;
+          }
+          at = sat_add(at, __popc(has), top);
+        }
       }
     }
   }
-  if (threadIdx.x == 0) {
-    if (s_all > room) raise_fault(kFaultCapacity);
-    if (s_all > 0 && room > 0) *a.n_free = n_free + (int)min(s_all, room);
+  if (tid == 0) {
+    if (before > room) raise_fault(kFaultCapacity);
+    if (before > 0 && room > 0) *a.n_free = n_free + (int)min(before, room);
   }
 }
 
