@@ -715,16 +715,16 @@ def _launch_ws(fn, dev, stream, size_fn, size_args, workspace, *args):
     _check(fn, _launch(fn, dev, stream, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size()))
 
 
-def _launch_ws8(fn, dev, stream, size_args, workspace, *args):
-    """_launch of a call on the 8-bit cache: most need a workspace, so it is
-    asked for first."""
-    if workspace is None:
+def _launch_ws8(fn, device, stream, size_args, workspace, *args):
+    """_launch of a call on the 8-bit cache: many need a workspace, so its
+    size is asked for first."""
+    if workspace is not None:
+        n = workspace.numel() * workspace.element_size()
+    else:
         n = _call(fn + "_workspace_size", *size_args)
-        if n == 0:
-            return _check(fn, _launch(fn, dev, stream, *args, None, 0))
-        torch = _torch()
-        workspace = _empty(n, torch.uint8, torch.device("cuda", dev), stream)
-    _check(fn, _launch(fn, dev, stream, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+        if n:
+            workspace = _empty((n,), _t()[3], device, stream)
+    _check(fn, _launch(fn, device.index, stream, *args, workspace.data_ptr() if n else None, n))
 
 
 def append_kv_fp4(k_new, v_new, req_tok_start, req_first_pos, k_codes, k_scales, v_codes, v_scales, page_table,
@@ -908,7 +908,7 @@ def _window_call(fn, cache_ptrs, scales, n_slots, h_kv, d, q, req_row_start, row
             page_table.data_ptr(), ld_pt, page_size, window, n_sink, d ** -0.5 if scale is None else scale, *scales,
             out.data_ptr(), _ptr(lse))
     if block:  # the 8-bit cache
-        _launch_ws8(fn, dev, stream, (n_rows, n_req, max_rows_per_req, *sizes), workspace, *args)
+        _launch_ws8(fn, q.device, stream, (n_rows, n_req, max_rows_per_req, *sizes), workspace, *args)
     else:
         _launch_ws(fn, dev, stream, "qsa_window_attn_workspace_size", (n_rows, *sizes), workspace, *args)
     return out, lse
@@ -1023,7 +1023,7 @@ def sparse_attn_fp8(q, k_codes, k_scales, v_codes, v_scales, slots, scale=None, 
         lse = None
     elif lse is None:
         lse = _empty((n_rows, h_q), f32, q.device, stream)
-    _launch_ws8("qsa_sparse_attn_fp8", dev, stream, (n_rows, h_q, h_kv, d, n_idx), workspace, q.data_ptr(),
+    _launch_ws8("qsa_sparse_attn_fp8", q.device, stream, (n_rows, h_q, h_kv, d, n_idx), workspace, q.data_ptr(),
                 q.stride(0) if n_rows > 1 else h_q * d, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                 v_scales.data_ptr(), n_slots, block, n_rows, h_q, h_kv, d, slots.data_ptr(), width, n_idx,
                 d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse))

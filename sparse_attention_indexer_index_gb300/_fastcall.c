@@ -335,6 +335,26 @@ static PyObject* fc_window_attn_fp8(PyObject* self, PyObject* const* a, Py_ssize
                                                    sinks, scale, out, lse, ws, ws_bytes, stream));
 }
 
+static PyObject* fc_sparse_attn_fp8_workspace_size(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 5, "sparse_attn_fp8_workspace_size")) return NULL;
+  const int32_t n_rows = arg_i32(a, 0), h_q = arg_i32(a, 1), h_kv = arg_i32(a, 2), d = arg_i32(a, 3);
+  const int32_t n_idx = arg_i32(a, 4);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromSize_t(qsa_sparse_attn_fp8_workspace_size(n_rows, h_q, h_kv, d, n_idx));
+}
+
+static PyObject* fc_window_attn_fp8_workspace_size(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!want_args(n, 9, "window_attn_fp8_workspace_size")) return NULL;
+  const int32_t n_rows = arg_i32(a, 0), n_req = arg_i32(a, 1), max_rows = arg_i32(a, 2), h_q = arg_i32(a, 3);
+  const int32_t h_kv = arg_i32(a, 4), d = arg_i32(a, 5), max_len = arg_i32(a, 6), window = arg_i32(a, 7);
+  const int32_t sinks = arg_i32(a, 8);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromSize_t(
+      qsa_window_attn_fp8_workspace_size(n_rows, n_req, max_rows, h_q, h_kv, d, max_len, window, sinks));
+}
+
 static PyObject* fc_plan_step(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   if (!want_args(n, 16, "plan_step")) return NULL;
@@ -388,6 +408,10 @@ static PyMethodDef fc_methods[] = {
     {"qsa_gather_kv_fp8", (PyCFunction)(void (*)(void))fc_gather_kv_fp8, METH_FASTCALL, "qsa_gather_kv_fp8"},
     {"qsa_sparse_attn_fp8", (PyCFunction)(void (*)(void))fc_sparse_attn_fp8, METH_FASTCALL, "qsa_sparse_attn_fp8"},
     {"qsa_window_attn_fp8", (PyCFunction)(void (*)(void))fc_window_attn_fp8, METH_FASTCALL, "qsa_window_attn_fp8"},
+    {"qsa_sparse_attn_fp8_workspace_size", (PyCFunction)(void (*)(void))fc_sparse_attn_fp8_workspace_size, METH_FASTCALL,
+     "qsa_sparse_attn_fp8_workspace_size"},
+    {"qsa_window_attn_fp8_workspace_size", (PyCFunction)(void (*)(void))fc_window_attn_fp8_workspace_size, METH_FASTCALL,
+     "qsa_window_attn_fp8_workspace_size"},
     {"qsa_plan_step", (PyCFunction)(void (*)(void))fc_plan_step, METH_FASTCALL, "qsa_plan_step"},
     {"qsa_release_pages", (PyCFunction)(void (*)(void))fc_release_pages, METH_FASTCALL, "qsa_release_pages"},
     {NULL, NULL, 0, NULL}};

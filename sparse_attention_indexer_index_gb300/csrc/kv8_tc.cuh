@@ -118,40 +118,44 @@ struct K8Tc {
     uint64_t full[12], empty[12];
     uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain;
     uint64_t met[kSlices + 1];   // softmax warps of a slice, of all
-    uint64_t join_free, join_full;  // the cluster's softmax warps: rings are free, sums are there
+    uint64_t join_full;          // the cluster's softmax warps: their sums are there
     uint64_t seg_full[kK8SegRing], seg_empty[kK8SegRing];
     Seg seg[kK8SegRing];
-    alignas(16) float mult[N];   // logit (base 2) = mult * 2^ek * S
     alignas(16) float mb[N];     // the reference M, less kK8Bias
-    int out[N];                  // (row, query head) of the pair, -1: none
-    int4 sees[kShared ? N : 1];  // the pair sees entries [0, x) and [y, z)
+    // a pair's words, for segments of even and odd number (one begins before the other's sums are out):
+    alignas(16) float mult[2][N];   // logit (base 2) = mult * 2^ek * S
+    int out[2][N];                  // (row, query head) of the pair, -1: none
+    int4 sees[2][kShared ? N : 1];  // the pair sees entries [0, x) and [y, z)
+    uint32_t nan[2][kShared ? N : 1][D / 32];  // columns that a NaN of V reached
+    int any_nan[2];
     alignas(16) float wmax[kSoft][kPer];
     float wsum[kSoft][kPer];
     alignas(16) int vote[2][kSoft];          // [block parity]: a weight of the warp's passes the limit
-    uint32_t nan[kShared ? N : 1][D / 32];   // columns that a NaN of V reached
     int scan[32];
-    int any_nan;
     uint32_t tmem;
     int abort;
     int base[kWindow ? kK8MaxTiles + 1 : 1];   // tiles before request r
     int pre[kWindow ? kK8MaxTiles + 1 : 1];    // blocks before tile t
     int4 tile[kWindow ? kK8MaxTiles : 1];      // its first row, request * 256 + rows, first, n
   };
-  // A cluster's join, [source][own pair][D + 2]: in memory of its own, or (48 pairs) in the ring,
-  // which takes one more meeting of the CTAs, before anything is written.
-  static constexpr int kJoin = N * (D + 2) * 4;
-  static constexpr bool kJoinRing = N == 48;
-  static constexpr int kFixed = kQ + 2 * kP + (kJoinRing ? 0 : kJoin) + (int)sizeof(Ctl) + 1024;
+  // A cluster's join, rows of D sums, M and L.  Up to 16 pairs: a CTA writes a pair's row into the
+  // memory of the one that joins it, [source][own pair].  More: there is no room, and each keeps its
+  // rows, [pair], in its ring, whose last tile has been used by then, for the others to read (48
+  // pairs, 4 CTAs: 1.3 us less than writing there behind one more meeting; 8 pairs: 0.4 us more).
+  static constexpr bool kPull = N > 16;
+  static constexpr int kJoin = D + 4;
+  static constexpr int kFixed = kQ + 2 * kP + (kPull ? 0 : N * kJoin * 4) + (int)sizeof(Ctl) + 1024;
   static constexpr int kFit = (227 * 1024 - kFixed) / kTile;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
-  static_assert(kStages >= 3 && kJoin <= kStages * kTile, "ring");
+  static_assert(kStages >= 3 && N * kJoin * 4 <= kStages * kTile, "ring");
   static constexpr int kSmem = kFixed + kStages * kTile;
 };
 
 // ---- waits and tensor-memory accesses --------------------------------------------------
-// Bounded wait by a whole warp, which stays together.
-__device__ __forceinline__ bool k8_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+// (What is rare is kept out of line: a kernel of 100 KB and more fetched its
+// instructions for longer than it ran them, where each is run once or twice.)
+__device__ __noinline__ void k8_fault(unsigned bits) { raise_fault(bits); }
+__device__ __noinline__ bool k8_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint64_t t0 = global_timer_ns();
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
     const bool late = global_timer_ns() - t0 > 2000000000ull;
@@ -164,6 +168,10 @@ __device__ __forceinline__ bool k8_wait(uint64_t* bar, uint32_t parity, volatile
     }
   }
   return true;
+}
+// Bounded wait by a whole warp, which stays together.
+__device__ __forceinline__ bool k8_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || k8_wait_long(bar, parity, abort);
 }
 // One arrival for a warp, behind what its lanes did.
 __device__ __forceinline__ void k8_arrive(uint64_t* bar) {
@@ -179,7 +187,21 @@ __device__ __forceinline__ void k8_arrive_all(uint64_t* bar, int n_cta) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_shared_rank(bar, lane)) : "memory");
   __syncwarp();
 }
-__device__ __forceinline__ bool k8_wait_cluster(uint64_t* bar, volatile int* abort) {
+// What another CTA of the cluster has in shared memory (several can be on the way, see ld_dsmem_u32).
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void st_cluster_f1(uint32_t at, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  return v;
+}
+__device__ __noinline__ bool k8_wait_cluster(uint64_t* bar, volatile int* abort) {
   auto arrived = [&]() -> bool {
     uint32_t done;
     asm volatile(
@@ -304,25 +326,25 @@ __device__ __forceinline__ int k8_pos(const Seg& w, int e) {
   return e < w.ns ? e : w.first + (e - w.ns);
 }
 // Where a window of rows t0 .. t0 + rows - 1 begins and ends: entries, first, ns.
-__device__ __forceinline__ int k8_window(const Kv8AttnArgs& a, int t0, int rows, int& first, int& ns) {
+__device__ __noinline__ int3 k8_window(const Kv8AttnArgs& a, int t0, int rows) {
   int lo = INT32_MAX, last = 0;
+  bool bad = false;
+#pragma unroll 1
   for (int i0 = 0; i0 < rows; i0 += 8) {
     int L[8];  // on the way together
 #pragma unroll
     for (int i = 0; i < 8; ++i) L[i] = i0 + i < rows ? ld_in(a.row_len + t0 + i0 + i) : 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (L[i] < 0 || L[i] > a.max_len) {
-        raise_fault(kFaultGrouping);
-      } else if (L[i] > 0) {
-        lo = min(lo, max(0, L[i] - a.window));
-        last = max(last, L[i]);
-      }
+      const bool ok = L[i] > 0 && L[i] <= a.max_len;
+      bad |= L[i] != 0 && !ok;
+      lo = min(lo, ok ? max(0, L[i] - a.window) : INT32_MAX);
+      last = max(last, ok ? L[i] : 0);
     }
   }
-  first = last > 0 ? lo : 0;
-  ns = min(a.n_sink, first);
-  return last > 0 ? ns + last - first : 0;
+  if (bad) raise_fault(kFaultGrouping);
+  const int first = last > 0 ? lo : 0, ns = min(a.n_sink, first);
+  return make_int3(last > 0 ? ns + last - first : 0, first, ns);
 }
 template <int kBlock>
 __device__ __forceinline__ int k8_blocks(int n) {
@@ -336,6 +358,7 @@ __device__ __noinline__ bool k8_seen(const Kv8AttnArgs& a, int t0, int rows, int
   }
   return false;
 }
+__device__ __noinline__ int k8_divide(int x, int y) { return x / y; }
 // An entry's slot in two parts, as in kv_attn.cuh: what is loaded, and what is
 // made of it (-1: none).
 template <bool kWindow, class Seg>
@@ -344,7 +367,7 @@ __device__ __forceinline__ KaFetch k8_fetch(const Kv8AttnArgs& a, const Seg& w, 
   if (e >= w.n) return f;
   if constexpr (kWindow) {
     const int pos = k8_pos(w, e);
-    const int pi = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;  // < ld_pt: pos < max_len
+    const int pi = a.page_shift >= 0 ? pos >> a.page_shift : k8_divide(pos, a.page_size);  // < ld_pt: pos < max_len
     f.raw = ld_in(a.page_table + (int64_t)w.r * a.ld_pt + pi);
     f.off = pos - pi * a.page_size;
   } else {
@@ -355,19 +378,19 @@ __device__ __forceinline__ KaFetch k8_fetch(const Kv8AttnArgs& a, const Seg& w, 
 template <bool kWindow, bool kFaults, class Seg>
 __device__ __forceinline__ int32_t k8_slot(const Kv8AttnArgs& a, const Seg& w, int e, const KaFetch& f) {
   if (e >= w.n || f.raw < 0) {
-    if (kWindow && kFaults && e < w.n && k8_seen(a, w.t0, w.rows, k8_pos(w, e))) raise_fault(kFaultIndex);
+    if (kWindow && kFaults && e < w.n && k8_seen(a, w.t0, w.rows, k8_pos(w, e))) k8_fault(kFaultIndex);
     return -1;
   }
   if constexpr (!kWindow) {
     if (f.raw >= a.n_slots) {
-      if (kFaults) raise_fault(kFaultIndex);
+      if (kFaults) k8_fault(kFaultIndex);
       return -1;
     }
     return f.raw;
   } else {
     // a page counts only if it lies wholly inside the cache
     if (((int64_t)f.raw + 1) * a.page_size > a.n_slots) {
-      if (kFaults && k8_seen(a, w.t0, w.rows, k8_pos(w, e))) raise_fault(kFaultIndex);
+      if (kFaults && k8_seen(a, w.t0, w.rows, k8_pos(w, e))) k8_fault(kFaultIndex);
       return -1;
     }
     return f.raw * a.page_size + f.off;
@@ -392,7 +415,7 @@ __device__ __forceinline__ K8Scales k8_scales(const Kv8AttnArgs& a, int32_t slot
 // ---- the CTA's work ----------------------------------------------------------------------
 // arr[0 .. n) becomes the sums before each, arr[n] the sum of all; by the whole CTA.
 template <int kThreads>
-__device__ __forceinline__ void k8_scan(int* arr, int n, int* tmp) {
+__device__ __noinline__ void k8_scan(int* arr, int n, int* tmp) {
   const int per = (n + kThreads - 1) / kThreads, i0 = threadIdx.x * per, i1 = min(i0 + per, n);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
@@ -407,6 +430,7 @@ __device__ __forceinline__ void k8_scan(int* arr, int n, int* tmp) {
   if (lane == 31) tmp[warp] = incl;
   __syncthreads();
   int before = incl - sum, all = 0;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     const int v = tmp[w];
     if (w < warp) before += v;
@@ -434,32 +458,23 @@ __device__ __forceinline__ int k8_search(const int* arr, int n, int x) {
 __device__ __forceinline__ int k8_request_tiles(const Kv8AttnArgs& a, int i) {
   const int row0 = ld_in(a.req_row_start + i), row1 = ld_in(a.req_row_start + i + 1);
   if (row0 < 0 || row1 < row0 || row1 > a.n_rows) {
-    raise_fault(kFaultGrouping);
+    k8_fault(kFaultGrouping);
     return 0;
   }
   return (row1 - row0 + a.rows - 1) / a.rows;
 }
-// Columns lane_e (and 128 + lane_e) of a finished pair.
-template <int D, bool kWindow>
-__device__ __forceinline__ void k8_write(const Kv8AttnArgs& a, int hq, int lane_e, const float (&sum)[D / 128][4], int y,
-                                         float M, float L) {
-  const float inv = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll
-  for (int h = 0; h < D / 128; ++h) {
-    const int64_t at = (int64_t)hq * D + h * 128 + lane_e;
-    if constexpr (kWindow) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(sum[h][y] * inv);
-    else static_cast<float*>(a.out)[at] = sum[h][y] * inv;
-  }
-  if (lane_e == 0 && a.lse != nullptr)
-    a.lse[hq] = L == 0.f ? -__int_as_float(0x7f800000)
-                         : (M == -__int_as_float(0x7f800000) ? L : M + log2f(L)) * 0.69314718055994531f;
+// A pair's log-sum-exp from M (base 2) and the sum of its weights (without any
+// weight, or with NaN only, M = -inf).
+__device__ __forceinline__ float k8_lse(float M, float L) {
+  const float ninf = -__int_as_float(0x7f800000);
+  return L == 0.f ? ninf : (M == ninf ? L : M + log2f(L)) * 0.69314718055994531f;
 }
 // Request of tile s and the tile's number in it, by a whole warp (-1: none).  Up
 // to kK8Exact requests the tiles are counted; else slot s holds request r's
 // tiles from slot start[r] / R + r on (enough room: the requests before have at
 // most that many), and slots past its last tile are empty.
 constexpr int kK8Exact = 1024;
-__device__ __forceinline__ int k8_find(const Kv8AttnArgs& a, int s, int& rank) {
+__device__ __noinline__ int k8_find(const Kv8AttnArgs& a, int s, int& rank) {
   const int lane = threadIdx.x & 31;
   if (a.n_req <= kK8Exact) {
     for (int g0 = 0; g0 < a.n_req; g0 += 32) {
@@ -508,8 +523,9 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   unsigned char* const ring = smem;
   unsigned char* const q_buf = ring + S * Sh::kTile;
   unsigned char* const p_buf = q_buf + Sh::kQ;
-  float* const join = reinterpret_cast<float*>(Sh::kJoinRing ? ring : p_buf + 2 * Sh::kP);
-  typename Sh::Ctl& ctl = *reinterpret_cast<typename Sh::Ctl*>(p_buf + 2 * Sh::kP + (Sh::kJoinRing ? 0 : Sh::kJoin));
+  float* const join = reinterpret_cast<float*>(Sh::kPull ? ring : p_buf + 2 * Sh::kP);
+  typename Sh::Ctl& ctl =
+      *reinterpret_cast<typename Sh::Ctl*>(p_buf + 2 * Sh::kP + (Sh::kPull ? 0 : N * Sh::kJoin * 4));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &ctl.abort;
   const float ninf = -__int_as_float(0x7f800000);
@@ -533,7 +549,6 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     mbar_init(&ctl.q_full, Sh::kSoft);
     for (int i = 0; i <= Sh::kSlices; ++i) mbar_init(&ctl.met[i], i < Sh::kSlices ? 4 * kSub : Sh::kSoft);
     mbar_init(&ctl.drain, 1);
-    mbar_init(&ctl.join_free, Sh::kSoft * a.cluster);
     mbar_init(&ctl.join_full, Sh::kSoft * a.cluster);
     for (int i = 0; i < kK8SegRing; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
@@ -565,10 +580,9 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         const int r = k8_search(ctl.base, a.n_req, t);
         const int t0 = ld_in(a.req_row_start + r) + (t - ctl.base[r]) * a.rows;
         const int rows = a.rows == 1 ? 1 : min(a.rows, ld_in(a.req_row_start + r + 1) - t0);
-        int first, ns;
-        const int n = k8_window(a, t0, rows, first, ns);
-        ctl.tile[t] = make_int4(t0, r * 256 + rows, first, n);
-        ctl.pre[t] = k8_blocks<kBlock>(n);
+        const int3 y = k8_window(a, t0, rows);
+        ctl.tile[t] = make_int4(t0, r * 256 + rows, y.y, y.x);
+        ctl.pre[t] = k8_blocks<kBlock>(y.x);
       }
       k8_scan<Sh::kThreads>(ctl.pre, tiles, ctl.scan);
     }
@@ -584,6 +598,9 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
 
   if (warp == Sh::kSoft + 1) {
     // ---- the CTA's segments ----------------------------------------------------------------
+    // (the rows' lengths on their way to L2 beside the requests' starts)
+    if (kWindow && a.mode != kK8Shares && lane * 32 < a.n_rows && a.n_rows <= 1024)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.row_len + lane * 32) : "memory");
     int k = 0;
     auto publish = [&](const Seg& w) -> bool {
       const int sl = k % kK8SegRing;
@@ -592,45 +609,53 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         ctl.seg[sl] = w;
         mbar_arrive(&ctl.seg_full[sl]);
       }
+      if (k > 0 && w.rows > 0) {  // q, and a list's first slots, on their way to L2 while the CTA is busy
+#pragma unroll 1
+        for (int i = lane; i < w.rows * a.group * (D / 64); i += 32) {
+          const int pair = i / (D / 64), row = (int)(pair * a.group_inv >> 16);
+          const uint16_t* src = a.q + (int64_t)(w.t0 + row) * a.ld_q + ((int64_t)w.g * a.group + pair - row * a.group) * D;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i % (D / 64) * 64) : "memory");
+        }
+        const int at = w.j0 * kBlock + lane * 32;
+        if (!kWindow && lane < 2 * kBlock / 32 && at < w.n)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.slots + w.t0 * a.ld_slots + at) : "memory");
+      }
       ++k;
       return true;
     };
-    // unit u; rows 0: none
-    auto unit = [&](int u) -> Seg {
-      Seg w{};
-      w.slot = -1;
-      const int t = u / a.h_kv;
-      w.t0 = t;
-      w.g = u - t * a.h_kv;
-      w.n = a.n_idx;
-      if constexpr (kWindow) {
-        int number = 0;
-        if constexpr (kShared) w.r = k8_find(a, t, number);
-        else w.r = warp_row_request(a.req_row_start, a.n_req, t);
-        if (w.r < 0) return w;
-        if constexpr (kShared) {
-          w.t0 = ld_in(a.req_row_start + w.r) + number * a.rows;
-          w.rows = min(a.rows, ld_in(a.req_row_start + w.r + 1) - w.t0);
-        }
-        w.n = k8_window(a, w.t0, kShared ? w.rows : 1, w.first, w.ns);
-      }
-      if constexpr (!kShared) w.rows = 1;
-      w.j1 = k8_blocks<kBlock>(w.n);
-      return w;
-    };
     bool ok = true;
-    if (a.mode == kK8Cluster) {
-      Seg w = unit((int)(blockIdx.x >> a.cluster_shift));
-      if (w.rows > 0) {
-        const int nb = w.j1;  // at most 2^23
+    if (a.mode != kK8Shares) {
+      // a cluster's unit, or whole ones in turn
+      const bool one = a.mode == kK8Cluster;
+      int u = one ? (int)(blockIdx.x >> a.cluster_shift) : (int)blockIdx.x;
+      const int end = one ? u + 1 : a.tile_slots * a.h_kv;
+#pragma unroll 1
+      for (; ok && u < end; u += gridDim.x) {
+        Seg w{};
+        w.slot = -1;
+        const int t = u / a.h_kv;
+        w.t0 = t;
+        w.g = u - t * a.h_kv;
+        w.n = a.n_idx;
+        w.rows = 1;
+        if constexpr (kWindow) {
+          int number = 0;
+          if constexpr (kShared) w.r = k8_find(a, t, number);
+          else w.r = warp_row_request(a.req_row_start, a.n_req, t);
+          if (w.r < 0) continue;               // no such tile
+          if constexpr (kShared) {
+            w.t0 = ld_in(a.req_row_start + w.r) + number * a.rows;
+            w.rows = min(a.rows, ld_in(a.req_row_start + w.r + 1) - w.t0);
+          }
+          const int3 y = k8_window(a, w.t0, w.rows);
+          w.n = y.x;
+          w.first = y.y;
+          w.ns = y.z;
+        }
+        const int nb = k8_blocks<kBlock>(w.n);  // at most 2^23
         w.j0 = nb * rank >> a.cluster_shift;
         w.j1 = nb * (rank + 1) >> a.cluster_shift;
         ok = publish(w);
-      }
-    } else if (a.mode == kK8Whole) {
-      for (int u = blockIdx.x; ok && u < a.tile_slots * a.h_kv; u += gridDim.x) {
-        const Seg w = unit(u);
-        if (w.rows > 0) ok = publish(w);
       }
     } else {
       const int cta = blockIdx.x, ctas = gridDim.x;
@@ -873,78 +898,268 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     };
     int x = 0;                                 // blocks so far
     int use = 0;                               // ring uses so far
-    Seg w;
-    bool ok = next_seg(0, w);
-    if (ok) load(w);
-    for (int k = 1; ok; ++k) {
-      const int pairs = w.rows * a.group, nb = w.j1 - w.j0;
-      K8Scales sc = k8_scales(a, k8_slot<kWindow, false>(a, w, entry(w, w.j0), f0), w.g);
-      // q: a warp for a pair, two parts
+    Seg w{};
+    w.rows = -1;
+    bool ok = true;
+    float l[kPer];                             // sums of weights
+    int nb = 0;
+    K8Scales sc{};
+#pragma unroll 1
+    for (int k = 0;; ++k) {
+      // the next segment's q, so that its products begin (those of the one before have been read), then
+      // the sums of the one before; nothing of the next is added to them before all warps are through
+      Seg after;
+      const bool more = next_seg(k, after);
+      if (more) {
+        load(after);
+        const int pairs = after.rows * a.group;
+        sc = k8_scales(a, k8_slot<kWindow, false>(a, after, entry(after, after.j0), f0), after.g);
+        // q: a warp for a pair, two parts
 #pragma unroll
-      for (int i = 0; i < Sh::kLoads; ++i) {
-        const int p = warp + i * Sh::kSoft;
-        if (p >= N) break;
-        const int row = (int)(p * a.group_inv >> 16), hd = p - row * a.group;
-        uint32_t mx = 0;
+        for (int i = 0; i < Sh::kLoads; ++i) {
+          const int p = warp + i * Sh::kSoft;
+          if (p >= N) break;
+          const int row = (int)(p * a.group_inv >> 16), hd = p - row * a.group;
+          uint32_t mx = 0;
 #pragma unroll
-        for (int y = 0; y < H * 2; ++y) mx = __vmaxu2(mx, qv[i][y] & 0x7fff7fffu);
-        const uint32_t top = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-        // the largest component to [128, 256)
-        const int ex = min(max((int)(top >> 7), 8), 254) - 127;
-        const float up = kv8_pow2(7 - ex);
-        uint32_t hi[H], lo[H];
+          for (int y = 0; y < H * 2; ++y) mx = __vmaxu2(mx, qv[i][y] & 0x7fff7fffu);
+          const uint32_t top = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+          // the largest component to [128, 256)
+          const int ex = min(max((int)(top >> 7), 8), 254) - 127;
+          const float up = kv8_pow2(7 - ex);
+          uint32_t hi[H], lo[H];
 #pragma unroll
-        for (int c = 0; c < H; ++c) {
-          uint32_t h2[2], l2[2];
+          for (int c = 0; c < H; ++c) {
+            uint32_t h2[2], l2[2];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float2 f = bf16x2_to_float2(qv[i][2 * c + y]);
-            f.x *= up;
-            f.y *= up;
-            h2[y] = kv8_pack2(f.x, f.y);
-            const float2 b = __half22float2(kv8_half2(h2[y]));
-            l2[y] = kv8_pack2((f.x - b.x) * 32.f, (f.y - b.y) * 32.f);
+            for (int y = 0; y < 2; ++y) {
+              float2 f = bf16x2_to_float2(qv[i][2 * c + y]);
+              f.x *= up;
+              f.y *= up;
+              h2[y] = kv8_pack2(f.x, f.y);
+              const float2 b = __half22float2(kv8_half2(h2[y]));
+              l2[y] = kv8_pack2((f.x - b.x) * 32.f, (f.y - b.y) * 32.f);
+            }
+            hi[c] = h2[0] | h2[1] << 16;
+            lo[c] = l2[0] | l2[1] << 16;
           }
-          hi[c] = h2[0] | h2[1] << 16;
-          lo[c] = l2[0] | l2[1] << 16;
-        }
-        // rows p and N + p of [D / 128][2 N][128 B], swizzled by row mod 8 (N is a multiple of 8)
-        const int d = lane * (D / 32), kh = d >> 7, ch = (d & 127) >> 4;
-        unsigned char* dst = q_buf + kh * NS * 128 + p * 128 + ((ch ^ (p & 7)) << 4) + (d & 15);
-        if constexpr (D == 256) {
-          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(dst + N * 128) = make_uint2(lo[0], lo[1]);
-        } else {
-          *reinterpret_cast<uint32_t*>(dst) = hi[0];
-          *reinterpret_cast<uint32_t*>(dst + N * 128) = lo[0];
-        }
-        if (lane == 0) {
-          // an infinity or a NaN in q shows in the whole pair
-          ctl.mult[p] = top >= 0x7f80u ? __int_as_float(0x7fffffff)
-                                       : a.scale * 1.4426950408889634f * kv8_pow2(ex - 7);
-          ctl.out[p] = p < pairs ? (w.t0 + row) * a.h_q + w.g * a.group + hd : -1;
-          if constexpr (kShared) {
-            int4 s = make_int4(0, 0, 0, 0);
-            const int L = q_len[i];
-            if (p >= pairs) s.z = INT32_MAX;   // nobody's: sees what there is
-            else if (L > 0 && L <= a.max_len)
-              s = make_int4(min(a.n_sink, L), w.ns + max(0, L - a.window) - w.first, w.ns + L - w.first, 0);
-            ctl.sees[p] = s;
+          // rows p and N + p of [D / 128][2 N][128 B], swizzled by row mod 8 (N is a multiple of 8)
+          const int d = lane * (D / 32), kh = d >> 7, ch = (d & 127) >> 4;
+          unsigned char* dst = q_buf + kh * NS * 128 + p * 128 + ((ch ^ (p & 7)) << 4) + (d & 15);
+          if constexpr (D == 256) {
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dst + N * 128) = make_uint2(lo[0], lo[1]);
+          } else {
+            *reinterpret_cast<uint32_t*>(dst) = hi[0];
+            *reinterpret_cast<uint32_t*>(dst + N * 128) = lo[0];
           }
+          if (lane == 0) {
+            // an infinity or a NaN in q shows in the whole pair
+            ctl.mult[k & 1][p] = top >= 0x7f80u ? __int_as_float(0x7fffffff)
+                                         : a.scale * 1.4426950408889634f * kv8_pow2(ex - 7);
+            ctl.out[k & 1][p] = p < pairs ? (after.t0 + row) * a.h_q + after.g * a.group + hd : -1;
+            if constexpr (kShared) {
+              int4 s = make_int4(0, 0, 0, 0);
+              const int L = q_len[i];
+              if (p >= pairs) s.z = INT32_MAX;   // nobody's: sees what there is
+              else if (L > 0 && L <= a.max_len)
+                s = make_int4(min(a.n_sink, L), after.ns + max(0, L - a.window) - after.first,
+                              after.ns + L - after.first, 0);
+              ctl.sees[k & 1][p] = s;
+            }
+          }
+          if constexpr (kShared)
+            if (lane < D / 32) ctl.nan[k & 1][p][lane] = 0u;
         }
-        if constexpr (kShared)
-          if (lane < D / 32) ctl.nan[p][lane] = 0u;
+        if (threadIdx.x == 0) ctl.any_nan[k & 1] = 0;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        k8_arrive(&ctl.q_full);
       }
-      if (threadIdx.x == 0) ctl.any_nan = 0;
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      k8_arrive(&ctl.q_full);
-      ok = meet_all();                         // the pairs' words
+      if (w.rows >= 0) {
+        // ---- outputs: a thread for a column of O ---------------------------------------------
+        {
+          // the lanes' sums: half of the pairs go to each half of the lanes, and so on; in the end lane
+          // 32 / kFold i has pair i (of kFold pairs, those past kPer zeros)
+          constexpr int kFold = kPer <= 8 ? 8 : 16;
+          float y[kFold];
+#pragma unroll
+          for (int p = 0; p < kFold; ++p) y[p] = p < kPer ? l[p] : 0.f;
+#pragma unroll
+          for (int d = 16, n = kFold / 2; n > 0; d >>= 1, n >>= 1) {
+            const bool up = (lane & d) != 0;
+#pragma unroll
+            for (int p = 0; p < n; ++p) {
+              const float give = up ? y[p] : y[p + n], keep = up ? y[p + n] : y[p];
+              y[p] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+            }
+          }
+#pragma unroll
+          for (int d = 16 / kFold; d > 0; d >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], d);
+          const int pair = lane / (32 / kFold);
+          if (lane % (32 / kFold) == 0 && pair < kPer) ctl.wsum[warp][pair] = y[0];
+        }
+        ok = meet() && (nb == 0 || k8_wait(&ctl.pv_done[(x - 1) & 1], (uint32_t)((x - 1) >> 1) & 1u, abort));
+        if (!ok) break;
+        __syncwarp();
+        tc_fence_after();
+        const bool nans = kShared && ctl.any_nan[(k - 1) & 1] != 0;
+        // a pair a lane: its M, sum and place
+        const int lp = min(lane, kPer - 1);
+        float sum_l = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) sum_l += ctl.wsum[slice * W + i][lp];
+        const float m_l = nb > 0 && ctl.mb[p0 + lp] != kK8None ? ctl.mb[p0 + lp] : ninf;
+        const int hq_l = ctl.out[(k - 1) & 1][p0 + lp];
+        const int own = N >> a.cluster_shift;  // pairs that a CTA of the cluster writes: rank, rank + C, ...
+        // where the pair's sums go: to the joining CTA, the partial results, or (times 1 / L) the output
+        uint32_t at_l = 0;
+        float* part_l = nullptr;
+        float inv_l = 1.f;
+        const bool one = (warp & 3) == 0 && sub == 0 && lane < kPer && hq_l >= 0;  // M, L and lse by one warp
+        if (C > 1) {
+          const int p = p0 + lp;
+          at_l = Sh::kPull ? smem_u32(join + p * Sh::kJoin)
+                           : map_shared_rank(join + (rank * own + (p >> a.cluster_shift)) * Sh::kJoin, (uint32_t)(p & (C - 1)));
+          if (one) {
+            st_cluster_f1(at_l + 4 * D, m_l);
+            st_cluster_f1(at_l + 4 * D + 4, sum_l);
+          }
+        } else if (w.slot >= 0) {
+          part_l = a.part + ((int64_t)w.slot * N + p0 + lp) * (D + 2);
+          if (one) {
+            part_l[0] = m_l;
+            part_l[1] = sum_l;
+          }
+        } else {
+          inv_l = sum_l == 0.f ? 0.f : 1.0f / sum_l;
+          if (one && a.lse != nullptr) a.lse[hq_l] = k8_lse(m_l, sum_l);
+        }
+        // (the sub-blocks' warps take a half of the pairs each)
+#pragma unroll 1
+        for (int c0 = kPer / kSub * sub; c0 < kPer / kSub * (sub + 1); c0 += 4) {
+          float sum[H][4];
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            uint32_t v[PARTS * 4];
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) k8_ld4(lanes + Sh::kColO + h * NP + i * N + p0 + c0, v + i * 4);
+            k8_wait_ld(v);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              float o = __uint_as_float(v[(PARTS - 1) * 4 + y]);
+#pragma unroll
+              for (int i = PARTS - 2; i >= 0; --i) o = fmaf(o, 0.03125f, __uint_as_float(v[i * 4 + y]));
+              sum[h][y] = nb > 0 ? o : 0.f;      // no block: nothing was written there
+            }
+          }
+          if (nans) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int h = 0; h < H; ++h)
+                if ((ctl.nan[(k - 1) & 1][kShared ? p0 + c0 + y : 0][h * 4 + (lane_e >> 5)] >> (lane_e & 31)) & 1u)
+                  sum[h][y] = __int_as_float(0x7fffffff);
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int hq = __shfl_sync(0xffffffffu, hq_l, c0 + y);
+            if (C > 1) {
+              const uint32_t at = __shfl_sync(0xffffffffu, at_l, c0 + y) + 4 * lane_e;
+              if (hq >= 0) {
+#pragma unroll
+                for (int h = 0; h < H; ++h) st_cluster_f1(at + h * 512, sum[h][y]);
+              }
+            } else if (w.slot >= 0) {
+              float* pp = part_l + (c0 + y - lp) * (D + 2) + 2 + lane_e;
+              if (hq >= 0) {
+#pragma unroll
+                for (int h = 0; h < H; ++h) pp[h * 128] = sum[h][y];
+              }
+            } else {
+              const float inv = __shfl_sync(0xffffffffu, inv_l, c0 + y);
+              const int64_t at = (int64_t)hq * D + lane_e;
+              if (hq >= 0) {
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                  if constexpr (kWindow) static_cast<__nv_bfloat16*>(a.out)[at + h * 128] = __float2bfloat16_rn(sum[h][y] * inv);
+                  else static_cast<float*>(a.out)[at + h * 128] = sum[h][y] * inv;
+                }
+              }
+            }
+          }
+        }
+        if (C > 1) {
+          k8_arrive_all(&ctl.join_full, C);
+          ok = k8_wait_cluster(&ctl.join_full, abort);
+          if (!ok) break;
+          // a warp for 128 columns of a pair, or (more than 16 pairs) for all, four sources at a time
+          constexpr int kCols = N <= 16 ? 128 : D, V = kCols / 128;
+#pragma unroll 1
+          for (int i = warp; i < own * (D / kCols); i += Sh::kSoft) {
+            const int p = i / (D / kCols) * C + rank, col = i % (D / kCols) * kCols + lane * 4;
+            if (p >= w.rows * a.group) break;
+            float M = ninf, L = 0.f, sum[V * 4] = {};
+#pragma unroll 1
+            for (int c0 = 0; c0 < C; c0 += 4) {
+              float v[4][V * 4], m[4], l4[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int from_c = min(c0 + c, C - 1);
+                const uint32_t from = Sh::kPull ? map_shared_rank(join + p * Sh::kJoin, (uint32_t)from_c)
+                                                : smem_u32(join + (from_c * own + (p >> a.cluster_shift)) * Sh::kJoin);
+#pragma unroll
+                for (int y = 0; y < V; ++y) {
+                  const float4 f = ld_cluster_f4(from + 4 * (col + y * 128));
+                  v[c][y * 4] = f.x; v[c][y * 4 + 1] = f.y; v[c][y * 4 + 2] = f.z; v[c][y * 4 + 3] = f.w;
+                }
+                const float2 f = ld_cluster_f2(from + 4 * D);
+                m[c] = c0 + c < C ? f.x : ninf;
+                l4[c] = c0 + c < C ? f.y : 0.f;
+              }
+              const float top = fmaxf(M, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+              const float fm = M == ninf ? 1.f : ka_ex2(M - top);
+              M = top;
+              L *= fm;
+#pragma unroll
+              for (int y = 0; y < V * 4; ++y) sum[y] *= fm;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                if (c0 + c >= C) break;
+                const float f = m[c] == ninf ? 0.f : ka_ex2(m[c] - M);
+                L += m[c] == ninf ? l4[c] : f * l4[c];  // without a weight (or with NaN only) M = -inf
+#pragma unroll
+                for (int y = 0; y < V * 4; ++y) sum[y] = fmaf(f, v[c][y], sum[y]);
+              }
+            }
+            const float inv = L == 0.f ? 0.f : 1.0f / L;
+            const int64_t at = (int64_t)ctl.out[(k - 1) & 1][p] * D + col;
+#pragma unroll
+            for (int y = 0; y < V; ++y) {
+              const float4 o = make_float4(sum[y * 4] * inv, sum[y * 4 + 1] * inv, sum[y * 4 + 2] * inv, sum[y * 4 + 3] * inv);
+              if constexpr (kWindow) {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at + y * 128) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+              } else {
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + y * 128) = o;
+              }
+            }
+            if (col == 0 && a.lse != nullptr)
+              a.lse[ctl.out[(k - 1) & 1][p]] = k8_lse(M, L);
+          }
+        }
+        tc_fence_before();
+      }
+      if (!more) break;
+      w = after;
+      nb = w.j1 - w.j0;
+      ok = meet_all();                         // the pairs' words are there, M's are free
       if (!ok) break;
       int4 both = make_int4(0, 0, 0, 0);       // shared tiles: every pair sees entries [0, x) and [y, z)
       if constexpr (kShared) {
         int va = INT32_MAX, vb = 0, vc = INT32_MAX;
-        for (int p = lane; p < pairs; p += 32) {
-          const int4 y = ctl.sees[p];
+        for (int p = lane; p < w.rows * a.group; p += 32) {
+          const int4 y = ctl.sees[k & 1][p];
           va = min(va, y.x);
           vb = max(vb, y.y);
           vc = min(vc, y.z);
@@ -957,7 +1172,6 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
         met = true;
       }
-      float l[kPer];                           // sums of weights
 #pragma unroll
       for (int p = 0; p < kPer; ++p) l[p] = 0.f;
       for (int b = 0; ok && b < nb; ++b, ++x) {
@@ -984,7 +1198,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           if (part) {
 #pragma unroll
             for (int p = 0; p < kPer; ++p) {
-              const int4 y = ctl.sees[p0 + p];
+              const int4 y = ctl.sees[k & 1][p0 + p];
               sees |= (uint32_t)(i_e < y.x || (i_e >= y.y && i_e < y.z)) << p;
             }
           }
@@ -995,7 +1209,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         k8_arrive(&ctl.s_free[sl]);
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-          t[p] = fmaf(__uint_as_float(v[kPer + p]), 0.03125f, __uint_as_float(v[p])) * (ctl.mult[p0 + p] * kf);
+          t[p] = fmaf(__uint_as_float(v[kPer + p]), 0.03125f, __uint_as_float(v[p])) * (ctl.mult[k & 1][p0 + p] * kf);
           if (!now.valid) t[p] = ninf;
         }
         if (part) {
@@ -1163,11 +1377,11 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
                 word[y] &= ~bad;
                 // columns d0 + 4 y .. + 3
                 const uint32_t bits = ((bad & 1u) | (bad >> 7 & 2u) | (bad >> 14 & 4u) | (bad >> 21 & 8u)) << ((d0 + 4 * y) & 31);
-                for (int p = 0; p < pairs; ++p) {
-                  const int4 s4 = ctl.sees[p];
-                  if (at_e < s4.x || (at_e >= s4.y && at_e < s4.z)) atomicOr(&ctl.nan[p][(d0 + 4 * y) >> 5], bits);
+                for (int p = 0; p < w.rows * a.group; ++p) {
+                  const int4 s4 = ctl.sees[k & 1][p];
+                  if (at_e < s4.x || (at_e >= s4.y && at_e < s4.z)) atomicOr(&ctl.nan[k & 1][p][(d0 + 4 * y) >> 5], bits);
                 }
-                ctl.any_nan = 1;
+                ctl.any_nan[k & 1] = 1;
               }
               __syncwarp();
             }
@@ -1179,137 +1393,10 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       if (!ok) break;
       use += 2 * nb;
 
-      // ---- outputs: a thread for a column of O -------------------------------------------------
-      {
-        // the lanes' sums: half of the pairs go to each half of the lanes, and so on; in the end lane
-        // 32 / kFold i has pair i (of kFold pairs, those past kPer zeros)
-        constexpr int kFold = kPer <= 8 ? 8 : 16;
-        float y[kFold];
-#pragma unroll
-        for (int p = 0; p < kFold; ++p) y[p] = p < kPer ? l[p] : 0.f;
-#pragma unroll
-        for (int d = 16, n = kFold / 2; n > 0; d >>= 1, n >>= 1) {
-          const bool up = (lane & d) != 0;
-#pragma unroll
-          for (int p = 0; p < n; ++p) {
-            const float give = up ? y[p] : y[p + n], keep = up ? y[p + n] : y[p];
-            y[p] = keep + __shfl_xor_sync(0xffffffffu, give, d);
-          }
-        }
-#pragma unroll
-        for (int d = 16 / kFold; d > 0; d >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], d);
-        const int pair = lane / (32 / kFold);
-        if (lane % (32 / kFold) == 0 && pair < kPer) ctl.wsum[warp][pair] = y[0];
-      }
-      // the next segment's loads on the way meanwhile
-      Seg after;
-      const bool more = next_seg(k, after);
-      if (more) load(after);
-      ok = meet() && (nb == 0 || k8_wait(&ctl.pv_done[(x - 1) & 1], (uint32_t)((x - 1) >> 1) & 1u, abort));
-      if (!ok) break;
-      __syncwarp();
-      tc_fence_after();
-      const bool nans = kShared && ctl.any_nan != 0;
-      // a pair a lane: its M, sum and place
-      const int lp = min(lane, kPer - 1);
-      float sum_l = 0.f;
-#pragma unroll
-      for (int i = 0; i < W; ++i) sum_l += ctl.wsum[slice * W + i][lp];
-      const float m_l = nb > 0 && ctl.mb[p0 + lp] != kK8None ? ctl.mb[p0 + lp] : ninf;
-      const int hq_l = ctl.out[p0 + lp];
-      if (Sh::kJoinRing && C > 1) {
-        // this CTA's ring is free: its products are done, and no copy is under way
-        k8_arrive_all(&ctl.join_free, C);
-        ok = k8_wait_cluster(&ctl.join_free, abort);
-        if (!ok) break;
-      }
-      const int own = (N + C - 1) >> a.cluster_shift;      // pairs that a CTA writes: rank, rank + C, ... (C divides N)
-      // (the sub-blocks' warps take a half of the pairs each)
-#pragma unroll 1
-      for (int c0 = kPer / kSub * sub; c0 < kPer / kSub * (sub + 1); c0 += 4) {
-        float sum[H][4];
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          uint32_t v[PARTS * 4];
-#pragma unroll
-          for (int i = 0; i < PARTS; ++i) k8_ld4(lanes + Sh::kColO + h * NP + i * N + p0 + c0, v + i * 4);
-          k8_wait_ld(v);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            float o = __uint_as_float(v[(PARTS - 1) * 4 + y]);
-#pragma unroll
-            for (int i = PARTS - 2; i >= 0; --i) o = fmaf(o, 0.03125f, __uint_as_float(v[i * 4 + y]));
-            sum[h][y] = nb > 0 ? o : 0.f;      // no block: nothing was written there
-          }
-        }
-        if (nans) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-              if ((ctl.nan[kShared ? p0 + c0 + y : 0][h * 4 + (lane_e >> 5)] >> (lane_e & 31)) & 1u)
-                sum[h][y] = __int_as_float(0x7fffffff);
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int p = p0 + c0 + y;
-          const int hq = __shfl_sync(0xffffffffu, hq_l, c0 + y);
-          const float L = __shfl_sync(0xffffffffu, sum_l, c0 + y), M = __shfl_sync(0xffffffffu, m_l, c0 + y);
-          if (hq < 0) continue;
-          if (C > 1) {
-            const uint32_t at = map_shared_rank(join + (rank * own + (p >> a.cluster_shift)) * (D + 2), (uint32_t)(p & (C - 1)));
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4 * (2 + h * 128 + lane_e)), "f"(sum[h][y]) : "memory");
-            if (lane_e < 2)
-              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4 * lane_e), "f"(lane_e == 0 ? M : L) : "memory");
-          } else if (w.slot >= 0) {
-            float* pp = a.part + ((int64_t)w.slot * N + p) * (D + 2);
-#pragma unroll
-            for (int h = 0; h < H; ++h) pp[2 + h * 128 + lane_e] = sum[h][y];
-            if (lane_e < 2) pp[lane_e] = lane_e == 0 ? M : L;
-          } else {
-            k8_write<D, kWindow>(a, hq, lane_e, sum, y, M, L);
-          }
-        }
-      }
-      if (C > 1) {
-        k8_arrive_all(&ctl.join_full, C);
-        ok = k8_wait_cluster(&ctl.join_full, abort);
-        if (!ok) break;
-        // the pairs that this CTA writes: a warp for a pair
-        for (int i = warp; i < own; i += Sh::kSoft) {
-          const int p = i * C + rank;
-          if (p >= pairs) break;
-          const float* src = join + i * (D + 2);
-          float M = ninf;
-          for (int c = 0; c < C; ++c) M = fmaxf(M, src[c * own * (D + 2)]);
-          float L = 0.f, sum[D / 32] = {};
-          for (int c = 0; c < C; ++c) {
-            const float* from = src + c * own * (D + 2);
-            const float ms = from[0], f = ms == ninf ? 0.f : ka_ex2(ms - M);
-            L += ms == ninf ? from[1] : f * from[1];  // without a weight (or with NaN only) M = -inf
-#pragma unroll
-            for (int y = 0; y < D / 32; ++y) sum[y] = fmaf(f, from[2 + y * 32 + lane], sum[y]);
-          }
-          const float inv = L == 0.f ? 0.f : 1.0f / L;
-          const int64_t at = (int64_t)ctl.out[p] * D + lane;
-#pragma unroll
-          for (int y = 0; y < D / 32; ++y) {
-            if constexpr (kWindow) static_cast<__nv_bfloat16*>(a.out)[at + y * 32] = __float2bfloat16_rn(sum[y] * inv);
-            else static_cast<float*>(a.out)[at + y * 32] = sum[y] * inv;
-          }
-          if (lane == 0 && a.lse != nullptr)
-            a.lse[ctl.out[p]] = L == 0.f ? ninf : (M == ninf ? L : M + log2f(L)) * 0.69314718055994531f;
-        }
-      }
-      tc_fence_before();
-      ok = meet_all() && more;                 // the pairs' words are free
-      w = after;
     }
   }
 
-  // no CTA of the cluster leaves before all have written to each other
+  // no CTA of the cluster leaves before all have read each other's sums
   if (C > 1) {
     if (!met) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
@@ -1390,7 +1477,7 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int n) {
   const float r = l == 0.f ? 0.f : o / l;
   if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[hq * D + d] = __float2bfloat16_rn(r);
   else static_cast<float*>(a.out)[hq * D + d] = r;
-  if (d == 0 && a.lse != nullptr) a.lse[hq] = l == 0.f ? ninf : (m == ninf ? l : m + log2f(l)) * 0.69314718055994531f;
+  if (d == 0 && a.lse != nullptr) a.lse[hq] = k8_lse(m, l);
 }
 
 }  // namespace qsa
