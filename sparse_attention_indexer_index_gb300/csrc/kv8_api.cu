@@ -148,7 +148,7 @@ K8Form window_form(int32_t n_rows, int32_t n_req, int32_t max_rows_per_req, int3
 // The jobs, then two partial results a CTA.
 constexpr size_t kJobBytes = (kK8Ctas * sizeof(int4) + 255) / 256 * 256;
 size_t form_bytes(const K8Form& f, int32_t d) {
-  return f.share ? kJobBytes + (size_t)2 * kK8Ctas * kK8Kernels[f.kind][0].pairs * (d + 2) * 4 : 0;
+  return f.share ? kJobBytes + (size_t)2 * kK8Ctas * kK8Kernels[f.kind][0].pairs * (d + 4) * 4 : 0;
 }
 
 qsa_status launch_k8(const K8Form& f, Kv8AttnArgs& a, int d, void* workspace, cudaStream_t stream) {

@@ -138,7 +138,7 @@ struct K8Tc {
     int pre[kWindow ? kK8MaxTiles + 1 : 1];    // blocks before tile t
     int4 tile[kWindow ? kK8MaxTiles : 1];      // its first row, request * 256 + rows, first, n
   };
-  // A cluster's join, rows of D sums, M and L.  Up to 16 pairs: a CTA writes a pair's row into the
+  // Rows of partial results: D sums, M and L.  A cluster's join:  Up to 16 pairs: a CTA writes a pair's row into the
   // memory of the one that joins it, [source][own pair].  More: there is no room, and each keeps its
   // rows, [pair], in its ring, whose last tile has been used by then, for the others to read (48
   // pairs, 4 CTAs: 1.3 us less than writing there behind one more meeting; 8 pairs: 0.4 us more).
@@ -193,8 +193,10 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t at) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
   return v;
 }
-__device__ __forceinline__ void st_cluster_f1(uint32_t at, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+__device__ __forceinline__ char* map_generic_rank(const void* p, uint32_t rank) {
+  uint64_t r;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+  return reinterpret_cast<char*>(r);
 }
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t at) {
   float2 v;
@@ -352,6 +354,7 @@ __device__ __forceinline__ int k8_blocks(int n) {
 }
 // Whether a row of the tile attends to a position.
 __device__ __noinline__ bool k8_seen(const Kv8AttnArgs& a, int t0, int rows, int pos) {
+#pragma unroll 1
   for (int i = 0; i < rows; ++i) {
     const int L = ld_in(a.row_len + t0 + i);
     if (L > 0 && L <= a.max_len && pos < L && (pos >= L - a.window || pos < a.n_sink)) return true;
@@ -420,6 +423,7 @@ __device__ __noinline__ void k8_scan(int* arr, int n, int* tmp) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
   int sum = 0;
+#pragma unroll 1
   for (int i = i0; i < i1; ++i) sum += arr[i];
   int incl = sum;
 #pragma unroll
@@ -436,6 +440,7 @@ __device__ __noinline__ void k8_scan(int* arr, int n, int* tmp) {
     if (w < warp) before += v;
     all += v;
   }
+#pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     const int v = arr[i];
     arr[i] = before;
@@ -447,6 +452,7 @@ __device__ __noinline__ void k8_scan(int* arr, int n, int* tmp) {
 // The last i with arr[i] <= x (arr[0] <= x < arr[n]).
 __device__ __forceinline__ int k8_search(const int* arr, int n, int x) {
   int lo = 0, hi = n;
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (arr[mid] <= x) lo = mid;
@@ -477,6 +483,7 @@ constexpr int kK8Exact = 1024;
 __device__ __noinline__ int k8_find(const Kv8AttnArgs& a, int s, int& rank) {
   const int lane = threadIdx.x & 31;
   if (a.n_req <= kK8Exact) {
+#pragma unroll 1
     for (int g0 = 0; g0 < a.n_req; g0 += 32) {
       const int n = g0 + lane < a.n_req ? k8_request_tiles(a, g0 + lane) : 0;
       int incl = n;
@@ -496,6 +503,7 @@ __device__ __noinline__ int k8_find(const Kv8AttnArgs& a, int s, int& rank) {
     return -1;
   }
   int lo = 0, n = a.n_req + 1;  // the last i with start[i] / R + i <= s, 32 samples a round
+#pragma unroll 1
   while (true) {
     const int step = (n + 31) / 32;
     const int i = lane * step;
@@ -535,26 +543,29 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&ctl.full[i], Sh::kProd);
-      mbar_init(&ctl.empty[i], 1);
+  if (warp == 0) {  // a barrier of each kind a lane
+    static_assert(S <= 32 && Sh::kSlices < 32, "lanes");
+    if (lane < S) {
+      mbar_init(&ctl.full[lane], Sh::kProd);
+      mbar_init(&ctl.empty[lane], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.s_free[i], Sh::kSoft);
-      mbar_init(&ctl.p_full[i], Sh::kSoft);
-      mbar_init(&ctl.pv_done[i], 1);
+    if (lane < 2) {
+      mbar_init(&ctl.s_full[lane], 1);
+      mbar_init(&ctl.s_free[lane], Sh::kSoft);
+      mbar_init(&ctl.p_full[lane], Sh::kSoft);
+      mbar_init(&ctl.pv_done[lane], 1);
     }
-    mbar_init(&ctl.q_full, Sh::kSoft);
-    for (int i = 0; i <= Sh::kSlices; ++i) mbar_init(&ctl.met[i], i < Sh::kSlices ? 4 * kSub : Sh::kSoft);
-    mbar_init(&ctl.drain, 1);
-    mbar_init(&ctl.join_full, Sh::kSoft * a.cluster);
-    for (int i = 0; i < kK8SegRing; ++i) {
-      mbar_init(&ctl.seg_full[i], 1);
-      mbar_init(&ctl.seg_empty[i], Sh::kSoft + 1 + Sh::kProd);  // softmax, MMA, producers
+    if (lane <= Sh::kSlices) mbar_init(&ctl.met[lane], lane < Sh::kSlices ? 4 * kSub : Sh::kSoft);
+    if (lane < kK8SegRing) {
+      mbar_init(&ctl.seg_full[lane], 1);
+      mbar_init(&ctl.seg_empty[lane], Sh::kSoft + 1 + Sh::kProd);  // softmax, MMA, producers
     }
-    ctl.abort = 0;
+    if (lane == 0) {
+      mbar_init(&ctl.q_full, Sh::kSoft);
+      mbar_init(&ctl.drain, 1);
+      mbar_init(&ctl.join_full, Sh::kSoft * a.cluster);
+      ctl.abort = 0;
+    }
     fence_mbar_init();
   }
   tc_fence_before();
@@ -573,9 +584,11 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     if (a.mode == kK8Shares) {
       // the lengths on their way to L2 beside the requests' starts
       if (threadIdx.x * 32 < a.n_rows) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.row_len + threadIdx.x * 32) : "memory");
+#pragma unroll 1
       for (int r = threadIdx.x; r < a.n_req; r += Sh::kThreads) ctl.base[r] = k8_request_tiles(a, r);
       k8_scan<Sh::kThreads>(ctl.base, a.n_req, ctl.scan);
       tiles = min(ctl.base[a.n_req], kK8MaxTiles);
+#pragma unroll 1
       for (int t = threadIdx.x; t < tiles; t += Sh::kThreads) {
         const int r = k8_search(ctl.base, a.n_req, t);
         const int t0 = ld_in(a.req_row_start + r) + (t - ctl.base[r]) * a.rows;
@@ -667,6 +680,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       const int per = total / ctas, more = total - per * ctas;
       int b = cta * per + min(cta, more);
       const int end = b + per + (cta < more ? 1 : 0);
+#pragma unroll 1
       while (ok && b < end) {
         const int bt = b / a.h_kv;  // at or behind the tile's first block, before its last head's end
         Seg w{};
@@ -714,6 +728,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       if (!a.jobs_by_unit) {
         if (lane == 0) a.jobs[cta] = job;
       } else if (cta == 0) {  // units that are none
+#pragma unroll 1
         for (int u = tiles * a.h_kv + lane; u < a.tile_slots * a.h_kv; u += 32) a.jobs[u] = no_job;
       }
     }
@@ -751,13 +766,16 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       asm volatile("cp.async.commit_group;" ::: "memory");
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
       ++u;
+#pragma unroll 1
       while (told <= u - kDepth) signal(told++);
       return true;
     };
-    auto flush = [&]() {
+    auto flush = [&]() {  // (loops of one or two passes, not unrolled)
       asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll 1
       while (told < u) signal(told++);
     };
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       Seg w;
       // the others may have to use what is on the way before the next segment is known
@@ -772,6 +790,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       int32_t last[kE], slot[kE] = {};
 #pragma unroll
       for (int i = 0; i < kE; ++i) next[i] = k8_fetch<kWindow>(a, w, entry(w.j0, i));
+#pragma unroll 1
       for (int j = w.j0; ok && j <= w.j1; ++j) {  // K(j), V(j - 1)
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
@@ -808,11 +827,13 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         ph ^= 1u;
       }
     };
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       Seg w;
       if (!next_seg(k, w)) break;
       const int nb = __reduce_max_sync(0xffffffffu, w.j1 - w.j0);  // uniform
       ok = k8_wait(&ctl.q_full, (uint32_t)k & 1u, abort);
+#pragma unroll 1
       for (int i = 0; ok && i <= nb; ++i) {
         if (i < nb) {  // S(i)
           const int sl = (x + i) & 1;
@@ -1011,28 +1032,27 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         const float m_l = nb > 0 && ctl.mb[p0 + lp] != kK8None ? ctl.mb[p0 + lp] : ninf;
         const int hq_l = ctl.out[(k - 1) & 1][p0 + lp];
         const int own = N >> a.cluster_shift;  // pairs that a CTA of the cluster writes: rank, rank + C, ...
-        // where the pair's sums go: to the joining CTA, the partial results, or (times 1 / L) the output
-        uint32_t at_l = 0;
-        float* part_l = nullptr;
+        // where the pair's sums go: to the joining CTA, the partial results, or (times 1 / L) the output.
+        // (One address for all three: code that runs once takes as long as its instructions to arrive.)
+        const bool done = C == 1 && w.slot < 0;
+        const bool half = kWindow && done;     // BF16
+        char* to_l = nullptr;
         float inv_l = 1.f;
-        const bool one = (warp & 3) == 0 && sub == 0 && lane < kPer && hq_l >= 0;  // M, L and lse by one warp
-        if (C > 1) {
+        if (hq_l >= 0) {
           const int p = p0 + lp;
-          at_l = Sh::kPull ? smem_u32(join + p * Sh::kJoin)
-                           : map_shared_rank(join + (rank * own + (p >> a.cluster_shift)) * Sh::kJoin, (uint32_t)(p & (C - 1)));
-          if (one) {
-            st_cluster_f1(at_l + 4 * D, m_l);
-            st_cluster_f1(at_l + 4 * D + 4, sum_l);
+          if (C > 1) {
+            float* mine = join + (Sh::kPull ? p : rank * own + (p >> a.cluster_shift)) * Sh::kJoin;
+            to_l = Sh::kPull ? reinterpret_cast<char*>(mine) : map_generic_rank(mine, (uint32_t)(p & (C - 1)));
+          } else if (!done) {
+            to_l = reinterpret_cast<char*>(a.part + ((int64_t)w.slot * N + p) * Sh::kJoin);
+          } else {
+            to_l = static_cast<char*>(a.out) + (int64_t)hq_l * (D * (kWindow ? 2 : 4));
+            inv_l = sum_l == 0.f ? 0.f : 1.0f / sum_l;
           }
-        } else if (w.slot >= 0) {
-          part_l = a.part + ((int64_t)w.slot * N + p0 + lp) * (D + 2);
-          if (one) {
-            part_l[0] = m_l;
-            part_l[1] = sum_l;
+          if ((warp & 3) == 0 && sub == 0 && lane < kPer) {  // M, L and lse by one warp
+            if (!done) *reinterpret_cast<float2*>(to_l + 4 * D) = make_float2(m_l, sum_l);
+            else if (a.lse != nullptr) a.lse[hq_l] = k8_lse(m_l, sum_l);
           }
-        } else {
-          inv_l = sum_l == 0.f ? 0.f : 1.0f / sum_l;
-          if (one && a.lse != nullptr) a.lse[hq_l] = k8_lse(m_l, sum_l);
         }
         // (the sub-blocks' warps take a half of the pairs each)
 #pragma unroll 1
@@ -1062,29 +1082,14 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           }
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const int hq = __shfl_sync(0xffffffffu, hq_l, c0 + y);
-            if (C > 1) {
-              const uint32_t at = __shfl_sync(0xffffffffu, at_l, c0 + y) + 4 * lane_e;
-              if (hq >= 0) {
+            char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to_l), c0 + y));
+            const float inv = __shfl_sync(0xffffffffu, inv_l, c0 + y);
+            if (to == nullptr) continue;
 #pragma unroll
-                for (int h = 0; h < H; ++h) st_cluster_f1(at + h * 512, sum[h][y]);
-              }
-            } else if (w.slot >= 0) {
-              float* pp = part_l + (c0 + y - lp) * (D + 2) + 2 + lane_e;
-              if (hq >= 0) {
-#pragma unroll
-                for (int h = 0; h < H; ++h) pp[h * 128] = sum[h][y];
-              }
-            } else {
-              const float inv = __shfl_sync(0xffffffffu, inv_l, c0 + y);
-              const int64_t at = (int64_t)hq * D + lane_e;
-              if (hq >= 0) {
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                  if constexpr (kWindow) static_cast<__nv_bfloat16*>(a.out)[at + h * 128] = __float2bfloat16_rn(sum[h][y] * inv);
-                  else static_cast<float*>(a.out)[at + h * 128] = sum[h][y] * inv;
-                }
-              }
+            for (int h = 0; h < H; ++h) {
+              const float o = sum[h][y] * inv;
+              if (half) reinterpret_cast<__nv_bfloat16*>(to)[h * 128 + lane_e] = __float2bfloat16_rn(o);
+              else reinterpret_cast<float*>(to)[h * 128 + lane_e] = o;
             }
           }
         }
@@ -1158,6 +1163,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       int4 both = make_int4(0, 0, 0, 0);       // shared tiles: every pair sees entries [0, x) and [y, z)
       if constexpr (kShared) {
         int va = INT32_MAX, vb = 0, vc = INT32_MAX;
+#pragma unroll 1
         for (int p = lane; p < w.rows * a.group; p += 32) {
           const int4 y = ctl.sees[k & 1][p];
           va = min(va, y.x);
@@ -1174,6 +1180,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       }
 #pragma unroll
       for (int p = 0; p < kPer; ++p) l[p] = 0.f;
+#pragma unroll 1
       for (int b = 0; ok && b < nb; ++b, ++x) {
         const int sl = x & 1, j = w.j0 + b;
         ok = k8_wait(&ctl.s_full[sl], (uint32_t)(x >> 1) & 1u, abort);
@@ -1364,6 +1371,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             // entries that some pairs see and others do not, one after the other by the whole warp: D / 32
             // codes a lane
             uint32_t todo = __ballot_sync(0xffffffffu, now.valid && !(i_e < both.x || (i_e >= both.y && i_e < both.z)));
+#pragma unroll 1
             while (todo != 0) {
               const int f = __ffs(todo) - 1;
               todo &= todo - 1;
@@ -1377,6 +1385,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
                 word[y] &= ~bad;
                 // columns d0 + 4 y .. + 3
                 const uint32_t bits = ((bad & 1u) | (bad >> 7 & 2u) | (bad >> 14 & 4u) | (bad >> 21 & 8u)) << ((d0 + 4 * y) & 31);
+#pragma unroll 1
                 for (int p = 0; p < w.rows * a.group; ++p) {
                   const int4 s4 = ctl.sees[k & 1][p];
                   if (at_e < s4.x || (at_e >= s4.y && at_e < s4.z)) atomicOr(&ctl.nan[k & 1][p][(d0 + 4 * y) >> 5], bits);
@@ -1428,7 +1437,7 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int n) {
   const float ninf = -__int_as_float(0x7f800000);
   // the first part begins the unit (its CTA's second slot), the others come from within it
   auto part = [&](int c) -> const float* {
-    return a.part + ((int64_t)(2 * c + (c == job.x ? 1 : 0)) * n + p) * (D + 2);
+    return a.part + ((int64_t)(2 * c + (c == job.x ? 1 : 0)) * n + p) * (D + 4);
   };
   float m = ninf, l = 0.f, o = 0.f;
   auto add = [&](float ms, float ls, float os) {  // with M at least ms
@@ -1442,9 +1451,10 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int n) {
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const float* pp = part(min(c0 + i * kStep, k));
-      ms[i] = ld_in(pp);
-      ls[i] = ld_in(pp + 1);
-      os[i] = ld_in(pp + 2 + d);
+      const float2 y = ld_in(reinterpret_cast<const float2*>(pp + D));
+      ms[i] = y.x;
+      ls[i] = y.y;
+      os[i] = ld_in(pp + d);
     }
     float mn = m;
 #pragma unroll

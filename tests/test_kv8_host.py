@@ -143,7 +143,7 @@ def test_workspace_sizes(L):
     """Room for two partial results of every CTA (152) where the blocks of long
     units are shared out; none where clusters or whole units take them."""
     f, w = L.qsa_sparse_attn_fp8_workspace_size, L.qsa_window_attn_fp8_workspace_size
-    size = lambda pairs, d: 2560 + 2 * 152 * pairs * (d + 2) * 4  # noqa: E731
+    size = lambda pairs, d: 2560 + 2 * 152 * pairs * (d + 4) * 4  # noqa: E731
     assert f(32, 16, 2, 256, 2051) == 0 and f(1, 16, 2, 256, 2051) == 0 and f(1, 32, 2, 128, 0) == 0
     assert f(1, 16, 2, 256, 9000) == size(8, 256) and f(1, 32, 2, 128, 20000) == size(16, 128)
     assert f(607, 16, 2, 256, 2051) == size(8, 256) and f(608, 16, 2, 256, 2051) == 0
