@@ -117,12 +117,12 @@ K8Form finish(int kind, int d, int rows, int64_t tile_slots, int64_t units, int6
   f.blocks = std::max<int64_t>(1, (entries + block - 1) / block);
   const bool list = kind <= kList16;
   const bool fits = units < kK8MaxUnits && (list || (tile_slots <= kK8MaxTiles && n_req <= kK8MaxTiles)) &&
-                    units * f.blocks < INT32_MAX / 2;  // blocks are counted in 32 bits
+                    units * (f.blocks + kK8Lead) < INT32_MAX / 2;  // blocks are counted in 32 bits
   int c = 1;
   while (c < kKaMaxCluster && units * 2 * c <= 144 && f.blocks >= 2 * c) c *= 2;
   const int64_t rounds = (units * c + 151) / 152;
   const int64_t by_cluster = rounds * ((f.blocks + c - 1) / c);
-  const int64_t by_share = (units * f.blocks + 151) / 152 + 5;
+  const int64_t by_share = (units * (f.blocks + kK8Lead) + 151) / 152 + 5;
   f.cluster = rounds == 1 && (by_cluster <= by_share || !fits);
   f.share = !f.cluster && fits;
   return f;
@@ -183,7 +183,7 @@ qsa_status launch_k8(const K8Form& f, Kv8AttnArgs& a, int d, void* workspace, cu
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, k.fn, a);
   if (e == cudaSuccess && f.share) {
     // parts of a unit, with blocks of equal number to every CTA; lengths may differ
-    const bool many = f.blocks > 8 * (f.units * f.blocks / grid + 1);
+    const bool many = f.blocks > 8 * (f.units * (f.blocks + kK8Lead) / grid + 1);
     const int cols = many ? 64 : d, pairs = f.rows * a.group;
     const dim3 shape((unsigned)(a.jobs_by_unit ? slots : grid), (unsigned)(many ? pairs : (pairs * d + kK8MergeThreads - 1) / kK8MergeThreads),
                      (unsigned)(d / cols));

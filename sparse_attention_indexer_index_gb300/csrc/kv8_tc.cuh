@@ -70,6 +70,7 @@ constexpr int kK8MaxTiles = 304;   // (windows: tiles that a CTA's tables hold)
 constexpr int kK8Ctas = 152;       // CTAs of shares and whole units at most (one an SM)
 constexpr int kK8Bias = 3;         // weights are held as 2^kK8Bias w, w <= 2^kKaGrow
 constexpr int kK8SegRing = 2;
+constexpr int kK8Lead = 2;         // blocks' time that a unit's begin costs a CTA (shares count it)
 constexpr float kK8None = -1e30f;  // M of a pair that has seen nothing (finite: -inf less it is -inf)
 enum { kK8Cluster = 0, kK8Shares = 1, kK8Whole = 2 };
 
@@ -135,7 +136,7 @@ struct K8Tc {
     uint32_t tmem;
     int abort;
     int base[kWindow ? kK8MaxTiles + 1 : 1];   // tiles before request r
-    int pre[kWindow ? kK8MaxTiles + 1 : 1];    // blocks before tile t
+    int pre[kWindow ? kK8MaxTiles + 1 : 1];    // blocks before tile t, kK8Lead more to each
     int4 tile[kWindow ? kK8MaxTiles : 1];      // its first row, request * 256 + rows, first, n
   };
   // Rows of partial results: D sums, M and L.  A cluster's join:  Up to 16 pairs: a CTA writes a pair's row into the
@@ -415,6 +416,15 @@ __device__ __forceinline__ K8Scales k8_scales(const Kv8AttnArgs& a, int32_t slot
   return f;
 }
 
+__device__ __forceinline__ int k8_warp_scan(int v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
 // ---- the CTA's work ----------------------------------------------------------------------
 // arr[0 .. n) becomes the sums before each, arr[n] the sum of all; by the whole CTA.
 template <int kThreads>
@@ -579,9 +589,19 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   if (C > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 
   // ---- shares of windows: tiles, and blocks before each --------------------------------------
+  // (up to 32 tiles, of up to 32 requests: by the warp that needs them)
+  auto tile_blocks = [&](int t) -> int {
+    const int r = k8_search(ctl.base, a.n_req, t);
+    const int t0 = ld_in(a.req_row_start + r) + (t - ctl.base[r]) * a.rows;
+    const int rows = a.rows == 1 ? 1 : min(a.rows, ld_in(a.req_row_start + r + 1) - t0);
+    const int3 y = k8_window(a, t0, rows);
+    ctl.tile[t] = make_int4(t0, r * 256 + rows, y.y, y.x);
+    return k8_blocks<kBlock>(y.x) + kK8Lead;
+  };
+  const bool few = a.n_req <= 32 && a.tile_slots <= 32;
   int tiles = a.n_rows;
   if constexpr (kWindow) {
-    if (a.mode == kK8Shares) {
+    if (a.mode == kK8Shares && !few) {
       // the lengths on their way to L2 beside the requests' starts
       if (threadIdx.x * 32 < a.n_rows) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.row_len + threadIdx.x * 32) : "memory");
 #pragma unroll 1
@@ -589,14 +609,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       k8_scan<Sh::kThreads>(ctl.base, a.n_req, ctl.scan);
       tiles = min(ctl.base[a.n_req], kK8MaxTiles);
 #pragma unroll 1
-      for (int t = threadIdx.x; t < tiles; t += Sh::kThreads) {
-        const int r = k8_search(ctl.base, a.n_req, t);
-        const int t0 = ld_in(a.req_row_start + r) + (t - ctl.base[r]) * a.rows;
-        const int rows = a.rows == 1 ? 1 : min(a.rows, ld_in(a.req_row_start + r + 1) - t0);
-        const int3 y = k8_window(a, t0, rows);
-        ctl.tile[t] = make_int4(t0, r * 256 + rows, y.y, y.x);
-        ctl.pre[t] = k8_blocks<kBlock>(y.x);
-      }
+      for (int t = threadIdx.x; t < tiles; t += Sh::kThreads) ctl.pre[t] = tile_blocks(t);
       k8_scan<Sh::kThreads>(ctl.pre, tiles, ctl.scan);
     }
   }
@@ -612,7 +625,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   if (warp == Sh::kSoft + 1) {
     // ---- the CTA's segments ----------------------------------------------------------------
     // (the rows' lengths on their way to L2 beside the requests' starts)
-    if (kWindow && a.mode != kK8Shares && lane * 32 < a.n_rows && a.n_rows <= 1024)
+    if (kWindow && (a.mode != kK8Shares || few) && lane * 32 < a.n_rows && a.n_rows <= 1024)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(a.row_len + lane * 32) : "memory");
     int k = 0;
     auto publish = [&](const Seg& w) -> bool {
@@ -671,10 +684,22 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         ok = publish(w);
       }
     } else {
+      if constexpr (kWindow) {
+        if (few) {
+          const int own = lane < a.n_req ? k8_request_tiles(a, lane) : 0, upto = k8_warp_scan(own);
+          ctl.base[lane] = upto - own;
+          tiles = min(__shfl_sync(0xffffffffu, upto, 31), 32);
+          __syncwarp();
+          const int blocks = lane < tiles ? tile_blocks(lane) : 0, sum = k8_warp_scan(blocks);
+          ctl.pre[lane] = sum - blocks;
+          if (lane == 31) ctl.pre[32] = sum;
+          __syncwarp();
+        }
+      }
       const int cta = blockIdx.x, ctas = gridDim.x;
       const int4 no_job = make_int4(-1, 0, 0, 0);
       int4 job = no_job;
-      const int same = k8_blocks<kBlock>(a.n_idx);  // a list's blocks
+      const int same = k8_blocks<kBlock>(a.n_idx) + kK8Lead;  // a list's blocks
       const int total = (kWindow ? ctl.pre[tiles] : tiles * same) * a.h_kv;
       // the first `more` CTAs take per + 1 blocks, the others per
       const int per = total / ctas, more = total - per * ctas;
@@ -685,12 +710,12 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         const int bt = b / a.h_kv;  // at or behind the tile's first block, before its last head's end
         Seg w{};
         w.slot = -1;
-        int first_b, nb, u_tile;
+        int first_b, nbl, u_tile;              // (nbl: with the lead)
         if constexpr (kWindow) {
           const int t = u_tile = k8_search(ctl.pre, tiles, bt);
           const int4 y = ctl.tile[t];
           first_b = ctl.pre[t];
-          nb = ctl.pre[t + 1] - first_b;
+          nbl = ctl.pre[t + 1] - first_b;
           w.t0 = y.x;
           w.rows = y.y & 255;
           w.r = y.y >> 8;
@@ -702,18 +727,22 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           w.rows = 1;
           w.n = a.n_idx;
           first_b = w.t0 * same;
-          nb = same;
+          nbl = same;
         }
         const int in = b - first_b * a.h_kv;  // within the tile, head by head
-        w.g = in / nb;
-        w.j0 = in - w.g * nb;
-        w.j1 = min(nb, w.j0 + (end - b));
+        w.g = in / nbl;
+        const int at = in - w.g * nbl, take = min(nbl - at, end - b), nb = nbl - kK8Lead;
+        const int unit0 = b - at + kK8Lead;    // the unit's first block
+        b += take;
+        w.j0 = max(at - kK8Lead, 0);
+        w.j1 = max(at + take - kK8Lead, 0);
+        if (w.j0 == w.j1) continue;            // nothing but (a part of) the lead
         if (w.j0 > 0) w.slot = 2 * cta;
         else if (w.j1 < nb) w.slot = 2 * cta + 1;
         if (w.j1 == nb) {  // the unit ends here: the job names the first CTA that has a part
           int4 y = no_job;
           if (w.j0 > 0) {
-            const int unit0 = b - w.j0, longer = more * (per + 1);
+            const int longer = more * (per + 1);
             y = make_int4(unit0 < longer ? unit0 / (per + 1) : more + (unit0 - longer) / per, cta, w.t0, w.g * 256 + w.rows);
           }
           if (!a.jobs_by_unit) {
@@ -722,7 +751,6 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             a.jobs[u_tile * a.h_kv + w.g] = y;
           }
         }
-        b += w.j1 - w.j0;
         ok = publish(w);
       }
       if (!a.jobs_by_unit) {
