@@ -908,9 +908,12 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     int n_slice = 0, n_all = 0;                // meetings so far
     // (bounded, unlike a named barrier: a warp that gives up holds none up)
-    auto meet = [&]() -> bool {                // the slice's warps have written what comes before
-      k8_arrive(&ctl.met[slice]);
-      return k8_wait(&ctl.met[slice], (uint32_t)n_slice++ & 1u, abort);
+    // the slice's warps have written what comes before
+    auto met_arrive = [&]() { k8_arrive(&ctl.met[slice]); };
+    auto met_wait = [&]() -> bool { return k8_wait(&ctl.met[slice], (uint32_t)n_slice++ & 1u, abort); };
+    auto meet = [&]() -> bool {
+      met_arrive();
+      return met_wait();
     };
     auto meet_all = [&]() -> bool {
       k8_arrive(&ctl.met[Sh::kSlices]);
@@ -959,8 +962,30 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       // the sums of the one before; nothing of the next is added to them before all warps are through
       Seg after;
       const bool more = next_seg(k, after);
+      if (more) load(after);
+      if (w.rows >= 0) {                       // (before the loads are waited for)
+        // the lanes' sums: half of the pairs go to each half of the lanes, and so on; in the end lane
+        // 32 / kFold i has pair i (of kFold pairs, those past kPer zeros)
+        constexpr int kFold = kPer <= 8 ? 8 : 16;
+        float y[kFold];
+#pragma unroll
+        for (int p = 0; p < kFold; ++p) y[p] = p < kPer ? l[p] : 0.f;
+#pragma unroll
+        for (int d = 16, n = kFold / 2; n > 0; d >>= 1, n >>= 1) {
+          const bool up = (lane & d) != 0;
+#pragma unroll
+          for (int p = 0; p < n; ++p) {
+            const float give = up ? y[p] : y[p + n], keep = up ? y[p + n] : y[p];
+            y[p] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+          }
+        }
+#pragma unroll
+        for (int d = 16 / kFold; d > 0; d >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], d);
+        const int pair = lane / (32 / kFold);
+        if (lane % (32 / kFold) == 0 && pair < kPer) ctl.wsum[warp][pair] = y[0];
+        met_arrive();
+      }
       if (more) {
-        load(after);
         const int pairs = after.rows * a.group;
         sc = k8_scales(a, k8_slot<kWindow, false>(a, after, entry(after, after.j0), f0), after.g);
         // q: a warp for a pair, two parts
@@ -1026,28 +1051,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       }
       if (w.rows >= 0) {
         // ---- outputs: a thread for a column of O ---------------------------------------------
-        {
-          // the lanes' sums: half of the pairs go to each half of the lanes, and so on; in the end lane
-          // 32 / kFold i has pair i (of kFold pairs, those past kPer zeros)
-          constexpr int kFold = kPer <= 8 ? 8 : 16;
-          float y[kFold];
-#pragma unroll
-          for (int p = 0; p < kFold; ++p) y[p] = p < kPer ? l[p] : 0.f;
-#pragma unroll
-          for (int d = 16, n = kFold / 2; n > 0; d >>= 1, n >>= 1) {
-            const bool up = (lane & d) != 0;
-#pragma unroll
-            for (int p = 0; p < n; ++p) {
-              const float give = up ? y[p] : y[p + n], keep = up ? y[p + n] : y[p];
-              y[p] = keep + __shfl_xor_sync(0xffffffffu, give, d);
-            }
-          }
-#pragma unroll
-          for (int d = 16 / kFold; d > 0; d >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], d);
-          const int pair = lane / (32 / kFold);
-          if (lane % (32 / kFold) == 0 && pair < kPer) ctl.wsum[warp][pair] = y[0];
-        }
-        ok = meet() && (nb == 0 || k8_wait(&ctl.pv_done[(x - 1) & 1], (uint32_t)((x - 1) >> 1) & 1u, abort));
+        ok = met_wait() && (nb == 0 || k8_wait(&ctl.pv_done[(x - 1) & 1], (uint32_t)((x - 1) >> 1) & 1u, abort));
         if (!ok) break;
         __syncwarp();
         tc_fence_after();
@@ -1458,64 +1462,76 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int n) {
   __shared__ float s_m[kMany ? G : 1], s_l[kMany ? G : 1], s_o[kMany ? G : 1][64];
   const int grp = threadIdx.x / kCols;
   const int p = kMany ? blockIdx.y : blockIdx.y * G + grp, d = blockIdx.z * kCols + threadIdx.x % kCols;
-  pdl_wait_primary();
-  const int4 job = ld_in(a.jobs + blockIdx.x);
-  const int k = job.y;
-  if (job.x < 0 || p >= (job.w & 255) * a.group) return;  // (with kMany the whole CTA)
   const float ninf = -__int_as_float(0x7f800000);
-  // the first part begins the unit (its CTA's second slot), the others come from within it
-  auto part = [&](int c) -> const float* {
-    return a.part + ((int64_t)(2 * c + (c == job.x ? 1 : 0)) * n + p) * (D + 4);
-  };
-  float m = ninf, l = 0.f, o = 0.f;
-  auto add = [&](float ms, float ls, float os) {  // with M at least ms
-    const float f = ms == ninf ? 0.f : ka_ex2(ms - m);
-    l += ms == ninf ? ls : f * ls;  // without a weight (or with NaN only) M = -inf
-    o = fmaf(f, os, o);
-  };
-  constexpr int kStep = kMany ? G : 1, kU = 4;
-  for (int c0 = job.x + (kMany ? grp : 0); c0 <= k; c0 += kU * kStep) {
-    float ms[kU], ls[kU], os[kU];  // on the way together
+  // A first pass of one warp loads and stores nothing: it runs beside the kernel before, and brings
+  // the instructions of the second.
+#pragma unroll 1
+  for (bool live = threadIdx.x >= 32;; live = true) {
+    if (live) pdl_wait_primary();
+    int4 job = make_int4(0, 0, 0, 1);
+    if (live) job = ld_in(a.jobs + blockIdx.x);
+    const int k = job.y;
+    if (job.x < 0 || (live && p >= (job.w & 255) * a.group)) return;  // (with kMany the whole CTA)
+    // the first part begins the unit (its CTA's second slot), the others come from within it
+    auto part = [&](int c) -> const float* {
+      return a.part + ((int64_t)(2 * c + (c == job.x ? 1 : 0)) * n + p) * (D + 4);
+    };
+    float m = ninf, l = 0.f, o = 0.f;
+    auto add = [&](float ms, float ls, float os) {  // with M at least ms
+      const float f = ms == ninf ? 0.f : ka_ex2(ms - m);
+      l += ms == ninf ? ls : f * ls;  // without a weight (or with NaN only) M = -inf
+      o = fmaf(f, os, o);
+    };
+    constexpr int kStep = kMany ? G : 1, kU = 4;
+#pragma unroll 1
+    for (int c0 = job.x + (kMany ? grp : 0); c0 <= k; c0 += kU * kStep) {
+      float2 ml[kU];
+      float os[kU];  // on the way together
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const float* pp = part(min(c0 + i * kStep, k));
-      const float2 y = ld_in(reinterpret_cast<const float2*>(pp + D));
-      ms[i] = y.x;
-      ls[i] = y.y;
-      os[i] = ld_in(pp + d);
+      for (int i = 0; i < kU; ++i) {
+        const float* pp = part(min(c0 + i * kStep, k));
+        ml[i] = live ? ld_in(reinterpret_cast<const float2*>(pp + D)) : make_float2(0.f, 1.f);
+        os[i] = live ? ld_in(pp + d) : 0.f;
+      }
+      float mn = m;
+#pragma unroll
+      for (int i = 0; i < kU; ++i) mn = fmaxf(mn, c0 + i * kStep <= k ? ml[i].x : ninf);
+      const float g = m == ninf ? 1.f : ka_ex2(m - mn);  // (nothing or a NaN yet)
+      l *= g;
+      o *= g;
+      m = mn;
+#pragma unroll
+      for (int i = 0; i < kU; ++i)
+        if (c0 + i * kStep <= k) add(ml[i].x, ml[i].y, os[i]);
     }
-    float mn = m;
+    if constexpr (kMany) {
+      const int col = threadIdx.x % 64;
+      if (live) {
+        s_o[grp][col] = o;
+        if (col == 0) {
+          s_m[grp] = m;
+          s_l[grp] = l;
+        }
+        __syncthreads();
+        if (grp != 0) return;
+      }
 #pragma unroll
-    for (int i = 0; i < kU; ++i) mn = fmaxf(mn, c0 + i * kStep <= k ? ms[i] : ninf);
-    const float g = m == ninf ? 1.f : ka_ex2(m - mn);  // (nothing or a NaN yet)
-    l *= g;
-    o *= g;
-    m = mn;
+      for (int i = 1; i < G; ++i) m = fmaxf(m, s_m[i]);
+      l = o = 0.f;
 #pragma unroll
-    for (int i = 0; i < kU; ++i)
-      if (c0 + i * kStep <= k) add(ms[i], ls[i], os[i]);
-  }
-  if constexpr (kMany) {
-    const int col = threadIdx.x % 64;
-    s_o[grp][col] = o;
-    if (col == 0) {
-      s_m[grp] = m;
-      s_l[grp] = l;
+      for (int i = 0; i < G; ++i) add(s_m[i], s_l[i], s_o[i][col]);
     }
-    __syncthreads();
-    if (grp != 0) return;
-#pragma unroll
-    for (int i = 1; i < G; ++i) m = fmaxf(m, s_m[i]);
-    l = o = 0.f;
-#pragma unroll
-    for (int i = 0; i < G; ++i) add(s_m[i], s_l[i], s_o[i][col]);
+    const int row = (int)(p * a.group_inv >> 16);
+    const int64_t hq = (int64_t)(job.z + row) * a.h_q + (int64_t)(job.w >> 8) * a.group + (p - row * a.group);
+    const float r = l == 0.f ? 0.f : o / l;
+    const float lse = k8_lse(m, l);
+    if (live) {
+      if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[hq * D + d] = __float2bfloat16_rn(r);
+      else static_cast<float*>(a.out)[hq * D + d] = r;
+      if (d == 0 && a.lse != nullptr) a.lse[hq] = lse;
+      return;
+    }
   }
-  const int row = (int)(p * a.group_inv >> 16);
-  const int64_t hq = (int64_t)(job.z + row) * a.h_q + (int64_t)(job.w >> 8) * a.group + (p - row * a.group);
-  const float r = l == 0.f ? 0.f : o / l;
-  if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[hq * D + d] = __float2bfloat16_rn(r);
-  else static_cast<float*>(a.out)[hq * D + d] = r;
-  if (d == 0 && a.lse != nullptr) a.lse[hq] = k8_lse(m, l);
 }
 
 }  // namespace qsa
