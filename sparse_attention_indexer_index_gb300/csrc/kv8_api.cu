@@ -176,6 +176,7 @@ qsa_status launch_k8(const K8Form& f, Kv8AttnArgs& a, int d, void* workspace, cu
     const int* at_once = dev->clusters[f.kind][d == 256];
     while (a.cluster < kKaMaxCluster && f.units <= at_once[2 * a.cluster] && f.blocks >= 2 * a.cluster) a.cluster *= 2;
     grid = slots * a.cluster;
+    a.n_units = (int32_t)f.units;
   }
   a.cluster_shift = log2_of(a.cluster);
   a.group_inv = (65536 + a.group - 1) / a.group;  // exact for pairs below 4,096

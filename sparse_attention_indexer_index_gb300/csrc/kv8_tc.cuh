@@ -82,6 +82,7 @@ struct Kv8AttnArgs : KvAttnArgs {
   int32_t rows;              // R: rows per tile
   int32_t tile_slots;        // tiles at most
   int32_t mode;              // how the work is dealt
+  int32_t n_units;           // (tile, KV head) pairs, for requests of equal length
   int4* jobs;                // [units or CTAs]: what kv8_merge_kernel joins: first CTA (-1: nothing), last CTA, first
                              // row, KV head * 256 + rows
   int32_t jobs_by_unit;      // a job for every unit, or (more units than CTAs) for the CTA where one ends
@@ -548,6 +549,13 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   volatile int* abort = &ctl.abort;
   const float ninf = -__int_as_float(0x7f800000);
 
+  // Tiles past those of requests of equal length are there only if lengths differ: their clusters
+  // look first, as the SMs are handed on from one to the next of them.
+  if (kShared && a.mode == kK8Cluster && (int)(blockIdx.x >> a.cluster_shift) >= a.n_units) {
+    pdl_wait_primary();
+    int number;
+    if (k8_find(a, (int)(blockIdx.x >> a.cluster_shift) / a.h_kv, number) < 0) return;
+  }
   if (warp == Sh::kSoft) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl.tmem))
                  : "memory");
@@ -1141,17 +1149,21 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
               float v[4][V * 4], m[4], l4[4];
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                const int from_c = min(c0 + c, C - 1);
-                const uint32_t from = Sh::kPull ? map_shared_rank(join + p * Sh::kJoin, (uint32_t)from_c)
-                                                : smem_u32(join + (from_c * own + (p >> a.cluster_shift)) * Sh::kJoin);
+                m[c] = ninf;
+                l4[c] = 0.f;
+#pragma unroll
+                for (int y = 0; y < V * 4; ++y) v[c][y] = 0.f;
+                if (c0 + c >= C) continue;
+                const uint32_t from = Sh::kPull ? map_shared_rank(join + p * Sh::kJoin, (uint32_t)(c0 + c))
+                                                : smem_u32(join + ((c0 + c) * own + (p >> a.cluster_shift)) * Sh::kJoin);
 #pragma unroll
                 for (int y = 0; y < V; ++y) {
                   const float4 f = ld_cluster_f4(from + 4 * (col + y * 128));
                   v[c][y * 4] = f.x; v[c][y * 4 + 1] = f.y; v[c][y * 4 + 2] = f.z; v[c][y * 4 + 3] = f.w;
                 }
                 const float2 f = ld_cluster_f2(from + 4 * D);
-                m[c] = c0 + c < C ? f.x : ninf;
-                l4[c] = c0 + c < C ? f.y : 0.f;
+                m[c] = f.x;
+                l4[c] = f.y;
               }
               const float top = fmaxf(M, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
               const float fm = M == ninf ? 1.f : ka_ex2(M - top);
