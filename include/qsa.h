@@ -464,17 +464,23 @@ qsa_status qsa_window_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
  *
  * qsa_sparse_attn_fp8 is qsa_sparse_attn_fp4 on this cache (h_q / h_kv up to
  * 16 for both head dims), qsa_window_attn_fp8 qsa_window_attn_fp4, with their
- * arguments, outputs, masks and faults.  The cache's values enter the dot
- * products and the value sums exactly; the softmax statistics are FP32 and
- * the weights keep 22 significant bits (tiny ones less: weight times V scale
- * is held to 2^-35 of the row's largest).
+ * arguments, outputs, masks and faults.  The cache's values enter both products
+ * exactly, which are summed in FP32, as the softmax statistics are.  q and the
+ * weights enter as sums of e4m3 numbers: a component of q is off by at most
+ * 2^-22 of its (row, head)'s largest one, a weight times its V scale by 2^-16
+ * of itself (small ones by 2^-28 of the row's largest); where rows of a request
+ * share tiles of more than 8 (row, query head) pairs, whose outputs are BF16,
+ * by 2^-12 (2^-23).
  *   max_rows_per_req  host upper bound of the rows of any one request: if it is
- *              above 1, rows of a request share what they read, up to 64 (row,
+ *              above 1, rows of a request share what they read, up to 48 (row,
  *              query head) pairs at a time.  It never changes which positions
  *              count.  Requests of very many rows (chunks, prompts) take less
  *              on rows read back (qsa_gather_kv_fp8) and qsa_window_attn.
- *   workspace  as the matching *_workspace_size(): 0 except for few rows with
- *              many entries.  Calls that may overlap on the GPU need one each.
+ *   workspace  as the matching *_workspace_size(): 0 where a (row, KV head)'s
+ *              entries are read by one CTA or one cluster, else room for what
+ *              152 CTAs have of the sums (2.5 MB for 8 pairs of head_dim 256).
+ *              Nothing has to be in it.  Calls that may overlap on the GPU need
+ *              one each.
  * ------------------------------------------------------------------- */
 qsa_status qsa_append_kv_fp8(const void* k_new, const void* v_new, int64_t ld_k, int64_t ld_v, int32_t n_tok,
                              int32_t h_kv, int32_t head_dim, const int32_t* req_tok_start,

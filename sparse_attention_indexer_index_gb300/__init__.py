@@ -625,7 +625,7 @@ def _indexer_select_call(fn, key_ptrs, pool_rows, q, req_row_start, row_len, pag
     return out
 
 
-# ----------------------------------------------------------------- 4-bit and 8-bit KV caches, window attention, paging
+# ----------------------------------------------------------------- 4-bit KV cache, window attention
 # The checks of these calls run in two forms: one pass over cheap attributes,
 # and only when that finds something (_explain) the one that says what.  A
 # decode step's calls cost the host a few microseconds each, mostly these.
@@ -713,18 +713,6 @@ def _launch_ws(fn, dev, stream, size_fn, size_args, workspace, *args):
         torch = _torch()
         workspace = _empty(_call(size_fn, *size_args), torch.uint8, torch.device("cuda", dev), stream)
     _check(fn, _launch(fn, dev, stream, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size()))
-
-
-def _launch_ws8(fn, device, stream, size_args, workspace, *args):
-    """_launch of a call on the 8-bit cache: many need a workspace, so its
-    size is asked for first."""
-    if workspace is not None:
-        n = workspace.numel() * workspace.element_size()
-    else:
-        n = _call(fn + "_workspace_size", *size_args)
-        if n:
-            workspace = _empty((n,), _t()[3], device, stream)
-    _check(fn, _launch(fn, device.index, stream, *args, workspace.data_ptr() if n else None, n))
 
 
 def append_kv_fp4(k_new, v_new, req_tok_start, req_first_pos, k_codes, k_scales, v_codes, v_scales, page_table,
@@ -877,7 +865,7 @@ def window_attn_fp4(q, k_codes, k_scales, v_codes, v_scales, req_row_start, row_
 
 
 def _window_call(fn, cache_ptrs, scales, n_slots, h_kv, d, q, req_row_start, row_len, page_table, page_size, max_len,
-                 window, n_sink, scale, max_rows_per_req, out, lse, want_lse, workspace, stream, block=()):
+                 window, n_sink, scale, max_rows_per_req, out, lse, want_lse, workspace, stream):
     bf16, f32, i32, _, _ = _t()
     try:
         dev = q.get_device()
@@ -902,26 +890,101 @@ def _window_call(fn, cache_ptrs, scales, n_slots, h_kv, d, q, req_row_start, row
         lse = None
     elif lse is None:
         lse = _empty((n_rows, h_q), f32, q.device, stream)
-    sizes = (h_q, h_kv, d, max_len, window, n_sink)
-    args = (q.data_ptr(), q.stride(0) if n_rows > 1 else h_q * d, *cache_ptrs, n_slots, *block, n_req,
-            req_row_start.data_ptr(), n_rows, row_len.data_ptr(), max_len, max_rows_per_req, h_q, h_kv, d,
-            page_table.data_ptr(), ld_pt, page_size, window, n_sink, d ** -0.5 if scale is None else scale, *scales,
-            out.data_ptr(), _ptr(lse))
-    if block:  # the 8-bit cache
-        _launch_ws8(fn, q.device, stream, (n_rows, n_req, max_rows_per_req, *sizes), workspace, *args)
-    else:
-        _launch_ws(fn, dev, stream, "qsa_window_attn_workspace_size", (n_rows, *sizes), workspace, *args)
+    _launch_ws(fn, dev, stream, "qsa_window_attn_workspace_size",
+               (n_rows, h_q, h_kv, d, max_len, window, n_sink), workspace, q.data_ptr(),
+               q.stride(0) if n_rows > 1 else h_q * d, *cache_ptrs, n_slots, n_req, req_row_start.data_ptr(), n_rows,
+               row_len.data_ptr(), max_len, max_rows_per_req, h_q, h_kv, d, page_table.data_ptr(), ld_pt, page_size,
+               window, n_sink, d ** -0.5 if scale is None else scale, *scales, out.data_ptr(), _ptr(lse))
     return out, lse
 
 
-def _cache8_ok(dev, k_codes, k_scales, v_codes, v_scales):
-    """The 8-bit cache's arrays fit together: codes [n_slots][h_kv][d], scales
-    [n_slots / block][h_kv]; (ok, tokens to a scale)."""
-    n_slots, h_kv, _ = k_codes.shape
-    n_blk = k_scales.shape[0]
+# ----------------------------------------------------------------- 8-bit KV cache, paging
+# These calls say what their tensors have to be in one line.  Per tensor: ?
+# where it may be None; its type (u uint8, i int32, h bfloat16, f float32, all
+# contiguous; q bfloat16 rows [n][heads][head_dim] that may lie apart; w a
+# workspace of any type); a letter a dimension (the same letter is the same
+# size, X+ one more than X; @ any dimensions, the same again where it comes
+# back).  The answer is None, or the device, the letters' sizes in the order in
+# which they come (-1: only in tensors that were None) and each tensor's
+# address (None), for q followed by the rows' distance, for w by its bytes, for
+# the first @ by the number of elements.
+def _fit(spec, *tensors):
+    global _fit
+    _torch()
+    try:
+        from ._tensors import fit
+    except ImportError:
+        fit = _fit_py
+    _fit = fit
+    return fit(spec, *tensors)
+
+
+def _fit_py(spec, *tensors):
+    bf16, f32, i32, u8, _ = _t()
+    types = {"u": u8, "i": i32, "f": f32, "h": bf16, "q": bf16}
+    dims, out, dev, any_dims = {}, [], None, None
+    try:
+        for part, t in zip(spec.split(), tensors, strict=True):
+            optional, part = part[0] == "?", part.lstrip("?")
+            kind, names = part[0], part[1:]
+            if optional and t is None:
+                for c in names:
+                    if c.isalpha():
+                        dims.setdefault(c, -1)
+                out += [None, 0] if kind == "w" else [None]
+                continue
+            if dev is None:
+                dev = t.get_device()
+            if not t.is_cuda or t.get_device() != dev or (kind != "w" and t.dtype is not types[kind]):
+                return None
+            sizes, first = list(t.shape), False
+            if kind != "w":
+                want, j = [], 0
+                for c in names:
+                    if c == "@":
+                        if any_dims is None:
+                            any_dims, first = sizes, True
+                        want += any_dims
+                    elif c == "+":
+                        want[-1] += 1
+                    else:
+                        plus = names[j + 1:j + 2] == "+"
+                        if dims.get(c, -1) < 0:
+                            dims[c] = sizes[len(want)] - plus
+                        want.append(dims[c])
+                    j += 1
+                if want != sizes or min(dims.values(), default=0) < 0 and any(dims[c] < 0 for c in names if c.isalpha()):
+                    return None
+            if kind == "q":
+                if not _rows_ok(t, dev, bf16):
+                    return None
+                out += [t.data_ptr(), t.stride(0) if sizes[0] > 1 else sizes[1] * sizes[2]]
+                continue
+            if not t.is_contiguous():
+                return None
+            out.append(t.data_ptr())
+            if kind == "w":
+                out.append(t.numel() * t.element_size())
+            elif first:
+                out.append(t.numel())
+    except (AttributeError, IndexError):
+        return None
+    return (dev, *dims.values(), *out)
+
+
+def _block8(n_slots, n_blk):
+    """Tokens to a scale of the 8-bit cache (None: the arrays do not fit)."""
     block = n_slots // n_blk if n_blk else 4
-    return (_all(dev, _t()[3], k_codes, k_scales, v_codes, v_scales) and v_codes.shape == k_codes.shape
-            and k_scales.shape == (n_blk, h_kv) == v_scales.shape and n_blk * block == n_slots), block
+    return block if n_blk * block == n_slots else None
+
+
+def _launch8(fn, q, dev, stream, n_bytes, workspace, ws_bytes, *args):
+    """_launch of an attention call on the 8-bit cache, whose workspace, if
+    none was given, has n_bytes."""
+    if workspace is None and n_bytes:
+        ws = _empty((n_bytes,), _t()[3], q.device, stream)  # (lives until the call has been launched)
+        workspace, ws_bytes = ws.data_ptr(), n_bytes
+    _check(fn, _launch(fn, dev, stream, *args, workspace, ws_bytes))
 
 
 def _explain8(fn, first, k_codes, k_scales, v_codes, v_scales, **more):
@@ -939,58 +1002,37 @@ def append_kv_fp8(k_new, v_new, req_tok_start, req_first_pos, k_codes, k_scales,
     block that already holds earlier tokens keeps at least its scale, and they
     are rounded once more where it grows.  The rows may be columns of one
     projection's output.  Returns the four arrays."""
-    bf16, _, i32, _, _ = _t()
-    try:
-        dev = k_codes.get_device()
-        n_slots, h_kv, d = k_codes.shape
-        n_tok = k_new.shape[0]
-        n_req, ld_pt = page_table.shape
-        ok, block = _cache8_ok(dev, k_codes, k_scales, v_codes, v_scales)
-        ok = (ok and dev >= 0 and _all(dev, i32, req_tok_start, req_first_pos, page_table)
-              and _rows_ok(k_new, dev, bf16) and _rows_ok(v_new, dev, bf16)
-              and k_new.shape == (n_tok, h_kv, d) == v_new.shape
-              and req_tok_start.shape == (n_req + 1,) and req_first_pos.shape == (n_req,))
-    except (AttributeError, ValueError, IndexError):
-        ok = False
-    if not ok:
+    x = _fit("iRP iR+ iR uSHD uBH uSHD uBH qTHD qTHD", page_table, req_tok_start, req_first_pos, k_codes, k_scales,
+             v_codes, v_scales, k_new, v_new)
+    block = _block8(x[3], x[6]) if x else None
+    if block is None:
         _explain8("append_kv_fp8", k_codes, k_codes, k_scales, v_codes, v_scales,
                   rows=((k_new, "k_new"), (v_new, "v_new")),
                   i32=((req_tok_start, "req_tok_start", 1), (req_first_pos, "req_first_pos", 1),
                        (page_table, "page_table", 2)))
-    row = h_kv * d
-    _check("qsa_append_kv_fp8", _launch(
-        "qsa_append_kv_fp8", dev, stream, k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0) if n_tok > 1 else row,
-        v_new.stride(0) if n_tok > 1 else row, n_tok, h_kv, d, req_tok_start.data_ptr(), req_first_pos.data_ptr(),
-        n_req, page_table.data_ptr(), ld_pt, page_size, block, k_codes.data_ptr(), k_scales.data_ptr(),
-        v_codes.data_ptr(), v_scales.data_ptr(), n_slots))
+    dev, n_req, ld_pt, n_slots, h_kv, d, _, n_tok, pt, start, first, kc, ks, vc, vs, k, ld_k, v, ld_v = x
+    _check("qsa_append_kv_fp8", _launch("qsa_append_kv_fp8", dev, stream, k, v, ld_k, ld_v, n_tok, h_kv, d, start, first,
+                                        n_req, pt, ld_pt, page_size, block, kc, ks, vc, vs, n_slots))
     return k_codes, k_scales, v_codes, v_scales
 
 
 def gather_kv_fp8(k_codes, k_scales, v_codes, v_scales, slots, k_out=None, v_out=None, stream=None):
     """Reads the rows at slots (int32, any shape) back from the 8-bit cache:
     (k, v) [*slots.shape][h_kv][head_dim] bf16; a negative slot gives zeros."""
-    bf16, _, i32, _, _ = _t()
-    try:
-        dev = k_codes.get_device()
-        n_slots, h_kv, d = k_codes.shape
-        out_shape = (*slots.shape, h_kv, d)
-        ok, block = _cache8_ok(dev, k_codes, k_scales, v_codes, v_scales)
-        ok = (ok and dev >= 0 and _all(dev, i32, slots)
-              and (k_out is None or _all(dev, bf16, k_out) and k_out.shape == out_shape)
-              and (v_out is None or _all(dev, bf16, v_out) and v_out.shape == out_shape))
-    except (AttributeError, ValueError, IndexError):
-        ok = False
-    if not ok:
+    x = _fit("uSHD uBH uSHD uBH i@ ?h@HD ?h@HD", k_codes, k_scales, v_codes, v_scales, slots, k_out, v_out)
+    block = _block8(x[1], x[4]) if x else None
+    if block is None:
         _explain8("gather_kv_fp8", k_codes, k_codes, k_scales, v_codes, v_scales, i32=((slots, "slots", None),),
                   bf16=((k_out, "k_out", None), (v_out, "v_out", None)))
+    dev, n_slots, h_kv, d, _, kc, ks, vc, vs, sl, n, ko, vo = x
     if k_out is None:
-        k_out = _empty(out_shape, bf16, slots.device, stream)
+        k_out = _empty((*slots.shape, h_kv, d), _t()[0], slots.device, stream)
+        ko = k_out.data_ptr()
     if v_out is None:
-        v_out = _empty(out_shape, bf16, slots.device, stream)
-    _check("qsa_gather_kv_fp8", _launch(
-        "qsa_gather_kv_fp8", dev, stream, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-        v_scales.data_ptr(), n_slots, h_kv, d, block, slots.data_ptr(), slots.numel(), k_out.data_ptr(),
-        v_out.data_ptr()))
+        v_out = _empty((*slots.shape, h_kv, d), _t()[0], slots.device, stream)
+        vo = v_out.data_ptr()
+    _check("qsa_gather_kv_fp8", _launch("qsa_gather_kv_fp8", dev, stream, kc, ks, vc, vs, n_slots, h_kv, d, block, sl, n,
+                                        ko, vo))
     return k_out, v_out
 
 
@@ -999,34 +1041,27 @@ def sparse_attn_fp8(q, k_codes, k_scales, v_codes, v_scales, slots, scale=None, 
     """sparse_attn over the 8-bit cache: softmax attention of q
     [n_rows][h_q][head_dim] bf16 over the rows at slots [n_rows][w] (int32,
     -1 skipped).  Returns (out float32, lse [n_rows][h_q] or None)."""
-    bf16, f32, i32, _, _ = _t()
-    try:
-        dev = q.get_device()
-        n_rows, h_q, d = q.shape
-        n_slots, h_kv, w = k_codes.shape
-        rows, width = slots.shape
-        ok, block = _cache8_ok(dev, k_codes, k_scales, v_codes, v_scales)
-        ok = (ok and dev >= 0 and _rows_ok(q, dev, bf16) and _all(dev, i32, slots) and d == w and rows == n_rows
-              and (out is None or _all(dev, f32, out) and out.shape == (n_rows, h_q, d))
-              and (lse is None or _all(dev, f32, lse) and lse.shape == (n_rows, h_q))
-              and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous()))
-    except (AttributeError, ValueError, IndexError):
-        ok = False
-    if not ok:
+    x = _fit("qNQD uSKD uBK uSKD uBK iNW ?fNQD ?fNQ ?w", q, k_codes, k_scales, v_codes, v_scales, slots, out, lse,
+             workspace)
+    block = _block8(x[4], x[6]) if x else None
+    if block is None:
         _explain8("sparse_attn_fp8", q, k_codes, k_scales, v_codes, v_scales, rows=((q, "q"),),
                   i32=((slots, "slots", 2),), f32=((out, "out", 3), (lse, "lse", 2)))
+    dev, n_rows, h_q, d, n_slots, h_kv, _, width, qp, ld_q, kc, ks, vc, vs, sl, op, lp, ws, ws_bytes = x
     if n_idx is None:
         n_idx = width
     if out is None:
-        out = _empty((n_rows, h_q, d), f32, q.device, stream)
+        out = _empty((n_rows, h_q, d), _t()[1], q.device, stream)
+        op = out.data_ptr()
     if not want_lse:
-        lse = None
+        lse = lp = None
     elif lse is None:
-        lse = _empty((n_rows, h_q), f32, q.device, stream)
-    _launch_ws8("qsa_sparse_attn_fp8", q.device, stream, (n_rows, h_q, h_kv, d, n_idx), workspace, q.data_ptr(),
-                q.stride(0) if n_rows > 1 else h_q * d, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                v_scales.data_ptr(), n_slots, block, n_rows, h_q, h_kv, d, slots.data_ptr(), width, n_idx,
-                d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse))
+        lse = _empty((n_rows, h_q), _t()[1], q.device, stream)
+        lp = lse.data_ptr()
+    _launch8("qsa_sparse_attn_fp8", q, dev, stream,
+             _call("qsa_sparse_attn_fp8_workspace_size", n_rows, h_q, h_kv, d, n_idx) if ws is None else 0, ws, ws_bytes,
+             qp, ld_q, kc, ks, vc, vs, n_slots, block, n_rows, h_q, h_kv, d, sl, width, n_idx,
+             d ** -0.5 if scale is None else scale, op, lp)
     return out, lse
 
 
@@ -1037,17 +1072,31 @@ def window_attn_fp8(q, k_codes, k_scales, v_codes, v_scales, req_row_start, row_
     attention).  max_rows_per_req (default: n_rows) bounds the rows of one
     request: above 1, a request's rows share what they read.  For whole prompts
     read the window back with gather_kv_fp8 and use window_attn."""
-    try:
-        n_slots, h_kv, d = k_codes.shape
-        ok, block = _cache8_ok(q.get_device(), k_codes, k_scales, v_codes, v_scales)
-    except (AttributeError, ValueError, IndexError):
-        ok = False
-    if not ok:
-        _explain8("window_attn_fp8", q, k_codes, k_scales, v_codes, v_scales)
-    return _window_call("qsa_window_attn_fp8",
-                        (k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr()), (), n_slots,
-                        h_kv, d, q, req_row_start, row_len, page_table, page_size, max_len, window, n_sink, scale,
-                        max_rows_per_req, out, lse, want_lse, workspace, stream, (block,))
+    x = _fit("qNQD uSKD uBK uSKD uBK iRP iR+ iN ?hNQD ?fNQ ?w", q, k_codes, k_scales, v_codes, v_scales, page_table,
+             req_row_start, row_len, out, lse, workspace)
+    block = _block8(x[4], x[6]) if x else None
+    if block is None:
+        _explain8("window_attn_fp8", q, k_codes, k_scales, v_codes, v_scales, rows=((q, "q"),),
+                  i32=((req_row_start, "req_row_start", 1), (row_len, "row_len", 1), (page_table, "page_table", 2)),
+                  bf16=((out, "out", 3),), f32=((lse, "lse", 2),))
+    dev, n_rows, h_q, d, n_slots, h_kv, _, n_req, ld_pt, qp, ld_q, kc, ks, vc, vs, pt, start, length, op, lp, ws, \
+        ws_bytes = x
+    if max_rows_per_req is None:
+        max_rows_per_req = n_rows
+    if out is None:
+        out = _empty((n_rows, h_q, d), _t()[0], q.device, stream)
+        op = out.data_ptr()
+    if not want_lse:
+        lse = lp = None
+    elif lse is None:
+        lse = _empty((n_rows, h_q), _t()[1], q.device, stream)
+        lp = lse.data_ptr()
+    _launch8("qsa_window_attn_fp8", q, dev, stream,
+             _call("qsa_window_attn_fp8_workspace_size", n_rows, n_req, max_rows_per_req, h_q, h_kv, d, max_len, window,
+                   n_sink) if ws is None else 0, ws, ws_bytes,
+             qp, ld_q, kc, ks, vc, vs, n_slots, block, n_req, start, n_rows, length, max_len, max_rows_per_req, h_q, h_kv,
+             d, pt, ld_pt, page_size, window, n_sink, d ** -0.5 if scale is None else scale, op, lp)
+    return out, lse
 
 
 def plan_step(ctx_len, n_new, page_table, page_size, free_pages, n_free, n_tok, req_row_start=None, new_len=None,
@@ -1060,27 +1109,22 @@ def plan_step(ctx_len, n_new, page_table, page_size, free_pages, n_free, n_tok, 
     padding (length 0, request and slot -1).  Returns (req_row_start [n_req+1],
     new_len [n_req], row_len, row_req, slots [n_tok]).  A request that does not
     fit is refused (new_len = ctx_len; see qsa_plan_step)."""
-    _, _, i32, _, _ = _t()
-    names = ("req_row_start", "new_len", "row_len", "row_req", "slots")
-    outs = [req_row_start, new_len, row_len, row_req, slots]
-    try:
-        dev = page_table.get_device()
-        n_req, ld_pt = page_table.shape
-        sizes = (n_req + 1, n_req, n_tok, n_tok, n_tok)
-        ok = (dev >= 0 and _all(dev, i32, ctx_len, n_new, page_table, free_pages, n_free)
-              and ctx_len.shape == (n_req,) == n_new.shape and free_pages.dim() == 1 and n_free.numel() == 1
-              and all(o is None or _all(dev, i32, o) and o.shape == (n,) for o, n in zip(outs, sizes)))
-    except (AttributeError, ValueError, IndexError):
-        ok = False
-    if not ok:
+    x = _fit("iRP iR iR iF iE ?iR+ ?iR ?iT ?iT ?iT", page_table, ctx_len, n_new, free_pages, n_free, req_row_start,
+             new_len, row_len, row_req, slots)
+    if x is None or x[4] != 1 or x[5] not in (-1, n_tok):
+        outs = ((req_row_start, "req_row_start", 1), (new_len, "new_len", 1), (row_len, "row_len", 1),
+                (row_req, "row_req", 1), (slots, "slots", 1))
         _explain("plan_step", page_table, i32=((ctx_len, "ctx_len", 1), (n_new, "n_new", 1),
                                                (page_table, "page_table", 2), (free_pages, "free_pages", 1),
-                                               (n_free, "n_free", 1), *((o, n, 1) for o, n in zip(outs, names))))
-    outs = [_empty((n,), i32, page_table.device, stream) if o is None else o for o, n in zip(outs, sizes)]
-    _check("qsa_plan_step", _launch(
-        "qsa_plan_step", dev, stream, ctx_len.data_ptr(), n_new.data_ptr(), n_req, page_table.data_ptr(), ld_pt,
-        page_size, free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(), n_tok, outs[0].data_ptr(),
-        outs[1].data_ptr(), outs[2].data_ptr(), outs[3].data_ptr(), outs[4].data_ptr()))
+                                               (n_free, "n_free", 1), *outs))
+    dev, n_req, ld_pt, n_pool, _, _, pt, ctx, new, pool, free, *ptrs = x
+    outs = [req_row_start, new_len, row_len, row_req, slots]
+    for i, n in enumerate((n_req + 1, n_req, n_tok, n_tok, n_tok)):
+        if outs[i] is None:
+            outs[i] = _empty((n,), _t()[2], page_table.device, stream)
+            ptrs[i] = outs[i].data_ptr()
+    _check("qsa_plan_step", _launch("qsa_plan_step", dev, stream, ctx, new, n_req, pt, ld_pt, page_size, pool, n_pool,
+                                    free, n_tok, *ptrs))
     return tuple(outs)
 
 
@@ -1089,19 +1133,11 @@ def release_pages(page_table, from_page, to_page, free_pages, n_free, stream=Non
     int32) go to the end of the list free_pages (n_free[0] pages long, which
     grows) and become -1; negative entries are skipped.  Returns (page_table,
     free_pages, n_free), updated in place."""
-    _, _, i32, _, _ = _t()
-    try:
-        dev = page_table.get_device()
-        n_req, ld_pt = page_table.shape
-        ok = (dev >= 0 and _all(dev, i32, page_table, from_page, to_page, free_pages, n_free)
-              and from_page.shape == (n_req,) == to_page.shape and free_pages.dim() == 1 and n_free.numel() == 1)
-    except (AttributeError, ValueError, IndexError):
-        ok = False
-    if not ok:
+    x = _fit("iRP iR iR iF iE", page_table, from_page, to_page, free_pages, n_free)
+    if x is None or x[4] != 1:
         _explain("release_pages", page_table, i32=((page_table, "page_table", 2), (from_page, "from_page", 1),
                                                    (to_page, "to_page", 1), (free_pages, "free_pages", 1),
                                                    (n_free, "n_free", 1)))
-    _check("qsa_release_pages", _launch(
-        "qsa_release_pages", dev, stream, page_table.data_ptr(), ld_pt, n_req, from_page.data_ptr(),
-        to_page.data_ptr(), free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr()))
+    dev, n_req, ld_pt, n_pool, _, pt, lo, hi, pool, free = x
+    _check("qsa_release_pages", _launch("qsa_release_pages", dev, stream, pt, ld_pt, n_req, lo, hi, pool, n_pool, free))
     return page_table, free_pages, n_free

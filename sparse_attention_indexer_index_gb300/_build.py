@@ -27,9 +27,12 @@ def _deps():
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every .cu under csrc/ into libqsa.so next to this file, then
-    the CPython entry points of the per-step calls (build_fastcall)."""
+    the CPython entry points of the per-step calls (build_fastcall); beside
+    both the checks of their tensors (build_tensors)."""
+    tensors = _start_tensors(force)
     _build_lib(force, verbose)
     build_fastcall(force)
+    _finish_tensors(tensors)
     return LIB_PATH
 
 
@@ -91,3 +94,55 @@ def build_fastcall(force: bool = False) -> str | None:
         return None
     os.replace(tmp, out)
     return out
+
+
+TENSORS_SRC = os.path.join(_HERE, "_tensors.cpp")
+
+
+def tensors_path() -> str:
+    import sysconfig
+    return os.path.join(_HERE, "_tensors" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+def _start_tensors(force: bool):
+    """Starts the compiler on _tensors.cpp: (process, its output), or None
+    where there is nothing to do or no way (the Python form is used then)."""
+    import importlib.util
+    import shutil
+    import sysconfig
+    out = tensors_path()
+    inc = sysconfig.get_paths().get("include", "")
+    cxx = os.environ.get("CXX", "g++")
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations or shutil.which(cxx) is None:
+        return None
+    torch_dir = spec.submodule_search_locations[0]
+    headers = os.path.join(torch_dir, "include")
+    if not inc or not os.path.exists(os.path.join(inc, "Python.h")) or not os.path.isdir(headers):
+        return None
+    deps = [TENSORS_SRC, os.path.join(torch_dir, "version.py")]
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(p) for p in deps):
+        return None
+    tmp = out + f".{os.getpid()}.tmp"
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-I", inc, "-isystem", headers, "-isystem",
+           os.path.join(headers, "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+           TENSORS_SRC, "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    return subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=subprocess.PIPE, text=True), tmp
+
+
+def _finish_tensors(started) -> str | None:
+    if started is None:
+        return None
+    run, tmp = started
+    run.communicate()
+    if run.returncode != 0:
+        return None
+    os.replace(tmp, tensors_path())
+    return tensors_path()
+
+
+def build_tensors(force: bool = False) -> str | None:
+    """Compile the checks of a call's tensors (_tensors.cpp) against the
+    installed torch; None where its headers or a compiler are missing."""
+    return _finish_tensors(_start_tensors(force))
