@@ -589,7 +589,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (a.mode == kK8Shares) pdl_launch_dependents();  // the merge may take its place beside this kernel; it waits for its end
+  pdl_launch_dependents();  // the next kernel (the merge) may take its place beside this one; it waits for its end
   pdl_wait_primary();
   const uint32_t tmem = ctl.tmem;
   const int C = a.cluster, rank = C > 1 ? (int)cluster_ctarank() : 0;
@@ -1475,6 +1475,7 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int n) {
   const int grp = threadIdx.x / kCols;
   const int p = kMany ? blockIdx.y : blockIdx.y * G + grp, d = blockIdx.z * kCols + threadIdx.x % kCols;
   const float ninf = -__int_as_float(0x7f800000);
+  pdl_launch_dependents();
   // A first pass of one warp loads and stores nothing: it runs beside the kernel before, and brings
   // the instructions of the second.
 #pragma unroll 1
