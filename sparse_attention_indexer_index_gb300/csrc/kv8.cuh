@@ -84,6 +84,8 @@ append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {
   const int64_t ld = is_v ? a.ld_v : a.ld_k;
   uint8_t* codes = is_v ? a.v_codes : a.k_codes;
   uint8_t* scales = is_v ? a.v_scales : a.k_scales;
+  // the thread's first row and column of a unit; the next piece is `step` rows on
+  const int row0 = tid >> a.per_shift, col = (tid & (per - 1)) * 8, step = kKv8Threads >> a.per_shift;
   int turn = 0;
   while (t < stop && r < a.n_req) {
     const int s0 = ld_in(a.req_tok_start + r), s1 = min(ld_in(a.req_tok_start + r + 1), a.n_tok);
@@ -105,17 +107,13 @@ append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {
     const int pi = lo / a.page_size;
     const int64_t page = pi < a.ld_pt ? ld_in(a.page_table + (int64_t)r * a.ld_pt + pi) : -1;
     // the unit's values, rows t0 .. t - 1, on the way beside the page and the block's scale
-    const int pieces = (t - t0) * per;
+    const int rows = t - t0;
     uint4 x[kPieces];
-    __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
+    const uint16_t* from = src + (int64_t)(t0 + row0) * ld + (int64_t)h * a.d + col;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int p = i * kKv8Threads + tid;
+    for (int i = 0; i < kPieces; ++i, from += (int64_t)step * ld) {
       x[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (p < pieces) {
-        const int row = p >> a.per_shift;
-        x[i] = ld_stream_16(src + (int64_t)(t0 + row) * ld + (int64_t)h * a.d + (p & (per - 1)) * 8);
-      }
+      if (row0 + i * step < rows) x[i] = ld_stream_16(from);
     }
     const int64_t slot = page * a.page_size + (lo - pi * a.page_size);
     if (page < 0 || slot + B > a.n_slots) {
@@ -124,11 +122,12 @@ append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {
     }
     const int64_t at = (slot >> a.block_shift) * a.h_kv + h;
     const int old = in != 0 ? (int)ld_in(scales + at) : 0;  // the scale of the block's earlier tokens
+    __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const uint32_t w[4] = {x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu, x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu};
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[j]));  // not a NaN
+      for (int j = 0; j < 4; ++j) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));  // not a NaN
     }
     auto reduce = [&](uint32_t v) -> uint32_t {
       v = __reduce_max_sync(0xffffffffu, v);
@@ -143,42 +142,38 @@ append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {
     const uint32_t mb = *reinterpret_cast<const uint32_t*>(&m);
     uint32_t top = reduce(max(mb & 0xffffu, mb >> 16));
     const bool inf = top >= 0x7f80u;
-    if (inf) {  // once more without the infinities
+    if (inf) {  // once more without the infinities, which become NaN
       uint32_t f = 0;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t l = w[j] & 0x7fffu, u = (w[j] >> 16) & 0x7fffu;
           f = max(f, max(l < 0x7f80u ? l : 0u, u < 0x7f80u ? u : 0u));
+          w[j] |= (l == 0x7f80u ? 0x7fffu : 0u) | (u == 0x7f80u ? 0x7fff0000u : 0u);
         }
+        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
       top = reduce(f);
     }
     const int byte = max(kv8_scale_byte(top), old);
-    const float down = kv8_pow2(127 - byte);
+    // x / 2^e: exact in BF16, but for what is 0 in e4m3 anyway
+    const __nv_bfloat162 down = __float2bfloat162_rn(kv8_pow2(127 - byte));
+    uint8_t* to = codes + ((slot + in + row0) * a.h_kv + h) * a.d + col;
+    const int64_t to_step = (int64_t)step * a.h_kv * a.d;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int p = i * kKv8Threads + tid;
-      if (p >= pieces) break;
-      const int row = p >> a.per_shift;
+    for (int i = 0; i < kPieces; ++i, to += to_step) {
+      if (row0 + i * step >= rows) break;
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       uint32_t c[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float2 f = bf16x2_to_float2(w[j]);
-        if (inf) {  // an infinity times zero is a NaN
-          f.x = fmaf(f.x, down, f.x * 0.f);
-          f.y = fmaf(f.y, down, f.y * 0.f);
-        } else {
-          f.x *= down;
-          f.y *= down;
-        }
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), down);
+        const float2 f = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(&y));
         c[j] = kv8_pack2(f.x, f.y);
       }
-      *reinterpret_cast<uint2*>(codes + ((slot + in + row) * a.h_kv + h) * a.d + (p & (per - 1)) * 8) =
-          make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+      *reinterpret_cast<uint2*>(to) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     }
     if (in != 0 && byte > old) {  // the earlier tokens' codes to the new scale
       const float f = kv8_pow2(max(old - byte, -126));
