@@ -18,6 +18,11 @@
 // has; where a new token makes it grow by 2^k, the earlier codes are rounded
 // to the new scale: code / 2^k, exact but below 2^-6.  An infinity or a NaN
 // takes no part in the maximum and becomes a NaN, alone.
+//
+// Bound.  Writing reads 2 B a value and writes 1, reading back the reverse: HBM
+// for prompts, latency for a step.  60,374 tokens (2 KV heads, D = 256) take
+// 64.7 us written and read back, 0.94 of the copy rate (6,784 GB/s); a step of 32
+// tokens 4.2 us in a graph, two launches.
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -66,7 +71,10 @@ struct Kv8WriteArgs {
 // one block, for one head of K or V; it belongs to the CTA that has its first
 // token among its `chunk` tokens.  The unit's values stay in registers between
 // the maximum and the codes (kPieces * 8 of them a thread, a whole block at
-// most), so they are read once.
+// most), so they are read once.  Issue slots were the limit of the large calls
+// (74 % busy, 143 instructions for 8 values): with addresses that only step on
+// and the scaling as one BF16 pair product it is 86 (39 -> 32 us for 60,374
+// tokens).
 template <int kPieces>
 __global__ void __launch_bounds__(kKv8Threads, kPieces <= 8 ? 4 : 2)
 append_kv_fp8_kernel(const __grid_constant__ Kv8WriteArgs a) {

@@ -31,24 +31,43 @@
 //    ev_j (in powers of two): the weights 2^(y_j - M) stay within e4m3 whatever
 //    the scales are, the normaliser sum 2^(x_j - M) within FP32 (|ev| <= 64).
 //    M follows only when a weight would pass 2^5: then O is rescaled.
-//  - One CTA an SM.  4 to 16 warps turn S into P: a thread has one entry and 8 or
-//    12 pairs, so the sums of weights are its own registers until the end, and
+//  - One CTA an SM.  4 to 16 warps turn S into P: a thread has one entry and 8 to
+//    16 pairs, so the sums of weights are its own registers until the end, and
 //    the only exchange between threads is the vote on whether M has to grow
-//    (taken while the weights are being computed as if not).  One warp issues the MMAs, QK(i+1) before
-//    PV(i); four copy K and V rows with cp.async into a ring of tiles, in the
-//    order in which they are used; one finds the CTA's work.
+//    (taken, with up to 16 pairs, while the weights are computed as if not).
+//    One warp issues the MMAs, QK(i+1) before PV(i); two or four copy K and V
+//    rows with cp.async into a ring of tiles, in the order in which they are
+//    used; one finds the CTA's work.
 //  - Work, three ways.  Clusters: where the (tile, KV head) units are few, the C
 //    CTAs of a cluster (1 to 8) share one, a part of its blocks each, and join
 //    through distributed shared memory; one launch, no workspace.  Shares: the
 //    blocks of all units are numbered through, and each CTA takes an equal
 //    share of them, wherever that begins and ends, so that requests of any
 //    lengths keep all SMs busy; sums of units that several CTAs share meet in
-//    kv8_merge_kernel, through the workspace.  Many units: CTAs take whole
-//    units in turn.
+//    kv8_merge_kernel, through the workspace.  A unit's begin costs a CTA two
+//    blocks' time (its q, the sums of the unit before, the first M), so every
+//    unit is numbered with two blocks more.  Many units: CTAs take whole units
+//    in turn.
+//  - From one unit to the next: q is prepared, and its first products begin,
+//    before the sums of the unit before go out.
 //  - Rows of a tile that do not see an entry give it the weight 0.  A NaN of V
 //    there is replaced by 0 in shared memory, and noted for the pairs that do
 //    see it, whose sum becomes NaN.
 // Tensor memory columns: S two times 2 N, O D / 128 times parts N.
+//
+// Measured, us a call in a graph of calls on different inputs (a GB300, copy
+// rate 6,784 GB/s; in brackets the form before on mma.sync, where the warps
+// unpacked the codes): 32 rows of 2,051 (2 KV heads, D = 256) 18.0 (24.9), 3.8
+// TB/s; 192 rows (1 KV head of 16, D = 128) 28.4 (35.9); one row 8.2 (9.6); a
+// window of 4,096 for 32 requests 29.7 (36.7), 4.5 TB/s; 32 requests x 6 rows in
+// a window of 1,024 24.5 (54.9); 8 requests of up to 131,072 tokens 126 (260),
+// 6.1 TB/s; one of 20,011 14.3 (20.6).  A block (64 KB) takes 1.15 to 1.4 us with
+// 8 or 16 pairs, what its bytes take of HBM's rate, and 1.8 with 48 (the weights'
+// parts).  The rest is a call's ends: 3 to 4 us from its start to the first S
+// (three dependent loads, cold instructions), 2 to 3 for the last sums and the
+// join of a cluster, 3 for the merge.  What runs once takes as long as its
+// instructions take to arrive: hence loops of few passes are not unrolled and
+// rare cases are calls (184 -> 121 KB for 48 pairs).
 //
 // Waits on stages.  The ring's uses are numbered in the order K(0), K(1), V(0),
 // K(2), V(1), ... of a segment, over all segments; use u is in stage u mod

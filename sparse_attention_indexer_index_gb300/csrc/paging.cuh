@@ -10,10 +10,15 @@
 // or the rows, are the last ones that need any: sums of what is needed do not
 // decrease, so that both tests are comparisons with a running sum.
 //
-// Bound.  A few bytes a request and twelve a row: latency.  plan_step_kernel
-// is one CTA, in which a warp takes 32 requests at a time (a request a lane
-// for the sums and small tables, a request a warp for many pages); it also
-// writes the rows where they are few, else step_rows_kernel follows.
+// Bound.  A few bytes a request and twelve a row: latency.  plan_step_kernel is
+// one cluster of up to 8 CTAs.  Each computes all sums (a warp takes 32 requests
+// at a time, a request a lane); up to 2,048 requests they stay in shared memory
+// as a table, by which the first CTA hands out the pages, one a thread, and all
+// of them write the rows, a row a thread, four on the way together.  More
+// requests: a warp for a request's pages, and step_rows_kernel for the rows.
+// Plan and release in a graph: 32 decode requests 5.9 us, 1,500 of 0 to 6 tokens
+// 13.1 (one CTA: 15.9), 37 prompts of some 65,000 tokens in all 14.7 (one warp
+// for a request's pages and rows: 35.7).
 #pragma once
 #include "common.cuh"
 

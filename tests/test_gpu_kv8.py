@@ -398,7 +398,7 @@ def test_window_attn_fp8_edges(qsa, h_q, h_kv, d, page, block, window, n_sink, m
     window_check(qsa, rng, EDGE_LENS, page, block, h_q, h_kv, d, window, n_sink, spare_rows=3, max_rows=max_rows, ld=1)
 
 
-# 16, 32, 48 and 64 pairs a tile, one request's rows in several tiles, heads that do not divide 16
+# 8, 16, 32 and 48 pairs a tile, one request's rows in several tiles, heads that do not divide 16
 @pytest.mark.parametrize("h_q,h_kv,d,rows", [(16, 2, 256, 2), (16, 2, 256, 4), (16, 2, 256, 6), (16, 2, 256, 8),
                                              (16, 2, 256, 21), (8, 8, 128, 70), (16, 4, 128, 6), (5, 1, 128, 9),
                                              (16, 1, 256, 3), (7, 1, 256, 30), (16, 2, 128, 2), (16, 2, 128, 4)])
@@ -407,6 +407,29 @@ def test_window_attn_fp8_shared_tiles(qsa, h_q, h_kv, d, rows, window, n_sink):
     rng = np.random.default_rng(window + h_q + d + rows)
     lens = [list(range(c - rows + 1, c + 1)) for c in (rows, 331, 1200)] + [[77], [], [0] * rows]
     window_check(qsa, rng, lens, 32, 16, h_q, h_kv, d, window, n_sink, 2, sample=60)
+
+
+@pytest.mark.parametrize("lens", [[1, 1, 30], [30, 1, 1], [1, 40, 0, 0, 1, 9], [60] + [1] * 9])
+@pytest.mark.parametrize("h_q,h_kv,d", [(16, 2, 256), (8, 2, 128)])
+def test_window_attn_fp8_more_tiles_than_even_requests_have(qsa, lens, h_q, h_kv, d):
+    """Requests of very different numbers of rows: tiles past those that as
+    many requests of equal length would have."""
+    rng = np.random.default_rng(sum(lens) + d)
+    window_check(qsa, rng, [list(range(200, 200 + n)) for n in lens], 32, 32, h_q, h_kv, d, 90, 2, 3, sample=50)
+
+
+@pytest.mark.parametrize("n_req,h_kv", [(20, 8), (32, 5), (40, 4), (150, 1), (33, 16)])
+@pytest.mark.parametrize("d,rows", [(256, 1), (128, 1), (256, 3), (128, 4)])
+def test_window_attn_fp8_shares_of_uneven_requests(qsa, n_req, h_kv, d, rows):
+    """More units than SMs, cut into equal shares of their blocks: lengths of
+    nothing, of one entry, of a block and around it, and long ones."""
+    rng = np.random.default_rng(n_req + d + rows)
+    some = [0, 1, 127, 128, 129, 256, 257, 600, 3001]
+    lens = []
+    for i in range(n_req):
+        c = some[i % len(some)]
+        lens.append([max(0, c - rows + 1 + j) for j in range(1 if i % 7 == 3 else rows)])
+    window_check(qsa, rng, lens, 16, 16, 4 * h_kv, h_kv, d, 100000, 0, 2, max_rows=rows, sample=60)
 
 
 def test_window_attn_fp8_rows_in_any_order(qsa):
