@@ -173,13 +173,7 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
   const uint32_t top_t = (uint32_t)a.n_tok + 1u, top_p = (uint32_t)a.n_pool + 1u;
   pdl_wait_primary();
   int n_free = ld_in(a.n_free);
-  if (n_free < 0 || n_free > a.n_pool) {
-    if (threadIdx.x == 0) raise_fault(kFaultGrouping);
-    n_free = 0;
-  }
-  // every CTA has read it before the first one writes it
-  if (a.cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-  // sums of 32 requests
+  // sums of 32 requests (n_free is looked at behind them: the loads are on the way together)
   StepNeed x{0, 0u, 0u, 0, true};
   uint32_t it = 0, ip = 0;
   for (int g = warp; g < groups; g += warps) {
@@ -191,6 +185,12 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
       s_pg[g] = ip;
     }
   }
+  if (n_free < 0 || n_free > a.n_pool) {
+    if (threadIdx.x == 0) raise_fault(kFaultGrouping);
+    n_free = 0;
+  }
+  // every CTA has read it before the first one writes it
+  if (a.cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   if (threadIdx.x == 0) s_taken = 0;
   __syncthreads();
   // and before them
@@ -361,6 +361,10 @@ release_pages_kernel(const __grid_constant__ ReleaseArgs a) {
   const uint32_t top = (uint32_t)a.n_pool + 1u;
   pdl_wait_primary();
   int n_free = ld_in(a.n_free);
+  if (tid < a.n_req) {  // on their way to L2 meanwhile
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.from_page + tid) : "memory");
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.to_page + tid) : "memory");
+  }
   if (n_free < 0 || n_free > a.n_pool) {  // an unusable list takes nothing
     if (tid == 0) raise_fault(kFaultGrouping);
     n_free = a.n_pool;
