@@ -108,6 +108,34 @@ bool kv_shape_ok(int32_t h_q, int32_t h_kv, int32_t d) {
   return (d == 128 && group <= 16) || (d == 256 && group <= 8);
 }
 
+// Clusters per (row, KV head).  One, unless the clusters of 8 CTAs are too
+// few to fill the GPU and a row is long enough to pay for the merge launch.
+// The size of the workspace follows from it, so it depends on the arguments
+// alone (152 SMs, two CTAs each).
+int ka_groups(int64_t units, int64_t entries) {
+  const int64_t fill = 304 / (units * kKaMaxCluster);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, 16), entries / 4096));
+}
+
+// CTAs per cluster: the least of waves * (steps + start and end, about 4).
+// How many clusters run at once is the device's answer: on 152 SMs, 16
+// clusters of 7 do not where a CTA fills an SM (1,028 entries of D = 256: 23.7
+// us, in clusters of 6, which do, 17.6).
+int ka_cluster(int64_t units, int64_t entries, const KaKernel& k, const int* resident) {
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int c = 1; c <= kKaMaxCluster && resident[c] > 0; ++c) {
+    const int64_t waves = (units + resident[c] - 1) / resident[c];
+    const int64_t steps = (entries + (int64_t)k.entries * c - 1) / ((int64_t)k.entries * c);
+    const int64_t cost = waves * (steps + 4);
+    if (cost < least) {
+      least = cost;
+      best = c;
+    }
+  }
+  return best;
+}
+
 enum { kKaBf16Window = 0, kKaFp4Window = 1, kKaFp4List = 2 };
 
 qsa_status launch_ka(int cache, KvAttnArgs& a, int d, int64_t entries, void* workspace, cudaStream_t stream) {
@@ -118,14 +146,17 @@ qsa_status launch_ka(int cache, KvAttnArgs& a, int d, int64_t entries, void* wor
   const KvDevice* dev = nullptr;
   if (qsa_status st = kv_device(&dev)) return st;
   a.n_group = ka_groups(units, entries);
-  a.cluster = a.n_group > 1 ? kKaMaxCluster : ka_cluster(units, entries, k.entries, dev->ka[cache][shape]);
+  a.cluster = a.n_group > 1 ? kKaMaxCluster : ka_cluster(units, entries, k, dev->ka[cache][shape]);
   a.part = static_cast<float*>(workspace);
   if ((int64_t)a.n_rows * std::max(a.cluster * a.n_group, a.h_q) > INT32_MAX) return QSA_ERR_UNSUPPORTED;
   if (entries > (1 << 30)) return QSA_ERR_UNSUPPORTED;  // entry indices stay clear of 2^31
   const ClusterLaunch l(dim3((unsigned)((int64_t)a.n_rows * a.cluster * a.n_group), (unsigned)a.h_kv), k.threads, k.smem,
                         a.cluster, stream);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, k.fn, a);
-  if (e == cudaSuccess && a.n_group > 1) e = launch_merge(a, d, cache == kKaBf16Window ? 0.0f : (float)kK4Bias, stream);
+  if (e == cudaSuccess && a.n_group > 1)
+    e = launch_pdl(d == 256 ? kv_attn_merge_kernel<256> : kv_attn_merge_kernel<128>,
+                   dim3((unsigned)((int64_t)a.n_rows * a.h_q)), dim3((unsigned)d), 0, stream, a,
+                   cache == kKaBf16Window ? 0.0f : (float)kK4Bias);
   return launched(e);
 }
 
@@ -268,11 +299,6 @@ qsa_status check_cache4(const void* kc, const void* ks, const void* vc, const vo
 }  // namespace
 
 namespace qsa {
-cudaError_t launch_merge(const KvAttnArgs& a, int d, float bias, cudaStream_t stream) {
-  return launch_pdl(d == 256 ? kv_attn_merge_kernel<256> : kv_attn_merge_kernel<128>,
-                    dim3((unsigned)((int64_t)a.n_rows * a.h_q)), dim3((unsigned)d), 0, stream, a, bias);
-}
-
 bool kv_fault_word(cudaStream_t stream, bool clear, unsigned* bits) {
   if (cudaMemcpyFromSymbolAsync(bits, g_fault_word, sizeof(*bits), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess)

@@ -56,40 +56,8 @@ bool resident_clusters(F fn, int threads, size_t smem, int c, int sms, int* n) {
 
 inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
-// The merge of n_group partial results (kv_attn_merge_kernel), behind the
-// kernel that wrote them.
-cudaError_t launch_merge(const KvAttnArgs& a, int d, float bias, cudaStream_t stream);
-
 inline int64_t window_entries(int32_t max_len, int32_t window, int32_t n_sink) {
   return std::min<int64_t>(max_len, (int64_t)window + n_sink);
-}
-
-// Clusters per (row, KV head).  One, unless the clusters of 8 CTAs are too
-// few to fill the GPU and a row is long enough to pay for the merge launch.
-// The size of the workspace follows from it, so it depends on the arguments
-// alone (152 SMs, two CTAs each).
-inline int ka_groups(int64_t units, int64_t entries) {
-  const int64_t fill = 304 / (units * kKaMaxCluster);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, 16), entries / 4096));
-}
-
-// CTAs per cluster, of `step` entries a step each: the least of waves * (steps + start and end, about 4).
-// How many clusters run at once is the device's answer: on 152 SMs, 16
-// clusters of 7 do not where a CTA fills an SM (1,028 entries of D = 256: 23.7
-// us, in clusters of 6, which do, 17.6).
-inline int ka_cluster(int64_t units, int64_t entries, int step, const int* resident) {
-  int best = 1;
-  int64_t least = INT64_MAX;
-  for (int c = 1; c <= kKaMaxCluster && resident[c] > 0; ++c) {
-    const int64_t waves = (units + resident[c] - 1) / resident[c];
-    const int64_t steps = (entries + (int64_t)step * c - 1) / ((int64_t)step * c);
-    const int64_t cost = waves * (steps + 4);
-    if (cost < least) {
-      least = cost;
-      best = c;
-    }
-  }
-  return best;
 }
 
 inline qsa_status check_workspace(size_t need, const void* workspace, size_t bytes) {
