@@ -173,16 +173,30 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
   const uint32_t top_t = (uint32_t)a.n_tok + 1u, top_p = (uint32_t)a.n_pool + 1u;
   pdl_wait_primary();
   int n_free = ld_in(a.n_free);
-  // sums of 32 requests (n_free is looked at behind them: the loads are on the way together)
-  StepNeed x{0, 0u, 0u, 0, true};
-  uint32_t it = 0, ip = 0;
-  for (int g = warp; g < groups; g += warps) {
-    x = step_need(a, g * 32 + lane);
-    it = warp_sat_scan(min(x.n, top_t), top_t);
-    ip = warp_sat_scan(min(x.pages, top_p), top_p);
-    if (lane == 31) {
-      s_tok[g] = it;
-      s_pg[g] = ip;
+  // sums of 32 requests (n_free is looked at behind them: the loads are on the way together); a warp's
+  // first two groups, all that a table has, stay in registers
+  constexpr int kKeep = 2;
+  StepNeed x[kKeep];
+  uint32_t it[kKeep], ip[kKeep];
+#pragma unroll
+  for (int y = 0; y < kKeep; ++y) x[y] = step_need(a, (warp + y * warps) * 32 + lane);
+  auto sums = [&](int g, const StepNeed& n, uint32_t& t, uint32_t& p) {
+    t = warp_sat_scan(min(n.n, top_t), top_t);
+    p = warp_sat_scan(min(n.pages, top_p), top_p);
+    if (lane == 31 && g < groups) {
+      s_tok[g] = t;
+      s_pg[g] = p;
+    }
+  };
+#pragma unroll
+  for (int y = 0; y < kKeep; ++y)
+    if (y == 0 || warps < groups) sums(warp + y * warps, x[y], it[y], ip[y]);
+  const bool keep = groups <= kKeep * warps;
+  if (!keep) {
+#pragma unroll 1
+    for (int g = warp + kKeep * warps; g < groups; g += warps) {
+      uint32_t t, p;
+      sums(g, step_need(a, g * 32 + lane), t, p);
     }
   }
   if (n_free < 0 || n_free > a.n_pool) {
@@ -220,35 +234,46 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
   }
   __syncthreads();
   const bool fits = s_all[0] <= (uint32_t)a.n_tok && s_all[1] <= (uint32_t)n_free;
-  const bool keep = groups <= warps;  // one group a warp: still in registers
   uint32_t taken = s_all[1];
-  // the request's sums up to itself, and whether it is served
-  auto ends = [&](int g, uint32_t& et, uint32_t& ep) -> bool {
-    if (!keep) {
-      x = step_need(a, g * 32 + lane);
-      it = warp_sat_scan(min(x.n, top_t), top_t);
-      ip = warp_sat_scan(min(x.pages, top_p), top_p);
+  // the sums up to request 32 g + lane itself, and whether it is served
+  auto ends = [&](int g, const StepNeed& n, uint32_t t, uint32_t p, uint32_t& et, uint32_t& ep) -> bool {
+    et = sat_add(s_tok[g], t, top_t);
+    ep = sat_add(s_pg[g], p, top_p);
+    return n.ok && et <= (uint32_t)a.n_tok && (n.pages == 0 || ep <= (uint32_t)n_free);
+  };
+  // f(group, what its requests need, sums within the group) for the warp's groups
+  auto each = [&](auto f) {
+    StepNeed n = x[0];
+    uint32_t t = it[0], p = ip[0];
+#pragma unroll 1
+    for (int g = warp; g < groups; g += warps) {
+      f(g, n, t, p);
+      n = x[1];
+      t = it[1];
+      p = ip[1];
+      if (!keep && g + warps < groups && g >= warps) {  // (the third and on)
+        n = step_need(a, (g + warps) * 32 + lane);
+        t = warp_sat_scan(min(n.n, top_t), top_t);
+        p = warp_sat_scan(min(n.pages, top_p), top_p);
+      }
     }
-    et = sat_add(s_tok[g], it, top_t);
-    ep = sat_add(s_pg[g], ip, top_p);
-    return x.ok && et <= (uint32_t)a.n_tok && (x.pages == 0 || ep <= (uint32_t)n_free);
   };
   if (!fits) {  // the pages of those that are served
     if (threadIdx.x == 0) raise_fault(kFaultCapacity);
-    for (int g = warp; g < groups; g += warps) {
+    each([&](int g, const StepNeed& n, uint32_t t, uint32_t p) {
       uint32_t et, ep;
-      const bool served = ends(g, et, ep);
-      const uint32_t most = __reduce_max_sync(0xffffffffu, served && x.pages > 0 ? ep : 0u);
+      const bool served = ends(g, n, t, p, et, ep);
+      const uint32_t most = __reduce_max_sync(0xffffffffu, served && n.pages > 0 ? ep : 0u);
       if (lane == 0) atomicMax(&s_taken, most);
-    }
+    });
     __syncthreads();
     taken = s_taken;
   }
   const int base = n_free - (int)taken;
-  for (int g = warp; g < groups; g += warps) {
+  each([&](int g, const StepNeed& x, uint32_t it, uint32_t ip) {
     const int r = g * 32 + lane;
     uint32_t et, ep;
-    const bool served = ends(g, et, ep);
+    const bool served = ends(g, x, it, ip, et, ep);
     uint32_t b = __shfl_up_sync(0xffffffffu, it, 1);
     b = lane == 0 ? s_tok[g] : sat_add(s_tok[g], b, top_t);
     if (r < a.n_req && rank == 0) {
@@ -265,7 +290,7 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
         s_page[r] = (int)min(bp, taken);
         s_ctx[r] = served && x.n > 0 ? x.ctx : -1;
       }
-      continue;
+      return;
     }
     // pages: a warp for a request
     uint32_t todo = __ballot_sync(0xffffffffu, served && x.pages > 0);
@@ -278,7 +303,7 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
 #pragma unroll 4
       for (int i = lane; i < pages; i += 32) row[i] = ld_in(a.free_pages + at + i);
     }
-  }
+  });
   if (table) __syncthreads();
   if (table && rank == 0) {
     for (int i = threadIdx.x; i < (int)taken; i += blockDim.x) {
