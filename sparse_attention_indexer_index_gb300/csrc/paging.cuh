@@ -160,7 +160,7 @@ __device__ __forceinline__ void step_rows(const StepArgs& a, int t0) {
   step_row(a, t, real ? r : -1, pos, pos >= 0 ? ld_in(a.page_table + (int64_t)r * a.ld_pt + step_pages(a, (uint32_t)pos)) : -1);
 }
 
-__global__ void __launch_bounds__(kStepThreads)
+__global__ void __launch_bounds__(kStepThreads, 1)
 plan_step_kernel(const __grid_constant__ StepArgs a) {
   __shared__ uint32_t s_tok[kStepMaxGroups], s_pg[kStepMaxGroups];
   __shared__ uint32_t s_all[2], s_taken;
