@@ -20,6 +20,8 @@
 // 13.1 (one CTA: 15.9), 37 prompts of some 65,000 tokens in all 14.7 (one warp
 // for a request's pages and rows: 35.7).
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace qsa {
@@ -321,16 +323,21 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
   const int rows = (int)min(s_all[0], (uint32_t)a.n_tok), stride = a.cluster * blockDim.x;
   int top = 1;
   while (2 * top < a.n_req) top *= 2;
-  for (int t0 = rank * blockDim.x + threadIdx.x; t0 < a.n_tok; t0 += 4 * stride) {
-    int r[4], pos[4], page[4];  // four rows on the way together
+  // K rows a thread, on the way together: one where that is all, else four (each a piece of code of its
+  // own: what runs once has to be fetched first)
+  auto write = [&](auto k, int first) {
+    constexpr int K = decltype(k)::value;
+    const int t0 = first + threadIdx.x;
+    int r[K], pos[K], page[K];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) r[y] = 0;
+    for (int y = 0; y < K; ++y) r[y] = 0;
+#pragma unroll 1
     for (int d = top; d > 0; d >>= 1)  // the last request that starts at or before the row
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
+      for (int y = 0; y < K; ++y)
         if (r[y] + d < a.n_req && s_start[r[y] + d] <= t0 + y * stride) r[y] += d;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
+    for (int y = 0; y < K; ++y) {
       const int t = t0 + y * stride;
       pos[y] = page[y] = -1;
       if (t >= rows) {
@@ -344,9 +351,13 @@ plan_step_kernel(const __grid_constant__ StepArgs a) {
       page[y] = ld_in(pi < held ? a.page_table + (int64_t)r[y] * a.ld_pt + pi : a.free_pages + base + s_page[r[y]] + (pi - held));
     }
 #pragma unroll
-    for (int y = 0; y < 4; ++y)
+    for (int y = 0; y < K; ++y)
       if (t0 + y * stride < a.n_tok) step_row(a, t0 + y * stride, r[y], pos[y], page[y]);
-  }
+  };
+  int first = rank * blockDim.x;
+#pragma unroll 1
+  for (; first + stride < a.n_tok; first += 4 * stride) write(std::integral_constant<int, 4>{}, first);
+  if (first < a.n_tok) write(std::integral_constant<int, 1>{}, first);
 }
 
 __global__ void __launch_bounds__(kStepRowsThreads)
