@@ -396,50 +396,47 @@ release_pages_kernel(const __grid_constant__ ReleaseArgs a) {
   const int threads = blockDim.x, batch = 2 * threads;
   const uint32_t top = (uint32_t)a.n_pool + 1u;
   pdl_wait_primary();
-  int n_free = ld_in(a.n_free);
-  if (tid < a.n_req) {  // on their way to L2 meanwhile
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.from_page + tid) : "memory");
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.to_page + tid) : "memory");
-  }
-  if (n_free < 0 || n_free > a.n_pool) {  // an unusable list takes nothing
-    if (tid == 0) raise_fault(kFaultGrouping);
-    n_free = a.n_pool;
-  }
-  const uint32_t room = (uint32_t)(a.n_pool - n_free);
+  int n_free = ld_in(a.n_free);                              // (looked at behind the first loads of a batch)
   uint32_t before = 0;                                       // pages of the batches before
   for (int r0 = 0; r0 < a.n_req; r0 += batch) {
     const int m = min(batch, a.n_req - r0);
     if (tid == 0) s_n_many = 0;
     __syncthreads();
     int few[2][kReleaseFew];                                 // pages of the thread's requests with few entries
+    int from[2], n[2];
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
       const int i = z * threads + tid;
-      int from = 0, n = 0;
+      from[z] = i < m ? ld_in(a.from_page + r0 + i) : 0;
+      n[z] = i < m ? ld_in(a.to_page + r0 + i) : 0;
+    }
+    if (n_free < 0 || n_free > a.n_pool) {                   // an unusable list takes nothing
+      if (tid == 0) raise_fault(kFaultGrouping);
+      n_free = a.n_pool;
+    }
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      if (from[z] < n[z] && (from[z] < 0 || n[z] > a.ld_pt)) raise_fault(kFaultIndex);
+      const bool some = from[z] < n[z] && from[z] >= 0 && n[z] <= a.ld_pt;
+      n[z] = some ? n[z] - from[z] : 0;
+      from[z] = some ? from[z] : 0;
+      const int32_t* row = a.page_table + (int64_t)(r0 + z * threads + tid) * a.ld_pt + from[z];
+#pragma unroll
+      for (int y = 0; y < kReleaseFew; ++y) {
+        few[z][y] = -1;
+        if (y < n[z] && n[z] <= kReleaseFew) few[z][y] = ld_in(row + y);
+      }
+    }
+    const uint32_t room = (uint32_t)(a.n_pool - n_free);
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const int i = z * threads + tid;
       uint32_t c = 0;
 #pragma unroll
-      for (int y = 0; y < kReleaseFew; ++y) few[z][y] = -1;
-      if (i < m) {
-        const int f = ld_in(a.from_page + r0 + i), t = ld_in(a.to_page + r0 + i);
-        if (f < t && (f < 0 || t > a.ld_pt)) {
-          raise_fault(kFaultIndex);
-        } else if (f < t) {
-          from = f;
-          n = t - f;
-        }
-      }
-      if (n > kReleaseFew) {
-        s_many[atomicAdd(&s_n_many, 1)] = i;                 // (in any order)
-      } else {
-        const int32_t* row = a.page_table + (int64_t)(r0 + i) * a.ld_pt + from;
-#pragma unroll
-        for (int y = 0; y < kReleaseFew; ++y)
-          if (y < n) few[z][y] = ld_in(row + y);
-#pragma unroll
-        for (int y = 0; y < kReleaseFew; ++y) c += few[z][y] >= 0;
-      }
-      s_from[i] = from;
-      s_n[i] = n;
+      for (int y = 0; y < kReleaseFew; ++y) c += few[z][y] >= 0;
+      if (n[z] > kReleaseFew) s_many[atomicAdd(&s_n_many, 1)] = i;  // (in any order)
+      s_from[i] = from[z];
+      s_n[i] = n[z];
       s_count[i] = c;
     }
     __syncthreads();
@@ -510,6 +507,7 @@ release_pages_kernel(const __grid_constant__ ReleaseArgs a) {
     }
   }
   if (tid == 0) {
+    const uint32_t room = (uint32_t)(a.n_pool - n_free);
     if (before > room) raise_fault(kFaultCapacity);
     if (before > 0 && room > 0) *a.n_free = n_free + (int)min(before, room);
   }
