@@ -31,7 +31,7 @@
 //    ev_j (in powers of two): the weights 2^(y_j - M) stay within e4m3 whatever
 //    the scales are, the normaliser sum 2^(x_j - M) within FP32 (|ev| <= 64).
 //    M follows only when a weight would pass 2^5: then O is rescaled.
-//  - One CTA an SM.  4 to 16 warps turn S into P: a thread has one entry and 8 to
+//  - One CTA an SM.  4 to 12 warps turn S into P: a thread has one entry and 8 or
 //    16 pairs, so the sums of weights are its own registers until the end, and
 //    the only exchange between threads is the vote on whether M has to grow
 //    (taken, with up to 16 pairs, while the weights are computed as if not).
@@ -114,7 +114,9 @@ template <int D, int N, int PARTS, bool kWindow, bool kShared>
 struct K8Tc {
   static constexpr int kSub = N <= 16 ? 256 / D : 1;   // products of 128 entries to a block
   static constexpr int kBlock = 128 * kSub;            // entries of a block
-  static constexpr int kPer = N == 48 ? 12 : N == 16 && kSub == 2 ? 16 : 8;  // pairs of a thread
+  // Pairs of a thread.  16 where there are enough of them: their weights of a part are one 16-byte
+  // store, without bank conflicts (48 pairs by 12s: 24.5 us where this takes 23.0).
+  static constexpr int kPer = N >= 32 || (N == 16 && kSub == 2) ? 16 : 8;
   static constexpr int kSlices = N / kPer;             // softmax warps to an entry
   static constexpr int kSoft = 4 * kSub * kSlices;     // softmax warps
   static constexpr int kLoads = (N + kSoft - 1) / kSoft;  // pairs whose q a warp prepares
@@ -265,21 +267,14 @@ __device__ __forceinline__ void k8_ld4(uint32_t taddr, uint32_t* v) {
                : "r"(taddr)
                : "memory");
 }
-__device__ __forceinline__ void k8_st4(uint32_t taddr, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3])
-               : "memory");
-}
 template <int n>
-__device__ __forceinline__ void k8_ld(uint32_t taddr, uint32_t* v) {  // n columns: 8, 12 or 16
+__device__ __forceinline__ void k8_ld(uint32_t taddr, uint32_t* v) {  // n columns: 8 or 16
   k8_ld8(taddr, v);
-  if constexpr (n == 12) k8_ld4(taddr + 8, v + 8);
   if constexpr (n == 16) k8_ld8(taddr + 8, v + 8);
 }
 template <int n>
 __device__ __forceinline__ void k8_st(uint32_t taddr, const uint32_t* v) {
   k8_st8(taddr, v);
-  if constexpr (n == 12) k8_st4(taddr + 8, v + 8);
   if constexpr (n == 16) k8_st8(taddr + 8, v + 8);
 }
 // The wait for loads, through which their registers pass: no use of one can be
@@ -992,13 +987,12 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       if (more) load(after);
       if (w.rows >= 0) {                       // (before the loads are waited for)
         // the lanes' sums: half of the pairs go to each half of the lanes, and so on; in the end lane
-        // 32 / kFold i has pair i (of kFold pairs, those past kPer zeros)
-        constexpr int kFold = kPer <= 8 ? 8 : 16;
-        float y[kFold];
+        // 32 / kPer i has pair i
+        float y[kPer];
 #pragma unroll
-        for (int p = 0; p < kFold; ++p) y[p] = p < kPer ? l[p] : 0.f;
+        for (int p = 0; p < kPer; ++p) y[p] = l[p];
 #pragma unroll
-        for (int d = 16, n = kFold / 2; n > 0; d >>= 1, n >>= 1) {
+        for (int d = 16, n = kPer / 2; n > 0; d >>= 1, n >>= 1) {
           const bool up = (lane & d) != 0;
 #pragma unroll
           for (int p = 0; p < n; ++p) {
@@ -1007,9 +1001,8 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           }
         }
 #pragma unroll
-        for (int d = 16 / kFold; d > 0; d >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], d);
-        const int pair = lane / (32 / kFold);
-        if (lane % (32 / kFold) == 0 && pair < kPer) ctl.wsum[warp][pair] = y[0];
+        for (int d = 16 / kPer; d > 0; d >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], d);
+        if (lane % (32 / kPer) == 0) ctl.wsum[warp][lane / (32 / kPer)] = y[0];
         met_arrive();
       }
       if (more) {
@@ -1408,16 +1401,10 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
               const int n = i * N + p0;
               *reinterpret_cast<uint4*>(pb + (n >> 5) * 4096 + ((((n >> 4) & 1) ^ flip) << 4)) =
                   make_uint4(words[i][0], words[i][1], words[i][2], words[i][3]);
-            } else if constexpr (kPer == 8) {
+            } else {
               const int n = i * N + p0;
               *reinterpret_cast<uint2*>(pb + (n >> 5) * 4096 + ((((n >> 4) & 1) ^ flip) << 4) + (n & 15)) =
                   make_uint2(words[i][0], words[i][1]);
-            } else {
-#pragma unroll
-              for (int c = 0; c < kPer / 4; ++c) {
-                const int n = i * N + p0 + 4 * c;
-                *reinterpret_cast<uint32_t*>(pb + (n >> 5) * 4096 + ((((n >> 4) & 1) ^ flip) << 4) + (n & 15)) = words[i][c];
-              }
             }
           }
           if (again || !Sh::kAhead) break;
