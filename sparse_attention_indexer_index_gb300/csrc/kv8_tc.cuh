@@ -31,7 +31,7 @@
 //    ev_j (in powers of two): the weights 2^(y_j - M) stay within e4m3 whatever
 //    the scales are, the normaliser sum 2^(x_j - M) within FP32 (|ev| <= 64).
 //    M follows only when a weight would pass 2^5: then O is rescaled.
-//  - One CTA an SM.  4 to 12 warps turn S into P: a thread has one entry and 8 or
+//  - One CTA an SM.  4 to 12 warps turn S into P: a thread has one entry and 4 to
 //    16 pairs, so the sums of weights are its own registers until the end, and
 //    the only exchange between threads is the vote on whether M has to grow
 //    (taken, with up to 16 pairs, while the weights are computed as if not).
@@ -115,15 +115,17 @@ struct K8Tc {
   static constexpr int kSub = N <= 16 ? 256 / D : 1;   // products of 128 entries to a block
   static constexpr int kBlock = 128 * kSub;            // entries of a block
   // Pairs of a thread.  16 where there are enough of them: their weights of a part are one 16-byte
-  // store, without bank conflicts (48 pairs by 12s: 24.5 us where this takes 23.0).
-  static constexpr int kPer = N >= 32 || (N == 16 && kSub == 2) ? 16 : 8;
+  // store, without bank conflicts (48 pairs by 12s: 24.5 us where this takes 23.0).  4 with 8 pairs of
+  // D = 256: twice the warps for the q, the first block and the sums of calls of a few blocks (by 8s:
+  // 29.6 us for a window of 4,096, where this takes 28.7).
+  static constexpr int kPer = N >= 32 || (N == 16 && kSub == 2) ? 16 : N == 8 && kSub == 1 ? 4 : 8;
   static constexpr int kSlices = N / kPer;             // softmax warps to an entry
   static constexpr int kSoft = 4 * kSub * kSlices;     // softmax warps
   static constexpr int kLoads = (N + kSoft - 1) / kSoft;  // pairs whose q a warp prepares
   static constexpr int kProd = N >= 32 ? 2 : 4;        // producer warps
   static constexpr int kThreads = 32 * (kSoft + 2 + kProd);  // and MMA, work
   // Whether the vote on M is taken beside the weights (with registers to spare) or before them.
-  static constexpr bool kAhead = N <= 16 && kPer == 8;
+  static constexpr bool kAhead = N <= 16 && kPer <= 8;
   static constexpr int kTile = kBlock * D;             // bytes
   static constexpr int kNS = 2 * N, kNP = PARTS * N;   // columns of S (of a product) and of a half of O
   static constexpr int kGroups = (kNP + 31) / 32;      // groups of 32 columns of P
@@ -267,14 +269,21 @@ __device__ __forceinline__ void k8_ld4(uint32_t taddr, uint32_t* v) {
                : "r"(taddr)
                : "memory");
 }
+__device__ __forceinline__ void k8_st4(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
+}
 template <int n>
-__device__ __forceinline__ void k8_ld(uint32_t taddr, uint32_t* v) {  // n columns: 8 or 16
-  k8_ld8(taddr, v);
+__device__ __forceinline__ void k8_ld(uint32_t taddr, uint32_t* v) {  // n columns: 4, 8 or 16
+  if constexpr (n == 4) k8_ld4(taddr, v);
+  else k8_ld8(taddr, v);
   if constexpr (n == 16) k8_ld8(taddr + 8, v + 8);
 }
 template <int n>
 __device__ __forceinline__ void k8_st(uint32_t taddr, const uint32_t* v) {
-  k8_st8(taddr, v);
+  if constexpr (n == 4) k8_st4(taddr, v);
+  else k8_st8(taddr, v);
   if constexpr (n == 16) k8_st8(taddr + 8, v + 8);
 }
 // The wait for loads, through which their registers pass: no use of one can be
@@ -1401,6 +1410,9 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
               const int n = i * N + p0;
               *reinterpret_cast<uint4*>(pb + (n >> 5) * 4096 + ((((n >> 4) & 1) ^ flip) << 4)) =
                   make_uint4(words[i][0], words[i][1], words[i][2], words[i][3]);
+            } else if constexpr (kPer == 4) {
+              const int n = i * N + p0;
+              *reinterpret_cast<uint32_t*>(pb + (n >> 5) * 4096 + ((((n >> 4) & 1) ^ flip) << 4) + (n & 15)) = words[i][0];
             } else {
               const int n = i * N + p0;
               *reinterpret_cast<uint2*>(pb + (n >> 5) * 4096 + ((((n >> 4) & 1) ^ flip) << 4) + (n & 15)) =
