@@ -57,17 +57,17 @@
 //
 // Measured, us a call in a graph of calls on different inputs (a GB300, copy
 // rate 6,784 GB/s; in brackets the form before on mma.sync, where the warps
-// unpacked the codes): 32 rows of 2,051 (2 KV heads, D = 256) 18.0 (24.9), 3.8
-// TB/s; 192 rows (1 KV head of 16, D = 128) 28.4 (35.9); one row 8.2 (9.6); a
-// window of 4,096 for 32 requests 29.7 (36.7), 4.5 TB/s; 32 requests x 6 rows in
-// a window of 1,024 24.5 (54.9); 8 requests of up to 131,072 tokens 126 (260),
-// 6.1 TB/s; one of 20,011 14.3 (20.6).  A block (64 KB) takes 1.15 to 1.4 us with
-// 8 or 16 pairs, what its bytes take of HBM's rate, and 1.8 with 48 (the weights'
-// parts).  The rest is a call's ends: 3 to 4 us from its start to the first S
+// unpacked the codes): 32 rows of 2,051 (2 KV heads, D = 256) 17.6 (24.9), 3.9
+// TB/s; 192 rows (1 KV head of 16, D = 128) 28.3 (35.9); one row 8.2 (9.6); a
+// window of 4,096 for 32 requests 29.0 (36.7), 4.6 TB/s; 32 requests x 6 rows in
+// a window of 1,024 23.0 (54.9); 8 requests of up to 131,072 tokens 127 (260),
+// 6.0 TB/s; one of 20,011 14.0 (20.6).  A block (64 KB) takes 1.15 to 1.4 us with
+// 8 or 16 pairs, what its bytes take of HBM's rate, and about 1.5 with 48 (the
+// weights' parts).  The rest is a call's ends: 3 to 4 us from its start to the first S
 // (three dependent loads, cold instructions), 2 to 3 for the last sums and the
 // join of a cluster, 3 for the merge.  What runs once takes as long as its
 // instructions take to arrive: hence loops of few passes are not unrolled and
-// rare cases are calls (184 -> 121 KB for 48 pairs).
+// rare cases are calls (184 -> 121 KB for 48 pairs, at the time).
 //
 // Waits on stages.  The ring's uses are numbered in the order K(0), K(1), V(0),
 // K(2), V(1), ... of a segment, over all segments; use u is in stage u mod

@@ -14,11 +14,11 @@
 // one cluster of up to 8 CTAs.  Each computes all sums (a warp takes 32 requests
 // at a time, a request a lane); up to 2,048 requests they stay in shared memory
 // as a table, by which the first CTA hands out the pages, one a thread, and all
-// of them write the rows, a row a thread, four on the way together.  More
+// of them write the rows, one a thread, or four on the way together.  More
 // requests: a warp for a request's pages, and step_rows_kernel for the rows.
-// Plan and release in a graph: 32 decode requests 5.9 us, 1,500 of 0 to 6 tokens
-// 13.1 (one CTA: 15.9), 37 prompts of some 65,000 tokens in all 14.7 (one warp
-// for a request's pages and rows: 35.7).
+// Plan and release in a graph: 32 decode requests 5.4 us, 1,500 of 0 to 6 tokens
+// 10.2 (one CTA, sums taken twice: 15.9), 37 prompts of some 65,000 tokens in all
+// 14.3 (one warp for a request's pages and rows: 35.7).
 #pragma once
 #include <type_traits>
 
