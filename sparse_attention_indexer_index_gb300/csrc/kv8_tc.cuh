@@ -163,10 +163,10 @@ struct K8Tc {
     int pre[kWindow ? kK8MaxTiles + 1 : 1];    // blocks before tile t, kK8Lead more to each
     int4 tile[kWindow ? kK8MaxTiles : 1];      // its first row, request * 256 + rows, first, n
   };
-  // Rows of partial results: D sums, M and L.  A cluster's join:  Up to 16 pairs: a CTA writes a pair's row into the
-  // memory of the one that joins it, [source][own pair].  More: there is no room, and each keeps its
-  // rows, [pair], in its ring, whose last tile has been used by then, for the others to read (48
-  // pairs, 4 CTAs: 1.3 us less than writing there behind one more meeting; 8 pairs: 0.4 us more).
+  // Rows of partial results: D sums, M and L.  In a cluster of up to 16 pairs a CTA writes a pair's row
+  // into the memory of the one that joins it, [source][own pair].  With more there is no room, and each
+  // keeps its rows, [pair], in its ring, whose last tile has been used by then, for the others to read
+  // (48 pairs, 2 CTAs: 1.3 us less than writing there behind one more meeting; 8 pairs: 0.4 us more).
   static constexpr bool kPull = N > 16;
   static constexpr int kJoin = D + 4;
   static constexpr int kFixed = kQ + 2 * kP + (kPull ? 0 : N * kJoin * 4) + (int)sizeof(Ctl) + 1024;
