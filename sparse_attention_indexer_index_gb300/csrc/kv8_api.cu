@@ -108,9 +108,16 @@ struct K8Form {
   bool cluster, share; // clusters, shares, else whole units
 };
 // Clusters where the units are few and their blocks, shared by the CTAs of a
-// cluster, few as well; shares of the blocks where units are long (their joins
-// take a second kernel, about 5 blocks' time); whole units where they are many.
-// It follows from the arguments alone (152 SMs), as the workspace does.
+// cluster, few as well; shares of the blocks where units are long; whole units
+// where they are many.  The parts' way through memory, and the second kernel,
+// count as 9 blocks, which is what they take where all SMs read at HBM's rate; up
+// to 4 units only a few would, in clusters of 8 at most, and it is 3 (with 1 a
+// list of 2,051 takes 7.6 us instead of 8.2, but the host, which has a workspace
+// to find and a second kernel to launch, 4 us more).  Measured in a graph,
+// clusters / shares: 38 lists of 2,051 on 2 heads of D = 256 19.1 / 22.5 us, 50 of
+// 4,000 39.1 / 41.0, 4 of 9,000 15.6 / 16.5, 14 windows of 16,000 43.7 / 47.9; one
+// list of 5,000 10.4 / 7.8, of 9,000 14.5 / 8.8, 2 of 6,000 12.0 / 9.7.  It follows
+// from the arguments alone (152 SMs), as the workspace does.
 K8Form finish(int kind, int d, int rows, int64_t tile_slots, int64_t units, int64_t n_req, int64_t entries) {
   K8Form f{kind, rows, tile_slots, units, 1, false, false};
   const int block = kK8Kernels[kind][d == 256].block;
@@ -122,7 +129,7 @@ K8Form finish(int kind, int d, int rows, int64_t tile_slots, int64_t units, int6
   while (c < kKaMaxCluster && units * 2 * c <= 144 && f.blocks >= 2 * c) c *= 2;
   const int64_t rounds = (units * c + 151) / 152;
   const int64_t by_cluster = rounds * ((f.blocks + c - 1) / c);
-  const int64_t by_share = (units * (f.blocks + kK8Lead) + 151) / 152 + 5;
+  const int64_t by_share = (units * (f.blocks + kK8Lead) + 151) / 152 + (units <= 4 ? 3 : 9);
   f.cluster = rounds == 1 && (by_cluster <= by_share || !fits);
   f.share = !f.cluster && fits;
   return f;
