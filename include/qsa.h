@@ -468,9 +468,8 @@ qsa_status qsa_window_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
  * exactly, which are summed in FP32, as the softmax statistics are.  q and the
  * weights enter as sums of e4m3 numbers: a component of q is off by at most
  * 2^-22 of its (row, head)'s largest one, a weight times its V scale by 2^-16
- * of itself (small ones by 2^-28 of the row's largest); where rows of a request
- * share tiles of more than 8 (row, query head) pairs, whose outputs are BF16,
- * by 2^-12 (2^-23).
+ * of itself (small ones by 2^-28 of the row's largest, so over n entries, in the
+ * output, by up to n 2^-28 of that one times the largest code).
  *   max_rows_per_req  host upper bound of the rows of any one request: if it is
  *              above 1, rows of a request share what they read, up to 48 (row,
  *              query head) pairs at a time.  It never changes which positions

@@ -38,9 +38,9 @@ constexpr K8Kernel kK8Kernels[kK8Kinds][2] = {
     {k8<128, 16, 4, false, false>(), k8<256, 16, 4, false, false>()},
     {k8<128, 8, 4, true, false>(), k8<256, 8, 4, true, false>()},
     {k8<128, 8, 4, true, true>(), k8<256, 8, 4, true, true>()},
-    {k8<128, 16, 3, true, true>(), k8<256, 16, 3, true, true>()},
-    {k8<128, 32, 3, true, true>(), k8<256, 32, 3, true, true>()},
-    {k8<128, 48, 3, true, true>(), k8<256, 48, 3, true, true>()},
+    {k8<128, 16, 4, true, true>(), k8<256, 16, 4, true, true>()},
+    {k8<128, 32, 4, true, true>(), k8<256, 32, 4, true, true>()},
+    {k8<128, 48, 4, true, true>(), k8<256, 48, 4, true, true>()},
 };
 
 // Per-device one-time set-up: the shared-memory opt-in of the kernels, and how

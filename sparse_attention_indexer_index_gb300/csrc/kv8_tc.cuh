@@ -22,10 +22,11 @@
 //    in parts of 4 significant bits, as columns of their own: part i holds what
 //    the parts before left, times 32^i, which keeps it clear of e4m3's lower
 //    end.  q takes two parts: exact down to 2^-14 of the pair's largest
-//    component, off by 2^-22 of that at most below.  Weights take four (off by
-//    2^-16 of themselves, or 2^-28 of the largest), or three where the output
-//    is BF16 and there are more than 8 pairs (2^-12, 2^-23).  The parts are
-//    added in FP32 when S and O are read.
+//    component, off by 2^-22 of that at most below.  Weights take four: off by
+//    2^-16 of themselves, or 2^-28 of the largest (with three, 2^-12 and 2^-23,
+//    the many small weights of a long row behind a first token that holds
+//    nearly all of it were lost, and the normaliser still counted them).  The
+//    parts are added in FP32 when S and O are read.
 //  - The scales enter once an entry: 2^ek as a factor of the logit, 2^ev of the
 //    weight.  The reference of both sums is a running maximum M of y_j = x_j +
 //    ev_j (in powers of two): the weights 2^(y_j - M) stay within e4m3 whatever
@@ -53,7 +54,8 @@
 //  - Rows of a tile that do not see an entry give it the weight 0.  A NaN of V
 //    there is replaced by 0 in shared memory, and noted for the pairs that do
 //    see it, whose sum becomes NaN.
-// Tensor memory columns: S two times 2 N, O D / 128 times parts N.
+// Tensor memory columns: S two times 2 N (48 pairs of D = 256: once), O D / 128
+// times parts N.
 //
 // Measured, us a call in a graph of calls on different inputs (a GB300, copy
 // rate 6,784 GB/s; in brackets the form before on mma.sync, where the warps
@@ -131,7 +133,10 @@ struct K8Tc {
   static constexpr int kGroups = (kNP + 31) / 32;      // groups of 32 columns of P
   static constexpr int kPSub = kGroups * 4096;         // P of a product: [group][128 entries][32 B]
   static constexpr int kQ = kNS * D, kP = kSub * kPSub;
-  static constexpr int kColO = 2 * kSub * kNS;
+  // Buffers of S: two, one where O leaves no room for more (48 pairs of D = 256).  Then S(i + 1) begins
+  // when S(i) has been read, which is long before P(i) is there.
+  static constexpr int kSBuf = 2 * kSub * kNS + D / 128 * kNP <= 512 ? 2 : 1;
+  static constexpr int kColO = kSBuf * kSub * kNS;
   static_assert(kColO + D / 128 * kNP <= 512 && kNS % 16 == 0 && kNP % 16 == 0, "tensor memory");
   struct Seg {
     int t0, rows, r, g;    // first row, rows (-1: no more), request, KV head
@@ -895,9 +900,9 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
 #pragma unroll 1
       for (int i = 0; ok && i <= nb; ++i) {
         if (i < nb) {  // S(i)
-          const int sl = (x + i) & 1;
+          const int sl = (x + i) & 1, had = x + i - Sh::kSBuf;  // the block that had this buffer
           ok = k8_wait(&ctl.full[st], ph, abort) &&
-               (x + i < 2 || k8_wait(&ctl.s_free[sl], (uint32_t)((x + i - 2) >> 1) & 1u, abort));
+               (had < 0 || k8_wait(&ctl.s_free[had & 1], (uint32_t)(had >> 1) & 1u, abort));
           if (!ok) break;
           __syncwarp();
           tc_fence_after();
@@ -905,7 +910,7 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
           for (int y = 0; y < kSub; ++y)
 #pragma unroll
             for (int h = 0; h < H; ++h)
-              k8_mma4<2, 2>(tmem + (sl * kSub + y) * NS, k_desc0 + (uint64_t)((st * Sh::kTile + (h + y) * 16384) >> 4),
+              k8_mma4<2, 2>(tmem + (sl % Sh::kSBuf * kSub + y) * NS, k_desc0 + (uint64_t)((st * Sh::kTile + (h + y) * 16384) >> 4),
                             q_desc + (uint64_t)((h * NS * 128) >> 4), k8_idesc(NS, false), h > 0 ? 1u : 0u);
           next_stage();
           k8_commit(&ctl.s_full[sl]);
@@ -1253,8 +1258,8 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
         __syncwarp();
         tc_fence_after();
         uint32_t v[2 * kPer];
-        k8_ld<kPer>(lanes + (sl * kSub + sub) * NS + p0, v);
-        k8_ld<kPer>(lanes + (sl * kSub + sub) * NS + N + p0, v + kPer);
+        k8_ld<kPer>(lanes + (sl % Sh::kSBuf * kSub + sub) * NS + p0, v);
+        k8_ld<kPer>(lanes + (sl % Sh::kSBuf * kSub + sub) * NS + N + p0, v + kPer);
         // meanwhile the scales of the next block, slots of the one behind it
         const K8Scales now = sc;
         sc = k8_scales(a, k8_slot<kWindow, false>(a, w, entry(w, j + 1), next), w.g);
