@@ -102,7 +102,7 @@ qsa_status check_cache8(const void* kc, const void* ks, const void* vc, const vo
 // How a call is cut into tiles, and how the work is dealt.
 struct K8Form {
   int kind, rows;      // kernel, rows per tile
-  int64_t tile_slots;  // tiles at most
+  int64_t tile_slots;  // slots of tiles (see k8_find): as many as tiles at least
   int64_t units;       // (tile, KV head) pairs, for requests of equal length
   int64_t blocks;      // of a unit at most
   bool cluster, share; // clusters, shares, else whole units
@@ -145,7 +145,7 @@ K8Form window_form(int32_t n_rows, int32_t n_req, int32_t max_rows_per_req, int3
   const int64_t pairs = (int64_t)std::max(max_rows_per_req, 1) * group;
   const int kind = pairs <= 8 ? kTile8 : pairs <= 16 ? kTile16 : pairs <= 32 ? kTile32 : kTile48;
   const int rows = kK8Kernels[kind][0].pairs / group;
-  const int64_t slots = std::min<int64_t>(n_rows, n_rows / rows + (int64_t)n_req);
+  const int64_t slots = k8_tile_slots(n_rows, n_req, rows);
   const int64_t per_req = ((int64_t)n_rows + n_req - 1) / n_req;
   // (a tile of rows in any order may span more than a row)
   return finish(kind, d, rows, slots, std::min<int64_t>(slots, (int64_t)n_req * ((per_req + rows - 1) / rows)) * h_kv, n_req,

@@ -101,7 +101,7 @@ struct Kv8AttnArgs : KvAttnArgs {
   int32_t cluster_shift;     // log2 of the CTAs to a cluster
   uint32_t group_inv;        // pair / group = pair * group_inv >> 16
   int32_t rows;              // R: rows per tile
-  int32_t tile_slots;        // tiles at most
+  int32_t tile_slots;        // slots of tiles (see k8_find)
   int32_t mode;              // how the work is dealt
   int32_t n_units;           // (tile, KV head) pairs, for requests of equal length
   int4* jobs;                // [units or CTAs]: what kv8_merge_kernel joins: first CTA (-1: nothing), last CTA, first
@@ -515,10 +515,18 @@ __device__ __forceinline__ float k8_lse(float M, float L) {
   return L == 0.f ? ninf : (M == ninf ? L : M + log2f(L)) * 0.69314718055994531f;
 }
 // Request of tile s and the tile's number in it, by a whole warp (-1: none).  Up
-// to kK8Exact requests the tiles are counted; else slot s holds request r's
-// tiles from slot start[r] / R + r on (enough room: the requests before have at
-// most that many), and slots past its last tile are empty.
+// to kK8Exact requests the tiles are counted.  Else a tile has a slot of its own
+// among some that are empty, of which there are a.tile_slots: that of its first
+// row, where these are all rows' (few rows to a request), or else, for request
+// r's tiles, those from start[r] / R + r on (the requests before have at most
+// that many tiles, and all have n_rows / R + n_req).
 constexpr int kK8Exact = 1024;
+// The slots of n_rows rows in tiles of R: as many as tiles at least, whichever
+// way they are numbered.
+constexpr int64_t k8_tile_slots(int64_t n_rows, int64_t n_req, int R) {
+  const int64_t by_request = n_rows / R + n_req;
+  return n_rows < by_request ? n_rows : by_request;
+}
 __device__ __noinline__ int k8_find(const Kv8AttnArgs& a, int s, int& rank) {
   const int lane = threadIdx.x & 31;
   if (a.n_req <= kK8Exact) {
@@ -540,6 +548,13 @@ __device__ __noinline__ int k8_find(const Kv8AttnArgs& a, int s, int& rank) {
       s -= __shfl_sync(0xffffffffu, incl, 31);
     }
     return -1;
+  }
+  if (a.tile_slots == a.n_rows) {
+    const int r = warp_row_request(a.req_row_start, a.n_req, s);
+    if (r < 0) return -1;
+    const int in = s - ld_in(a.req_row_start + r);
+    rank = in / a.rows;
+    return in >= 0 && in == rank * a.rows && rank < k8_request_tiles(a, r) ? r : -1;
   }
   int lo = 0, n = a.n_req + 1;  // the last i with start[i] / R + i <= s, 32 samples a round
 #pragma unroll 1
