@@ -31,7 +31,9 @@
 //    weight.  The reference of both sums is a running maximum M of y_j = x_j +
 //    ev_j (in powers of two): the weights 2^(y_j - M) stay within e4m3 whatever
 //    the scales are, the normaliser sum 2^(x_j - M) within FP32 (|ev| <= 64).
-//    M follows only when a weight would pass 2^5: then O is rescaled.
+//    M follows only when a weight would pass 2^5: then O is rescaled.  Two such
+//    M may be 127 apart for the same logits, and the sum be as far from 1 the
+//    other way: it is scaled by 2^(d/2) twice (k8_half), as 2^-127 alone is 0.
 //  - One CTA an SM.  4 to 12 warps turn S into P: a thread has one entry and 4 to
 //    16 pairs, so the sums of weights are its own registers until the end, and
 //    the only exchange between threads is the vote on whether M has to grow
@@ -508,6 +510,10 @@ __device__ __forceinline__ int k8_request_tiles(const Kv8AttnArgs& a, int i) {
   }
   return (row1 - row0 + a.rows - 1) / a.rows;
 }
+// A step d of a reference is 2^d, here its half 2^(d/2): a sum of weights, which
+// may be as large as 2^d is small, is multiplied by it twice, a sum of weighted
+// values by its square.
+__device__ __forceinline__ float k8_half(float d) { return ka_ex2(0.5f * d); }
 // A pair's log-sum-exp from M (base 2) and the sum of its weights (without any
 // weight, or with NaN only, M = -inf).
 __device__ __forceinline__ float k8_lse(float M, float L) {
@@ -1207,16 +1213,16 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
                 l4[c] = f.y;
               }
               const float top = fmaxf(M, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
-              const float fm = M == ninf ? 1.f : ka_ex2(M - top);
+              const float hm = M == ninf ? 1.f : k8_half(M - top), fm = hm * hm;
               M = top;
-              L *= fm;
+              L = L * hm * hm;
 #pragma unroll
               for (int y = 0; y < V * 4; ++y) sum[y] *= fm;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 if (c0 + c >= C) break;
-                const float f = m[c] == ninf ? 0.f : ka_ex2(m[c] - M);
-                L += m[c] == ninf ? l4[c] : f * l4[c];  // without a weight (or with NaN only) M = -inf
+                const float h = m[c] == ninf ? 0.f : k8_half(m[c] - M), f = h * h;
+                L += m[c] == ninf ? l4[c] : l4[c] * h * h;  // without a weight (or with NaN only) M = -inf
 #pragma unroll
                 for (int y = 0; y < V * 4; ++y) sum[y] = fmaf(f, v[c][y], sum[y]);
               }
@@ -1364,12 +1370,15 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
             const float old = first ? kK8None : ctl.mb[p0 + lp];
             const float mn = top > old + (float)kKaGrow ? top : old;
             if (!first) {
-              const float fl = old == kK8None ? 1.f : ka_ex2(old - mn);
+              const float hl = old == kK8None ? 1.f : k8_half(old - mn), fl = hl * hl;
               float f[kPer];
 #pragma unroll
               for (int p = 0; p < kPer; ++p) {
-                f[p] = __shfl_sync(0xffffffffu, fl, p);
-                l[p] = (Sh::kAhead ? was[Sh::kAhead ? p : 0] : l[p]) * f[p];
+                const float h = __shfl_sync(0xffffffffu, hl, p);
+                // (a second exchange with 16 pairs a thread, where the product spilled 30 bytes more: 192 x 2051 28.4 us
+                // instead of 30.5; with fewer the product, 127.6 instead of 129.1 us for 8 long requests)
+                f[p] = Sh::kAhead ? h * h : __shfl_sync(0xffffffffu, fl, p);
+                l[p] = (Sh::kAhead ? was[Sh::kAhead ? p : 0] : l[p]) * h * h;
               }
               // O holds every product before this block's
               ok = meet() && k8_wait(&ctl.pv_done[sl ^ 1], (uint32_t)((x - 1) >> 1) & 1u, abort);
@@ -1529,9 +1538,9 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int n) {
     };
     float m = ninf, l = 0.f, o = 0.f;
     auto add = [&](float ms, float ls, float os) {  // with M at least ms
-      const float f = ms == ninf ? 0.f : ka_ex2(ms - m);
-      l += ms == ninf ? ls : f * ls;  // without a weight (or with NaN only) M = -inf
-      o = fmaf(f, os, o);
+      const float h = ms == ninf ? 0.f : k8_half(ms - m);
+      l += ms == ninf ? ls : ls * h * h;  // without a weight (or with NaN only) M = -inf
+      o = fmaf(h * h, os, o);
     };
     constexpr int kStep = kMany ? G : 1, kU = 4;
 #pragma unroll 1
@@ -1547,9 +1556,9 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a, int n) {
       float mn = m;
 #pragma unroll
       for (int i = 0; i < kU; ++i) mn = fmaxf(mn, c0 + i * kStep <= k ? ml[i].x : ninf);
-      const float g = m == ninf ? 1.f : ka_ex2(m - mn);  // (nothing or a NaN yet)
-      l *= g;
-      o *= g;
+      const float g = m == ninf ? 1.f : k8_half(m - mn);  // (nothing or a NaN yet)
+      l = l * g * g;
+      o *= g * g;
       m = mn;
 #pragma unroll
       for (int i = 0; i < kU; ++i)

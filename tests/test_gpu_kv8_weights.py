@@ -125,3 +125,43 @@ def test_same_window_call_gives_the_same_bits(qsa, n_req, rows, h_q, h_kv, d, ct
             torch.cuda.synchronize()
         for g in got:
             assert all(torch.equal(a, b) for a, b in zip(g, want)), i
+
+
+# -------------------------------------------------------- scales far apart
+def far_apart(n, h_kv, d, block, first, lo, hi):
+    """Codes 1 in K and V, V scales 2^lo in the first entries and 2^hi behind them."""
+    codes = np.full((n, h_kv, d), ref.encode(np.array([1.0]))[0], np.uint8)
+    ks = np.full((n // block, h_kv), 127, np.uint8)
+    vs = np.full((n // block, h_kv), 127 + hi, np.uint8)
+    vs[:first // block] = 127 + lo
+    return [codes, ks, codes.copy(), vs]
+
+
+@pytest.mark.parametrize("lo,hi", [(-64, 63), (63, -64), (-63, 63), (-40, 60)])
+@pytest.mark.parametrize("d,h_q", [(256, 8), (128, 8), (128, 16)])
+@pytest.mark.parametrize("n,first,rows", [(1024, 512, 300), (1024, 512, 2), (20480, 10240, 1), (512, 256, 400)])
+def test_sparse_attn_fp8_normaliser_with_v_scales_far_apart(qsa, lo, hi, d, h_q, n, first, rows):
+    """All logits 0: the log-sum-exp is log n, whatever the V scales are, in a
+    CTA alone, in a cluster and in shares; the output the mean of the values."""
+    cache = far_apart(n, 1, d, 64, first, lo, hi)
+    q = np.zeros((rows, h_q, d), np.uint16)
+    slots = np.broadcast_to(np.arange(n, dtype=np.int32), (rows, n)).copy()
+    out, lse = qsa.sparse_attn_fp8(bf16_dev(q), *map(to_dev, cache), to_dev(slots))
+    assert np.abs(host(lse) - np.log(n)).max() <= 2.0 ** -20 + (n / 16 + 64) * 2.0 ** -22 + 2.0 ** -20 * 2
+    want = (first * 2.0 ** lo + (n - first) * 2.0 ** hi) / n
+    assert np.abs(host(out) / want - 1).max() <= 2.0 ** -15 + (n / 16 + 64) * 2.0 ** -21
+
+
+@pytest.mark.parametrize("lo,hi", [(-64, 63), (63, -64), (-63, 62)])
+@pytest.mark.parametrize("d,rows", [(256, 1), (256, 6), (128, 1), (128, 4), (256, 2)])
+@pytest.mark.parametrize("n_req,n", [(1, 1024), (150, 1024), (1, 20480)])
+def test_window_attn_fp8_normaliser_with_v_scales_far_apart(qsa, lo, hi, d, rows, n_req, n):
+    cache = far_apart(n, 1, d, 64, n // 2, lo, hi)
+    q = np.zeros((n_req * rows, 8, d), np.uint16)
+    pt = np.broadcast_to(np.arange(n // 64, dtype=np.int32), (n_req, n // 64)).copy()
+    lens = np.full(n_req * rows, n, np.int32)
+    out, lse = qsa.window_attn_fp8(bf16_dev(q), *map(to_dev, cache), to_dev((np.arange(n_req + 1) * rows).astype(np.int32)),
+                                   to_dev(lens), to_dev(pt), 64, n, n, max_rows_per_req=rows)
+    assert np.abs(host(lse) - np.log(n)).max() <= 2.0 ** -20 * 3 + (n / 16 + 64) * 2.0 ** -22
+    want = (2.0 ** lo + 2.0 ** hi) / 2
+    assert np.abs(bits_to_f64(out) / want - 1).max() <= 2.0 ** -8 + 2.0 ** -14 + (n / 16 + 64) * 2.0 ** -21
