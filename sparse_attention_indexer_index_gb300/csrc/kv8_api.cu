@@ -104,7 +104,7 @@ struct K8Form {
   int kind, rows;      // kernel, rows per tile
   int64_t tile_slots;  // slots of tiles (see k8_find): as many as tiles at least
   int64_t units;       // (tile, KV head) pairs, for requests of equal length
-  int64_t blocks;      // of a unit at most
+  int64_t blocks;      // of a unit, where a tile's rows are neighbours
   bool cluster, share; // clusters, shares, else whole units
 };
 // Clusters where the units are few and their blocks, shared by the CTAs of a
@@ -118,13 +118,15 @@ struct K8Form {
 // 4,000 39.1 / 41.0, 4 of 9,000 15.6 / 16.5, 14 windows of 16,000 43.7 / 47.9; one
 // list of 5,000 10.4 / 7.8, of 9,000 14.5 / 8.8, 2 of 6,000 12.0 / 9.7.  It follows
 // from the arguments alone (152 SMs), as the workspace does.
-K8Form finish(int kind, int d, int rows, int64_t tile_slots, int64_t units, int64_t n_req, int64_t entries) {
+// `most` is what the rows of a tile can span in any order.
+K8Form finish(int kind, int d, int rows, int64_t tile_slots, int64_t units, int64_t n_req, int64_t entries, int64_t most) {
   K8Form f{kind, rows, tile_slots, units, 1, false, false};
   const int block = kK8Kernels[kind][d == 256].block;
   f.blocks = std::max<int64_t>(1, (entries + block - 1) / block);
   const bool list = kind <= kList16;
   const bool fits = units < kK8MaxUnits && (list || (tile_slots <= kK8MaxTiles && n_req <= kK8MaxTiles)) &&
-                    units * (f.blocks + kK8Lead) < INT32_MAX / 2;  // blocks are counted in 32 bits
+                    // blocks are counted in 32 bits (there are at most two slots to a unit)
+                    units * ((most + block - 1) / block + 1 + kK8Lead) < INT32_MAX / 2;
   int c = 1;
   while (c < kKaMaxCluster && units * 2 * c <= 144 && f.blocks >= 2 * c) c *= 2;
   const int64_t rounds = (units * c + 151) / 152;
@@ -135,13 +137,14 @@ K8Form finish(int kind, int d, int rows, int64_t tile_slots, int64_t units, int6
   return f;
 }
 K8Form list_form(int32_t n_rows, int32_t h_q, int32_t h_kv, int32_t d, int64_t n_idx) {
-  return finish(h_q / h_kv > 8 ? kList16 : kList8, d, 1, n_rows, (int64_t)n_rows * h_kv, 0, n_idx);
+  return finish(h_q / h_kv > 8 ? kList16 : kList8, d, 1, n_rows, (int64_t)n_rows * h_kv, 0, n_idx, n_idx);
 }
 K8Form window_form(int32_t n_rows, int32_t n_req, int32_t max_rows_per_req, int32_t h_q, int32_t h_kv, int32_t d,
                    int32_t max_len, int32_t window, int32_t n_sink) {
   const int group = h_q / h_kv;
   const int64_t entries = window_entries(max_len, window, n_sink);
-  if (max_rows_per_req <= 1 && group <= 8) return finish(kRow8, d, 1, n_rows, (int64_t)n_rows * h_kv, n_req, entries);
+  if (max_rows_per_req <= 1 && group <= 8)
+    return finish(kRow8, d, 1, n_rows, (int64_t)n_rows * h_kv, n_req, entries, entries);
   const int64_t pairs = (int64_t)std::max(max_rows_per_req, 1) * group;
   const int kind = pairs <= 8 ? kTile8 : pairs <= 16 ? kTile16 : pairs <= 32 ? kTile32 : kTile48;
   const int rows = kK8Kernels[kind][0].pairs / group;
@@ -149,7 +152,7 @@ K8Form window_form(int32_t n_rows, int32_t n_req, int32_t max_rows_per_req, int3
   const int64_t per_req = ((int64_t)n_rows + n_req - 1) / n_req;
   // (a tile of rows in any order may span more than a row)
   return finish(kind, d, rows, slots, std::min<int64_t>(slots, (int64_t)n_req * ((per_req + rows - 1) / rows)) * h_kv, n_req,
-                std::min<int64_t>(max_len, entries + rows));
+                std::min<int64_t>(max_len, entries + rows), rows == 1 ? entries : max_len);
 }
 
 // The jobs, then two partial results a CTA.
