@@ -94,6 +94,7 @@ constexpr int kK8Ctas = 152;       // CTAs of shares and whole units at most (on
 constexpr int kK8Bias = 3;         // weights are held as 2^kK8Bias w, w <= 2^kKaGrow
 constexpr int kK8SegRing = 2;
 constexpr int kK8Lead = 2;         // blocks' time that a unit's begin costs a CTA (shares count it)
+constexpr uint64_t kK8WaitNs = 2000000000ull;  // limit of a wait
 constexpr float kK8None = -1e30f;  // M of a pair that has seen nothing (finite: -inf less it is -inf)
 enum { kK8Cluster = 0, kK8Shares = 1, kK8Whole = 2 };
 
@@ -190,7 +191,7 @@ __device__ __noinline__ void k8_fault(unsigned bits) { raise_fault(bits); }
 __device__ __noinline__ bool k8_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint64_t t0 = global_timer_ns();
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-    const bool late = global_timer_ns() - t0 > 2000000000ull;
+    const bool late = global_timer_ns() - t0 > kK8WaitNs;
     if (__any_sync(0xffffffffu, late || *abort != 0)) {
       if ((threadIdx.x & 31) == 0) {
         if (*abort == 0) raise_fault(kFaultWait);
@@ -248,7 +249,7 @@ __device__ __noinline__ bool k8_wait_cluster(uint64_t* bar, volatile int* abort)
   };
   const uint64_t t0 = global_timer_ns();
   while (!__all_sync(0xffffffffu, arrived())) {
-    const bool late = global_timer_ns() - t0 > 2000000000ull;
+    const bool late = global_timer_ns() - t0 > kK8WaitNs;
     if (__any_sync(0xffffffffu, late || *abort != 0)) {
       if ((threadIdx.x & 31) == 0) {
         if (*abort == 0) raise_fault(kFaultWait);
@@ -955,9 +956,9 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
       }
       x += nb;
     }
-    // every MMA has finished before the memories are released
+    // every MMA has finished before the memories are released (also where a wait has been given up)
     k8_commit(&ctl.drain);
-    mbar_wait_bounded(&ctl.drain, 0u, 20000000ull);
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&ctl.drain, 0u, kK8WaitNs)) && lane == 0) k8_fault(kFaultWait);
   } else {
     // ---- softmax and outputs: a thread for an entry and a slice of the pairs --------------------
     const int slice = warp / (4 * kSub), p0 = slice * kPer, sub = (warp >> 2) % kSub;
