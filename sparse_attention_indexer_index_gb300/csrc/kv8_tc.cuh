@@ -94,7 +94,8 @@ constexpr int kK8Ctas = 152;       // CTAs of shares and whole units at most (on
 constexpr int kK8Bias = 3;         // weights are held as 2^kK8Bias w, w <= 2^kKaGrow
 constexpr int kK8SegRing = 2;
 constexpr int kK8Lead = 2;         // blocks' time that a unit's begin costs a CTA (shares count it)
-constexpr uint64_t kK8WaitNs = 2000000000ull;  // limit of a wait
+constexpr uint64_t kK8WaitNs = 2000000000ull;  // limit of a wait for a few blocks' work (a block takes 1.5 us at most)
+constexpr uint32_t kK8BlockNs = 20000;         // and for every block of a segment where one lies in between
 constexpr float kK8None = -1e30f;  // M of a pair that has seen nothing (finite: -inf less it is -inf)
 enum { kK8Cluster = 0, kK8Shares = 1, kK8Whole = 2 };
 
@@ -188,10 +189,10 @@ struct K8Tc {
 // (What is rare is kept out of line: a kernel of 100 KB and more fetched its
 // instructions for longer than it ran them, where each is run once or twice.)
 __device__ __noinline__ void k8_fault(unsigned bits) { raise_fault(bits); }
-__device__ __noinline__ bool k8_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __noinline__ bool k8_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int blocks) {
   const uint64_t t0 = global_timer_ns();
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-    const bool late = global_timer_ns() - t0 > kK8WaitNs;
+    const bool late = global_timer_ns() - t0 > kK8WaitNs + (uint64_t)blocks * kK8BlockNs;
     if (__any_sync(0xffffffffu, late || *abort != 0)) {
       if ((threadIdx.x & 31) == 0) {
         if (*abort == 0) raise_fault(kFaultWait);
@@ -203,8 +204,8 @@ __device__ __noinline__ bool k8_wait_long(uint64_t* bar, uint32_t parity, volati
   return true;
 }
 // Bounded wait by a whole warp, which stays together.
-__device__ __forceinline__ bool k8_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || k8_wait_long(bar, parity, abort);
+__device__ __forceinline__ bool k8_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int blocks = 0) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || k8_wait_long(bar, parity, abort, blocks);
 }
 // One arrival for a warp, behind what its lanes did.
 __device__ __forceinline__ void k8_arrive(uint64_t* bar) {
@@ -685,10 +686,13 @@ kv8_tc_kernel(const __grid_constant__ Kv8AttnArgs a) {
     // (the rows' lengths on their way to L2 beside the requests' starts)
     if (kWindow && (a.mode != kK8Shares || few) && lane * 32 < a.n_rows && a.n_rows <= 1024)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(a.row_len + lane * 32) : "memory");
-    int k = 0;
+    int k = 0, most = 0;  // segments, and the blocks of the longest
     auto publish = [&](const Seg& w) -> bool {
       const int sl = k % kK8SegRing;
-      if (k >= kK8SegRing && !k8_wait(&ctl.seg_empty[sl], (uint32_t)(k / kK8SegRing - 1) & 1u, abort)) return false;
+      // a segment is taken up when the one before it is done: that may be a whole long one (the other roles,
+      // for which segments lie ready, wait for a few blocks)
+      if (k >= kK8SegRing && !k8_wait(&ctl.seg_empty[sl], (uint32_t)(k / kK8SegRing - 1) & 1u, abort, most)) return false;
+      most = max(most, w.j1 - w.j0);
       if (lane == 0) {
         ctl.seg[sl] = w;
         mbar_arrive(&ctl.seg_full[sl]);

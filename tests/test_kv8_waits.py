@@ -31,3 +31,14 @@ def test_loops_on_a_barrier_have_a_limit():
         body = SRC[m.start():m.start() + 300]
         assert "kK8WaitNs" in body, body
     assert len(re.findall(r"while \(!", SRC)) == 2
+
+
+def test_the_wait_that_spans_a_segment_allows_for_its_blocks():
+    """The warp that finds the work waits until a segment is taken up, which is
+    when the one before it is done.  That may have 2^23 blocks (2^30 entries), at
+    1.5 us or more each: far more than the limit of the other waits."""
+    publish = KERNEL[KERNEL.index("auto publish = "):KERNEL.index("bool ok = true;")]
+    assert re.search(r"k8_wait\(&ctl\.seg_empty\[sl\], [^;]*, abort, most\)\) return false;\s*most = max\(most, w\.j1 - w\.j0\);", publish)
+    assert "t0 > kK8WaitNs + (uint64_t)blocks * kK8BlockNs" in SRC
+    limit = [int(re.search(rf"constexpr uint(64|32)_t {n} = (\d+)(ull)?;", SRC).group(2)) for n in ("kK8WaitNs", "kK8BlockNs")]
+    assert all(limit[0] + n * limit[1] >= 10 * n * 1500 for n in (1, 1000, 2 ** 23))
