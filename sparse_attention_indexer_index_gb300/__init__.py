@@ -910,11 +910,14 @@ def _window_call(fn, cache_ptrs, scales, n_slots, h_kv, d, q, req_row_start, row
 # the first @ by the number of elements.
 def _fit(spec, *tensors):
     global _fit
-    _torch()
+    torch = _torch()
     try:
-        from ._tensors import fit
+        from ._tensors import fit, torch_version
     except ImportError:
         fit = _fit_py
+    else:
+        if torch_version != torch.__version__:  # it reads tensors as that torch lays them out
+            fit = _fit_py
     _fit = fit
     return fit(spec, *tensors)
 

@@ -104,6 +104,32 @@ def tensors_path() -> str:
     return os.path.join(_HERE, "_tensors" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 
+def _tensors_stamp() -> str:
+    """The file that says for which torch tensors_path() was built.  The
+    extension has torch's tensor layout compiled in, and another torch's files
+    may be older than it."""
+    return tensors_path() + ".torch"
+
+
+def _torch_version(torch_dir: str) -> str | None:
+    """The version that torch.__version__ gives, without importing torch."""
+    import re
+    try:
+        with open(os.path.join(torch_dir, "version.py")) as f:
+            m = re.search(r"^__version__\s*=\s*['\"]([^'\"]+)['\"]", f.read(), re.M)
+    except OSError:
+        return None
+    return m.group(1) if m else None
+
+
+def _read(path: str) -> str | None:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def _start_tensors(force: bool):
     """Starts the compiler on _tensors.cpp: (process, its output), or None
     where there is nothing to do or no way (the Python form is used then)."""
@@ -120,25 +146,31 @@ def _start_tensors(force: bool):
     headers = os.path.join(torch_dir, "include")
     if not inc or not os.path.exists(os.path.join(inc, "Python.h")) or not os.path.isdir(headers):
         return None
-    deps = [TENSORS_SRC, os.path.join(torch_dir, "version.py")]
-    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(p) for p in deps):
+    version = _torch_version(torch_dir)
+    if version is None:
+        return None
+    if (not force and os.path.exists(out) and os.path.getmtime(out) >= os.path.getmtime(TENSORS_SRC)
+            and _read(_tensors_stamp()) == version):
         return None
     tmp = out + f".{os.getpid()}.tmp"
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-I", inc, "-isystem", headers, "-isystem",
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", f'-DQSA_TORCH_VERSION="{version}"', "-I", inc, "-isystem", headers, "-isystem",
            os.path.join(headers, "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
            TENSORS_SRC, "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
-    return subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=subprocess.PIPE, text=True), tmp
+    return subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=subprocess.PIPE, text=True), tmp, version
 
 
 def _finish_tensors(started) -> str | None:
     if started is None:
         return None
-    run, tmp = started
+    run, tmp, version = started
     run.communicate()
     if run.returncode != 0:
         return None
     os.replace(tmp, tensors_path())
+    with open(tmp, "w") as f:
+        f.write(version)
+    os.replace(tmp, _tensors_stamp())
     return tensors_path()
 
 

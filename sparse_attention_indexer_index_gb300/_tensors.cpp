@@ -5,7 +5,8 @@
 // call, more than the launch (2.5 us) and for small steps more than the
 // kernels; here it takes 1.  `fit` only looks: what does not fit is None, and
 // the Python module says what it was.  It has the same function in Python for
-// where this was not built.
+// where this was not built, or was built for another torch (torch_version),
+// whose tensors may be laid out differently.
 #define PY_SSIZE_T_CLEAN
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -142,4 +143,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", "Checks of a call's ten
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensors(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__tensors(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", QSA_TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
