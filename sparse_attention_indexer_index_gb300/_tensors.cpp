@@ -38,8 +38,7 @@ struct Dims {
   }
 };
 
-// fit(spec, tensors...): see _fit_py in the Python module.
-PyObject* fit(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+PyObject* look(PyObject* const* a, Py_ssize_t n_args) {
   Py_ssize_t len = 0;
   const char* s = n_args > 0 ? PyUnicode_AsUTF8AndSize(a[0], &len) : nullptr;
   if (s == nullptr) {
@@ -133,6 +132,20 @@ PyObject* fit(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     return nullptr;
   }
   return r;
+}
+
+// fit(spec, tensors...): see _fit_py in the Python module.  Tensors without
+// sizes, strides or an address (sparse ones, those inside vmap) throw when they
+// are asked for them.
+PyObject* fit(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  try {
+    return look(a, n_args);
+  } catch (const c10::Error& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+  } catch (const std::exception& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
 }
 
 PyMethodDef methods[] = {
