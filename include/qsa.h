@@ -473,8 +473,9 @@ qsa_status qsa_window_attn_fp4(const void* q, int64_t ld_q, const void* k_codes,
  *   max_rows_per_req  host upper bound of the rows of any one request: if it is
  *              above 1, rows of a request share what they read, up to 48 (row,
  *              query head) pairs at a time.  It never changes which positions
- *              count.  Requests of very many rows (chunks, prompts) take less
- *              on rows read back (qsa_gather_kv_fp8) and qsa_window_attn.
+ *              count.  Requests of many rows (from some 64 on: chunks, prompts)
+ *              take less on rows read back (qsa_gather_kv_fp8) and
+ *              qsa_window_attn.
  *   workspace  as the matching *_workspace_size(): 0 where a (row, KV head)'s
  *              entries are read by one CTA or one cluster, else room for what
  *              152 CTAs have of the sums (2.5 MB for 8 pairs of head_dim 256).

@@ -114,10 +114,16 @@ struct K8Form {
 // to 4 units only a few would, in clusters of 8 at most, and it is 3 (with 1 a
 // list of 2,051 takes 7.6 us instead of 8.2, but the host, which has a workspace
 // to find and a second kernel to launch, 4 us more).  Measured in a graph,
-// clusters / shares: 38 lists of 2,051 on 2 heads of D = 256 19.1 / 22.5 us, 50 of
-// 4,000 39.1 / 41.0, 4 of 9,000 15.6 / 16.5, 14 windows of 16,000 43.7 / 47.9; one
-// list of 5,000 10.4 / 7.8, of 9,000 14.5 / 8.8, 2 of 6,000 12.0 / 9.7.  It follows
-// from the arguments alone (152 SMs), as the workspace does.
+// clusters / shares: 38 lists of 2,051 on 2 heads of D = 256 19.6 / 22.9 us, 50 of
+// 4,000 39.2 / 41.6, 4 of 9,000 15.7 / 16.2, 14 windows of 16,000 43.5 / 48.7; one
+// list of 5,000 10.4 / 7.8, of 9,000 14.9 / 8.8, 2 of 6,000 12.1 / 9.7.  In a stream
+// of calls, where the host's time for shares shows, those three take 11.9 / 14 to
+// 17, 16.2 / 13 to 18 and 13.3 / 19 to 21: decode steps are captured.
+// The choice follows from the arguments alone, as the workspace does: for 152 SMs,
+// of which clusters of 2 fill 152 at once, of 4 144 and of 8 120.  144 stands for
+// all sizes here; a launch takes the sizes that fit the device (launch_k8): with 73
+// to 76 units clusters of 2 where this counts on single CTAs, with 16 to 18 units
+// clusters of 4 where it counts on 8.
 // `most` is what the rows of a tile can span in any order.
 K8Form finish(int kind, int d, int rows, int64_t tile_slots, int64_t units, int64_t n_req, int64_t entries, int64_t most) {
   K8Form f{kind, rows, tile_slots, units, 1, false, false};

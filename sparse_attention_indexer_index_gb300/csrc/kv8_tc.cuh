@@ -61,13 +61,13 @@
 //
 // Measured, us a call in a graph of calls on different inputs (a GB300, copy
 // rate 6,784 GB/s; in brackets the form before on mma.sync, where the warps
-// unpacked the codes): 32 rows of 2,051 (2 KV heads, D = 256) 17.6 (24.9), 3.9
-// TB/s; 192 rows (1 KV head of 16, D = 128) 28.3 (35.9); one row 8.2 (9.6); a
+// unpacked the codes): 32 rows of 2,051 (2 KV heads, D = 256) 17.7 (24.9), 3.9
+// TB/s; 192 rows (1 KV head of 16, D = 128) 28.5 (35.9); one row 8.3 (9.6); a
 // window of 4,096 for 32 requests 29.0 (36.7), 4.6 TB/s; 32 requests x 6 rows in
-// a window of 1,024 23.0 (54.9); 8 requests of up to 131,072 tokens 127 (260),
-// 6.0 TB/s; one of 20,011 14.0 (20.6).  A block (64 KB) takes 1.15 to 1.4 us with
-// 8 or 16 pairs, what its bytes take of HBM's rate, and about 1.5 with 48 (the
-// weights' parts).  The rest is a call's ends: 3 to 4 us from its start to the first S
+// a window of 1,024 24.2 (54.9; 23.0 with three parts to a weight); 8 requests of
+// up to 131,072 tokens 125 to 128 (260), 6.0 TB/s; one of 20,011 14.1 (20.6).  A
+// block (64 KB) takes 1.15 to 1.4 us with 8 or 16 pairs, what its bytes take of
+// HBM's rate, and about 1.5 with 48 (the weights' parts).  The rest is a call's ends: 3 to 4 us from its start to the first S
 // (three dependent loads, cold instructions), 2 to 3 for the last sums and the
 // join of a cluster, 3 for the merge.  What runs once takes as long as its
 // instructions take to arrive: hence loops of few passes are not unrolled and
@@ -88,8 +88,18 @@
 
 namespace qsa {
 
-constexpr int kK8MaxUnits = 1216;  // shares below, whole units from there on
-constexpr int kK8MaxTiles = 304;   // (windows: tiles that a CTA's tables hold)
+// Shares below so many units, whole units in turn from there on.  Shares keep all
+// SMs busy where lengths differ, and cost the merge.  Measured in a graph, whole
+// units / shares: 100, 150 and 300 requests of 2,000 to 40,000 tokens 595 / 312,
+// 678 / 475, 1294 / 944 us; rows of equal length, at worst 300, 600 and 1,200
+// lists of 2,051 on 1 KV head of D = 128 34.7 / 38.9, 63.8 / 68.2, 122.6 / 126.0;
+// 1,600 and 2,400 units of 2,051 on 2 heads of D = 256 259 / 259 and 377 / 383.
+constexpr int kK8MaxUnits = 1216;
+// Tiles, and requests, that a CTA's tables of shares hold.  More of them take whole
+// units in turn, whatever their lengths: 304 and 305 of the uneven requests above
+// 955 and 1298 us, 400 of them 1495; of equal length no matter (608 windows of
+// 4,096 374 us, the copy rate).
+constexpr int kK8MaxTiles = 304;
 constexpr int kK8Ctas = 152;       // CTAs of shares and whole units at most (one an SM)
 constexpr int kK8Bias = 3;         // weights are held as 2^kK8Bias w, w <= 2^kKaGrow
 constexpr int kK8SegRing = 2;
@@ -121,7 +131,7 @@ struct K8Tc {
   static constexpr int kSub = N <= 16 ? 256 / D : 1;   // products of 128 entries to a block
   static constexpr int kBlock = 128 * kSub;            // entries of a block
   // Pairs of a thread.  16 where there are enough of them: their weights of a part are one 16-byte
-  // store, without bank conflicts (48 pairs by 12s: 24.5 us where this takes 23.0).  4 with 8 pairs of
+  // store, without bank conflicts (48 pairs by 12s: 24.5 us where this took 23.0, with three parts).  4 with 8 pairs of
   // D = 256: twice the warps for the q, the first block and the sums of calls of a few blocks (by 8s:
   // 29.6 us for a window of 4,096, where this takes 28.7).
   static constexpr int kPer = N >= 32 || (N == 16 && kSub == 2) ? 16 : N == 8 && kSub == 1 ? 4 : 8;
